@@ -14,7 +14,9 @@ Entry points (same names as the C ABI):
   ``(dx, dw)``;
 * ``cake_rmsnorm_bwd_workspace_size`` / ``cake_rmsnorm_bwd_workspace``;
 * ``cake_rmsnorm_bwd_select`` (the window table's choice; host only);
-* ``cake_rmsnorm_device_status``, ``cake_status_str``.
+* ``cake_rmsnorm_device_status``, ``cake_status_str``;
+* the training-step operators around the norm (sandwich norm, gradient norm
+  and clipping, embedding): the module ``step``, whose names are here too.
 
 Names follow the pages' Python facade (PR #8208 page, description:
 forward / backward / workspace entry points taking ``deterministic``, default
@@ -124,6 +126,7 @@ def load_library(path: str = LIB_PATH):
                                                     _P(ctypes.c_int), _P(ctypes.c_int)]
         lib.cake_rmsnorm_device_status.restype = ctypes.c_int
         lib.cake_rmsnorm_device_status.argtypes = [_P(ctypes.c_int), ctypes.c_int]
+        step._bind(lib)
         _lib = lib
         return lib
 
@@ -461,7 +464,8 @@ def cake_rmsnorm_plan_occupancy(shape, backward=True, has_extra=False, determini
 
 
 def cake_rmsnorm_device_status(clear: bool = True) -> int:
-    """The kernels' device status word (0, or 5 after a bounded wait ran out).  Synchronises."""
+    """The kernels' device status word (0; 5 after a bounded wait ran out; 1 after an embedding
+    met an id outside its table).  Synchronises."""
     lib = load_library()
     code = ctypes.c_int(0)
     _check(lib.cake_rmsnorm_device_status(ctypes.byref(code), int(bool(clear))), "cake_rmsnorm_device_status")
@@ -475,3 +479,9 @@ from .train import (CakeRMSNormFunction, cake_rmsnorm, cake_rmsnorm_train_backwa
 
 __all__ += ["CakeRMSNormFunction", "cake_rmsnorm", "cake_rmsnorm_train_forward", "cake_rmsnorm_train_backward",
             "cake_rmsnorm_train_backward_workspace_bytes", "cake_rmsnorm_train_backward_workspace"]
+
+# the training-step operators around the norm
+from . import step  # noqa: E402
+from .step import *  # noqa: E402,F401,F403
+
+__all__ += step.__all__

@@ -1,6 +1,6 @@
 """Build ``libcake_rmsnorm.so`` in-tree with nvcc for sm_103a.
 
-Each ``csrc/*.cu`` file compiles in its own nvcc process (in parallel), then
+Each ``csrc/*.cu`` and ``csrc_step/*.cu`` file compiles in its own nvcc process (in parallel), then
 nvcc links them into one shared library next to this file.  The CUDA runtime
 is linked statically, so the library needs only the driver at run time.
 """
@@ -14,6 +14,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
+CSRC_STEP = os.path.join(HERE, "csrc_step")  # the training-step operators around the norm
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libcake_rmsnorm.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
@@ -30,12 +31,13 @@ def _nvcc() -> str:
 
 
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+    return sorted(os.path.join(d, f) for d in (CSRC, CSRC_STEP) for f in os.listdir(d) if f.endswith(".cu"))
 
 
 def _inputs():
-    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    files.append(os.path.join(INCLUDE, "cake_rmsnorm.h"))
+    files = sources()
+    for d in (CSRC, CSRC_STEP, INCLUDE):
+        files += [os.path.join(d, f) for f in os.listdir(d) if f.endswith((".cuh", ".h"))]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -1,0 +1,268 @@
+// cake_grads.cu -- the global L2 norm of many gradient tensors, and clipping
+// by it, for sm_103a.
+//
+//   norm = sqrt(sum g^2),  coef = min(1, max_norm / (norm + eps)),  out = round(g * coef)
+//
+// The tensors' addresses travel in the launch parameters, so a call uses no
+// device memory but one FP64 partial per CTA.  All tensors are cut into chunks
+// of kGradChunk values; CTA b takes chunks b, b + ctas, ...  Two kernels: the
+// first leaves a partial sum of squares per CTA, the second adds the partials
+// up (every CTA does, in the same order, so that no third launch and no wait
+// between CTAs is needed) and scales.  Both orders depend on the shapes alone.
+//
+// Sums: a thread adds the squares of the 32 values that it has of a chunk in
+// FP32, and the sum to its FP64 accumulator.  An FP32 sum outside
+// [2^-60, 2^80] of values that are not all zero may have lost terms to
+// underflow or overflowed: those 32 values are summed again in FP64, which
+// holds every square of the types.  Inside it, a term lost to underflow is
+// below 2^-149 against a sum of 2^-60 or more.
+#include "../csrc/cake_device.cuh"
+#include "cake_step_launch.h"
+
+namespace cake {
+
+constexpr int kGradWarps = kGradThreads / 32;
+constexpr int kPerThread = kGradChunk / kGradThreads; // 32 values
+
+template <int N>
+__device__ __forceinline__ int find_tensor(const GradParams<N> &p, uint32_t chunk, int from)
+{
+    int lo = from, hi = p.n - 1; // the last tensor whose first chunk is <= chunk
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.t[mid].chunk0 <= chunk)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float load_one(const void *src, int64_t i, bool f32)
+{
+    return f32 ? static_cast<const float *>(src)[i]
+               : __uint_as_float((uint32_t)static_cast<const uint16_t *>(src)[i] << 16);
+}
+
+// This thread's values of a chunk: 4 groups of 8, group u at value
+// u * 8 * kGradThreads + 8 * thread of the chunk; missing ones are zero.
+// (Plain loads: clipping in place writes what it has read.)
+__device__ __forceinline__ void load_chunk(const GradDesc &d, int64_t first, float (&v)[kPerThread])
+{
+    const bool f32 = d.flags & kGradSrcF32;
+    const int64_t left = d.count - first;
+    if ((d.flags & kGradVector) && left >= kGradChunk) {
+        if (f32) {
+            const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(d.src) + first);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float4 a = s[u * 2 * kGradThreads + k * kGradThreads + threadIdx.x];
+                    v[u * 8 + k * 4 + 0] = a.x;
+                    v[u * 8 + k * 4 + 1] = a.y;
+                    v[u * 8 + k * 4 + 2] = a.z;
+                    v[u * 8 + k * 4 + 3] = a.w;
+                }
+        } else {
+            const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(d.src) + first);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float f[8];
+                unpack8(s[u * kGradThreads + threadIdx.x], f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[u * 8 + k] = f[k];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k) {
+            const int64_t i = first + k * kGradThreads + threadIdx.x;
+            v[k] = i < d.count ? load_one(d.src, i, f32) : 0.f;
+        }
+    }
+}
+
+__device__ __forceinline__ double chunk_sumsq(const float (&v)[kPerThread])
+{
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k)
+        s[k & 3] = __fmaf_rn(v[k], v[k], s[k & 3]);
+    const float t = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
+    if (t >= 0x1p-60f && t <= 0x1p80f)
+        return (double)t;
+    double e = 0.0; // small, zero, huge or not finite
+#pragma unroll 1
+    for (int k = 0; k < kPerThread; ++k)
+        e = fma((double)v[k], (double)v[k], e);
+    return e;
+}
+
+// The sum over the CTA in a fixed order, in thread 0.
+__device__ __forceinline__ double cta_sum(double v)
+{
+    __shared__ double part[kGradWarps];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        v = part[0];
+        for (int w = 1; w < kGradWarps; ++w)
+            v += part[w];
+    }
+    return v;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const __grid_constant__ GradParams<N> p)
+{
+    double acc = 0.0;
+    int i = 0;
+    for (uint32_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+        i = find_tensor(p, c, i);
+        const GradDesc &d = p.t[i];
+        float v[kPerThread];
+        load_chunk(d, (int64_t)(c - d.chunk0) * kGradChunk, v);
+        acc += chunk_sumsq(v);
+    }
+    acc = cta_sum(acc);
+    if (threadIdx.x == 0)
+        p.partials[blockIdx.x] = acc;
+    pdl_launch_dependents();
+}
+
+// Every thread gets the sum of all partials, in an order that is the same in every CTA.
+__device__ __forceinline__ double all_partials(const double *partials, int n)
+{
+    double v = 0.0;
+    for (int i = threadIdx.x; i < n; i += kGradThreads)
+        v += __ldcg(partials + i);
+    __shared__ double total;
+    v = cta_sum(v);
+    if (threadIdx.x == 0)
+        total = v;
+    __syncthreads();
+    return total;
+}
+
+__global__ void __launch_bounds__(kGradThreads) grad_final_kernel(const double *partials, int n, float *norm)
+{
+    pdl_wait();
+    const double v = all_partials(partials, n);
+    if (threadIdx.x == 0)
+        *norm = (float)sqrt(v);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_constant__ GradParams<N> p)
+{
+    pdl_wait();
+    const double norm = sqrt(all_partials(p.partials, p.npartials));
+    if (p.norm && blockIdx.x == 0 && threadIdx.x == 0)
+        *p.norm = (float)norm;
+    // min(1, q) that keeps a NaN
+    const double q = (double)p.max_norm / (norm + (double)p.eps);
+    const float coef = q >= 1.0 ? 1.0f : (float)q;
+    if (p.in_place && coef == 1.0f)
+        return;
+    int i = 0;
+    for (uint32_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
+        i = find_tensor(p, c, i);
+        const GradDesc &d = p.t[i];
+        const int64_t first = (int64_t)(c - d.chunk0) * kGradChunk;
+        float v[kPerThread];
+        load_chunk(d, first, v);
+        const bool f32 = d.flags & kGradSrcF32, o32 = d.flags & kGradDstF32;
+        if ((d.flags & kGradVector) && d.count - first >= kGradChunk) {
+            // v[u * 8 ...]: 8 consecutive values of a BF16 source; two groups of 4 of an FP32 one
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    w[k] = __fmul_rn(v[u * 8 + k], coef);
+                if (o32) {
+                    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(d.dst) + first);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int at = f32 ? u * 2 * kGradThreads + k * kGradThreads + threadIdx.x
+                                           : (u * kGradThreads + threadIdx.x) * 2 + k;
+                        o[at] = make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    }
+                } else if (f32) {
+                    uint2 *o = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(d.dst) + first);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        o[u * 2 * kGradThreads + k * kGradThreads + threadIdx.x] =
+                            make_uint2(pack_bf16(w[4 * k], w[4 * k + 1]), pack_bf16(w[4 * k + 2], w[4 * k + 3]));
+                } else {
+                    reinterpret_cast<uint4 *>(static_cast<uint16_t *>(d.dst) + first)[u * kGradThreads + threadIdx.x] =
+                        pack8(w);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kPerThread; ++k) {
+                const int64_t at = first + k * kGradThreads + threadIdx.x;
+                if (at < d.count) {
+                    const float w = __fmul_rn(v[k], coef);
+                    if (o32)
+                        static_cast<float *>(d.dst)[at] = w;
+                    else
+                        static_cast<uint16_t *>(d.dst)[at] = (uint16_t)pack_bf16(w, 0.f);
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ launch
+
+template <int N>
+cudaError_t launch_grad_sumsq(const GradParams<N> &p, int ctas, cudaStream_t stream)
+{
+    grad_sumsq_kernel<N><<<ctas, kGradThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+static cudaLaunchConfig_t dependent_config(int ctas, cudaLaunchAttribute *attr, bool dependent, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kGradThreads);
+    cfg.stream = stream;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cfg;
+}
+
+template <int N>
+cudaError_t launch_grad_clip(const GradParams<N> &p, int ctas, bool after_norm, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = dependent_config(ctas, &attr, after_norm, stream);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, grad_clip_kernel<N>, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+cudaError_t launch_grad_final(const double *partials, int n, float *norm, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = dependent_config(1, &attr, true, stream);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, grad_final_kernel, partials, n, norm);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template cudaError_t launch_grad_sumsq<kGradFewTensors>(const GradParams<kGradFewTensors> &, int, cudaStream_t);
+template cudaError_t launch_grad_sumsq<kGradMaxTensors>(const GradParams<kGradMaxTensors> &, int, cudaStream_t);
+template cudaError_t launch_grad_clip<kGradFewTensors>(const GradParams<kGradFewTensors> &, int, bool, cudaStream_t);
+template cudaError_t launch_grad_clip<kGradMaxTensors>(const GradParams<kGradMaxTensors> &, int, bool, cudaStream_t);
+
+} // namespace cake

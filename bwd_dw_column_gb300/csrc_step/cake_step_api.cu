@@ -1,0 +1,548 @@
+// cake_step_api.cu -- the C ABI of the training-step operators: argument
+// validation, workspace layout and dispatch to the launchers.  Host code only.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include <cuda_runtime.h>
+
+#include "../../include/cake_step.h"
+#include "cake_check.h"
+#include "cake_step_launch.h"
+
+using namespace cake;
+
+namespace {
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+cudaStream_t cu(cake_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+bool good_dtype(int d) { return d == CAKE_BF16 || d == CAKE_FP32; }
+
+cake_status check_workspace(const void *ws, size_t bytes, size_t need)
+{
+    if (need > 0 && (!ws || bytes < need))
+        return CAKE_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+        return CAKE_ERR_UNSUPPORTED;
+    return CAKE_OK;
+}
+
+bool has(const cake_tensor *t) { return t && t->data; }
+
+cake_status check_rows_f32(const void *p)
+{
+    if (!p)
+        return CAKE_ERR_INVALID;
+    return (reinterpret_cast<uintptr_t>(p) & 3u) ? CAKE_ERR_UNSUPPORTED : CAKE_OK;
+}
+
+// The weights and the gate of a sandwich norm.
+cake_status check_sandwich(const cake_shape *shape, const void *w_post, cake_dtype post_dtype, const void *w_pre,
+                           cake_dtype pre_dtype, const float *gate_rows, const cake_tensor *gate, float scale)
+{
+    if (!good_dtype(post_dtype) || !good_dtype(pre_dtype) || std::isnan(scale))
+        return CAKE_ERR_INVALID;
+    if (gate_rows && has(gate))
+        return CAKE_ERR_INVALID;
+    if (shape->tokens == 0)
+        return CAKE_OK;
+    if (!w_post || !w_pre)
+        return CAKE_ERR_INVALID;
+    if (!aligned16(w_post) || !aligned16(w_pre))
+        return CAKE_ERR_UNSUPPORTED;
+    if (gate_rows && (reinterpret_cast<uintptr_t>(gate_rows) & 3u))
+        return CAKE_ERR_UNSUPPORTED;
+    return has(gate) ? check_tensor(gate, shape) : CAKE_OK;
+}
+
+} // namespace
+
+// ------------------------------------------------------------ sandwich norm
+
+extern "C" cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_tensor *z, const cake_tensor *x,
+                                         const void *w_post, cake_dtype w_post_dtype, const void *w_pre,
+                                         cake_dtype w_pre_dtype, const float *gate_rows, const cake_tensor *gate,
+                                         float scale, float eps, const cake_tensor *y, const cake_tensor *h_new,
+                                         float *rstd_post, float *rstd_pre, cake_stream_t stream)
+{
+    uint32_t rows = 0;
+    cake_status st = check_shape(shape, &rows);
+    if (st != CAKE_OK)
+        return st;
+    if (!(eps >= 0.0f))
+        return CAKE_ERR_INVALID;
+    if ((st = check_sandwich(shape, w_post, w_post_dtype, w_pre, w_pre_dtype, gate_rows, gate, scale)) != CAKE_OK)
+        return st;
+    if (rows == 0)
+        return CAKE_OK;
+    if ((st = check_tensor(z, shape)) != CAKE_OK || (st = check_tensor(x, shape)) != CAKE_OK ||
+        (st = check_out_tensor(y, shape)) != CAKE_OK || (st = check_out_tensor(h_new, shape)) != CAKE_OK ||
+        (st = check_rows_f32(rstd_post)) != CAKE_OK || (st = check_rows_f32(rstd_pre)) != CAKE_OK)
+        return st;
+    // a row is written after it is read: an output may be an input's view
+    // exactly, and not straddle other rows of one
+    if (overlap(y, h_new, shape))
+        return CAKE_ERR_INVALID;
+    const cake_tensor *outs[2] = {y, h_new}, *ins[3] = {z, x, has(gate) ? gate : nullptr};
+    for (const cake_tensor *o : outs)
+        for (const cake_tensor *i : ins)
+            if (i && overlap(o, i, shape) && !same_view(o, i, shape))
+                return CAKE_ERR_INVALID;
+    SandwichFwdParams p{};
+    p.H = (int)shape->hidden;
+    p.nvec = p.H / 8;
+    p.rows = rows;
+    p.nh = (uint32_t)shape->heads;
+    p.inv_h = 1.0f / (float)p.H;
+    p.eps = eps;
+    p.scale = scale;
+    p.z = make_view(z, shape);
+    p.x = make_view(x, shape);
+    p.gate = make_view(gate, shape);
+    p.y = make_view(y, shape);
+    p.h_new = make_view(h_new, shape);
+    p.gate_rows = gate_rows;
+    p.w_post = w_post;
+    p.w_pre = w_pre;
+    p.post_f32 = w_post_dtype == CAKE_FP32;
+    p.pre_f32 = w_pre_dtype == CAKE_FP32;
+    p.rstd_post = rstd_post;
+    p.rstd_pre = rstd_pre;
+    return cuda_status(launch_sandwich_fwd(p, cu(stream)));
+}
+
+extern "C" size_t cake_sandwich_bwd_workspace_size(const cake_shape *shape)
+{
+    uint32_t rows = 0;
+    if (check_shape(shape, &rows) != CAKE_OK || rows == 0)
+        return 0;
+    return (size_t)2 * sandwich_bwd_ctas((int)shape->hidden, rows) * shape->hidden * sizeof(float2);
+}
+
+extern "C" cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_tensor *dy, const cake_tensor *dh,
+                                         const cake_tensor *h_new, const cake_tensor *z, const float *rstd_post,
+                                         const float *rstd_pre, const void *w_post, cake_dtype w_post_dtype,
+                                         const void *w_pre, cake_dtype w_pre_dtype, const float *gate_rows,
+                                         const cake_tensor *gate, float scale, const cake_tensor *dx,
+                                         const cake_tensor *dz, float *dw_post, float *dw_pre, float *dgate_rows,
+                                         const cake_tensor *dgate, void *workspace, size_t workspace_bytes,
+                                         cake_stream_t stream)
+{
+    uint32_t rows = 0;
+    cake_status st = check_shape(shape, &rows);
+    if (st != CAKE_OK)
+        return st;
+    if ((st = check_sandwich(shape, w_post, w_post_dtype, w_pre, w_pre_dtype, gate_rows, gate, scale)) != CAKE_OK)
+        return st;
+    if (!dw_post || !dw_pre || dw_post == dw_pre)
+        return CAKE_ERR_INVALID;
+    if (!aligned16(dw_post) || !aligned16(dw_pre))
+        return CAKE_ERR_UNSUPPORTED;
+    if ((dgate_rows && !gate_rows) || (has(dgate) && !has(gate)))
+        return CAKE_ERR_INVALID;
+    const int H = (int)shape->hidden;
+    if (rows == 0) {
+        cudaError_t e = cudaMemsetAsync(dw_post, 0, (size_t)H * sizeof(float), cu(stream));
+        if (e == cudaSuccess)
+            e = cudaMemsetAsync(dw_pre, 0, (size_t)H * sizeof(float), cu(stream));
+        return cuda_status(e);
+    }
+    if ((st = check_tensor(dy, shape)) != CAKE_OK || (st = check_tensor(h_new, shape)) != CAKE_OK ||
+        (st = check_tensor(z, shape)) != CAKE_OK || (has(dh) && (st = check_tensor(dh, shape)) != CAKE_OK) ||
+        (st = check_out_tensor(dx, shape)) != CAKE_OK || (st = check_out_tensor(dz, shape)) != CAKE_OK ||
+        (has(dgate) && (st = check_out_tensor(dgate, shape)) != CAKE_OK) ||
+        (st = check_rows_f32(rstd_post)) != CAKE_OK || (st = check_rows_f32(rstd_pre)) != CAKE_OK ||
+        (dgate_rows && (st = check_rows_f32(dgate_rows)) != CAKE_OK))
+        return st;
+    // outputs are written while later rows of the inputs are still being read
+    const cake_tensor *outs[3] = {dx, dz, has(dgate) ? dgate : nullptr};
+    const cake_tensor *ins[5] = {dy, h_new, z, has(dh) ? dh : nullptr, has(gate) ? gate : nullptr};
+    for (int o = 0; o < 3; ++o) {
+        for (const cake_tensor *i : ins)
+            if (overlap(outs[o], i, shape))
+                return CAKE_ERR_INVALID;
+        for (int q = 0; q < o; ++q)
+            if (overlap(outs[o], outs[q], shape))
+                return CAKE_ERR_INVALID;
+    }
+    if ((st = check_workspace(workspace, workspace_bytes, cake_sandwich_bwd_workspace_size(shape))) != CAKE_OK)
+        return st;
+    SandwichBwdParams p{};
+    const int ctas = sandwich_bwd_ctas(H, rows);
+    p.H = H;
+    p.nvec = H / 8;
+    p.rows = rows;
+    p.nh = (uint32_t)shape->heads;
+    p.rows_per_cta = (rows + ctas - 1) / ctas;
+    p.inv_h = 1.0f / (float)H;
+    p.scale = scale;
+    p.dy = make_view(dy, shape);
+    p.dh = make_view(dh, shape);
+    p.h = make_view(h_new, shape);
+    p.z = make_view(z, shape);
+    p.gate = make_view(gate, shape);
+    p.dx = make_view(dx, shape);
+    p.dz = make_view(dz, shape);
+    p.dgate = make_view(dgate, shape);
+    p.gate_rows = gate_rows;
+    p.dgate_rows = dgate_rows;
+    p.rstd_post = rstd_post;
+    p.rstd_pre = rstd_pre;
+    p.w_post = w_post;
+    p.w_pre = w_pre;
+    p.post_f32 = w_post_dtype == CAKE_FP32;
+    p.pre_f32 = w_pre_dtype == CAKE_FP32;
+    p.partials = static_cast<float2 *>(workspace);
+    cudaError_t e = launch_sandwich_bwd(p, ctas, cu(stream));
+    if (e != cudaSuccess)
+        return CAKE_ERR_CUDA;
+    SandwichReduceParams rp{p.partials, ctas, H, {dw_post, dw_pre}};
+    return cuda_status(launch_sandwich_reduce(rp, cu(stream)));
+}
+
+// ----------------------------------------------- gradient norm and clipping
+
+namespace {
+
+struct Range {
+    uintptr_t lo, hi;
+    int64_t id; // tensor; an output's is -1 - tensor where it is not the input itself
+};
+
+// The tensors of a call, checked; `clip`: outputs too.
+cake_status check_grads(const void *const *data, const int64_t *counts, const int32_t *dtypes, void *const *outs,
+                        const int32_t *out_dtypes, int64_t n, bool clip)
+{
+    if (n < 0 || (n > 0 && (!data || !counts || !dtypes)) || (outs == nullptr) != (out_dtypes == nullptr))
+        return CAKE_ERR_INVALID;
+    std::vector<Range> written, read;
+    if (clip)
+        written.reserve((size_t)n);
+    for (int64_t i = 0; i < n; ++i) {
+        if (counts[i] < 0 || !good_dtype(dtypes[i]) || (outs && !good_dtype(out_dtypes[i])))
+            return CAKE_ERR_INVALID;
+        if (counts[i] >= (int64_t(1) << 44)) // 2^32 chunks are more than any memory holds
+            return CAKE_ERR_UNSUPPORTED;
+        if (counts[i] == 0)
+            continue;
+        const uintptr_t size = dtypes[i] == CAKE_FP32 ? 4 : 2, a = reinterpret_cast<uintptr_t>(data[i]);
+        if (!a)
+            return CAKE_ERR_INVALID;
+        if (a % size)
+            return CAKE_ERR_UNSUPPORTED;
+        if (!clip)
+            continue;
+        const Range in{a, a + size * (uintptr_t)counts[i], i};
+        if (!outs) {
+            written.push_back(in);
+            continue;
+        }
+        const uintptr_t osize = out_dtypes[i] == CAKE_FP32 ? 4 : 2, o = reinterpret_cast<uintptr_t>(outs[i]);
+        if (!o)
+            return CAKE_ERR_INVALID;
+        if (o % osize)
+            return CAKE_ERR_UNSUPPORTED;
+        written.push_back({o, o + osize * (uintptr_t)counts[i], o == a && osize == size ? i : -1 - i});
+        read.push_back(in);
+    }
+    // written ranges share memory with no other range but their own input
+    const auto by_lo = [](const Range &x, const Range &y) { return x.lo < y.lo; };
+    std::sort(written.begin(), written.end(), by_lo);
+    for (size_t k = 1; k < written.size(); ++k)
+        if (written[k].lo < written[k - 1].hi)
+            return CAKE_ERR_INVALID;
+    for (const Range &r : read) {
+        // the written ranges are disjoint, so those that meet r follow one another
+        auto it = std::upper_bound(written.begin(), written.end(), r, by_lo);
+        if (it != written.begin())
+            --it;
+        for (; it != written.end() && it->lo < r.hi; ++it)
+            if (it->hi > r.lo && it->id != r.id)
+                return CAKE_ERR_INVALID;
+    }
+    return CAKE_OK;
+}
+
+int64_t grad_launches(int64_t n) { return n <= 0 ? 0 : (n + kGradMaxTensors - 1) / kGradMaxTensors; }
+
+// The launches' tensors [i0, i1) as parameters; returns the CTAs.
+template <int N>
+int fill_grads(GradParams<N> &p, const void *const *data, const int64_t *counts, const int32_t *dtypes,
+               void *const *outs, const int32_t *out_dtypes, int64_t i0, int64_t i1)
+{
+    uint64_t chunks = 0;
+    int k = 0;
+    for (int64_t i = i0; i < i1; ++i) {
+        if (counts[i] == 0)
+            continue;
+        GradDesc &d = p.t[k++];
+        d.src = data[i];
+        d.dst = outs ? outs[i] : const_cast<void *>(data[i]);
+        d.count = counts[i];
+        d.chunk0 = (uint32_t)chunks;
+        const bool o32 = outs ? out_dtypes[i] == CAKE_FP32 : dtypes[i] == CAKE_FP32;
+        d.flags = (dtypes[i] == CAKE_FP32 ? kGradSrcF32 : 0) | (o32 ? kGradDstF32 : 0) |
+                  (aligned16(d.src) && aligned16(d.dst) ? kGradVector : 0);
+        chunks += (uint64_t)((counts[i] + kGradChunk - 1) / kGradChunk);
+    }
+    p.n = k;
+    p.chunks = (uint32_t)chunks;
+    return (int)std::min<uint64_t>(chunks, kGradCtas);
+}
+
+template <int N>
+cudaError_t run_grads(const void *const *data, const int64_t *counts, const int32_t *dtypes, void *const *outs,
+                      const int32_t *out_dtypes, int64_t n, bool clip, float max_norm, float eps, float *norm,
+                      double *partials, cudaStream_t s)
+{
+    // the parameters of a launch are too large for the stack of a small thread
+    static thread_local GradParams<N> p;
+    int total = 0;
+    for (int64_t i0 = 0; i0 < n; i0 += N) {
+        const int ctas = fill_grads(p, data, counts, dtypes, outs, out_dtypes, i0, std::min(n, i0 + N));
+        if (ctas == 0)
+            continue;
+        p.partials = partials + total;
+        total += ctas;
+        cudaError_t e = launch_grad_sumsq(p, ctas, s);
+        if (e != cudaSuccess)
+            return e;
+    }
+    if (total == 0)
+        return cudaMemsetAsync(norm, 0, sizeof(float), s);
+    if (!clip)
+        return launch_grad_final(partials, total, norm, s);
+    bool first = true;
+    for (int64_t i0 = 0; i0 < n; i0 += N) {
+        const int ctas = fill_grads(p, data, counts, dtypes, outs, out_dtypes, i0, std::min(n, i0 + N));
+        if (ctas == 0)
+            continue;
+        p.partials = partials;
+        p.npartials = total;
+        p.max_norm = max_norm;
+        p.eps = eps;
+        p.in_place = outs == nullptr;
+        p.norm = first ? norm : nullptr;
+        cudaError_t e = launch_grad_clip(p, ctas, first, s);
+        if (e != cudaSuccess)
+            return e;
+        first = false;
+    }
+    return cudaSuccess;
+}
+
+cake_status grads(const void *const *data, const int64_t *counts, const int32_t *dtypes, void *const *outs,
+                  const int32_t *out_dtypes, int64_t n, bool clip, float max_norm, float eps, float *norm,
+                  void *workspace, size_t workspace_bytes, cake_stream_t stream)
+{
+    cake_status st = check_grads(data, counts, dtypes, outs, out_dtypes, n, clip);
+    if (st != CAKE_OK)
+        return st;
+    if ((st = check_rows_f32(norm)) != CAKE_OK)
+        return st;
+    if (n == 0)
+        return cuda_status(cudaMemsetAsync(norm, 0, sizeof(float), cu(stream)));
+    if ((st = check_workspace(workspace, workspace_bytes, cake_grad_norm_workspace_size(n))) != CAKE_OK)
+        return st;
+    double *partials = static_cast<double *>(workspace);
+    return cuda_status(n <= kGradFewTensors
+                           ? run_grads<kGradFewTensors>(data, counts, dtypes, outs, out_dtypes, n, clip, max_norm, eps,
+                                                        norm, partials, cu(stream))
+                           : run_grads<kGradMaxTensors>(data, counts, dtypes, outs, out_dtypes, n, clip, max_norm, eps,
+                                                        norm, partials, cu(stream)));
+}
+
+} // namespace
+
+extern "C" size_t cake_grad_norm_workspace_size(int64_t n)
+{
+    return (size_t)grad_launches(n) * kGradCtas * sizeof(double);
+}
+
+extern "C" cake_status cake_grad_norm(const void *const *data, const int64_t *counts, const int32_t *dtypes, int64_t n,
+                                      float *norm, void *workspace, size_t workspace_bytes, cake_stream_t stream)
+{
+    return grads(data, counts, dtypes, nullptr, nullptr, n, false, 0.f, 0.f, norm, workspace, workspace_bytes, stream);
+}
+
+extern "C" cake_status cake_grad_clip(void *const *data, const int64_t *counts, const int32_t *dtypes,
+                                      void *const *outs, const int32_t *out_dtypes, int64_t n, float max_norm,
+                                      float eps, float *norm, void *workspace, size_t workspace_bytes,
+                                      cake_stream_t stream)
+{
+    if (!(max_norm >= 0.0f) || !(eps >= 0.0f) || std::isinf(eps))
+        return CAKE_ERR_INVALID;
+    return grads(data, counts, dtypes, outs, out_dtypes, n, true, max_norm, eps, norm, workspace, workspace_bytes,
+                 stream);
+}
+
+// ---------------------------------------------------------------- embedding
+
+namespace {
+
+cake_status check_embedding(const void *ids, int ids_int64, int64_t tokens, const void *table, int dtype,
+                            int64_t vocab, int64_t hidden, int64_t stride, float scale, const cake_tensor *rows,
+                            bool rows_out)
+{
+    if (tokens < 0 || vocab < 1 || hidden < 1 || !good_dtype(dtype) || (ids_int64 != 0 && ids_int64 != 1) ||
+        std::isnan(scale) || !table || (tokens > 0 && !ids))
+        return CAKE_ERR_INVALID;
+    if (hidden % 8 != 0 || hidden > CAKE_MAX_HIDDEN || tokens >= (int64_t(1) << 31) || vocab >= (int64_t(1) << 31))
+        return CAKE_ERR_UNSUPPORTED;
+    if (!aligned16(table) || stride % (dtype == CAKE_FP32 ? 4 : 8) != 0 || (vocab > 1 && stride < hidden) ||
+        stride >= (int64_t(1) << 31))
+        return CAKE_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(ids) & (ids_int64 ? 7u : 3u))
+        return CAKE_ERR_UNSUPPORTED;
+    if (tokens == 0)
+        return CAKE_OK;
+    const cake_shape shape{tokens, 1, hidden};
+    cake_status st = rows_out ? check_out_tensor(rows, &shape) : check_tensor(rows, &shape);
+    if (st != CAKE_OK)
+        return st;
+    // the rows and the table share no memory
+    const auto e = extent(rows, &shape);
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(table);
+    const uintptr_t hi = lo + (uintptr_t)((vocab - 1) * stride + hidden) * (dtype == CAKE_FP32 ? 4 : 2);
+    return e.first < hi && lo < e.second ? CAKE_ERR_INVALID : CAKE_OK;
+}
+
+// Sizes of a gradient call; they depend on the shape alone.
+struct EmbedPlan {
+    int bits, passes, tiles, window, windows, slices;
+    uint32_t tile_keys;
+    size_t present_bytes, hist_bytes, pairs_bytes, part_bytes, meta_bytes, total;
+};
+
+EmbedPlan embed_plan(int64_t T, int64_t V, int64_t H)
+{
+    EmbedPlan e{};
+    int key_bits = 1;
+    while ((V >> key_bits) != 0) // keys 0 .. V
+        ++key_bits;
+    e.passes = (key_bits + kSortMaxBits - 1) / kSortMaxBits;
+    e.bits = (key_bits + e.passes - 1) / e.passes;
+    const int64_t per = ((T + kSortMaxTiles - 1) / kSortMaxTiles + kSortBlock - 1) / kSortBlock * kSortBlock;
+    e.tile_keys = (uint32_t)per;
+    e.tiles = (int)((T + per - 1) / per);
+    e.slices = (int)((H + 1023) / 1024);
+    e.window = 128;
+    while (e.window > 32 && ((T + e.window - 1) / e.window) * e.slices < 152 * 8)
+        e.window /= 2;
+    e.windows = (int)((T + e.window - 1) / e.window);
+    e.present_bytes = align256(((size_t)V + 31) / 32 * 4);
+    e.hist_bytes = align256((size_t)e.passes * e.tiles * ((size_t)4 << e.bits));
+    e.pairs_bytes = align256((size_t)T * 8);
+    e.part_bytes = align256((size_t)e.windows * 2 * H * 4);
+    e.meta_bytes = align256((size_t)e.windows * 8);
+    e.total = e.present_bytes + e.hist_bytes + 2 * e.pairs_bytes + e.part_bytes + e.meta_bytes;
+    return e;
+}
+
+} // namespace
+
+extern "C" cake_status cake_embedding_fwd(const void *ids, int ids_int64, int64_t tokens, const void *table,
+                                          cake_dtype table_dtype, int64_t vocab, int64_t hidden, int64_t table_stride,
+                                          float scale, const cake_tensor *y, cake_stream_t stream)
+{
+    cake_status st = check_embedding(ids, ids_int64, tokens, table, table_dtype, vocab, hidden, table_stride, scale, y,
+                                     true);
+    if (st != CAKE_OK || tokens == 0)
+        return st;
+    EmbedFwdParams p{};
+    if (step_status_ptr(&p.status) != cudaSuccess)
+        return CAKE_ERR_CUDA;
+    p.ids = ids;
+    p.ids_i64 = ids_int64;
+    p.tokens = (uint32_t)tokens;
+    p.nvec = (int)(hidden / 8);
+    p.table = table;
+    p.table_f32 = table_dtype == CAKE_FP32;
+    p.vocab = vocab;
+    p.table_stride = table_stride;
+    p.scale = scale;
+    p.y = static_cast<uint16_t *>(y->data);
+    p.y_stride = y->stride_token;
+    return cuda_status(launch_embed_fwd(p, cu(stream)));
+}
+
+extern "C" size_t cake_embedding_bwd_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden)
+{
+    if (tokens <= 0 || vocab < 1 || hidden < 1 || tokens >= (int64_t(1) << 31) || vocab >= (int64_t(1) << 31) ||
+        hidden > CAKE_MAX_HIDDEN)
+        return 0;
+    return embed_plan(tokens, vocab, hidden).total;
+}
+
+extern "C" cake_status cake_embedding_bwd(const cake_tensor *dy, const void *ids, int ids_int64, int64_t tokens,
+                                          int64_t vocab, int64_t hidden, float scale, int64_t padding_idx,
+                                          void *dtable, cake_dtype dtable_dtype, int64_t dtable_stride, int accumulate,
+                                          void *workspace, size_t workspace_bytes, cake_stream_t stream)
+{
+    cake_status st = check_embedding(ids, ids_int64, tokens, dtable, dtable_dtype, vocab, hidden, dtable_stride, scale,
+                                     dy, false);
+    if (st != CAKE_OK)
+        return st;
+    if (padding_idx < -1 || padding_idx >= vocab || (vocab > 1 && dtable_stride < hidden))
+        return CAKE_ERR_INVALID;
+    cudaStream_t s = cu(stream);
+    const size_t size = dtable_dtype == CAKE_FP32 ? 4 : 2;
+    if (tokens == 0) {
+        if (accumulate)
+            return CAKE_OK;
+        return cuda_status(cudaMemset2DAsync(dtable, (size_t)std::max(dtable_stride, hidden) * size, 0,
+                                             (size_t)hidden * size, (size_t)vocab, s));
+    }
+    const EmbedPlan e = embed_plan(tokens, vocab, hidden);
+    if ((st = check_workspace(workspace, workspace_bytes, e.total)) != CAKE_OK)
+        return st;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    SortParams q{};
+    if (step_status_ptr(&q.status) != cudaSuccess)
+        return CAKE_ERR_CUDA;
+    q.ids = ids;
+    q.ids_i64 = ids_int64;
+    q.tokens = (uint32_t)tokens;
+    q.vocab = (uint32_t)vocab;
+    q.padding_idx = padding_idx;
+    q.tile_keys = e.tile_keys;
+    q.tiles = e.tiles;
+    q.passes = e.passes;
+    q.bits = e.bits;
+    q.present = reinterpret_cast<uint32_t *>(ws);
+    q.hist = reinterpret_cast<uint32_t *>(ws + e.present_bytes);
+    uint8_t *at = ws + e.present_bytes + e.hist_bytes;
+    q.pairs[0] = reinterpret_cast<uint64_t *>(at);
+    q.pairs[1] = reinterpret_cast<uint64_t *>(at + e.pairs_bytes);
+    cudaError_t r = cudaMemsetAsync(ws, 0, e.present_bytes + e.hist_bytes, s);
+    uint64_t *sorted = nullptr;
+    if (r == cudaSuccess)
+        r = launch_embed_sort(q, &sorted, s);
+    if (r != cudaSuccess)
+        return CAKE_ERR_CUDA;
+    SegmentParams g{};
+    g.pairs = sorted;
+    g.tokens = q.tokens;
+    g.vocab = q.vocab;
+    g.window = e.window;
+    g.windows = e.windows;
+    g.slices = e.slices;
+    g.nvec = (int)(hidden / 8);
+    g.dy = static_cast<const uint16_t *>(dy->data);
+    g.dy_stride = dy->stride_token;
+    g.scale = scale;
+    g.dtable = dtable;
+    g.dtable_f32 = dtable_dtype == CAKE_FP32;
+    g.dtable_stride = dtable_stride;
+    g.accumulate = accumulate != 0;
+    g.present = q.present;
+    g.fill_ctas = accumulate ? 0 : (int)std::min<int64_t>((vocab + 3) / 4, 152 * 16);
+    g.partials = reinterpret_cast<float *>(at + 2 * e.pairs_bytes);
+    g.meta = reinterpret_cast<uint32_t *>(at + 2 * e.pairs_bytes + e.part_bytes);
+    r = launch_embed_segments(g, s);
+    if (r == cudaSuccess)
+        r = launch_embed_join(g, s);
+    return cuda_status(r);
+}

@@ -1,0 +1,157 @@
+// cake_step_launch.h -- launch parameters and private launchers of the
+// training-step operators (plain structs, passed by value to the kernels).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../csrc/cake_params.h"
+
+namespace cake {
+
+// ------------------------------------------------------------ sandwich norm
+
+struct SandwichFwdParams {
+    int H, nvec;
+    uint32_t rows, nh;
+    float inv_h, eps, scale;
+    RowView z, x, gate;    // gate.base == nullptr: no element gate
+    RowView y, h_new;      // outputs (written through base)
+    const float *gate_rows;
+    const void *w_post, *w_pre;
+    int post_f32, pre_f32;
+    float *rstd_post, *rstd_pre;
+};
+
+struct SandwichBwdParams {
+    int H, nvec;
+    uint32_t rows, nh, rows_per_cta;
+    float inv_h, scale;
+    RowView dy, dh, h, z, gate;
+    RowView dx, dz, dgate; // outputs
+    const float *gate_rows;
+    float *dgate_rows;
+    const float *rstd_post, *rstd_pre;
+    const void *w_post, *w_pre;
+    int post_f32, pre_f32;
+    float2 *partials;      // [2][ctas][H] (hi, lo): dw_post's, then dw_pre's
+};
+
+struct SandwichReduceParams {
+    const float2 *partials; // [2][P][H]
+    int P, H;
+    float *dw[2];           // dw_post, dw_pre
+};
+
+int sandwich_bwd_ctas(int H, uint32_t rows);
+cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, cudaStream_t stream);
+cudaError_t launch_sandwich_bwd(const SandwichBwdParams &p, int ctas, cudaStream_t stream);
+cudaError_t launch_sandwich_reduce(const SandwichReduceParams &p, cudaStream_t stream);
+
+// ----------------------------------------------- gradient norm and clipping
+
+// Values of one chunk, the unit of work of a CTA.
+constexpr int kGradChunk = 8192;
+// Tensors one launch takes: they travel in the launch parameters (32 KB).
+constexpr int kGradMaxTensors = 1000;
+constexpr int kGradFewTensors = 32;
+constexpr int kGradThreads = 256;
+constexpr int kGradCtas = 152 * 4;
+
+struct GradDesc {
+    const void *src;
+    void *dst;
+    int64_t count;
+    uint32_t chunk0;       // the tensor's first chunk in this launch
+    uint32_t flags;        // kGrad*
+};
+constexpr uint32_t kGradSrcF32 = 1, kGradDstF32 = 2, kGradVector = 4; // kGradVector: 16-byte accesses are aligned
+
+template <int N>
+struct GradParams {
+    int n;
+    int npartials;         // clip: partials of the whole norm
+    uint32_t chunks;
+    float max_norm, eps;
+    int in_place;          // clip: nothing to write where coef is 1
+    float *norm;           // clip: where CTA 0 of the first launch writes the norm (else nullptr)
+    double *partials;      // norm: this launch's [ctas]; clip: all
+    GradDesc t[N];
+};
+
+template <int N>
+cudaError_t launch_grad_sumsq(const GradParams<N> &p, int ctas, cudaStream_t stream);
+template <int N>
+cudaError_t launch_grad_clip(const GradParams<N> &p, int ctas, bool after_norm, cudaStream_t stream);
+cudaError_t launch_grad_final(const double *partials, int n, float *norm, cudaStream_t stream);
+
+// ---------------------------------------------------------------- embedding
+
+struct EmbedFwdParams {
+    const void *ids;
+    int ids_i64;
+    uint32_t tokens;
+    int nvec;              // H / 8
+    const void *table;
+    int table_f32;
+    int64_t vocab, table_stride;
+    float scale;
+    uint16_t *y;
+    int64_t y_stride;
+    int *status;
+};
+
+// Sorting: keys (id, token), the tokens without a gradient under key `vocab`.
+constexpr int kSortThreads = 256;
+constexpr int kSortPerThread = 8;
+constexpr int kSortBlock = kSortThreads * kSortPerThread; // keys ranked together
+constexpr int kSortMaxTiles = 304;
+constexpr int kSortMaxBits = 8;                            // bits of a pass
+constexpr int kSortMaxPasses = 4;
+
+struct SortParams {
+    const void *ids;
+    int ids_i64;
+    uint32_t tokens;
+    uint32_t vocab;
+    int64_t padding_idx;
+    uint32_t tile_keys;    // keys of a tile (a CTA's), a multiple of kSortBlock
+    int tiles;
+    int passes;
+    int bits;              // of each pass
+    uint64_t *pairs[2];    // (key << 32) | token, ping-pong
+    uint32_t *hist;        // [passes][tiles][1 << bits], zero before the first pass
+    uint32_t *present;     // bitmap of ids with a token, zero before the first pass
+    int *status;
+};
+
+struct SegmentParams {
+    const uint64_t *pairs; // sorted
+    uint32_t tokens;
+    uint32_t vocab;
+    int window;            // sorted positions of a CTA
+    int windows, slices;   // CTAs of the sums: windows x column slices
+    int nvec;
+    const uint16_t *dy;
+    int64_t dy_stride;
+    float scale;
+    void *dtable;
+    int dtable_f32;
+    int64_t dtable_stride;
+    int accumulate;
+    const uint32_t *present;
+    int fill_ctas;         // CTAs after the sums' that zero the rows without a token
+    float *partials;       // [windows][2][H]: sums of the leading and the trailing piece
+    uint32_t *meta;        // [windows][2]: flags and the trailing piece's id
+};
+
+cudaError_t launch_embed_fwd(const EmbedFwdParams &p, cudaStream_t stream);
+cudaError_t launch_embed_sort(const SortParams &p, uint64_t **sorted, cudaStream_t stream);
+cudaError_t launch_embed_segments(const SegmentParams &p, cudaStream_t stream);
+cudaError_t launch_embed_join(const SegmentParams &p, cudaStream_t stream);
+
+cudaError_t step_status(int *code, int clear);
+cudaError_t step_status_ptr(int **out);
+
+} // namespace cake

@@ -1,0 +1,498 @@
+"""Training-step operators around the RMSNorm: Python binding and autograd.
+
+Three groups of operators that a training step needs next to the norm, each in
+hand-written kernels behind the C ABI of ``include/cake_step.h`` (formulas and
+conventions there).  They have no counterpart in the pages; they are additions
+of this library.
+
+* Sandwich norm -- the norm after a block, a gate, the residual scale and
+  addition, and the norm before the next block in one pass:
+  ``cake_sandwich_fwd``, ``cake_sandwich_bwd`` and the differentiable
+  ``cake_sandwich_norm``;
+* gradient norm and clipping over many tensors: ``cake_grad_norm`` and
+  ``cake_clip_grad_norm``;
+* embedding lookup with a scale, and its gradient by sorted tokens:
+  ``cake_embedding_fwd``, ``cake_embedding_bwd`` and the differentiable
+  ``cake_embedding``.
+
+Every result is bitwise reproducible for equal inputs and shapes.  Workspaces
+hold nothing between calls; without one from the caller a call takes it from
+torch's allocator, so calls on several streams and in several captured graphs
+never share one.  A call runs on the tensors' device, on its current stream or
+on ``stream``, where its outputs and workspace are allocated too.
+"""
+from __future__ import annotations
+
+import ctypes
+from array import array
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import (CAKE_BF16, CAKE_FP32, _check, _P, _rows_of, _same_rows, _Shape, _Tensor, _tensor, _w_dtype,
+               load_library)
+
+__all__ = [
+    "cake_sandwich_fwd", "cake_sandwich_bwd", "cake_sandwich_bwd_workspace_size", "cake_sandwich_norm",
+    "CakeSandwichFunction", "cake_grad_norm", "cake_clip_grad_norm", "cake_grad_norm_workspace_size",
+    "cake_embedding_fwd", "cake_embedding_bwd", "cake_embedding_bwd_workspace_size", "cake_embedding",
+    "CakeEmbeddingFunction",
+]
+
+_vp, _i64, _f32, _int, _size = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int, ctypes.c_size_t
+
+
+def _bind(lib):
+    """Declare the operators' C signatures on the library handle."""
+    T, S = _P(_Tensor), _P(_Shape)
+    for name, res, args in (
+        ("cake_sandwich_fwd", _int, [S, T, T, _vp, _int, _vp, _int, _vp, T, _f32, _f32, T, T, _vp, _vp, _vp]),
+        ("cake_sandwich_bwd_workspace_size", _size, [S]),
+        ("cake_sandwich_bwd", _int, [S, T, T, T, T, _vp, _vp, _vp, _int, _vp, _int, _vp, T, _f32, T, T, _vp, _vp, _vp,
+                                     T, _vp, _size, _vp]),
+        ("cake_grad_norm_workspace_size", _size, [_i64]),
+        ("cake_grad_norm", _int, [_vp, _vp, _vp, _i64, _vp, _vp, _size, _vp]),
+        ("cake_grad_clip", _int, [_vp, _vp, _vp, _vp, _vp, _i64, _f32, _f32, _vp, _vp, _size, _vp]),
+        ("cake_embedding_fwd", _int, [_vp, _int, _i64, _vp, _int, _i64, _i64, _i64, _f32, T, _vp]),
+        ("cake_embedding_bwd_workspace_size", _size, [_i64, _i64, _i64]),
+        ("cake_embedding_bwd", _int, [T, _vp, _int, _i64, _i64, _i64, _f32, _i64, _vp, _int, _i64, _int, _vp, _size,
+                                      _vp]),
+    ):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = res, args
+
+
+# ------------------------------------------------------------- devices, streams
+
+class _Here:
+    """No change of device or stream."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *a):
+        return None
+
+
+_here = _Here()
+
+
+class _On:
+    """The tensors' device, and the given stream of it."""
+
+    def __init__(self, device, stream):
+        self.contexts = [torch.cuda.device(device)] + ([torch.cuda.stream(stream)] if stream is not None else [])
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+
+    def __exit__(self, *a):
+        for c in reversed(self.contexts):
+            c.__exit__(*a)
+
+
+def _on(stream, *tensors):
+    """Context of a call: every tensor (None: left out) on one CUDA device, which becomes
+    the current one, with `stream` (None: its current stream) the current stream."""
+    dev = -1
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("every tensor must be on a CUDA device (no CPU path)")
+        d = t.get_device()
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError("every tensor must be on the same device")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError("the stream belongs to another device than the tensors")
+    if stream is None and torch.cuda.current_device() == dev:
+        return _here
+    return _On(dev, stream)
+
+
+def _current() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _ref(t):
+    return None if t is None else ctypes.byref(_tensor(t))
+
+
+def _weight(w, H, what):
+    if w.dim() != 1 or w.shape[0] != H:
+        raise ValueError(f"{what} has shape {tuple(w.shape)}, expected ({H},)")
+    return w if w.is_contiguous() else w.contiguous()
+
+
+def _rows_f32(t, shape, what):
+    if t.dtype != torch.float32 or t.numel() != shape.tokens * shape.heads or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous FP32 tensor of T*nh elements")
+    return t
+
+
+def _workspace(workspace, size, device):
+    if workspace is None:
+        return torch.empty(max(size, 256), dtype=torch.uint8, device=device)
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return workspace
+
+
+# ---------------------------------------------------------------- sandwich norm
+
+def _gate(gate, z):
+    """(row gate or None, element gate or None)."""
+    if gate is None:
+        return None, None
+    if gate.shape == z.shape:
+        return None, gate
+    if gate.shape == z.shape[:-1]:
+        if gate.dtype != torch.float32:
+            raise TypeError(f"a gate of one value per row is FP32, got {gate.dtype}")
+        return (gate if gate.is_contiguous() else gate.contiguous()), None
+    raise ValueError(f"gate has shape {tuple(gate.shape)}, expected {tuple(z.shape[:-1])} (rows) or {tuple(z.shape)}")
+
+
+def cake_sandwich_fwd(z: torch.Tensor, x: torch.Tensor, w_post: torch.Tensor, w_pre: torch.Tensor,
+                      eps: float = 1e-6, gate: torch.Tensor | None = None, scale: float = 1.0, *,
+                      y: torch.Tensor | None = None, h_new: torch.Tensor | None = None,
+                      rstd_post: torch.Tensor | None = None, rstd_pre: torch.Tensor | None = None, stream=None):
+    """Forward: (y, h_new, rstd_post, rstd_pre).
+
+    z: a block's output, x: the residual stream, BF16 [T, H] or [T, nh, H]
+    views (hidden dim contiguous); w_post, w_pre: [H] BF16 or FP32 each;
+    gate: None, FP32 of z's leading shape (a value per row) or BF16 of z's
+    shape.  h_new = bf16(x + scale * gate * norm(z) * w_post) is the new
+    residual stream and y = norm(h_new) * w_pre the next block's input.
+    h_new may be x itself and y z itself (in place).
+    """
+    lib = load_library()
+    with _on(stream, z, x, w_post, w_pre, gate, y, h_new, rstd_post, rstd_pre):
+        T, nh, H, _, _ = _rows_of(z)
+        _same_rows(z, x, "x")
+        w_post, w_pre = _weight(w_post, H, "w_post"), _weight(w_pre, H, "w_pre")
+        g_row, g_elem = _gate(gate, z)
+        shape = _Shape(T, nh, H)
+        if y is None:
+            y = torch.empty(z.shape, dtype=torch.bfloat16, device=z.device)
+        if h_new is None:
+            h_new = torch.empty(z.shape, dtype=torch.bfloat16, device=z.device)
+        if rstd_post is None:
+            rstd_post = torch.empty(T * nh, dtype=torch.float32, device=z.device)
+        if rstd_pre is None:
+            rstd_pre = torch.empty(T * nh, dtype=torch.float32, device=z.device)
+        _same_rows(z, y, "y")
+        _same_rows(z, h_new, "h_new")
+        _rows_f32(rstd_post, shape, "rstd_post")
+        _rows_f32(rstd_pre, shape, "rstd_pre")
+        st = lib.cake_sandwich_fwd(ctypes.byref(shape), _ref(z), _ref(x), w_post.data_ptr(), _w_dtype(w_post),
+                                   w_pre.data_ptr(), _w_dtype(w_pre), g_row.data_ptr() if g_row is not None else None,
+                                   _ref(g_elem), scale, eps, _ref(y), _ref(h_new), rstd_post.data_ptr(),
+                                   rstd_pre.data_ptr(), _current())
+        _check(st, "cake_sandwich_fwd")
+    return y, h_new, rstd_post, rstd_pre
+
+
+def cake_sandwich_bwd_workspace_size(x_or_shape) -> int:
+    """Workspace bytes the backward needs for this row set ([T, H] / [T, nh, H] tensor or (T, nh, H))."""
+    lib = load_library()
+    shape = _Shape(*(_rows_of(x_or_shape)[:3] if isinstance(x_or_shape, torch.Tensor) else x_or_shape))
+    return int(lib.cake_sandwich_bwd_workspace_size(ctypes.byref(shape)))
+
+
+def cake_sandwich_bwd(dy: torch.Tensor, h_new: torch.Tensor, z: torch.Tensor, rstd_post: torch.Tensor,
+                      rstd_pre: torch.Tensor, w_post: torch.Tensor, w_pre: torch.Tensor,
+                      dh: torch.Tensor | None = None, gate: torch.Tensor | None = None, scale: float = 1.0, *,
+                      need_dgate: bool = True, workspace: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                      dz: torch.Tensor | None = None, dw_post: torch.Tensor | None = None,
+                      dw_pre: torch.Tensor | None = None, dgate: torch.Tensor | None = None, stream=None):
+    """Backward: (dx, dz, dw_post, dw_pre, dgate).
+
+    dy: gradient of y; dh: that reaching h_new directly, or None; h_new and the
+    rstd as the forward gave them.  dx (of the residual stream) and dz (of the
+    block's output) are BF16, dw_post and dw_pre FP32 [H].  dgate has the
+    gate's shape and type, or is None without a gate or with need_dgate false.
+    """
+    lib = load_library()
+    with _on(stream, dy, h_new, z, rstd_post, rstd_pre, w_post, w_pre, dh, gate, workspace, dx, dz, dw_post, dw_pre,
+             dgate):
+        T, nh, H, _, _ = _rows_of(z)
+        for t, what in ((dy, "dy"), (h_new, "h_new"), (dh, "dh"), (dx, "dx"), (dz, "dz")):
+            if t is not None:
+                _same_rows(z, t, what)
+        w_post, w_pre = _weight(w_post, H, "w_post"), _weight(w_pre, H, "w_pre")
+        g_row, g_elem = _gate(gate, z)
+        shape = _Shape(T, nh, H)
+        _rows_f32(rstd_post, shape, "rstd_post")
+        _rows_f32(rstd_pre, shape, "rstd_pre")
+        dev = z.device
+        if dx is None:
+            dx = torch.empty(z.shape, dtype=torch.bfloat16, device=dev)
+        if dz is None:
+            dz = torch.empty(z.shape, dtype=torch.bfloat16, device=dev)
+        if dw_post is None:
+            dw_post = torch.empty(H, dtype=torch.float32, device=dev)
+        if dw_pre is None:
+            dw_pre = torch.empty(H, dtype=torch.float32, device=dev)
+        for t, what in ((dw_post, "dw_post"), (dw_pre, "dw_pre")):
+            if t.dtype != torch.float32 or t.numel() != H or not t.is_contiguous():
+                raise ValueError(f"{what} must be a contiguous FP32 tensor of H elements")
+        if gate is None or not need_dgate:
+            if dgate is not None:
+                raise ValueError("dgate is given, but no gradient of a gate is asked for")
+        elif dgate is None:
+            dgate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
+        elif dgate.shape != gate.shape or (g_row is not None and (dgate.dtype != torch.float32 or
+                                                                  not dgate.is_contiguous())):
+            raise ValueError("dgate must have the gate's shape (and be contiguous FP32 for a value per row)")
+        workspace = _workspace(workspace, lib.cake_sandwich_bwd_workspace_size(ctypes.byref(shape)), dev)
+        st = lib.cake_sandwich_bwd(ctypes.byref(shape), _ref(dy), _ref(dh), _ref(h_new), _ref(z), rstd_post.data_ptr(),
+                                   rstd_pre.data_ptr(), w_post.data_ptr(), _w_dtype(w_post), w_pre.data_ptr(),
+                                   _w_dtype(w_pre), g_row.data_ptr() if g_row is not None else None, _ref(g_elem),
+                                   scale, _ref(dx), _ref(dz), dw_post.data_ptr(), dw_pre.data_ptr(),
+                                   dgate.data_ptr() if g_row is not None and dgate is not None else None,
+                                   _ref(dgate) if g_elem is not None else None, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _current())
+        _check(st, "cake_sandwich_bwd")
+    return dx, dz, dw_post, dw_pre, dgate
+
+
+class CakeSandwichFunction(torch.autograd.Function):
+    """(y, h_new) of the sandwich norm with the library's forward and backward:
+    ``apply(z, x, w_post, w_pre, eps, gate, scale)``."""
+
+    @staticmethod
+    def forward(ctx, z, x, w_post, w_pre, eps=1e-6, gate=None, scale=1.0):
+        y, h, r_post, r_pre = cake_sandwich_fwd(z, x, w_post, w_pre, eps, gate, scale)
+        ctx.save_for_backward(h, z, r_post, r_pre, w_post, w_pre, gate)
+        ctx.scale = float(scale)
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh):
+        if dy is None and dh is None:
+            return (None,) * 7
+        h, z, r_post, r_pre, w_post, w_pre, gate = ctx.saved_tensors
+        dy = torch.zeros_like(h) if dy is None else dy.to(torch.bfloat16).contiguous()
+        dh = None if dh is None else dh.to(torch.bfloat16).contiguous()
+        dx, dz, dwo, dwr, dgate = cake_sandwich_bwd(dy, h, z, r_post, r_pre, w_post, w_pre, dh, gate, ctx.scale,
+                                                    need_dgate=ctx.needs_input_grad[5])
+        return dz, dx, dwo.to(w_post.dtype), dwr.to(w_pre.dtype), None, dgate, None
+
+
+def cake_sandwich_norm(z: torch.Tensor, x: torch.Tensor, w_post: torch.Tensor, w_pre: torch.Tensor, eps: float = 1e-6,
+                       gate: torch.Tensor | None = None, scale: float = 1.0):
+    """Differentiable sandwich norm: (y, h_new); see ``cake_sandwich_fwd``."""
+    return CakeSandwichFunction.apply(z, x, w_post, w_pre, eps, gate, scale)
+
+
+# --------------------------------------------------- gradient norm and clipping
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether the tensor's values fill one block of memory, in any order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+def _tensors(grads, what):
+    """The tensors of a list (None: left out) as the ABI's arrays (pointers, counts, dtypes)."""
+    ptrs, counts, types = array("Q"), array("q"), array("i")
+    for t in grads:
+        if t.dtype is torch.bfloat16:
+            types.append(CAKE_BF16)
+        elif t.dtype is torch.float32:
+            types.append(CAKE_FP32)
+        else:
+            raise TypeError(f"{what} are BF16 or FP32, got {t.dtype}")
+        if not _dense(t):
+            raise ValueError(f"{what} must fill one block of memory each (strides {t.stride()} of {tuple(t.shape)})")
+        ptrs.append(t.data_ptr())
+        counts.append(t.numel())
+    return ptrs, counts, types
+
+
+def _addr(a):
+    return a.buffer_info()[0] if len(a) else None
+
+
+def cake_grad_norm_workspace_size(n: int) -> int:
+    """Workspace bytes of a norm over (or clipping of) n tensors."""
+    return int(load_library().cake_grad_norm_workspace_size(int(n)))
+
+
+def _grad_call(grads, outs, clip, max_norm, eps, norm, workspace, stream):
+    lib = load_library()
+    with _on(stream, *grads, *(outs or ()), norm, workspace):
+        ptrs, counts, types = _tensors(grads, "gradients")
+        n = len(ptrs)
+        if not grads and norm is None:
+            raise ValueError("no gradients: give the norm's tensor")
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        elif norm.dtype != torch.float32 or norm.numel() != 1:
+            raise ValueError("norm must be an FP32 tensor of one element")
+        workspace = _workspace(workspace, lib.cake_grad_norm_workspace_size(n), norm.device)
+        ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), _current())
+        if not clip:
+            st = lib.cake_grad_norm(_addr(ptrs), _addr(counts), _addr(types), n, norm.data_ptr(), *ws)
+            _check(st, "cake_grad_norm")
+            return norm
+        optrs = otypes = None
+        if outs is not None:
+            for g, o in zip(grads, outs):
+                if o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
+                    raise ValueError("an output must have its gradient's shape and order of dimensions")
+            optrs, _, otypes = _tensors(outs, "outputs")
+        st = lib.cake_grad_clip(_addr(ptrs), _addr(counts), _addr(types), _addr(optrs) if outs else None,
+                                _addr(otypes) if outs else None, n, max_norm, eps, norm.data_ptr(), *ws)
+        _check(st, "cake_grad_clip")
+        return norm
+
+
+def cake_grad_norm(grads, *, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """The L2 norm of all values of all tensors together: an FP32 device scalar.
+
+    grads: a tensor or an iterable of them (None entries are left out), BF16
+    and FP32 mixed as they come, each filling one block of memory.
+    """
+    grads = [grads] if isinstance(grads, torch.Tensor) else [g for g in grads if g is not None]
+    return _grad_call(grads, None, False, 0.0, 0.0, norm, workspace, stream)
+
+
+def cake_clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, *, norm: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """Scale all gradients by min(1, max_norm / (norm + eps)); returns the norm before it.
+
+    In place, or into ``out`` (a tensor per gradient, same shape, BF16 or FP32:
+    for instance the optimizer's FP32 buffers).  The host waits for nothing: a
+    NaN or infinite norm is for the caller to look at, and makes the gradients
+    NaN as the formula says.  No tensor may be given twice, nor share memory
+    with another.
+    """
+    if isinstance(grads, torch.Tensor):
+        grads, out = [grads], (None if out is None else [out] if isinstance(out, torch.Tensor) else list(out))
+    grads = list(grads)
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
+        out = [o for g, o in zip(grads, out) if g is not None]
+        if any(o is None for o in out):
+            raise ValueError("an output is missing for a gradient")
+    grads = [g for g in grads if g is not None]
+    return _grad_call(grads, out, True, max_norm, eps, norm, workspace, stream)
+
+
+# -------------------------------------------------------------------- embedding
+
+def _ids(ids):
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids are int32 or int64, got {ids.dtype}")
+    return ids if ids.is_contiguous() else ids.contiguous()
+
+
+def _table(table, what):
+    if table.dim() != 2:
+        raise ValueError(f"{what} has shape {tuple(table.shape)}, expected [V, H]")
+    if table.numel() and table.stride(1) != 1:
+        raise ValueError("the hidden dimension must be contiguous")
+    return table.shape
+
+
+def cake_embedding_fwd(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, *, y: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """y = bf16(scale * table[ids]), of ids' shape and [H].
+
+    ids: int32 or int64; a negative one means no token (a zero row), one
+    outside the table gives a zero row and sets the device status.  table:
+    [V, H] BF16 or FP32.
+    """
+    lib = load_library()
+    with _on(stream, ids, table, y):
+        ids = _ids(ids)
+        V, H = _table(table, "table")
+        T = ids.numel()
+        if y is None:
+            y = torch.empty((*ids.shape, H), dtype=torch.bfloat16, device=table.device)
+        elif y.shape != (*ids.shape, H):
+            raise ValueError(f"y has shape {tuple(y.shape)}, expected {(*ids.shape, H)}")
+        st = lib.cake_embedding_fwd(ids.data_ptr(), int(ids.dtype is torch.int64), T, table.data_ptr(),
+                                    _w_dtype(table), V, H, table.stride(0), scale, _ref(y if y.dim() == 2 else y.view(T, H)), _current())
+        _check(st, "cake_embedding_fwd")
+    return y
+
+
+def cake_embedding_bwd_workspace_size(tokens: int, vocab: int, hidden: int) -> int:
+    """Workspace bytes of an embedding's gradient."""
+    return int(load_library().cake_embedding_bwd_workspace_size(int(tokens), int(vocab), int(hidden)))
+
+
+def cake_embedding_bwd(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float = 1.0,
+                       padding_idx: int | None = None, out: torch.Tensor | None = None, accumulate: bool = False,
+                       dtype: torch.dtype = torch.float32, *, workspace: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """The table's gradient [vocab, H]: scale * the sum of dy over the tokens of each id.
+
+    dy: BF16, of ids' shape and [H].  out: a BF16 or FP32 table that is written
+    whole, or with ``accumulate`` added to (where it has tokens); without one a
+    new table of ``dtype``.  Tokens with id ``padding_idx``, a negative id or
+    one outside the table add nothing.
+    """
+    lib = load_library()
+    with _on(stream, dy, ids, out, workspace):
+        ids = _ids(ids)
+        T, H = ids.numel(), dy.shape[-1]
+        if dy.shape[:-1] != ids.shape:
+            raise ValueError(f"dy has shape {tuple(dy.shape)}, expected {(*ids.shape, H)}")
+        rows = dy if dy.dim() == 2 else dy.reshape(T, H)
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs the table that is added to")
+            out = torch.empty((vocab, H), dtype=dtype, device=dy.device)
+        if _table(out, "out") != (vocab, H):
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(vocab, H)}")
+        if padding_idx is not None and not 0 <= padding_idx < vocab:
+            raise ValueError(f"padding_idx {padding_idx} is outside the table")
+        workspace = _workspace(workspace, lib.cake_embedding_bwd_workspace_size(T, vocab, H), dy.device)
+        st = lib.cake_embedding_bwd(_ref(rows), ids.data_ptr(), int(ids.dtype is torch.int64), T, vocab, H, scale,
+                                    -1 if padding_idx is None else padding_idx, out.data_ptr(), _w_dtype(out),
+                                    out.stride(0), int(bool(accumulate)), workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), _current())
+        _check(st, "cake_embedding_bwd")
+    return out
+
+
+class CakeEmbeddingFunction(torch.autograd.Function):
+    """Embedding lookup with the library's forward and gradient:
+    ``apply(ids, table, scale, padding_idx)``."""
+
+    @staticmethod
+    def forward(ctx, ids, table, scale=1.0, padding_idx=None):
+        ctx.save_for_backward(ids)
+        ctx.vocab, ctx.dtype, ctx.scale, ctx.padding_idx = table.shape[0], table.dtype, float(scale), padding_idx
+        return cake_embedding_fwd(ids, table, scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        ids, = ctx.saved_tensors
+        dtable = cake_embedding_bwd(dy.to(torch.bfloat16).contiguous(), ids, ctx.vocab, ctx.scale, ctx.padding_idx,
+                                    dtype=ctx.dtype)
+        return None, dtable, None, None
+
+
+def cake_embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
+                   padding_idx: int | None = None) -> torch.Tensor:
+    """Differentiable embedding lookup; the table's gradient has the table's type."""
+    return CakeEmbeddingFunction.apply(ids, table, scale, padding_idx)
