@@ -8,216 +8,458 @@
 //   c2 = rstd_pre S1 / H,     t = dh + rstd_pre a - k2 h,  k2 = rstd_pre^2 c2
 //   sum t b z = S2 - k2 S3,   dz = scale g_row rstd_post (b t - k1 z),
 //   k1 = rstd_post^2 (S2 - k2 S3) / H,  row gate: dgate = scale rstd_post (S2 - k2 S3)
-// so that one pass and one reduction over the row give every scalar.
-#include "../csrc/cake_device.cuh"
+// so that one pass and one reduction over the row give every scalar, instead
+// of a pass for c2 and, after it, one for the mean of dn w_post zh.  Rounding
+// errors are of the same order: t is linear in k2, and both forms round terms
+// of the magnitudes |dh|, rstd_pre |a| and |k2 h|.
+//
+// Both kernels stream rows through shared memory as the RMSNorm kernels do
+// (a producer warp with bulk copies, row groups of W warps as consumers,
+// bounded waits); HBM bounds both at large T.
+#include "../csrc/cake_rows.cuh"
 #include "cake_step_launch.h"
 
 namespace cake {
 
-constexpr int kSwThreads = 256;
-constexpr int kSwWarps = kSwThreads / 32;
+cudaError_t ensure_smem_attr(const void *kernel, size_t smem);
+
 constexpr int kSMsStep = 152;
+constexpr int kSwMaxStages = 16;
+constexpr int kSwMaxTile = 24;            // rows of a stage, at most
+constexpr int kSwMisc = 2048;             // barriers and the row sums' slots
+constexpr int kSwScalars = kSwMaxStages * kSwMaxTile * 16; // a float4 of each staged row's scalars
+constexpr int kSwFixed = kSwMisc + kSwScalars;
 
-__device__ __forceinline__ void load_w8(const void *w, int f32, int v, float (&f)[8])
+struct SwSmem {
+    Smem s;               // barriers, reduction slots, flag, ring
+    float4 *scalars;      // [stages][tile rows] (rstd_post, rstd_pre, row gate, -)
+    float *w[2];          // w_post, w_pre as FP32, two planes each (see stage_weight)
+};
+
+__device__ __forceinline__ SwSmem sw_carve(uint8_t *base, const SandwichLayout &L)
 {
-    if (f32) {
-        const float4 a = __ldg(static_cast<const float4 *>(w) + 2 * v), b = __ldg(static_cast<const float4 *>(w) + 2 * v + 1);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else {
-        unpack8(__ldg(static_cast<const uint4 *>(w) + v), f);
-    }
+    SwSmem m;
+    m.s.full = reinterpret_cast<uint64_t *>(base);
+    m.s.empty = m.s.full + L.stages;
+    m.s.red = reinterpret_cast<float *>(base + 256);
+    m.s.flag = reinterpret_cast<int *>(base + kSwMisc - 16);
+    m.scalars = reinterpret_cast<float4 *>(base + kSwMisc);
+    m.w[0] = reinterpret_cast<float *>(base + kSwFixed);
+    m.w[1] = m.w[0] + weight_smem_bytes(L.H) / 4;
+    m.s.ring = base + kSwFixed + 2 * weight_smem_bytes(L.H);
+    m.s.tens_bytes = (uint32_t)L.groups * L.r2 * L.H * 2;
+    m.s.stage_bytes = m.s.tens_bytes * L.ntens;
+    return m;
 }
 
-__device__ __forceinline__ const uint4 *row_ptr(const RowView &v, uint32_t r, uint32_t nh)
+// The layout in the form that the shared pieces of the row pipeline take.
+__device__ __forceinline__ Layout sw_rows_layout(const SandwichLayout &L)
 {
-    return reinterpret_cast<const uint4 *>(v.base + row_off(v, r, nh));
-}
-__device__ __forceinline__ uint4 *out_ptr(const RowView &v, uint32_t r, uint32_t nh)
-{
-    return reinterpret_cast<uint4 *>(const_cast<uint16_t *>(v.base) + row_off(v, r, nh));
-}
-
-// Sums of N values over the CTA, in every thread.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[kSwWarps])
-{
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        v[n] = warp_sum(v[n]);
-    __syncthreads(); // the previous row's sums are read
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-            red[n][threadIdx.x >> 5] = v[n];
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        float s = red[n][0];
-        for (int w = 1; w < kSwWarps; ++w)
-            s += red[n][w];
-        v[n] = s;
-    }
+    Layout r = {};
+    r.H = L.H;
+    r.nvec = L.nvec;
+    r.warps_per_row = L.W;
+    r.groups = L.groups;
+    r.stages = L.stages;
+    return r;
 }
 
-template <int VPT>
-__global__ void __launch_bounds__(kSwThreads) sandwich_fwd_kernel(const __grid_constant__ SandwichFwdParams p)
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// The 8 weights of vector v (plane 0: columns 0-3 of the vectors, plane 1: 4-7).
+__device__ __forceinline__ void sw_weight(const float *w, int nvec, int v, float2 (&w2)[4])
 {
-    __shared__ float red[1][kSwWarps];
-    for (uint32_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        float z[VPT][8], h[VPT][8];
-        float ss[1] = {0.f};
-        const float g_row = p.gate_rows ? p.gate_rows[r] : 1.f;
+    const float4 a = reinterpret_cast<const float4 *>(w)[v], b = reinterpret_cast<const float4 *>(w)[nvec + v];
+    w2[0] = make_float2(a.x, a.y);
+    w2[1] = make_float2(a.z, a.w);
+    w2[2] = make_float2(b.x, b.y);
+    w2[3] = make_float2(b.z, b.w);
+}
+
+// Producer warp: streams the CTA's rows of every staged tensor into the ring;
+// a row's scalars go along through plain shared stores, loaded a tile ahead
+// and published by the arrival on the stage's full barrier.
+template <int NT>
+__device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout &L, const RowView (&in)[NT],
+                                           const float *sc0, const float *sc1, const float *sc2, uint32_t r0,
+                                           uint32_t r_end, int *status, uint64_t wait_ns)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    const uint64_t pol = policy_evict_first();
+    const uint32_t row_bytes = (uint32_t)L.H * 2, tile = (uint32_t)L.groups * L.r2;
+    auto scalars = [&](uint32_t row0) {
+        float4 v = make_float4(0.f, 0.f, 1.f, 0.f);
+        if (lane < tile && row0 + lane < r_end) {
+            if (sc0)
+                v.x = __ldg(sc0 + row0 + lane);
+            if (sc1)
+                v.y = __ldg(sc1 + row0 + lane);
+            if (sc2)
+                v.z = __ldg(sc2 + row0 + lane);
+        }
+        return v;
+    };
+    float4 next = scalars(r0);
+    uint32_t st = 0, ph = 0, it = 0;
+    for (uint32_t row0 = r0; row0 < r_end; row0 += tile, ++it) {
+        if (it >= (uint32_t)L.stages &&
+            !__all_sync(0xffffffffu, mbar_wait(smem_addr(&m.s.empty[st]), ph ^ 1u, wait_ns))) {
+            if (lane == 0)
+                set_status(status, kStatusTimeout);
+            break;
+        }
+        const uint32_t n = min(tile, r_end - row0);
+        const uint32_t bar = smem_addr(&m.s.full[st]);
+        if (lane < n)
+            m.scalars[st * kSwMaxTile + lane] = next;
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive_expect_tx(bar, (uint32_t)L.ntens * n * row_bytes);
+        __syncwarp();
+        const uint32_t dst0 = smem_addr(m.s.ring) + st * m.s.stage_bytes;
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = k * kSwThreads + threadIdx.x;
-            if (v < p.nvec) {
-                unpack8(row_ptr(p.z, r, p.nh)[v], z[k]);
-                unpack8(row_ptr(p.x, r, p.nh)[v], h[k]);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    ss[0] = __fmaf_rn(z[k][q], z[k][q], ss[0]);
+        for (int t = 0; t < NT; ++t) {
+            if (t >= L.ntens)
+                break;
+            const uint32_t dst = dst0 + t * m.s.tens_bytes;
+            if (in[t].dense) {
+                if (lane == 0)
+                    bulk_g2s(dst, in[t].base + (int64_t)row0 * in[t].row_stride, n * row_bytes, bar, pol);
+            } else if (lane < n) {
+                bulk_g2s(dst + lane * row_bytes, in[t].base + row_off(in[t], row0 + lane, L.nh), row_bytes, bar, pol);
             }
         }
-        block_sum(ss, red);
-        const float r1 = 1.0f / sqrtf(__fadd_rn(__fmul_rn(ss[0], p.inv_h), p.eps));
-        const float sg = p.scale * g_row;
-        ss[0] = 0.f;
+        next = scalars(row0 + tile);
+        if (++st == (uint32_t)L.stages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+    // no copy of this CTA is left in flight
+    const uint32_t first = it > (uint32_t)L.stages ? it - L.stages : 0;
+    for (uint32_t j = first; j < it; ++j)
+        if (!mbar_wait(smem_addr(&m.s.full[j % L.stages]), (j / L.stages) & 1, wait_ns) && lane == 0)
+            set_status(status, kStatusTimeout);
+}
+
+// ------------------------------------------------------------------ forward
+
+constexpr int kSwFwdThreads = 416;  // 12 consumer warps and the producer
+constexpr int kSwWideThreads = 544; // 16: rows of more than 6144 columns
+
+template <int VPT, bool GATE, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) sandwich_fwd_kernel(const __grid_constant__ SandwichFwdParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const SandwichLayout &L = p.L;
+    const SwSmem m = sw_carve(smem_raw, L);
+    const Layout RL = sw_rows_layout(L);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t r0 = blockIdx.x * L.rows_per_cta, r_end = min(L.rows, r0 + L.rows_per_cta);
+    init_ring(m.s, RL);
+    if (warp == L.groups * L.W) {
+        sw_produce(m, L, p.in, nullptr, nullptr, p.gate_rows, r0, r_end, p.status, p.wait_ns);
+        return;
+    }
+    const int gid = warp / L.W, wig = warp - gid * L.W, gtid = wig * 32 + lane, vstride = 32 * L.W;
+    const int nvec = L.nvec;
+    {
+        Smem sw = m.s;
+        sw.wsm = m.w[0];
+        stage_weight(sw, RL, p.w_post, p.post_f32);
+        sw.wsm = m.w[1];
+        stage_weight(sw, RL, p.w_pre, p.pre_f32);
+    }
+    bool abort = false;
+    uint32_t slot = 0, st = 0, ph = 0;
+    const uint32_t tile = (uint32_t)L.groups;
+    for (uint32_t row0 = r0; row0 < r_end && !abort; row0 += tile) {
+        abort = !mbar_wait(smem_addr(&m.s.full[st]), ph, p.wait_ns);
+        const uint32_t r = row0 + gid;
+        if (r < r_end) { // uniform across the group
+            const uint8_t *stage = m.s.ring + st * m.s.stage_bytes + (size_t)gid * L.H * 2;
+            const uint4 *zs = reinterpret_cast<const uint4 *>(stage);
+            const uint4 *xs = reinterpret_cast<const uint4 *>(stage + m.s.tens_bytes);
+            const uint4 *gs = reinterpret_cast<const uint4 *>(stage + 2 * m.s.tens_bytes);
+            const float sg = __fmul_rn(p.scale, m.scalars[st * kSwMaxTile + gid].z);
+            uint4 z[VPT];
+            float2 ss = both(0.f);
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = k * kSwThreads + threadIdx.x;
-            if (v < p.nvec) {
-                float w[8], g[8];
-                load_w8(p.w_post, p.post_f32, v, w);
-                if (p.gate.base)
-                    unpack8(row_ptr(p.gate, r, p.nh)[v], g);
+            for (int k = 0; k < VPT; ++k) {
+                const int v = k * vstride + gtid;
+                z[k] = v < nvec ? zs[v] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float n = __fmul_rn(__fmul_rn(z[k][q], r1), w[q]);
-                    h[k][q] = __fmaf_rn(p.gate.base ? __fmul_rn(sg, g[q]) : sg, n, h[k][q]);
+                for (int q = 0; q < 4; ++q) {
+                    const float2 a = bf2(word(z[k], q));
+                    ss = fma2(a, a, ss);
                 }
-                const uint4 raw = pack8(h[k]);
-                unpack8(raw, h[k]);
-                out_ptr(p.h_new, r, p.nh)[v] = raw;
+            }
+            float tot = group_sum(__fadd_rn(ss.x, ss.y), m.s, RL, gid, wig, lane, slot++, abort);
+            const float r1 = 1.0f / sqrtf(__fadd_rn(__fmul_rn(tot, L.inv_h), p.eps));
+            uint4 h[VPT];
+            ss = both(0.f);
+            uint4 *hrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.h_new.base) + row_off(p.h_new, r, L.nh));
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    ss[0] = __fmaf_rn(h[k][q], h[k][q], ss[0]);
+            for (int k = 0; k < VPT; ++k) {
+                const int v = k * vstride + gtid;
+                h[k] = make_uint4(0, 0, 0, 0);
+                if (v < nvec) {
+                    const uint4 x = xs[v];
+                    uint4 g = make_uint4(0, 0, 0, 0);
+                    if (GATE)
+                        g = gs[v];
+                    float2 w2[4];
+                    sw_weight(m.w[0], nvec, v, w2);
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 n = mul2(mul2(bf2(word(z[k], q)), both(r1)), w2[q]);
+                        const float2 f = GATE ? mul2(both(sg), bf2(word(g, q))) : both(sg);
+                        o[q] = pack2(fma2(f, n, bf2(word(x, q))));
+                        const float2 a = bf2(o[q]);
+                        ss = fma2(a, a, ss);
+                    }
+                    h[k] = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (!abort)
+                        __stcs(hrow + v, h[k]);
+                }
+            }
+            tot = group_sum(__fadd_rn(ss.x, ss.y), m.s, RL, gid, wig, lane, slot++, abort);
+            const float r2 = 1.0f / sqrtf(__fadd_rn(__fmul_rn(tot, L.inv_h), p.eps));
+            uint4 *yrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.y.base) + row_off(p.y, r, L.nh));
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = k * vstride + gtid;
+                if (v < nvec && !abort) {
+                    float2 w2[4];
+                    sw_weight(m.w[1], nvec, v, w2);
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        o[q] = pack2(mul2(mul2(bf2(word(h[k], q)), both(r2)), w2[q]));
+                    __stcs(yrow + v, make_uint4(o[0], o[1], o[2], o[3]));
+                }
+            }
+            if (gtid == 0 && !abort) {
+                p.rstd_post[r] = r1;
+                p.rstd_pre[r] = r2;
             }
         }
-        block_sum(ss, red);
-        const float r2 = 1.0f / sqrtf(__fadd_rn(__fmul_rn(ss[0], p.inv_h), p.eps));
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = k * kSwThreads + threadIdx.x;
-            if (v < p.nvec) {
-                float w[8], y[8];
-                load_w8(p.w_pre, p.pre_f32, v, w);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    y[q] = __fmul_rn(__fmul_rn(h[k][q], r2), w[q]);
-                out_ptr(p.y, r, p.nh)[v] = pack8(y);
-            }
-        }
-        if (threadIdx.x == 0) {
-            p.rstd_post[r] = r1;
-            p.rstd_pre[r] = r2;
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_addr(&m.s.empty[st]));
+        if (++st == (uint32_t)L.stages) {
+            st = 0;
+            ph ^= 1u;
         }
     }
+    if (abort && lane == 0)
+        set_status(p.status, kStatusTimeout);
 }
 
-template <int VPT>
-__global__ void __launch_bounds__(kSwThreads) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p)
+// ----------------------------------------------------------------- backward
+
+// Kahan-compensated hi += a * b of column pairs; lo holds the part of the
+// last term that hi has not taken up.
+__device__ __forceinline__ void kahan2(float2 &hi, float2 &lo, float2 a, float2 b)
 {
-    extern __shared__ float2 acc[]; // [2][H] compensated (hi, lo)
-    __shared__ float red[3][kSwWarps];
-    float2 *acc_post = acc, *acc_pre = acc + p.H;
-    for (int j = threadIdx.x; j < 2 * p.H; j += kSwThreads)
-        acc[j] = make_float2(0.f, 0.f);
-    __syncthreads();
-    const uint32_t r0 = blockIdx.x * p.rows_per_cta, r1 = min(p.rows, r0 + p.rows_per_cta);
-    for (uint32_t r = r0; r < r1; ++r) {
-        const float rp = p.rstd_post[r], rn = p.rstd_pre[r];
-        const float sg = p.gate_rows ? p.scale * p.gate_rows[r] : p.scale;
-        float s[3] = {0.f, 0.f, 0.f};
-        uint4 rh[VPT], rz[VPT], rd[VPT], re[VPT], rg[VPT];
+    const float2 y = fma2(a, b, lo);
+    const float2 t = add2(hi, y);
+    lo = add2(sub2(hi, t), y);
+    hi = t;
+}
+
+// GATE: 0 none, 1 a value per row, 2 a value per element.  A thread sums 2 x
+// 8 VPT columns in 4 x 8 VPT registers, which is why rows are spread at no
+// more than 16 columns a thread; R2 rows of a group share a reduction, its
+// barrier and the loads of the weights.
+template <int VPT, int R2, int GATE, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const SandwichLayout &L = p.L;
+    const SwSmem m = sw_carve(smem_raw, L);
+    const Layout RL = sw_rows_layout(L);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t r0 = blockIdx.x * L.rows_per_cta, r_end = min(L.rows, r0 + L.rows_per_cta);
+    init_ring(m.s, RL);
+    if (warp == L.groups * L.W) {
+        sw_produce(m, L, p.in, p.rstd_post, p.rstd_pre, p.gate_rows, r0, r_end, p.status, p.wait_ns);
+        return;
+    }
+    const int gid = warp / L.W, wig = warp - gid * L.W, gtid = wig * 32 + lane, vstride = 32 * L.W;
+    const int nvec = L.nvec;
+    const bool has_dh = p.has_dh;
+    {
+        Smem sw = m.s;
+        sw.wsm = m.w[0];
+        stage_weight(sw, RL, p.w_post, p.post_f32);
+        sw.wsm = m.w[1];
+        stage_weight(sw, RL, p.w_pre, p.pre_f32);
+    }
+    float2 hi1[VPT][4], lo1[VPT][4], hi2[VPT][4], lo2[VPT][4]; // dw_post, dw_pre
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = k * kSwThreads + threadIdx.x;
-            if (v < p.nvec) {
-                rh[k] = row_ptr(p.h, r, p.nh)[v];
-                rz[k] = row_ptr(p.z, r, p.nh)[v];
-                rd[k] = row_ptr(p.dy, r, p.nh)[v];
-                re[k] = p.dh.base ? row_ptr(p.dh, r, p.nh)[v] : make_uint4(0, 0, 0, 0);
-                if (p.gate.base)
-                    rg[k] = row_ptr(p.gate, r, p.nh)[v];
-                float h[8], z[8], d[8], e[8], g[8], w1[8], w2[8];
-                unpack8(rh[k], h);
-                unpack8(rz[k], z);
-                unpack8(rd[k], d);
-                unpack8(re[k], e);
-                load_w8(p.w_post, p.post_f32, v, w1);
-                load_w8(p.w_pre, p.pre_f32, v, w2);
-                if (p.gate.base)
-                    unpack8(rg[k], g);
+    for (int k = 0; k < VPT; ++k)
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float a = __fmul_rn(d[q], w2[q]);
-                    const float b = p.gate.base ? __fmul_rn(w1[q], g[q]) : w1[q];
-                    const float bz = __fmul_rn(b, z[q]);
-                    s[0] = __fmaf_rn(a, h[q], s[0]);
-                    s[1] = __fmaf_rn(__fmaf_rn(rn, a, e[q]), bz, s[1]);
-                    s[2] = __fmaf_rn(bz, h[q], s[2]);
+        for (int q = 0; q < 4; ++q)
+            hi1[k][q] = lo1[k][q] = hi2[k][q] = lo2[k][q] = both(0.f);
+
+    bool abort = false;
+    uint32_t slot = 0, st = 0, ph = 0;
+    const uint32_t tile = (uint32_t)L.groups * R2, tb = m.s.tens_bytes;
+    const uint32_t dh_off = (GATE == 2 ? 4 : 3) * tb;
+    for (uint32_t row0 = r0; row0 < r_end && !abort; row0 += tile) {
+        abort = !mbar_wait(smem_addr(&m.s.full[st]), ph, p.wait_ns);
+        const uint32_t rb = row0 + gid * R2; // the group's first row
+        if (rb < r_end) { // uniform across the group
+            const uint8_t *stage = m.s.ring + st * m.s.stage_bytes + (size_t)gid * R2 * L.H * 2;
+            float4 sc[R2];
+            float2 s1[R2], s2[R2], s3[R2];
+            bool live[R2];
+#pragma unroll
+            for (int i = 0; i < R2; ++i) {
+                live[i] = rb + i < r_end;
+                sc[i] = live[i] ? m.scalars[st * kSwMaxTile + gid * R2 + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+                s1[i] = s2[i] = s3[i] = both(0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = k * vstride + gtid;
+                if (v < nvec) {
+                    float2 w1[4], w2[4];
+                    sw_weight(m.w[0], nvec, v, w1);
+                    sw_weight(m.w[1], nvec, v, w2);
+#pragma unroll
+                    for (int i = 0; i < R2; ++i) {
+                        if (!live[i])
+                            continue;
+                        const uint4 *row = reinterpret_cast<const uint4 *>(stage + (size_t)i * L.H * 2) + v;
+                        const uint4 h = row[0], z = row[tb / 16], d = row[2 * (tb / 16)];
+                        uint4 g = make_uint4(0, 0, 0, 0), e = make_uint4(0, 0, 0, 0);
+                        if (GATE == 2)
+                            g = row[3 * (tb / 16)];
+                        if (has_dh)
+                            e = row[dh_off / 16];
+                        const float2 rn = both(sc[i].y);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float2 hq = bf2(word(h, q)), dq = bf2(word(d, q));
+                            const float2 a = mul2(dq, w2[q]);
+                            float2 bz = mul2(bf2(word(z, q)), GATE == 2 ? mul2(w1[q], bf2(word(g, q))) : w1[q]);
+                            s1[i] = fma2(a, hq, s1[i]);
+                            s2[i] = fma2(fma2(rn, a, bf2(word(e, q))), bz, s2[i]);
+                            s3[i] = fma2(bz, hq, s3[i]);
+                            kahan2(hi2[k][q], lo2[k][q], mul2(dq, hq), rn);
+                        }
+                    }
+                }
+            }
+            float sum[3 * R2], tot[3 * R2];
+#pragma unroll
+            for (int i = 0; i < R2; ++i) {
+                sum[3 * i] = __fadd_rn(s1[i].x, s1[i].y);
+                sum[3 * i + 1] = __fadd_rn(s2[i].x, s2[i].y);
+                sum[3 * i + 2] = __fadd_rn(s3[i].x, s3[i].y);
+            }
+            group_sum_n<3 * R2>(sum, tot, m.s, RL, gid, wig, lane, slot++, abort);
+            float nk2[R2], nk1[R2], sr[R2];
+#pragma unroll
+            for (int i = 0; i < R2; ++i) {
+                const float rp = sc[i].x, rn = sc[i].y;
+                const float k2 = __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(tot[3 * i], L.inv_h), rn), rn), rn);
+                const float dot = __fmaf_rn(-k2, tot[3 * i + 2], tot[3 * i + 1]);
+                nk2[i] = -k2;
+                nk1[i] = -__fmul_rn(__fmul_rn(__fmul_rn(dot, L.inv_h), rp), rp);
+                sr[i] = __fmul_rn(GATE == 1 ? __fmul_rn(p.scale, sc[i].z) : p.scale, rp);
+                if (GATE == 1 && p.dgate_rows && gtid == 0 && live[i] && !abort)
+                    p.dgate_rows[rb + i] = __fmul_rn(__fmul_rn(p.scale, rp), dot);
+            }
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = k * vstride + gtid;
+                if (v < nvec && !abort) {
+                    float2 w1[4], w2[4];
+                    sw_weight(m.w[0], nvec, v, w1);
+                    sw_weight(m.w[1], nvec, v, w2);
+#pragma unroll
+                    for (int i = 0; i < R2; ++i) {
+                        if (!live[i])
+                            continue;
+                        const uint32_t r = rb + i;
+                        const uint4 *row = reinterpret_cast<const uint4 *>(stage + (size_t)i * L.H * 2) + v;
+                        const uint4 h = row[0], z = row[tb / 16], d = row[2 * (tb / 16)];
+                        uint4 g = make_uint4(0, 0, 0, 0), e = make_uint4(0, 0, 0, 0);
+                        if (GATE == 2)
+                            g = row[3 * (tb / 16)];
+                        if (has_dh)
+                            e = row[dh_off / 16];
+                        const float2 rn = both(sc[i].y);
+                        uint32_t ox[4], oz[4], og[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float2 zq = bf2(word(z, q));
+                            const float2 a = mul2(bf2(word(d, q)), w2[q]);
+                            const float2 t = fma2(both(nk2[i]), bf2(word(h, q)), fma2(rn, a, bf2(word(e, q))));
+                            const float2 tg = GATE == 2 ? mul2(t, bf2(word(g, q))) : t;
+                            const float2 tz = mul2(both(sr[i]), zq);
+                            ox[q] = pack2(t);
+                            oz[q] = pack2(mul2(both(sr[i]), fma2(tg, w1[q], mul2(both(nk1[i]), zq))));
+                            if (GATE == 2)
+                                og[q] = pack2(mul2(mul2(t, tz), w1[q]));
+                            kahan2(hi1[k][q], lo1[k][q], tg, tz);
+                        }
+                        __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.dx.base) + row_off(p.dx, r, L.nh)) + v,
+                               make_uint4(ox[0], ox[1], ox[2], ox[3]));
+                        __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.dz.base) + row_off(p.dz, r, L.nh)) + v,
+                               make_uint4(oz[0], oz[1], oz[2], oz[3]));
+                        if (GATE == 2 && p.dgate.base)
+                            __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.dgate.base) +
+                                                             row_off(p.dgate, r, L.nh)) + v,
+                                   make_uint4(og[0], og[1], og[2], og[3]));
+                    }
                 }
             }
         }
-        block_sum(s, red);
-        const float c2 = __fmul_rn(__fmul_rn(s[0], p.inv_h), rn);
-        const float k2 = __fmul_rn(__fmul_rn(c2, rn), rn);
-        const float dot = __fmaf_rn(-k2, s[2], s[1]);
-        const float k1 = __fmul_rn(__fmul_rn(__fmul_rn(dot, p.inv_h), rp), rp);
-        const float sr = __fmul_rn(sg, rp);
-        if (threadIdx.x == 0 && p.dgate_rows)
-            p.dgate_rows[r] = __fmul_rn(__fmul_rn(p.scale, rp), dot);
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = k * kSwThreads + threadIdx.x;
-            if (v < p.nvec) {
-                float h[8], z[8], d[8], e[8], g[8], w1[8], w2[8], dx[8], dz[8], dg[8];
-                unpack8(rh[k], h);
-                unpack8(rz[k], z);
-                unpack8(rd[k], d);
-                unpack8(re[k], e);
-                load_w8(p.w_post, p.post_f32, v, w1);
-                load_w8(p.w_pre, p.pre_f32, v, w2);
-                if (p.gate.base)
-                    unpack8(rg[k], g);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float a = __fmul_rn(d[q], w2[q]);
-                    const float t = __fmaf_rn(-k2, h[q], __fmaf_rn(rn, a, e[q]));
-                    const float gq = p.gate.base ? g[q] : 1.f;
-                    dx[q] = t;
-                    const float tg = __fmul_rn(t, gq);
-                    dz[q] = __fmul_rn(sr, __fmaf_rn(tg, w1[q], -__fmul_rn(k1, z[q])));
-                    const float tz = __fmul_rn(sr, z[q]);
-                    dg[q] = __fmul_rn(__fmul_rn(t, tz), w1[q]);
-                    float2 m = acc_post[8 * v + q];
-                    comp_add(m.x, m.y, __fmul_rn(tg, tz));
-                    acc_post[8 * v + q] = m;
-                    m = acc_pre[8 * v + q];
-                    comp_add(m.x, m.y, __fmul_rn(__fmul_rn(d[q], h[q]), rn));
-                    acc_pre[8 * v + q] = m;
-                }
-                out_ptr(p.dx, r, p.nh)[v] = pack8(dx);
-                out_ptr(p.dz, r, p.nh)[v] = pack8(dz);
-                if (p.dgate.base)
-                    out_ptr(p.dgate, r, p.nh)[v] = pack8(dg);
-            }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_addr(&m.s.empty[st]));
+        if (++st == (uint32_t)L.stages) {
+            st = 0;
+            ph ^= 1u;
         }
     }
-    __syncthreads();
-    for (int j = threadIdx.x; j < p.H; j += kSwThreads) {
-        p.partials[(size_t)blockIdx.x * p.H + j] = acc_post[j];
-        p.partials[((size_t)gridDim.x + blockIdx.x) * p.H + j] = acc_pre[j];
+    if (abort && lane == 0)
+        set_status(p.status, kStatusTimeout);
+
+    // The CTA partial: the groups' sums in group order, through the drained
+    // ring ([group][w][4 nvec] float4 (hi, lo, hi, lo) of a column pair).
+    const int nct = L.groups * L.W * 32, nslot = 4 * nvec;
+    float4 *comb = reinterpret_cast<float4 *>(m.s.ring);
+    consumer_sync(RL);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int v = k * vstride + gtid;
+        if (v < nvec)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                comb[(size_t)(2 * gid) * nslot + 4 * v + q] =
+                    make_float4(hi1[k][q].x, lo1[k][q].x, hi1[k][q].y, lo1[k][q].y);
+                comb[(size_t)(2 * gid + 1) * nslot + 4 * v + q] =
+                    make_float4(hi2[k][q].x, lo2[k][q].x, hi2[k][q].y, lo2[k][q].y);
+            }
+    }
+    consumer_sync(RL);
+    for (int i = threadIdx.x; i < 2 * nslot; i += nct) {
+        const int w = i >= nslot, c = i - w * nslot;
+        float4 a = comb[i];
+        for (int g = 1; g < L.groups; ++g) {
+            const float4 b = comb[(size_t)2 * g * nslot + i];
+            comp_add(a.x, a.y, b.x);
+            a.y = __fadd_rn(a.y, b.y);
+            comp_add(a.z, a.w, b.z);
+            a.w = __fadd_rn(a.w, b.w);
+        }
+        reinterpret_cast<float4 *>(p.partials + ((size_t)w * gridDim.x + blockIdx.x) * L.H)[c] = a;
     }
     pdl_launch_dependents();
 }
@@ -254,54 +496,93 @@ __global__ void __launch_bounds__(32 * kSwReduceWarps)
 
 // ------------------------------------------------------------------ launch
 
-cudaError_t ensure_smem_attr(const void *kernel, size_t smem);
-
-int sandwich_bwd_ctas(int H, uint32_t rows)
+// The shape of a CTA.  It depends on H and the staged tensors, the number of
+// CTAs on the rows too, and on nothing else, so the sums' orders do not either.
+SandwichPlan sandwich_plan(int H, uint32_t rows, int ntens, bool backward)
 {
-    (void)H;
-    const uint32_t most = kSMsStep;
-    if (rows == 0)
-        return 0;
-    const uint32_t per = (rows + most - 1) / most;
-    return (int)((rows + per - 1) / per);
-}
-
-template <int VPT>
-static cudaError_t fwd_vpt(const SandwichFwdParams &p, cudaStream_t stream)
-{
-    const int ctas = (int)(p.rows < (uint32_t)kSMsStep * 8 ? p.rows : (uint32_t)kSMsStep * 8);
-    sandwich_fwd_kernel<VPT><<<ctas, kSwThreads, 0, stream>>>(p);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, cudaStream_t stream)
-{
-    switch ((p.nvec + kSwThreads - 1) / kSwThreads) {
-    case 1: return fwd_vpt<1>(p, stream);
-    case 2: return fwd_vpt<2>(p, stream);
-    case 3: return fwd_vpt<3>(p, stream);
-    default: return fwd_vpt<4>(p, stream);
+    SandwichPlan p{};
+    const int nvec = H / 8;
+    p.vpt = nvec <= 32 ? 1 : 2;
+    p.W = (nvec + 32 * p.vpt - 1) / (32 * p.vpt);
+    p.groups = p.W >= 12 ? 1 : 12 / p.W;
+    p.r2 = backward && p.W > 1 && p.groups == 1 ? 2 : 1;
+    // CTAs per SM: 16 warps of 128 registers (backward), 28 of 72 (forward)
+    int per_sm = (backward ? 16 : 28) / (p.groups * p.W + 1);
+    per_sm = per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm;
+    const size_t fixed = (size_t)kSwFixed + 2 * weight_smem_bytes(H);
+    const size_t limit = 227 * 1024;
+    for (;; ) {
+        const size_t stage = (size_t)ntens * p.groups * p.r2 * H * 2;
+        const size_t room = limit / per_sm - 1024; // 1 KB of each CTA is the system's
+        p.stages = room > fixed ? (int)((room - fixed) / stage) : 0;
+        if (p.stages >= 2)
+            break;
+        if (per_sm > 1)
+            --per_sm;
+        else if (p.r2 > 1)
+            p.r2 = 1;
+        else if (p.groups > 1)
+            --p.groups;
+        else
+            break; // the widest rows with five tensors: one stage
     }
+    if (p.stages > kSwMaxStages)
+        p.stages = kSwMaxStages;
+    const uint32_t tile = (uint32_t)p.groups * p.r2;
+    p.smem = fixed + (size_t)p.stages * ntens * tile * H * 2;
+    const size_t comb = fixed + (size_t)(backward ? p.groups : 0) * H * 16;
+    if (comb > p.smem)
+        p.smem = comb;
+    uint32_t ctas = (rows + tile - 1) / tile;
+    if (ctas > (uint32_t)kSMsStep * per_sm)
+        ctas = (uint32_t)kSMsStep * per_sm;
+    p.rows_per_cta = ctas ? (rows + ctas - 1) / ctas : 0;
+    p.ctas = p.rows_per_cta ? (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta) : 0;
+    return p;
 }
 
-template <int VPT>
-static cudaError_t bwd_vpt(const SandwichBwdParams &p, int ctas, cudaStream_t stream)
+template <class P>
+static cudaError_t launch_rows(void (*kern)(P), const P &p, const SandwichPlan &plan, cudaStream_t stream)
 {
-    const size_t smem = (size_t)16 * p.H;
-    cudaError_t e = ensure_smem_attr((const void *)sandwich_bwd_kernel<VPT>, smem);
+    const int threads = 32 * (plan.groups * plan.W + 1);
+    cudaError_t e = ensure_smem_attr((const void *)kern, plan.smem);
     if (e != cudaSuccess)
         return e;
-    sandwich_bwd_kernel<VPT><<<ctas, kSwThreads, smem, stream>>>(p);
+    kern<<<plan.ctas, threads, plan.smem, stream>>>(p);
     return cudaGetLastError();
 }
 
-cudaError_t launch_sandwich_bwd(const SandwichBwdParams &p, int ctas, cudaStream_t stream)
+cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
 {
-    switch ((p.nvec + kSwThreads - 1) / kSwThreads) {
-    case 1: return bwd_vpt<1>(p, ctas, stream);
-    case 2: return bwd_vpt<2>(p, ctas, stream);
-    case 3: return bwd_vpt<3>(p, ctas, stream);
-    default: return bwd_vpt<4>(p, ctas, stream);
+    const bool g = p.L.ntens == 3;
+    if (plan.vpt == 1)
+        return g ? launch_rows(sandwich_fwd_kernel<1, true, kSwFwdThreads>, p, plan, stream)
+                 : launch_rows(sandwich_fwd_kernel<1, false, kSwFwdThreads>, p, plan, stream);
+    if (plan.W <= 12)
+        return g ? launch_rows(sandwich_fwd_kernel<2, true, kSwFwdThreads>, p, plan, stream)
+                 : launch_rows(sandwich_fwd_kernel<2, false, kSwFwdThreads>, p, plan, stream);
+    return g ? launch_rows(sandwich_fwd_kernel<2, true, kSwWideThreads>, p, plan, stream)
+             : launch_rows(sandwich_fwd_kernel<2, false, kSwWideThreads>, p, plan, stream);
+}
+
+template <int GATE>
+static cudaError_t launch_bwd_gate(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
+{
+    if (plan.vpt == 1)
+        return launch_rows(sandwich_bwd_kernel<1, 1, GATE, kSwFwdThreads>, p, plan, stream);
+    if (plan.W > 12)
+        return plan.r2 == 2 ? launch_rows(sandwich_bwd_kernel<2, 2, GATE, kSwWideThreads>, p, plan, stream)
+                            : launch_rows(sandwich_bwd_kernel<2, 1, GATE, kSwWideThreads>, p, plan, stream);
+    return plan.r2 == 2 ? launch_rows(sandwich_bwd_kernel<2, 2, GATE, kSwFwdThreads>, p, plan, stream)
+                        : launch_rows(sandwich_bwd_kernel<2, 1, GATE, kSwFwdThreads>, p, plan, stream);
+}
+
+cudaError_t launch_sandwich_bwd(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
+{
+    switch (p.gate) {
+    case 0: return launch_bwd_gate<0>(p, plan, stream);
+    case 1: return launch_bwd_gate<1>(p, plan, stream);
+    default: return launch_bwd_gate<2>(p, plan, stream);
     }
 }
 

@@ -57,6 +57,23 @@ cake_status check_sandwich(const cake_shape *shape, const void *w_post, cake_dty
     return has(gate) ? check_tensor(gate, shape) : CAKE_OK;
 }
 
+SandwichLayout sandwich_layout(const SandwichPlan &plan, const cake_shape *shape, uint32_t rows, int ntens)
+{
+    SandwichLayout L;
+    L.H = (int)shape->hidden;
+    L.nvec = L.H / 8;
+    L.W = plan.W;
+    L.groups = plan.groups;
+    L.r2 = plan.r2;
+    L.stages = plan.stages;
+    L.ntens = ntens;
+    L.rows = rows;
+    L.nh = (uint32_t)shape->heads;
+    L.rows_per_cta = plan.rows_per_cta;
+    L.inv_h = 1.0f / (float)L.H;
+    return L;
+}
+
 } // namespace
 
 // ------------------------------------------------------------ sandwich norm
@@ -91,16 +108,13 @@ extern "C" cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_ten
             if (i && overlap(o, i, shape) && !same_view(o, i, shape))
                 return CAKE_ERR_INVALID;
     SandwichFwdParams p{};
-    p.H = (int)shape->hidden;
-    p.nvec = p.H / 8;
-    p.rows = rows;
-    p.nh = (uint32_t)shape->heads;
-    p.inv_h = 1.0f / (float)p.H;
+    const SandwichPlan plan = sandwich_plan((int)shape->hidden, rows, has(gate) ? 3 : 2, false);
+    p.L = sandwich_layout(plan, shape, rows, has(gate) ? 3 : 2);
     p.eps = eps;
     p.scale = scale;
-    p.z = make_view(z, shape);
-    p.x = make_view(x, shape);
-    p.gate = make_view(gate, shape);
+    p.in[0] = make_view(z, shape);
+    p.in[1] = make_view(x, shape);
+    p.in[2] = make_view(gate, shape);
     p.y = make_view(y, shape);
     p.h_new = make_view(h_new, shape);
     p.gate_rows = gate_rows;
@@ -110,7 +124,10 @@ extern "C" cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_ten
     p.pre_f32 = w_pre_dtype == CAKE_FP32;
     p.rstd_post = rstd_post;
     p.rstd_pre = rstd_pre;
-    return cuda_status(launch_sandwich_fwd(p, cu(stream)));
+    p.wait_ns = kWaitLimitNs;
+    if (step_status_ptr(&p.status) != cudaSuccess)
+        return CAKE_ERR_CUDA;
+    return cuda_status(launch_sandwich_fwd(p, plan, cu(stream)));
 }
 
 extern "C" size_t cake_sandwich_bwd_workspace_size(const cake_shape *shape)
@@ -118,7 +135,11 @@ extern "C" size_t cake_sandwich_bwd_workspace_size(const cake_shape *shape)
     uint32_t rows = 0;
     if (check_shape(shape, &rows) != CAKE_OK || rows == 0)
         return 0;
-    return (size_t)2 * sandwich_bwd_ctas((int)shape->hidden, rows) * shape->hidden * sizeof(float2);
+    // the CTAs depend on the number of staged tensors: room for each choice
+    int ctas = 0;
+    for (int ntens = 3; ntens <= 5; ++ntens)
+        ctas = std::max(ctas, sandwich_plan((int)shape->hidden, rows, ntens, true).ctas);
+    return (size_t)2 * ctas * shape->hidden * sizeof(float2);
 }
 
 extern "C" cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_tensor *dy, const cake_tensor *dh,
@@ -170,19 +191,19 @@ extern "C" cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_ten
     if ((st = check_workspace(workspace, workspace_bytes, cake_sandwich_bwd_workspace_size(shape))) != CAKE_OK)
         return st;
     SandwichBwdParams p{};
-    const int ctas = sandwich_bwd_ctas(H, rows);
-    p.H = H;
-    p.nvec = H / 8;
-    p.rows = rows;
-    p.nh = (uint32_t)shape->heads;
-    p.rows_per_cta = (rows + ctas - 1) / ctas;
-    p.inv_h = 1.0f / (float)H;
+    p.in[0] = make_view(h_new, shape);
+    p.in[1] = make_view(z, shape);
+    p.in[2] = make_view(dy, shape);
+    int ntens = 3;
+    if (has(gate))
+        p.in[ntens++] = make_view(gate, shape);
+    if (has(dh))
+        p.in[ntens++] = make_view(dh, shape);
+    const SandwichPlan plan = sandwich_plan(H, rows, ntens, true);
+    p.L = sandwich_layout(plan, shape, rows, ntens);
     p.scale = scale;
-    p.dy = make_view(dy, shape);
-    p.dh = make_view(dh, shape);
-    p.h = make_view(h_new, shape);
-    p.z = make_view(z, shape);
-    p.gate = make_view(gate, shape);
+    p.gate = has(gate) ? 2 : gate_rows ? 1 : 0;
+    p.has_dh = has(dh);
     p.dx = make_view(dx, shape);
     p.dz = make_view(dz, shape);
     p.dgate = make_view(dgate, shape);
@@ -195,10 +216,10 @@ extern "C" cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_ten
     p.post_f32 = w_post_dtype == CAKE_FP32;
     p.pre_f32 = w_pre_dtype == CAKE_FP32;
     p.partials = static_cast<float2 *>(workspace);
-    cudaError_t e = launch_sandwich_bwd(p, ctas, cu(stream));
-    if (e != cudaSuccess)
+    p.wait_ns = kWaitLimitNs;
+    if (step_status_ptr(&p.status) != cudaSuccess || launch_sandwich_bwd(p, plan, cu(stream)) != cudaSuccess)
         return CAKE_ERR_CUDA;
-    SandwichReduceParams rp{p.partials, ctas, H, {dw_post, dw_pre}};
+    SandwichReduceParams rp{p.partials, plan.ctas, H, {dw_post, dw_pre}};
     return cuda_status(launch_sandwich_reduce(rp, cu(stream)));
 }
 

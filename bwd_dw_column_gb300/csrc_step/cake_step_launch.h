@@ -12,30 +12,48 @@ namespace cake {
 
 // ------------------------------------------------------------ sandwich norm
 
+// A row of a sandwich norm spans W warps of VPT 8-column vectors a thread;
+// `groups` rows (times R2) are in flight per CTA, staged by a producer warp.
+struct SandwichPlan {
+    int vpt, W, groups, r2, stages, ctas;
+    uint32_t rows_per_cta;
+    size_t smem;
+};
+
+struct SandwichLayout {
+    int H, nvec, W, groups, r2, stages, ntens;
+    uint32_t rows, nh, rows_per_cta;
+    float inv_h;
+};
+
 struct SandwichFwdParams {
-    int H, nvec;
-    uint32_t rows, nh;
-    float inv_h, eps, scale;
-    RowView z, x, gate;    // gate.base == nullptr: no element gate
+    SandwichLayout L;
+    float eps, scale;
+    RowView in[3];         // staged: z, x[, gate]
     RowView y, h_new;      // outputs (written through base)
     const float *gate_rows;
     const void *w_post, *w_pre;
     int post_f32, pre_f32;
     float *rstd_post, *rstd_pre;
+    int *status;
+    uint64_t wait_ns;
 };
 
 struct SandwichBwdParams {
-    int H, nvec;
-    uint32_t rows, nh, rows_per_cta;
-    float inv_h, scale;
-    RowView dy, dh, h, z, gate;
-    RowView dx, dz, dgate; // outputs
+    SandwichLayout L;
+    float scale;
+    RowView in[5];         // staged: h, z, dy[, gate][, dh]
+    int gate;              // 0 none, 1 a value per row, 2 a value per element
+    int has_dh;
+    RowView dx, dz, dgate; // outputs; dgate.base == nullptr: not wanted
     const float *gate_rows;
     float *dgate_rows;
     const float *rstd_post, *rstd_pre;
     const void *w_post, *w_pre;
     int post_f32, pre_f32;
     float2 *partials;      // [2][ctas][H] (hi, lo): dw_post's, then dw_pre's
+    int *status;
+    uint64_t wait_ns;
 };
 
 struct SandwichReduceParams {
@@ -44,9 +62,9 @@ struct SandwichReduceParams {
     float *dw[2];           // dw_post, dw_pre
 };
 
-int sandwich_bwd_ctas(int H, uint32_t rows);
-cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, cudaStream_t stream);
-cudaError_t launch_sandwich_bwd(const SandwichBwdParams &p, int ctas, cudaStream_t stream);
+SandwichPlan sandwich_plan(int H, uint32_t rows, int ntens, bool backward);
+cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, const SandwichPlan &plan, cudaStream_t stream);
+cudaError_t launch_sandwich_bwd(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream);
 cudaError_t launch_sandwich_reduce(const SandwichReduceParams &p, cudaStream_t stream);
 
 // ----------------------------------------------- gradient norm and clipping

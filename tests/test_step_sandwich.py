@@ -104,7 +104,7 @@ def test_fp64_backward_is_the_derivative(gate):
 # ------------------------------------------------------------------- kernels
 
 SHAPES = [(1, 8), (1, 2048), (2, 64), (5, 256), (7, 264), (33, 520), (3, 1024), (129, 1536), (3, 4104), (17, 5120),
-          (2, 6144), (3, 8192), (311, 2048), (613, 128)]
+          (2, 6144), (3, 8192), (4, 8192), (305, 7936), (311, 2048), (613, 128)]
 
 
 @pytest.mark.gpu
