@@ -25,29 +25,36 @@ cudaError_t ensure_smem_attr(const void *kernel, size_t smem);
 
 constexpr int kSMsStep = 152;
 constexpr int kSwMaxStages = 16;
-constexpr int kSwMaxTile = 24;            // rows of a stage, at most
-constexpr int kSwMisc = 2048;             // barriers and the row sums' slots
-constexpr int kSwScalars = kSwMaxStages * kSwMaxTile * 16; // a float4 of each staged row's scalars
-constexpr int kSwFixed = kSwMisc + kSwScalars;
+constexpr int kSwMaxTile = 12;            // rows of a stage, at most
+constexpr int kSwSlots = 4;               // backward: rows whose partial sums may be in use
+constexpr int kSwSlotFloats = 64;         // ... [4 sums][16 warps]
+// Shared memory before the weights: the ring's barriers (256 bytes), the row
+// sums' barriers (256), a flag (64), the row sums' partials, the rows' scalars.
+constexpr int kSwRed = 576;
+constexpr int kSwScalarsAt = kSwRed + kSwMaxTile * kSwSlots * kSwSlotFloats * 4;
+constexpr int kSwFixed = (kSwScalarsAt + kSwMaxStages * kSwMaxTile * 16 + 1023) / 1024 * 1024;
 
 struct SwSmem {
     Smem s;               // barriers, reduction slots, flag, ring
+    uint64_t *sums;       // [groups][2] backward: a row's partial sums are written
     float4 *scalars;      // [stages][tile rows] (rstd_post, rstd_pre, row gate, -)
     float *w[2];          // w_post, w_pre as FP32, two planes each (see stage_weight)
 };
 
+template <bool WS>
 __device__ __forceinline__ SwSmem sw_carve(uint8_t *base, const SandwichLayout &L)
 {
     SwSmem m;
     m.s.full = reinterpret_cast<uint64_t *>(base);
     m.s.empty = m.s.full + L.stages;
-    m.s.red = reinterpret_cast<float *>(base + 256);
-    m.s.flag = reinterpret_cast<int *>(base + kSwMisc - 16);
-    m.scalars = reinterpret_cast<float4 *>(base + kSwMisc);
+    m.sums = reinterpret_cast<uint64_t *>(base + 256);
+    m.s.flag = reinterpret_cast<int *>(base + 512);
+    m.s.red = reinterpret_cast<float *>(base + kSwRed);
+    m.scalars = reinterpret_cast<float4 *>(base + kSwScalarsAt);
     m.w[0] = reinterpret_cast<float *>(base + kSwFixed);
     m.w[1] = m.w[0] + weight_smem_bytes(L.H) / 4;
-    m.s.ring = base + kSwFixed + 2 * weight_smem_bytes(L.H);
-    m.s.tens_bytes = (uint32_t)L.groups * L.r2 * L.H * 2;
+    m.s.ring = base + kSwFixed + (WS ? 2 * weight_smem_bytes(L.H) : 0);
+    m.s.tens_bytes = (uint32_t)L.groups * L.H * 2;
     m.s.stage_bytes = m.s.tens_bytes * L.ntens;
     return m;
 }
@@ -76,6 +83,28 @@ __device__ __forceinline__ void sw_weight(const float *w, int nvec, int v, float
     w2[3] = make_float2(b.z, b.w);
 }
 
+__device__ __forceinline__ void sw_weight_global(const void *w, int f32, int v, float2 (&w2)[4])
+{
+    if (f32) {
+        const float4 a = __ldg(static_cast<const float4 *>(w) + 2 * v);
+        const float4 b = __ldg(static_cast<const float4 *>(w) + 2 * v + 1);
+        w2[0] = make_float2(a.x, a.y);
+        w2[1] = make_float2(a.z, a.w);
+        w2[2] = make_float2(b.x, b.y);
+        w2[3] = make_float2(b.z, b.w);
+    } else {
+        const uint4 a = __ldg(static_cast<const uint4 *>(w) + v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            w2[q] = bf2(word(a, q));
+    }
+}
+
+__device__ __forceinline__ uint4 *out_row(const RowView &v, uint32_t r, uint32_t nh)
+{
+    return reinterpret_cast<uint4 *>(const_cast<uint16_t *>(v.base) + row_off(v, r, nh));
+}
+
 // Producer warp: streams the CTA's rows of every staged tensor into the ring;
 // a row's scalars go along through plain shared stores, loaded a tile ahead
 // and published by the arrival on the stage's full barrier.
@@ -86,7 +115,7 @@ __device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout
 {
     const uint32_t lane = threadIdx.x & 31;
     const uint64_t pol = policy_evict_first();
-    const uint32_t row_bytes = (uint32_t)L.H * 2, tile = (uint32_t)L.groups * L.r2;
+    const uint32_t row_bytes = (uint32_t)L.H * 2, tile = (uint32_t)L.groups;
     auto scalars = [&](uint32_t row0) {
         float4 v = make_float4(0.f, 0.f, 1.f, 0.f);
         if (lane < tile && row0 + lane < r_end) {
@@ -152,7 +181,7 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_fwd_kernel(const __grid_c
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const SandwichLayout &L = p.L;
-    const SwSmem m = sw_carve(smem_raw, L);
+    const SwSmem m = sw_carve<true>(smem_raw, L);
     const Layout RL = sw_rows_layout(L);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t r0 = blockIdx.x * L.rows_per_cta, r_end = min(L.rows, r0 + L.rows_per_cta);
@@ -198,7 +227,7 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_fwd_kernel(const __grid_c
             const float r1 = 1.0f / sqrtf(__fadd_rn(__fmul_rn(tot, L.inv_h), p.eps));
             uint4 h[VPT];
             ss = both(0.f);
-            uint4 *hrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.h_new.base) + row_off(p.h_new, r, L.nh));
+            uint4 *hrow = out_row(p.h_new, r, L.nh);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int v = k * vstride + gtid;
@@ -226,7 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_fwd_kernel(const __grid_c
             }
             tot = group_sum(__fadd_rn(ss.x, ss.y), m.s, RL, gid, wig, lane, slot++, abort);
             const float r2 = 1.0f / sqrtf(__fadd_rn(__fmul_rn(tot, L.inv_h), p.eps));
-            uint4 *yrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.y.base) + row_off(p.y, r, L.nh));
+            uint4 *yrow = out_row(p.y, r, L.nh);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int v = k * vstride + gtid;
@@ -269,19 +298,50 @@ __device__ __forceinline__ void kahan2(float2 &hi, float2 &lo, float2 a, float2 
     hi = t;
 }
 
-// GATE: 0 none, 1 a value per row, 2 a value per element.  A thread sums 2 x
-// 8 VPT columns in 4 x 8 VPT registers, which is why rows are spread at no
-// more than 16 columns a thread; R2 rows of a group share a reduction, its
-// barrier and the loads of the weights.
-template <int VPT, int R2, int GATE, int THREADS>
+// The three sums of a row over a warp: lanes [8 n, 8 n + 8) end with sum n
+// (n = 3: zero).  Each of the first two steps halves the values that a lane
+// still carries, so three sums take 6 shuffles instead of 15.
+__device__ __forceinline__ float warp_sum3(float v0, float v1, float v2, int lane)
+{
+    const bool up = lane & 16, hi = lane & 8;
+    float a = up ? v2 : v0, b = up ? 0.f : v1;
+    a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, up ? v0 : v2, 16));
+    b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, up ? v1 : 0.f, 16));
+    float r = hi ? b : a;
+    r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, hi ? a : b, 8));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+        r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, o));
+    return r;
+}
+
+// GATE: 0 none, 1 a value per row, 2 a value per element.  WS: the weights
+// are staged in shared memory (else read through L2, for rows so wide that
+// fewer than three stages would be left).
+//
+// A thread holds the two column sums of 8 VPT columns as Kahan pairs, 32 VPT
+// registers, which is why it takes no more than 16 columns.
+//
+// Order of work: first pass of row j + 1 (its three sums and dw_pre), then
+// the second pass of row j (its outputs and dw_post).  The sums of a row
+// travel between the group's warps through shared memory behind an mbarrier
+// that a warp arrives on after its first pass and tests after the next row's,
+// so that no warp waits for a reduction.  Two barriers alternate: a warp is
+// never more than two rows ahead of another, and four slots hold the partials
+// of the rows that may be in use.
+template <int VPT, int GATE, bool WS, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const SandwichLayout &L = p.L;
-    const SwSmem m = sw_carve(smem_raw, L);
+    const SwSmem m = sw_carve<WS>(smem_raw, L);
     const Layout RL = sw_rows_layout(L);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t r0 = blockIdx.x * L.rows_per_cta, r_end = min(L.rows, r0 + L.rows_per_cta);
+    if (threadIdx.x < 2 * L.groups)
+        mbar_init(smem_addr(m.sums + threadIdx.x), L.W);
+    for (int i = threadIdx.x; i < L.groups * kSwSlots * kSwSlotFloats; i += blockDim.x)
+        m.s.red[i] = 0.f; // the parts of warps that a row does not have stay zero
     init_ring(m.s, RL);
     if (warp == L.groups * L.W) {
         sw_produce(m, L, p.in, p.rstd_post, p.rstd_pre, p.gate_rows, r0, r_end, p.status, p.wait_ns);
@@ -290,13 +350,19 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_bwd_kernel(const __grid_c
     const int gid = warp / L.W, wig = warp - gid * L.W, gtid = wig * 32 + lane, vstride = 32 * L.W;
     const int nvec = L.nvec;
     const bool has_dh = p.has_dh;
-    {
+    if (WS) {
         Smem sw = m.s;
         sw.wsm = m.w[0];
         stage_weight(sw, RL, p.w_post, p.post_f32);
         sw.wsm = m.w[1];
         stage_weight(sw, RL, p.w_pre, p.pre_f32);
     }
+    auto weight = [&](int which, int v, float2(&w2)[4]) {
+        if (WS)
+            sw_weight(m.w[which], nvec, v, w2);
+        else
+            sw_weight_global(which ? p.w_pre : p.w_post, which ? p.pre_f32 : p.post_f32, v, w2);
+    };
     float2 hi1[VPT][4], lo1[VPT][4], hi2[VPT][4], lo2[VPT][4]; // dw_post, dw_pre
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
@@ -304,129 +370,131 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_bwd_kernel(const __grid_c
         for (int q = 0; q < 4; ++q)
             hi1[k][q] = lo1[k][q] = hi2[k][q] = lo2[k][q] = both(0.f);
 
-    bool abort = false;
-    uint32_t slot = 0, st = 0, ph = 0;
-    const uint32_t tile = (uint32_t)L.groups * R2, tb = m.s.tens_bytes;
+    const uint32_t tile = (uint32_t)L.groups, tb = m.s.tens_bytes / 16;
     const uint32_t dh_off = (GATE == 2 ? 4 : 3) * tb;
-    for (uint32_t row0 = r0; row0 < r_end && !abort; row0 += tile) {
-        abort = !mbar_wait(smem_addr(&m.s.full[st]), ph, p.wait_ns);
-        const uint32_t rb = row0 + gid * R2; // the group's first row
-        if (rb < r_end) { // uniform across the group
-            const uint8_t *stage = m.s.ring + st * m.s.stage_bytes + (size_t)gid * R2 * L.H * 2;
-            float4 sc[R2];
-            float2 s1[R2], s2[R2], s3[R2];
-            bool live[R2];
+    const uint32_t ntiles = r_end > r0 ? (r_end - r0 + tile - 1) / tile : 0;
+    const uint4 *gbase = reinterpret_cast<const uint4 *>(m.s.ring + (size_t)gid * L.H * 2);
+    const uint32_t sbytes = m.s.stage_bytes / 16;
+    float *red = m.s.red + gid * kSwSlots * kSwSlotFloats;
+    float own = 0.f; // rows of one warp: the sums of the row between its passes
+    bool abort = false;
+    uint32_t st1 = 0, ph1 = 0, st2 = 0; // ring slots of the first and the second pass
+    for (uint32_t j = 0; j <= ntiles && !abort; ++j) {
+        float mine = 0.f;
+        if (j < ntiles) {
+            abort = !mbar_wait(smem_addr(&m.s.full[st1]), ph1, p.wait_ns);
+            if (r0 + j * tile + gid < r_end && !abort) { // uniform across the group
+                const float2 rn = both(m.scalars[st1 * kSwMaxTile + gid].y);
+                float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f);
 #pragma unroll
-            for (int i = 0; i < R2; ++i) {
-                live[i] = rb + i < r_end;
-                sc[i] = live[i] ? m.scalars[st * kSwMaxTile + gid * R2 + i] : make_float4(0.f, 0.f, 0.f, 0.f);
-                s1[i] = s2[i] = s3[i] = both(0.f);
-            }
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int v = k * vstride + gtid;
-                if (v < nvec) {
-                    float2 w1[4], w2[4];
-                    sw_weight(m.w[0], nvec, v, w1);
-                    sw_weight(m.w[1], nvec, v, w2);
-#pragma unroll
-                    for (int i = 0; i < R2; ++i) {
-                        if (!live[i])
-                            continue;
-                        const uint4 *row = reinterpret_cast<const uint4 *>(stage + (size_t)i * L.H * 2) + v;
-                        const uint4 h = row[0], z = row[tb / 16], d = row[2 * (tb / 16)];
+                for (int k = 0; k < VPT; ++k) {
+                    const int v = k * vstride + gtid;
+                    if (v < nvec) {
+                        const uint4 *row = gbase + st1 * sbytes + v;
+                        const uint4 h = row[0], z = row[tb], d = row[2 * tb];
                         uint4 g = make_uint4(0, 0, 0, 0), e = make_uint4(0, 0, 0, 0);
                         if (GATE == 2)
-                            g = row[3 * (tb / 16)];
+                            g = row[3 * tb];
                         if (has_dh)
-                            e = row[dh_off / 16];
-                        const float2 rn = both(sc[i].y);
+                            e = row[dh_off];
+                        float2 w1[4], w2[4];
+                        weight(0, v, w1);
+                        weight(1, v, w2);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const float2 hq = bf2(word(h, q)), dq = bf2(word(d, q));
                             const float2 a = mul2(dq, w2[q]);
-                            float2 bz = mul2(bf2(word(z, q)), GATE == 2 ? mul2(w1[q], bf2(word(g, q))) : w1[q]);
-                            s1[i] = fma2(a, hq, s1[i]);
-                            s2[i] = fma2(fma2(rn, a, bf2(word(e, q))), bz, s2[i]);
-                            s3[i] = fma2(bz, hq, s3[i]);
+                            const float2 bz =
+                                mul2(bf2(word(z, q)), GATE == 2 ? mul2(w1[q], bf2(word(g, q))) : w1[q]);
+                            s1 = fma2(a, hq, s1);
+                            s2 = fma2(fma2(rn, a, bf2(word(e, q))), bz, s2);
+                            s3 = fma2(bz, hq, s3);
                             kahan2(hi2[k][q], lo2[k][q], mul2(dq, hq), rn);
                         }
                     }
                 }
+                mine = warp_sum3(__fadd_rn(s1.x, s1.y), __fadd_rn(s2.x, s2.y), __fadd_rn(s3.x, s3.y), lane);
+                if (L.W > 1) {
+                    if ((lane & 7) == 0)
+                        red[(j & 3) * kSwSlotFloats + (lane >> 3) * 16 + wig] = mine;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(m.sums + 2 * gid + (j & 1)));
+                }
             }
-            float sum[3 * R2], tot[3 * R2];
-#pragma unroll
-            for (int i = 0; i < R2; ++i) {
-                sum[3 * i] = __fadd_rn(s1[i].x, s1[i].y);
-                sum[3 * i + 1] = __fadd_rn(s2[i].x, s2[i].y);
-                sum[3 * i + 2] = __fadd_rn(s3[i].x, s3[i].y);
+            if (++st1 == (uint32_t)L.stages) {
+                st1 = 0;
+                ph1 ^= 1u;
             }
-            group_sum_n<3 * R2>(sum, tot, m.s, RL, gid, wig, lane, slot++, abort);
-            float nk2[R2], nk1[R2], sr[R2];
+        }
+        if (j > 0) {
+            const uint32_t i = j - 1, r = r0 + i * tile + gid;
+            if (r < r_end) {
+                float t3 = own;
+                if (L.W > 1) {
+                    if (!mbar_wait(smem_addr(m.sums + 2 * gid + (i & 1)), (i >> 1) & 1, p.wait_ns))
+                        abort = true;
+                    const float2 a = *reinterpret_cast<const float2 *>(red + (i & 3) * kSwSlotFloats + (lane >> 3) * 16 +
+                                                                       2 * (lane & 7));
+                    t3 = __fadd_rn(a.x, a.y);
 #pragma unroll
-            for (int i = 0; i < R2; ++i) {
-                const float rp = sc[i].x, rn = sc[i].y;
-                const float k2 = __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(tot[3 * i], L.inv_h), rn), rn), rn);
-                const float dot = __fmaf_rn(-k2, tot[3 * i + 2], tot[3 * i + 1]);
-                nk2[i] = -k2;
-                nk1[i] = -__fmul_rn(__fmul_rn(__fmul_rn(dot, L.inv_h), rp), rp);
-                sr[i] = __fmul_rn(GATE == 1 ? __fmul_rn(p.scale, sc[i].z) : p.scale, rp);
-                if (GATE == 1 && p.dgate_rows && gtid == 0 && live[i] && !abort)
-                    p.dgate_rows[rb + i] = __fmul_rn(__fmul_rn(p.scale, rp), dot);
-            }
+                    for (int o = 4; o > 0; o >>= 1)
+                        t3 = __fadd_rn(t3, __shfl_xor_sync(0xffffffffu, t3, o));
+                }
+                const float t1 = __shfl_sync(0xffffffffu, t3, 0), t2 = __shfl_sync(0xffffffffu, t3, 8);
+                t3 = __shfl_sync(0xffffffffu, t3, 16);
+                const float4 sc = m.scalars[st2 * kSwMaxTile + gid];
+                const float k2 = __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(t1, L.inv_h), sc.y), sc.y), sc.y);
+                const float dot = __fmaf_rn(-k2, t3, t2);
+                const float2 nk2 = both(-k2), rn = both(sc.y);
+                const float2 nk1 = both(-__fmul_rn(__fmul_rn(__fmul_rn(dot, L.inv_h), sc.x), sc.x));
+                const float2 sr = both(__fmul_rn(GATE == 1 ? __fmul_rn(p.scale, sc.z) : p.scale, sc.x));
+                if (GATE == 1 && p.dgate_rows && gtid == 0 && !abort)
+                    p.dgate_rows[r] = __fmul_rn(__fmul_rn(p.scale, sc.x), dot);
+                uint4 *dx = out_row(p.dx, r, L.nh), *dz = out_row(p.dz, r, L.nh);
+                uint4 *dg = GATE == 2 && p.dgate.base ? out_row(p.dgate, r, L.nh) : nullptr;
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int v = k * vstride + gtid;
-                if (v < nvec && !abort) {
-                    float2 w1[4], w2[4];
-                    sw_weight(m.w[0], nvec, v, w1);
-                    sw_weight(m.w[1], nvec, v, w2);
-#pragma unroll
-                    for (int i = 0; i < R2; ++i) {
-                        if (!live[i])
-                            continue;
-                        const uint32_t r = rb + i;
-                        const uint4 *row = reinterpret_cast<const uint4 *>(stage + (size_t)i * L.H * 2) + v;
-                        const uint4 h = row[0], z = row[tb / 16], d = row[2 * (tb / 16)];
+                for (int k = 0; k < VPT; ++k) {
+                    const int v = k * vstride + gtid;
+                    if (v < nvec && !abort) {
+                        const uint4 *row = gbase + st2 * sbytes + v;
+                        const uint4 h = row[0], z = row[tb], d = row[2 * tb];
                         uint4 g = make_uint4(0, 0, 0, 0), e = make_uint4(0, 0, 0, 0);
                         if (GATE == 2)
-                            g = row[3 * (tb / 16)];
+                            g = row[3 * tb];
                         if (has_dh)
-                            e = row[dh_off / 16];
-                        const float2 rn = both(sc[i].y);
+                            e = row[dh_off];
+                        float2 w1[4], w2[4];
+                        weight(0, v, w1);
+                        weight(1, v, w2);
                         uint32_t ox[4], oz[4], og[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const float2 zq = bf2(word(z, q));
                             const float2 a = mul2(bf2(word(d, q)), w2[q]);
-                            const float2 t = fma2(both(nk2[i]), bf2(word(h, q)), fma2(rn, a, bf2(word(e, q))));
+                            const float2 t = fma2(nk2, bf2(word(h, q)), fma2(rn, a, bf2(word(e, q))));
                             const float2 tg = GATE == 2 ? mul2(t, bf2(word(g, q))) : t;
-                            const float2 tz = mul2(both(sr[i]), zq);
+                            const float2 tz = mul2(sr, zq);
                             ox[q] = pack2(t);
-                            oz[q] = pack2(mul2(both(sr[i]), fma2(tg, w1[q], mul2(both(nk1[i]), zq))));
+                            oz[q] = pack2(mul2(sr, fma2(tg, w1[q], mul2(nk1, zq))));
                             if (GATE == 2)
                                 og[q] = pack2(mul2(mul2(t, tz), w1[q]));
                             kahan2(hi1[k][q], lo1[k][q], tg, tz);
                         }
-                        __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.dx.base) + row_off(p.dx, r, L.nh)) + v,
-                               make_uint4(ox[0], ox[1], ox[2], ox[3]));
-                        __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.dz.base) + row_off(p.dz, r, L.nh)) + v,
-                               make_uint4(oz[0], oz[1], oz[2], oz[3]));
-                        if (GATE == 2 && p.dgate.base)
-                            __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.dgate.base) +
-                                                             row_off(p.dgate, r, L.nh)) + v,
-                                   make_uint4(og[0], og[1], og[2], og[3]));
+                        __stcs(dx + v, make_uint4(ox[0], ox[1], ox[2], ox[3]));
+                        __stcs(dz + v, make_uint4(oz[0], oz[1], oz[2], oz[3]));
+                        if (GATE == 2 && dg)
+                            __stcs(dg + v, make_uint4(og[0], og[1], og[2], og[3]));
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&m.s.empty[st2]));
+            if (++st2 == (uint32_t)L.stages)
+                st2 = 0;
         }
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(smem_addr(&m.s.empty[st]));
-        if (++st == (uint32_t)L.stages) {
-            st = 0;
-            ph ^= 1u;
-        }
+        own = mine;
     }
     if (abort && lane == 0)
         set_status(p.status, kStatusTimeout);
@@ -505,34 +573,31 @@ SandwichPlan sandwich_plan(int H, uint32_t rows, int ntens, bool backward)
     p.vpt = nvec <= 32 ? 1 : 2;
     p.W = (nvec + 32 * p.vpt - 1) / (32 * p.vpt);
     p.groups = p.W >= 12 ? 1 : 12 / p.W;
-    p.r2 = backward && p.W > 1 && p.groups == 1 ? 2 : 1;
     // CTAs per SM: 16 warps of 128 registers (backward), 28 of 72 (forward)
     int per_sm = (backward ? 16 : 28) / (p.groups * p.W + 1);
     per_sm = per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm;
-    const size_t fixed = (size_t)kSwFixed + 2 * weight_smem_bytes(H);
-    const size_t limit = 227 * 1024;
-    for (;; ) {
-        const size_t stage = (size_t)ntens * p.groups * p.r2 * H * 2;
-        const size_t room = limit / per_sm - 1024; // 1 KB of each CTA is the system's
-        p.stages = room > fixed ? (int)((room - fixed) / stage) : 0;
-        if (p.stages >= 2)
-            break;
-        if (per_sm > 1)
-            --per_sm;
-        else if (p.r2 > 1)
-            p.r2 = 1;
-        else if (p.groups > 1)
-            --p.groups;
-        else
-            break; // the widest rows with five tensors: one stage
+    // the backward holds two rows of a group at once and a third is to be
+    // on its way; the forward works on one
+    const int want = backward ? 3 : 2;
+    p.weights_smem = true;
+    size_t fixed = (size_t)kSwFixed + 2 * weight_smem_bytes(H);
+    const size_t stage = (size_t)ntens * p.groups * H * 2;
+    auto stages = [&]() {
+        const size_t room = 227 * 1024 / per_sm - 1024; // 1 KB of each CTA is the system's
+        return room > fixed ? (int)((room - fixed) / stage) : 0;
+    };
+    while (per_sm > 1 && stages() < want)
+        --per_sm;
+    if (backward && stages() < want) { // rows of about 6000 columns and more
+        p.weights_smem = false;
+        fixed = kSwFixed;
     }
-    if (p.stages > kSwMaxStages)
-        p.stages = kSwMaxStages;
-    const uint32_t tile = (uint32_t)p.groups * p.r2;
-    p.smem = fixed + (size_t)p.stages * ntens * tile * H * 2;
+    p.stages = stages() < kSwMaxStages ? stages() : kSwMaxStages;
+    p.smem = fixed + (size_t)p.stages * stage;
     const size_t comb = fixed + (size_t)(backward ? p.groups : 0) * H * 16;
     if (comb > p.smem)
         p.smem = comb;
+    const uint32_t tile = (uint32_t)p.groups;
     uint32_t ctas = (rows + tile - 1) / tile;
     if (ctas > (uint32_t)kSMsStep * per_sm)
         ctas = (uint32_t)kSMsStep * per_sm;
@@ -568,13 +633,15 @@ cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, const SandwichPlan &
 template <int GATE>
 static cudaError_t launch_bwd_gate(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
 {
+    if (plan.stages < 2) // a row is held while the next one is read
+        return cudaErrorInvalidValue;
     if (plan.vpt == 1)
-        return launch_rows(sandwich_bwd_kernel<1, 1, GATE, kSwFwdThreads>, p, plan, stream);
+        return launch_rows(sandwich_bwd_kernel<1, GATE, true, kSwFwdThreads>, p, plan, stream);
     if (plan.W > 12)
-        return plan.r2 == 2 ? launch_rows(sandwich_bwd_kernel<2, 2, GATE, kSwWideThreads>, p, plan, stream)
-                            : launch_rows(sandwich_bwd_kernel<2, 1, GATE, kSwWideThreads>, p, plan, stream);
-    return plan.r2 == 2 ? launch_rows(sandwich_bwd_kernel<2, 2, GATE, kSwFwdThreads>, p, plan, stream)
-                        : launch_rows(sandwich_bwd_kernel<2, 1, GATE, kSwFwdThreads>, p, plan, stream);
+        return plan.weights_smem ? launch_rows(sandwich_bwd_kernel<2, GATE, true, kSwWideThreads>, p, plan, stream)
+                                 : launch_rows(sandwich_bwd_kernel<2, GATE, false, kSwWideThreads>, p, plan, stream);
+    return plan.weights_smem ? launch_rows(sandwich_bwd_kernel<2, GATE, true, kSwFwdThreads>, p, plan, stream)
+                             : launch_rows(sandwich_bwd_kernel<2, GATE, false, kSwFwdThreads>, p, plan, stream);
 }
 
 cudaError_t launch_sandwich_bwd(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)

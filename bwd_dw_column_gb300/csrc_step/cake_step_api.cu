@@ -64,7 +64,6 @@ SandwichLayout sandwich_layout(const SandwichPlan &plan, const cake_shape *shape
     L.nvec = L.H / 8;
     L.W = plan.W;
     L.groups = plan.groups;
-    L.r2 = plan.r2;
     L.stages = plan.stages;
     L.ntens = ntens;
     L.rows = rows;

@@ -13,15 +13,16 @@ namespace cake {
 // ------------------------------------------------------------ sandwich norm
 
 // A row of a sandwich norm spans W warps of VPT 8-column vectors a thread;
-// `groups` rows (times R2) are in flight per CTA, staged by a producer warp.
+// a CTA stages `groups` rows at a time with a producer warp.
 struct SandwichPlan {
-    int vpt, W, groups, r2, stages, ctas;
+    int vpt, W, groups, stages, ctas;
+    bool weights_smem;
     uint32_t rows_per_cta;
     size_t smem;
 };
 
 struct SandwichLayout {
-    int H, nvec, W, groups, r2, stages, ntens;
+    int H, nvec, W, groups, stages, ntens;
     uint32_t rows, nh, rows_per_cta;
     float inv_h;
 };
