@@ -27,44 +27,46 @@ constexpr int kSMsStep = 152;
 constexpr int kSwMaxStages = 16;
 constexpr int kSwMaxTile = 12;            // rows of a stage, at most
 constexpr int kSwSlots = 4;               // backward: rows whose partial sums may be in use
-constexpr int kSwSlotFloats = 64;         // ... [4 sums][16 warps]
+constexpr int kSwRowWarps = 32;           // warps of a row (over its cluster) that a slot has room for
+constexpr int kSwSlotFloats = 4 * kSwRowWarps;
+constexpr int kSwMaxJoined = 6;           // groups whose rows span several warps, at most
+constexpr int kSwMaxCluster = 4;
 // Shared memory before the weights: the ring's barriers (256 bytes), the row
-// sums' barriers (256), a flag (64), the row sums' partials, the rows' scalars.
-constexpr int kSwRed = 576;
-constexpr int kSwScalarsAt = kSwRed + kSwMaxTile * kSwSlots * kSwSlotFloats * 4;
+// sums' barriers (384), a flag (64), the row sums' partials, the rows' scalars.
+constexpr int kSwRed = 704;
+constexpr int kSwScalarsAt = kSwRed + kSwMaxJoined * kSwSlots * kSwSlotFloats * 4;
 constexpr int kSwFixed = (kSwScalarsAt + kSwMaxStages * kSwMaxTile * 16 + 1023) / 1024 * 1024;
 
 struct SwSmem {
     Smem s;               // barriers, reduction slots, flag, ring
-    uint64_t *sums;       // [groups][2] backward: a row's partial sums are written
+    uint64_t *sums;       // [groups][slots] backward: a row's partial sums are written
     float4 *scalars;      // [stages][tile rows] (rstd_post, rstd_pre, row gate, -)
     float *w[2];          // w_post, w_pre as FP32, two planes each (see stage_weight)
 };
 
-template <bool WS>
 __device__ __forceinline__ SwSmem sw_carve(uint8_t *base, const SandwichLayout &L)
 {
     SwSmem m;
     m.s.full = reinterpret_cast<uint64_t *>(base);
     m.s.empty = m.s.full + L.stages;
     m.sums = reinterpret_cast<uint64_t *>(base + 256);
-    m.s.flag = reinterpret_cast<int *>(base + 512);
+    m.s.flag = reinterpret_cast<int *>(base + 640);
     m.s.red = reinterpret_cast<float *>(base + kSwRed);
     m.scalars = reinterpret_cast<float4 *>(base + kSwScalarsAt);
     m.w[0] = reinterpret_cast<float *>(base + kSwFixed);
-    m.w[1] = m.w[0] + weight_smem_bytes(L.H) / 4;
-    m.s.ring = base + kSwFixed + (WS ? 2 * weight_smem_bytes(L.H) : 0);
-    m.s.tens_bytes = (uint32_t)L.groups * L.H * 2;
+    m.w[1] = m.w[0] + weight_smem_bytes(L.cols) / 4;
+    m.s.ring = base + kSwFixed + 2 * weight_smem_bytes(L.cols);
+    m.s.tens_bytes = (uint32_t)L.groups * L.cols * 2;
     m.s.stage_bytes = m.s.tens_bytes * L.ntens;
     return m;
 }
 
 // The layout in the form that the shared pieces of the row pipeline take.
-__device__ __forceinline__ Layout sw_rows_layout(const SandwichLayout &L)
+__device__ __forceinline__ Layout sw_rows_layout(const SandwichLayout &L, int nvec)
 {
     Layout r = {};
-    r.H = L.H;
-    r.nvec = L.nvec;
+    r.H = 8 * nvec;
+    r.nvec = nvec;
     r.warps_per_row = L.W;
     r.groups = L.groups;
     r.stages = L.stages;
@@ -83,21 +85,15 @@ __device__ __forceinline__ void sw_weight(const float *w, int nvec, int v, float
     w2[3] = make_float2(b.z, b.w);
 }
 
-__device__ __forceinline__ void sw_weight_global(const void *w, int f32, int v, float2 (&w2)[4])
+// Store to the shared memory of a CTA of the cluster, counted as 4 bytes on
+// an mbarrier there.  Unlike a store and a releasing arrival, it does not wait
+// for this thread's earlier stores to global memory (GB300, H = 4096: that
+// release took the backward from 371 to 606 us at T = 32768).
+__device__ __forceinline__ void st_async_f32(uint32_t cluster_addr, float v, uint32_t cluster_bar)
 {
-    if (f32) {
-        const float4 a = __ldg(static_cast<const float4 *>(w) + 2 * v);
-        const float4 b = __ldg(static_cast<const float4 *>(w) + 2 * v + 1);
-        w2[0] = make_float2(a.x, a.y);
-        w2[1] = make_float2(a.z, a.w);
-        w2[2] = make_float2(b.x, b.y);
-        w2[3] = make_float2(b.z, b.w);
-    } else {
-        const uint4 a = __ldg(static_cast<const uint4 *>(w) + v);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            w2[q] = bf2(word(a, q));
-    }
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(cluster_addr),
+                 "r"(__float_as_uint(v)), "r"(cluster_bar)
+                 : "memory");
 }
 
 __device__ __forceinline__ uint4 *out_row(const RowView &v, uint32_t r, uint32_t nh)
@@ -105,17 +101,18 @@ __device__ __forceinline__ uint4 *out_row(const RowView &v, uint32_t r, uint32_t
     return reinterpret_cast<uint4 *>(const_cast<uint16_t *>(v.base) + row_off(v, r, nh));
 }
 
-// Producer warp: streams the CTA's rows of every staged tensor into the ring;
+// Producer warp: streams vectors [v0, v0 + nvec) of the CTA's rows of every
+// staged tensor into the ring;
 // a row's scalars go along through plain shared stores, loaded a tile ahead
 // and published by the arrival on the stage's full barrier.
 template <int NT>
 __device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout &L, const RowView (&in)[NT],
-                                           const float *sc0, const float *sc1, const float *sc2, uint32_t r0,
-                                           uint32_t r_end, int *status, uint64_t wait_ns)
+                                           const float *sc0, const float *sc1, const float *sc2, int v0, int nvec,
+                                           uint32_t r0, uint32_t r_end, int *status, uint64_t wait_ns)
 {
     const uint32_t lane = threadIdx.x & 31;
     const uint64_t pol = policy_evict_first();
-    const uint32_t row_bytes = (uint32_t)L.H * 2, tile = (uint32_t)L.groups;
+    const uint32_t row_bytes = (uint32_t)nvec * 16, tile = (uint32_t)L.groups, pitch = (uint32_t)L.cols * 2;
     auto scalars = [&](uint32_t row0) {
         float4 v = make_float4(0.f, 0.f, 1.f, 0.f);
         if (lane < tile && row0 + lane < r_end) {
@@ -151,11 +148,12 @@ __device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout
             if (t >= L.ntens)
                 break;
             const uint32_t dst = dst0 + t * m.s.tens_bytes;
-            if (in[t].dense) {
+            if (in[t].dense && L.cluster == 1) {
                 if (lane == 0)
                     bulk_g2s(dst, in[t].base + (int64_t)row0 * in[t].row_stride, n * row_bytes, bar, pol);
             } else if (lane < n) {
-                bulk_g2s(dst + lane * row_bytes, in[t].base + row_off(in[t], row0 + lane, L.nh), row_bytes, bar, pol);
+                bulk_g2s(dst + lane * pitch, in[t].base + row_off(in[t], row0 + lane, L.nh) + 8 * v0, row_bytes, bar,
+                         pol);
             }
         }
         next = scalars(row0 + tile);
@@ -181,17 +179,17 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_fwd_kernel(const __grid_c
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const SandwichLayout &L = p.L;
-    const SwSmem m = sw_carve<true>(smem_raw, L);
-    const Layout RL = sw_rows_layout(L);
+    const SwSmem m = sw_carve(smem_raw, L);
+    const int nvec = L.cols / 8;
+    const Layout RL = sw_rows_layout(L, nvec);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t r0 = blockIdx.x * L.rows_per_cta, r_end = min(L.rows, r0 + L.rows_per_cta);
     init_ring(m.s, RL);
     if (warp == L.groups * L.W) {
-        sw_produce(m, L, p.in, nullptr, nullptr, p.gate_rows, r0, r_end, p.status, p.wait_ns);
+        sw_produce(m, L, p.in, nullptr, nullptr, p.gate_rows, 0, nvec, r0, r_end, p.status, p.wait_ns);
         return;
     }
     const int gid = warp / L.W, wig = warp - gid * L.W, gtid = wig * 32 + lane, vstride = 32 * L.W;
-    const int nvec = L.nvec;
     {
         Smem sw = m.s;
         sw.wsm = m.w[0];
@@ -206,7 +204,7 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_fwd_kernel(const __grid_c
         abort = !mbar_wait(smem_addr(&m.s.full[st]), ph, p.wait_ns);
         const uint32_t r = row0 + gid;
         if (r < r_end) { // uniform across the group
-            const uint8_t *stage = m.s.ring + st * m.s.stage_bytes + (size_t)gid * L.H * 2;
+            const uint8_t *stage = m.s.ring + st * m.s.stage_bytes + (size_t)gid * L.cols * 2;
             const uint4 *zs = reinterpret_cast<const uint4 *>(stage);
             const uint4 *xs = reinterpret_cast<const uint4 *>(stage + m.s.tens_bytes);
             const uint4 *gs = reinterpret_cast<const uint4 *>(stage + 2 * m.s.tens_bytes);
@@ -315,54 +313,63 @@ __device__ __forceinline__ float warp_sum3(float v0, float v1, float v2, int lan
     return r;
 }
 
-// GATE: 0 none, 1 a value per row, 2 a value per element.  WS: the weights
-// are staged in shared memory (else read through L2, for rows so wide that
-// fewer than three stages would be left).
+// GATE: 0 none, 1 a value per row, 2 a value per element.
 //
 // A thread holds the two column sums of 8 VPT columns as Kahan pairs, 32 VPT
-// registers, which is why it takes no more than 16 columns.
+// registers, which is why it takes no more than 16 columns.  With 12 consumer
+// warps of 128 registers an SM then holds 6144 columns of rows.  A warp's own
+// latencies bound its rate (GB300, ncu at H = 4096 on 8 warps: issue slots 43 %
+// used, 5.2 cycles a warp and instruction), so rows that leave warps unused at
+// this width, or do not fit three stages, are split over a cluster of 2 or 4
+// CTAs, each with its share of the columns and, so, of the weights.
 //
 // Order of work: first pass of row j + 1 (its three sums and dw_pre), then
 // the second pass of row j (its outputs and dw_post).  The sums of a row
-// travel between the group's warps through shared memory behind an mbarrier
-// that a warp arrives on after its first pass and tests after the next row's,
-// so that no warp waits for a reduction.  Two barriers alternate: a warp is
-// never more than two rows ahead of another, and four slots hold the partials
-// of the rows that may be in use.
-template <int VPT, int GATE, bool WS, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p)
+// travel between the row's warps, in every CTA of its cluster, through shared
+// memory behind an mbarrier that a warp arrives on after its first pass and
+// tests after the next row's, so that no warp waits for a reduction.  A warp
+// writes row j + 2's sums only after row j's have all come to its CTA, which
+// needs every warp of the row to have read row j - 2's: four slots, each with
+// a barrier of its own, hold the rows that may be in use, also where sums
+// reach one CTA of a cluster later than another.
+template <int VPT, int GATE, bool CL>
+__global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const SandwichLayout &L = p.L;
-    const SwSmem m = sw_carve<WS>(smem_raw, L);
-    const Layout RL = sw_rows_layout(L);
+    const SwSmem m = sw_carve(smem_raw, L);
+    const int C = CL ? L.cluster : 1;
+    const uint32_t rank = CL ? cluster_ctarank() : 0, cid = CL ? blockIdx.x / C : blockIdx.x;
+    const int v0 = (int)rank * (L.cols / 8), nvec = CL ? min(L.cols / 8, L.nvec - v0) : L.nvec; // this CTA's vectors
+    const Layout RL = sw_rows_layout(L, nvec);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t r0 = blockIdx.x * L.rows_per_cta, r_end = min(L.rows, r0 + L.rows_per_cta);
-    if (threadIdx.x < 2 * L.groups)
-        mbar_init(smem_addr(m.sums + threadIdx.x), L.W);
-    for (int i = threadIdx.x; i < L.groups * kSwSlots * kSwSlotFloats; i += blockDim.x)
+    const uint32_t r0 = cid * L.rows_per_cta, r_end = min(L.rows, r0 + L.rows_per_cta);
+    if (threadIdx.x < kSwSlots * L.groups) // in a cluster: one arrival, and the bytes that come
+        mbar_init(smem_addr(m.sums + threadIdx.x), CL ? 1 : L.W);
+    for (int i = threadIdx.x; i < kSwMaxJoined * kSwSlots * kSwSlotFloats; i += blockDim.x)
         m.s.red[i] = 0.f; // the parts of warps that a row does not have stay zero
+    if (CL && threadIdx.x < kSwSlots * L.groups)
+        fence_mbar_init();
     init_ring(m.s, RL);
+    if (CL)
+        cluster_sync_all(); // every CTA's barriers and slots exist before a remote access
     if (warp == L.groups * L.W) {
-        sw_produce(m, L, p.in, p.rstd_post, p.rstd_pre, p.gate_rows, r0, r_end, p.status, p.wait_ns);
+        sw_produce(m, L, p.in, p.rstd_post, p.rstd_pre, p.gate_rows, v0, nvec, r0, r_end, p.status, p.wait_ns);
+        __syncwarp();
+        if (CL)
+            cluster_sync_all();
         return;
     }
     const int gid = warp / L.W, wig = warp - gid * L.W, gtid = wig * 32 + lane, vstride = 32 * L.W;
-    const int nvec = L.nvec;
-    const bool has_dh = p.has_dh;
-    if (WS) {
+    const bool has_dh = p.has_dh, joined = CL || L.W > 1;
+    {
         Smem sw = m.s;
         sw.wsm = m.w[0];
-        stage_weight(sw, RL, p.w_post, p.post_f32);
+        stage_weight(sw, RL, static_cast<const uint8_t *>(p.w_post) + v0 * (p.post_f32 ? 32 : 16), p.post_f32);
         sw.wsm = m.w[1];
-        stage_weight(sw, RL, p.w_pre, p.pre_f32);
+        stage_weight(sw, RL, static_cast<const uint8_t *>(p.w_pre) + v0 * (p.pre_f32 ? 32 : 16), p.pre_f32);
     }
-    auto weight = [&](int which, int v, float2(&w2)[4]) {
-        if (WS)
-            sw_weight(m.w[which], nvec, v, w2);
-        else
-            sw_weight_global(which ? p.w_pre : p.w_post, which ? p.pre_f32 : p.post_f32, v, w2);
-    };
+    auto weight = [&](int which, int v, float2(&w2)[4]) { sw_weight(m.w[which], nvec, v, w2); };
     float2 hi1[VPT][4], lo1[VPT][4], hi2[VPT][4], lo2[VPT][4]; // dw_post, dw_pre
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
@@ -373,7 +380,7 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_bwd_kernel(const __grid_c
     const uint32_t tile = (uint32_t)L.groups, tb = m.s.tens_bytes / 16;
     const uint32_t dh_off = (GATE == 2 ? 4 : 3) * tb;
     const uint32_t ntiles = r_end > r0 ? (r_end - r0 + tile - 1) / tile : 0;
-    const uint4 *gbase = reinterpret_cast<const uint4 *>(m.s.ring + (size_t)gid * L.H * 2);
+    const uint4 *gbase = reinterpret_cast<const uint4 *>(m.s.ring + (size_t)gid * L.cols * 2);
     const uint32_t sbytes = m.s.stage_bytes / 16;
     float *red = m.s.red + gid * kSwSlots * kSwSlotFloats;
     float own = 0.f; // rows of one warp: the sums of the row between its passes
@@ -414,12 +421,22 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_bwd_kernel(const __grid_c
                     }
                 }
                 mine = warp_sum3(__fadd_rn(s1.x, s1.y), __fadd_rn(s2.x, s2.y), __fadd_rn(s3.x, s3.y), lane);
-                if (L.W > 1) {
-                    if ((lane & 7) == 0)
-                        red[(j & 3) * kSwSlotFloats + (lane >> 3) * 16 + wig] = mine;
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_addr(m.sums + 2 * gid + (j & 1)));
+                if (joined) {
+                    float *at = red + (j & 3) * kSwSlotFloats + (lane >> 3) * kSwRowWarps + rank * L.W + wig;
+                    const uint32_t bar = smem_addr(m.sums + kSwSlots * gid + (j & 3));
+                    if (CL) {
+                        // to every CTA of the cluster, each sum by a lane that holds it
+                        if (wig == 0 && lane == 0)
+                            mbar_arrive_expect_tx(bar, 12u * L.W * C);
+                        if ((lane & 7) < C && lane < 24)
+                            st_async_f32(map_to_rank(smem_addr(at), lane & 7), mine, map_to_rank(bar, lane & 7));
+                    } else {
+                        if ((lane & 7) == 0)
+                            *at = mine;
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar);
+                    }
                 }
             }
             if (++st1 == (uint32_t)L.stages) {
@@ -431,12 +448,11 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_bwd_kernel(const __grid_c
             const uint32_t i = j - 1, r = r0 + i * tile + gid;
             if (r < r_end) {
                 float t3 = own;
-                if (L.W > 1) {
-                    if (!mbar_wait(smem_addr(m.sums + 2 * gid + (i & 1)), (i >> 1) & 1, p.wait_ns))
+                if (joined) {
+                    if (!mbar_wait(smem_addr(m.sums + kSwSlots * gid + (i & 3)), (i >> 2) & 1, p.wait_ns))
                         abort = true;
-                    const float2 a = *reinterpret_cast<const float2 *>(red + (i & 3) * kSwSlotFloats + (lane >> 3) * 16 +
-                                                                       2 * (lane & 7));
-                    t3 = __fadd_rn(a.x, a.y);
+                    const float4 a = ld_shared_f4(smem_addr(red + (i & 3) * kSwSlotFloats + 4 * lane));
+                    t3 = __fadd_rn(__fadd_rn(a.x, a.y), __fadd_rn(a.z, a.w));
 #pragma unroll
                     for (int o = 4; o > 0; o >>= 1)
                         t3 = __fadd_rn(t3, __shfl_xor_sync(0xffffffffu, t3, o));
@@ -449,10 +465,10 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_bwd_kernel(const __grid_c
                 const float2 nk2 = both(-k2), rn = both(sc.y);
                 const float2 nk1 = both(-__fmul_rn(__fmul_rn(__fmul_rn(dot, L.inv_h), sc.x), sc.x));
                 const float2 sr = both(__fmul_rn(GATE == 1 ? __fmul_rn(p.scale, sc.z) : p.scale, sc.x));
-                if (GATE == 1 && p.dgate_rows && gtid == 0 && !abort)
+                if (GATE == 1 && p.dgate_rows && gtid == 0 && rank == 0 && !abort)
                     p.dgate_rows[r] = __fmul_rn(__fmul_rn(p.scale, sc.x), dot);
-                uint4 *dx = out_row(p.dx, r, L.nh), *dz = out_row(p.dz, r, L.nh);
-                uint4 *dg = GATE == 2 && p.dgate.base ? out_row(p.dgate, r, L.nh) : nullptr;
+                uint4 *dx = out_row(p.dx, r, L.nh) + v0, *dz = out_row(p.dz, r, L.nh) + v0;
+                uint4 *dg = GATE == 2 && p.dgate.base ? out_row(p.dgate, r, L.nh) + v0 : nullptr;
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) {
                     const int v = k * vstride + gtid;
@@ -527,8 +543,11 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_bwd_kernel(const __grid_c
             comp_add(a.z, a.w, b.z);
             a.w = __fadd_rn(a.w, b.w);
         }
-        reinterpret_cast<float4 *>(p.partials + ((size_t)w * gridDim.x + blockIdx.x) * L.H)[c] = a;
+        reinterpret_cast<float4 *>(p.partials + ((size_t)w * (gridDim.x / C) + cid) * L.H)[4 * v0 + c] = a;
     }
+    __syncwarp();
+    if (CL)
+        cluster_sync_all(); // no CTA leaves while another may still write to its slots
     pdl_launch_dependents();
 }
 
@@ -566,43 +585,65 @@ __global__ void __launch_bounds__(32 * kSwReduceWarps)
 
 // The shape of a CTA.  It depends on H and the staged tensors, the number of
 // CTAs on the rows too, and on nothing else, so the sums' orders do not either.
-SandwichPlan sandwich_plan(int H, uint32_t rows, int ntens, bool backward)
+static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int cluster)
 {
-    SandwichPlan p{};
-    const int nvec = H / 8;
-    p.vpt = nvec <= 32 ? 1 : 2;
+    const int nvec = (H / 8 + cluster - 1) / cluster; // of a CTA
+    p.cluster = cluster;
+    p.cols = 8 * nvec;
+    p.vpt = H <= 256 ? 1 : 2;
     p.W = (nvec + 32 * p.vpt - 1) / (32 * p.vpt);
     p.groups = p.W >= 12 ? 1 : 12 / p.W;
     // CTAs per SM: 16 warps of 128 registers (backward), 28 of 72 (forward)
-    int per_sm = (backward ? 16 : 28) / (p.groups * p.W + 1);
-    per_sm = per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm;
+    p.per_sm = (backward ? 16 : 28) / (p.groups * p.W + 1);
+    p.per_sm = p.per_sm < 1 || cluster > 1 ? 1 : p.per_sm > 2 ? 2 : p.per_sm;
+    const size_t fixed = (size_t)kSwFixed + 2 * weight_smem_bytes(p.cols);
+    const size_t stage = (size_t)ntens * p.groups * p.cols * 2;
     // the backward holds two rows of a group at once and a third is to be
     // on its way; the forward works on one
     const int want = backward ? 3 : 2;
-    p.weights_smem = true;
-    size_t fixed = (size_t)kSwFixed + 2 * weight_smem_bytes(H);
-    const size_t stage = (size_t)ntens * p.groups * H * 2;
-    auto stages = [&]() {
-        const size_t room = 227 * 1024 / per_sm - 1024; // 1 KB of each CTA is the system's
-        return room > fixed ? (int)((room - fixed) / stage) : 0;
-    };
-    while (per_sm > 1 && stages() < want)
-        --per_sm;
-    if (backward && stages() < want) { // rows of about 6000 columns and more
-        p.weights_smem = false;
-        fixed = kSwFixed;
+    for (;; --p.per_sm) {
+        const size_t room = 227 * 1024 / p.per_sm - 1024; // 1 KB of each CTA is the system's
+        p.stages = room > fixed ? (int)((room - fixed) / stage) : 0;
+        if (p.stages >= want || p.per_sm == 1)
+            break;
     }
-    p.stages = stages() < kSwMaxStages ? stages() : kSwMaxStages;
+    if (p.stages > kSwMaxStages)
+        p.stages = kSwMaxStages;
     p.smem = fixed + (size_t)p.stages * stage;
-    const size_t comb = fixed + (size_t)(backward ? p.groups : 0) * H * 16;
+    const size_t comb = fixed + (size_t)(backward ? p.groups : 0) * p.cols * 16;
     if (comb > p.smem)
         p.smem = comb;
+    const bool slots = p.W * cluster == 1 || (p.groups <= kSwMaxJoined && p.W * cluster <= kSwRowWarps);
+    return p.stages >= want && p.W <= (backward ? 12 : 16) && slots && p.cols * (cluster - 1) < H;
+}
+
+SandwichPlan sandwich_plan(int H, uint32_t rows, int ntens, bool backward)
+{
+    SandwichPlan p{};
+    try_plan(p, H, ntens, backward, 1);
+    if (backward) {
+        // the smallest cluster that keeps the most lanes of the 12 warps busy
+        int best = 0;
+        for (int c = 1; c <= kSwMaxCluster; c *= 2) {
+            SandwichPlan q{};
+            if (!try_plan(q, H, ntens, backward, c))
+                continue;
+            const int busy = q.cols * q.groups * q.per_sm; // columns in work on an SM
+            if (busy > best) {
+                best = busy;
+                p = q;
+            }
+            if (H <= 2048 || best >= 12 * 512)
+                break;
+        }
+    }
     const uint32_t tile = (uint32_t)p.groups;
-    uint32_t ctas = (rows + tile - 1) / tile;
-    if (ctas > (uint32_t)kSMsStep * per_sm)
-        ctas = (uint32_t)kSMsStep * per_sm;
+    uint32_t ctas = (rows + tile - 1) / tile; // clusters, where a row has one
+    const uint32_t most = (uint32_t)kSMsStep * p.per_sm / p.cluster;
+    if (ctas > most)
+        ctas = most;
     p.rows_per_cta = ctas ? (rows + ctas - 1) / ctas : 0;
-    p.ctas = p.rows_per_cta ? (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta) : 0;
+    p.parts = p.rows_per_cta ? (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta) : 0;
     return p;
 }
 
@@ -613,8 +654,20 @@ static cudaError_t launch_rows(void (*kern)(P), const P &p, const SandwichPlan &
     cudaError_t e = ensure_smem_attr((const void *)kern, plan.smem);
     if (e != cudaSuccess)
         return e;
-    kern<<<plan.ctas, threads, plan.smem, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(plan.parts * plan.cluster));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = plan.smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)plan.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = plan.cluster > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
@@ -633,15 +686,12 @@ cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, const SandwichPlan &
 template <int GATE>
 static cudaError_t launch_bwd_gate(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
 {
-    if (plan.stages < 2) // a row is held while the next one is read
+    if (plan.stages < 2 || plan.W > 12) // a row is held while the next one is read
         return cudaErrorInvalidValue;
-    if (plan.vpt == 1)
-        return launch_rows(sandwich_bwd_kernel<1, GATE, true, kSwFwdThreads>, p, plan, stream);
-    if (plan.W > 12)
-        return plan.weights_smem ? launch_rows(sandwich_bwd_kernel<2, GATE, true, kSwWideThreads>, p, plan, stream)
-                                 : launch_rows(sandwich_bwd_kernel<2, GATE, false, kSwWideThreads>, p, plan, stream);
-    return plan.weights_smem ? launch_rows(sandwich_bwd_kernel<2, GATE, true, kSwFwdThreads>, p, plan, stream)
-                             : launch_rows(sandwich_bwd_kernel<2, GATE, false, kSwFwdThreads>, p, plan, stream);
+    if (plan.cluster > 1)
+        return launch_rows(sandwich_bwd_kernel<2, GATE, true>, p, plan, stream);
+    return plan.vpt == 1 ? launch_rows(sandwich_bwd_kernel<1, GATE, false>, p, plan, stream)
+                         : launch_rows(sandwich_bwd_kernel<2, GATE, false>, p, plan, stream);
 }
 
 cudaError_t launch_sandwich_bwd(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)

@@ -62,6 +62,8 @@ SandwichLayout sandwich_layout(const SandwichPlan &plan, const cake_shape *shape
     SandwichLayout L;
     L.H = (int)shape->hidden;
     L.nvec = L.H / 8;
+    L.cluster = plan.cluster;
+    L.cols = plan.cols;
     L.W = plan.W;
     L.groups = plan.groups;
     L.stages = plan.stages;
@@ -134,11 +136,11 @@ extern "C" size_t cake_sandwich_bwd_workspace_size(const cake_shape *shape)
     uint32_t rows = 0;
     if (check_shape(shape, &rows) != CAKE_OK || rows == 0)
         return 0;
-    // the CTAs depend on the number of staged tensors: room for each choice
-    int ctas = 0;
+    // the plan depends on the number of staged tensors: room for each choice
+    int parts = 0;
     for (int ntens = 3; ntens <= 5; ++ntens)
-        ctas = std::max(ctas, sandwich_plan((int)shape->hidden, rows, ntens, true).ctas);
-    return (size_t)2 * ctas * shape->hidden * sizeof(float2);
+        parts = std::max(parts, sandwich_plan((int)shape->hidden, rows, ntens, true).parts);
+    return (size_t)2 * parts * shape->hidden * sizeof(float2);
 }
 
 extern "C" cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_tensor *dy, const cake_tensor *dh,
@@ -218,7 +220,7 @@ extern "C" cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_ten
     p.wait_ns = kWaitLimitNs;
     if (step_status_ptr(&p.status) != cudaSuccess || launch_sandwich_bwd(p, plan, cu(stream)) != cudaSuccess)
         return CAKE_ERR_CUDA;
-    SandwichReduceParams rp{p.partials, plan.ctas, H, {dw_post, dw_pre}};
+    SandwichReduceParams rp{p.partials, plan.parts, H, {dw_post, dw_pre}};
     return cuda_status(launch_sandwich_reduce(rp, cu(stream)));
 }
 

@@ -12,17 +12,18 @@ namespace cake {
 
 // ------------------------------------------------------------ sandwich norm
 
-// A row of a sandwich norm spans W warps of VPT 8-column vectors a thread;
-// a CTA stages `groups` rows at a time with a producer warp.
+// A row of a sandwich norm spans a cluster of CTAs with `cols` of its columns
+// each, and W warps of VPT 8-column vectors a thread in each of them; a CTA
+// stages `groups` rows at a time with a producer warp.  `parts` CTAs (or
+// clusters) share the rows.
 struct SandwichPlan {
-    int vpt, W, groups, stages, ctas;
-    bool weights_smem;
+    int cluster, cols, vpt, W, groups, stages, per_sm, parts;
     uint32_t rows_per_cta;
     size_t smem;
 };
 
 struct SandwichLayout {
-    int H, nvec, W, groups, stages, ntens;
+    int H, nvec, cluster, cols, W, groups, stages, ntens;
     uint32_t rows, nh, rows_per_cta;
     float inv_h;
 };
@@ -52,7 +53,7 @@ struct SandwichBwdParams {
     const float *rstd_post, *rstd_pre;
     const void *w_post, *w_pre;
     int post_f32, pre_f32;
-    float2 *partials;      // [2][ctas][H] (hi, lo): dw_post's, then dw_pre's
+    float2 *partials;      // [2][parts][H] (hi, lo): dw_post's, then dw_pre's
     int *status;
     uint64_t wait_ns;
 };

@@ -11,9 +11,10 @@
  *
  * Workspaces here hold nothing between calls: they need no initialisation
  * (and none after an error), must be 256-byte aligned, and may be shared by
- * calls that are ordered on one stream.  The kernels of one call never wait
- * for one another's CTAs.  Every result is bitwise reproducible for equal
- * inputs and shapes.
+ * calls that are ordered on one stream.  Every result is bitwise reproducible
+ * for equal inputs and shapes.  Waits inside the kernels (for staged copies,
+ * and between the CTAs of a thread-block cluster) are bounded and report
+ * through cake_rmsnorm_device_status().
  */
 #ifndef CAKE_STEP_H
 #define CAKE_STEP_H
