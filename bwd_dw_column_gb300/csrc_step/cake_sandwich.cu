@@ -27,15 +27,20 @@ constexpr int kSMsStep = 152;
 constexpr int kSwMaxStages = 16;
 constexpr int kSwMaxTile = 12;            // rows of a stage, at most
 constexpr int kSwSlots = 4;               // backward: rows whose partial sums may be in use
-constexpr int kSwRowWarps = 32;           // warps of a row (over its cluster) that a slot has room for
-constexpr int kSwSlotFloats = 4 * kSwRowWarps;
 constexpr int kSwMaxJoined = 6;           // groups whose rows span several warps, at most
+constexpr int kSwMaxRowWarps = 32;        // warps of a row over its cluster, at most
 constexpr int kSwMaxCluster = 4;
+constexpr int kSwClustersOf4 = 36;        // that a GB300 holds at a time
 // Shared memory before the weights: the ring's barriers (256 bytes), the row
-// sums' barriers (384), a flag (64), the row sums' partials, the rows' scalars.
-constexpr int kSwRed = 704;
-constexpr int kSwScalarsAt = kSwRed + kSwMaxJoined * kSwSlots * kSwSlotFloats * 4;
-constexpr int kSwFixed = (kSwScalarsAt + kSwMaxStages * kSwMaxTile * 16 + 1023) / 1024 * 1024;
+// sums' barriers (512), a flag (64), the row sums' partials, the rows' scalars.
+constexpr int kSwRed = 832;
+constexpr int kSwRedBytes = 4096;
+constexpr int kSwScalarsAt = kSwRed + kSwRedBytes;
+constexpr int kSwFixed = (kSwScalarsAt + kSwMaxStages * kSwMaxTile * 16 + 127) / 128 * 128;
+
+// Room for the warps of a row in a slot of partial sums: 8, 16 or 32; 1: rows
+// of one warp, which need no slots.
+__host__ __device__ constexpr int row_warps(int n) { return n == 1 ? 1 : n <= 8 ? 8 : n <= 16 ? 16 : 32; }
 
 struct SwSmem {
     Smem s;               // barriers, reduction slots, flag, ring
@@ -50,7 +55,7 @@ __device__ __forceinline__ SwSmem sw_carve(uint8_t *base, const SandwichLayout &
     m.s.full = reinterpret_cast<uint64_t *>(base);
     m.s.empty = m.s.full + L.stages;
     m.sums = reinterpret_cast<uint64_t *>(base + 256);
-    m.s.flag = reinterpret_cast<int *>(base + 640);
+    m.s.flag = reinterpret_cast<int *>(base + 768);
     m.s.red = reinterpret_cast<float *>(base + kSwRed);
     m.scalars = reinterpret_cast<float4 *>(base + kSwScalarsAt);
     m.w[0] = reinterpret_cast<float *>(base + kSwFixed);
@@ -313,7 +318,8 @@ __device__ __forceinline__ float warp_sum3(float v0, float v1, float v2, int lan
     return r;
 }
 
-// GATE: 0 none, 1 a value per row, 2 a value per element.
+// GATE: 0 none, 1 a value per row, 2 a value per element.  CL: rows span a
+// cluster.  RW: row_warps of the layout.
 //
 // A thread holds the two column sums of 8 VPT columns as Kahan pairs, 32 VPT
 // registers, which is why it takes no more than 16 columns.  With 12 consumer
@@ -332,8 +338,11 @@ __device__ __forceinline__ float warp_sum3(float v0, float v1, float v2, int lan
 // needs every warp of the row to have read row j - 2's: four slots, each with
 // a barrier of its own, hold the rows that may be in use, also where sums
 // reach one CTA of a cluster later than another.
-template <int VPT, int GATE, bool CL>
-__global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p)
+constexpr int kSwBwdWarps = 12;     // consumer warps; four more hold the producer
+constexpr int kSwBwdThreads = 32 * (kSwBwdWarps + 4);
+
+template <int VPT, int GATE, bool CL, int RW>
+__global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const SandwichLayout &L = p.L;
@@ -346,22 +355,33 @@ __global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __
     const uint32_t r0 = cid * L.rows_per_cta, r_end = min(L.rows, r0 + L.rows_per_cta);
     if (threadIdx.x < kSwSlots * L.groups) // in a cluster: one arrival, and the bytes that come
         mbar_init(smem_addr(m.sums + threadIdx.x), CL ? 1 : L.W);
-    for (int i = threadIdx.x; i < kSwMaxJoined * kSwSlots * kSwSlotFloats; i += blockDim.x)
+    for (int i = threadIdx.x; i < kSwRedBytes / 4; i += blockDim.x)
         m.s.red[i] = 0.f; // the parts of warps that a row does not have stay zero
     if (CL && threadIdx.x < kSwSlots * L.groups)
         fence_mbar_init();
     init_ring(m.s, RL);
     if (CL)
         cluster_sync_all(); // every CTA's barriers and slots exist before a remote access
-    if (warp == L.groups * L.W) {
-        sw_produce(m, L, p.in, p.rstd_post, p.rstd_pre, p.gate_rows, v0, nvec, r0, r_end, p.status, p.wait_ns);
+    // Registers: 16 warps start with 128 each; the last four give 72 up, and
+    // the twelve consumer warps take 24 more (12 x 152 + 4 x 56 = 16 x 128).
+    if (warp >= kSwBwdWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == kSwBwdWarps)
+            sw_produce(m, L, p.in, p.rstd_post, p.rstd_pre, p.gate_rows, v0, nvec, r0, r_end, p.status, p.wait_ns);
         __syncwarp();
         if (CL)
             cluster_sync_all();
         return;
     }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    if (warp >= L.groups * L.W) { // no row for this warp
+        if (CL)
+            cluster_sync_all();
+        return;
+    }
     const int gid = warp / L.W, wig = warp - gid * L.W, gtid = wig * 32 + lane, vstride = 32 * L.W;
-    const bool has_dh = p.has_dh, joined = CL || L.W > 1;
+    const bool has_dh = p.has_dh;
+    constexpr bool joined = RW > 1;
     {
         Smem sw = m.s;
         sw.wsm = m.w[0];
@@ -382,10 +402,10 @@ __global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __
     const uint32_t ntiles = r_end > r0 ? (r_end - r0 + tile - 1) / tile : 0;
     const uint4 *gbase = reinterpret_cast<const uint4 *>(m.s.ring + (size_t)gid * L.cols * 2);
     const uint32_t sbytes = m.s.stage_bytes / 16;
-    float *red = m.s.red + gid * kSwSlots * kSwSlotFloats;
+    float *red = m.s.red + gid * kSwSlots * 4 * RW; // a slot: [4 sums][RW]
     float own = 0.f; // rows of one warp: the sums of the row between its passes
     bool abort = false;
-    uint32_t st1 = 0, ph1 = 0, st2 = 0; // ring slots of the first and the second pass
+    uint32_t st1 = 0, ph1 = 0; // ring slot of the first pass
     for (uint32_t j = 0; j <= ntiles && !abort; ++j) {
         float mine = 0.f;
         if (j < ntiles) {
@@ -422,7 +442,7 @@ __global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __
                 }
                 mine = warp_sum3(__fadd_rn(s1.x, s1.y), __fadd_rn(s2.x, s2.y), __fadd_rn(s3.x, s3.y), lane);
                 if (joined) {
-                    float *at = red + (j & 3) * kSwSlotFloats + (lane >> 3) * kSwRowWarps + rank * L.W + wig;
+                    float *at = red + ((j & 3) * 4 + (lane >> 3)) * RW + (CL ? cluster_ctarank() * L.W : 0) + wig;
                     const uint32_t bar = smem_addr(m.sums + kSwSlots * gid + (j & 3));
                     if (CL) {
                         // to every CTA of the cluster, each sum by a lane that holds it
@@ -446,13 +466,24 @@ __global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __
         }
         if (j > 0) {
             const uint32_t i = j - 1, r = r0 + i * tile + gid;
+            // the second pass's slot, one before the first pass's
+            const uint32_t back = j < ntiles ? 2 : 1, st2 = st1 >= back ? st1 - back : st1 + L.stages - back;
             if (r < r_end) {
                 float t3 = own;
                 if (joined) {
                     if (!mbar_wait(smem_addr(m.sums + kSwSlots * gid + (i & 3)), (i >> 2) & 1, p.wait_ns))
                         abort = true;
-                    const float4 a = ld_shared_f4(smem_addr(red + (i & 3) * kSwSlotFloats + 4 * lane));
-                    t3 = __fadd_rn(__fadd_rn(a.x, a.y), __fadd_rn(a.z, a.w));
+                    // eight lanes to a sum
+                    const float *from = red + (i & 3) * 4 * RW;
+                    if (RW == 8) {
+                        t3 = from[lane];
+                    } else if (RW == 16) {
+                        const float2 a = reinterpret_cast<const float2 *>(from)[lane];
+                        t3 = __fadd_rn(a.x, a.y);
+                    } else {
+                        const float4 a = reinterpret_cast<const float4 *>(from)[lane];
+                        t3 = __fadd_rn(__fadd_rn(a.x, a.y), __fadd_rn(a.z, a.w));
+                    }
 #pragma unroll
                     for (int o = 4; o > 0; o >>= 1)
                         t3 = __fadd_rn(t3, __shfl_xor_sync(0xffffffffu, t3, o));
@@ -463,12 +494,15 @@ __global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __
                 const float k2 = __fmul_rn(__fmul_rn(__fmul_rn(__fmul_rn(t1, L.inv_h), sc.y), sc.y), sc.y);
                 const float dot = __fmaf_rn(-k2, t3, t2);
                 const float2 nk2 = both(-k2), rn = both(sc.y);
-                const float2 nk1 = both(-__fmul_rn(__fmul_rn(__fmul_rn(dot, L.inv_h), sc.x), sc.x));
-                const float2 sr = both(__fmul_rn(GATE == 1 ? __fmul_rn(p.scale, sc.z) : p.scale, sc.x));
-                if (GATE == 1 && p.dgate_rows && gtid == 0 && rank == 0 && !abort)
+                const float s_r = __fmul_rn(GATE == 1 ? __fmul_rn(p.scale, sc.z) : p.scale, sc.x);
+                const float k1 = __fmul_rn(__fmul_rn(__fmul_rn(dot, L.inv_h), sc.x), sc.x);
+                const float2 sr = both(s_r), nks = both(-__fmul_rn(k1, s_r));
+                if (GATE == 1 && p.dgate_rows && gtid == 0 && (!CL || cluster_ctarank() == 0) && !abort)
                     p.dgate_rows[r] = __fmul_rn(__fmul_rn(p.scale, sc.x), dot);
-                uint4 *dx = out_row(p.dx, r, L.nh) + v0, *dz = out_row(p.dz, r, L.nh) + v0;
-                uint4 *dg = GATE == 2 && p.dgate.base ? out_row(p.dgate, r, L.nh) + v0 : nullptr;
+                // (the rank is read again where it is needed: a register less over the loop)
+                const int vo = CL ? (int)cluster_ctarank() * (L.cols / 8) : 0;
+                uint4 *dx = out_row(p.dx, r, L.nh) + vo, *dz = out_row(p.dz, r, L.nh) + vo;
+                uint4 *dg = GATE == 2 && p.dgate.base ? out_row(p.dgate, r, L.nh) + vo : nullptr;
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) {
                     const int v = k * vstride + gtid;
@@ -489,13 +523,13 @@ __global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __
                             const float2 zq = bf2(word(z, q));
                             const float2 a = mul2(bf2(word(d, q)), w2[q]);
                             const float2 t = fma2(nk2, bf2(word(h, q)), fma2(rn, a, bf2(word(e, q))));
-                            const float2 tg = GATE == 2 ? mul2(t, bf2(word(g, q))) : t;
-                            const float2 tz = mul2(sr, zq);
                             ox[q] = pack2(t);
-                            oz[q] = pack2(mul2(sr, fma2(tg, w1[q], mul2(nk1, zq))));
+                            const float2 st = mul2(sr, t);
+                            const float2 mt = GATE == 2 ? mul2(st, bf2(word(g, q))) : st;
+                            oz[q] = pack2(fma2(mt, w1[q], mul2(nks, zq)));
                             if (GATE == 2)
-                                og[q] = pack2(mul2(mul2(t, tz), w1[q]));
-                            kahan2(hi1[k][q], lo1[k][q], tg, tz);
+                                og[q] = pack2(mul2(mul2(st, zq), w1[q]));
+                            kahan2(hi1[k][q], lo1[k][q], mt, zq);
                         }
                         __stcs(dx + v, make_uint4(ox[0], ox[1], ox[2], ox[3]));
                         __stcs(dz + v, make_uint4(oz[0], oz[1], oz[2], oz[3]));
@@ -507,8 +541,6 @@ __global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_addr(&m.s.empty[st2]));
-            if (++st2 == (uint32_t)L.stages)
-                st2 = 0;
         }
         own = mine;
     }
@@ -518,6 +550,7 @@ __global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __
     // The CTA partial: the groups' sums in group order, through the drained
     // ring ([group][w][4 nvec] float4 (hi, lo, hi, lo) of a column pair).
     const int nct = L.groups * L.W * 32, nslot = 4 * nvec;
+    const int vp = CL ? (int)cluster_ctarank() * (L.cols / 8) : 0;
     float4 *comb = reinterpret_cast<float4 *>(m.s.ring);
     consumer_sync(RL);
 #pragma unroll
@@ -543,7 +576,7 @@ __global__ void __launch_bounds__(kSwFwdThreads, 1) sandwich_bwd_kernel(const __
             comp_add(a.z, a.w, b.z);
             a.w = __fadd_rn(a.w, b.w);
         }
-        reinterpret_cast<float4 *>(p.partials + ((size_t)w * (gridDim.x / C) + cid) * L.H)[4 * v0 + c] = a;
+        reinterpret_cast<float4 *>(p.partials + ((size_t)w * (gridDim.x / C) + cid) * L.H)[4 * vp + c] = a;
     }
     __syncwarp();
     if (CL)
@@ -585,24 +618,26 @@ __global__ void __launch_bounds__(32 * kSwReduceWarps)
 
 // The shape of a CTA.  It depends on H and the staged tensors, the number of
 // CTAs on the rows too, and on nothing else, so the sums' orders do not either.
-static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int cluster)
+// false: such a CTA does not fit.
+static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int cluster, int groups)
 {
     const int nvec = (H / 8 + cluster - 1) / cluster; // of a CTA
     p.cluster = cluster;
     p.cols = 8 * nvec;
     p.vpt = H <= 256 ? 1 : 2;
     p.W = (nvec + 32 * p.vpt - 1) / (32 * p.vpt);
-    p.groups = p.W >= 12 ? 1 : 12 / p.W;
-    // CTAs per SM: 16 warps of 128 registers (backward), 28 of 72 (forward)
-    p.per_sm = (backward ? 16 : 28) / (p.groups * p.W + 1);
-    p.per_sm = p.per_sm < 1 || cluster > 1 ? 1 : p.per_sm > 2 ? 2 : p.per_sm;
+    p.groups = groups;
+    if (p.groups * p.W > (backward ? kSwBwdWarps : 16))
+        return false;
+    // CTAs per SM: the backward's takes all registers, 28 of the forward's warps fit
+    p.per_sm = backward ? 1 : 28 / (p.groups * p.W + 1) >= 2 ? 2 : 1;
     const size_t fixed = (size_t)kSwFixed + 2 * weight_smem_bytes(p.cols);
     const size_t stage = (size_t)ntens * p.groups * p.cols * 2;
     // the backward holds two rows of a group at once and a third is to be
     // on its way; the forward works on one
     const int want = backward ? 3 : 2;
     for (;; --p.per_sm) {
-        const size_t room = 227 * 1024 / p.per_sm - 1024; // 1 KB of each CTA is the system's
+        const size_t room = 228 * 1024 / p.per_sm - 1024; // 1 KB of each CTA is the system's
         p.stages = room > fixed ? (int)((room - fixed) / stage) : 0;
         if (p.stages >= want || p.per_sm == 1)
             break;
@@ -613,33 +648,48 @@ static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int clust
     const size_t comb = fixed + (size_t)(backward ? p.groups : 0) * p.cols * 16;
     if (comb > p.smem)
         p.smem = comb;
-    const bool slots = p.W * cluster == 1 || (p.groups <= kSwMaxJoined && p.W * cluster <= kSwRowWarps);
-    return p.stages >= want && p.W <= (backward ? 12 : 16) && slots && p.cols * (cluster - 1) < H;
+    if (p.smem > 227 * 1024 || p.cols * (cluster - 1) >= H)
+        return false;
+    if (p.W * cluster > 1 && (p.groups > kSwMaxJoined || p.W * cluster > kSwMaxRowWarps ||
+                              p.groups * kSwSlots * 16 * row_warps(p.W * cluster) > kSwRedBytes))
+        return false;
+    return p.stages >= want;
 }
 
 SandwichPlan sandwich_plan(int H, uint32_t rows, int ntens, bool backward)
 {
     SandwichPlan p{};
-    try_plan(p, H, ntens, backward, 1);
-    if (backward) {
-        // the smallest cluster that keeps the most lanes of the 12 warps busy
+    if (!backward) {
+        const int W = H <= 256 ? 1 : (H + 511) / 512;
+        try_plan(p, H, ntens, false, 1, W >= 12 ? 1 : 12 / W);
+    } else {
+        // The most columns in work on an SM, up to the 6144 that keep HBM
+        // busy; of equals the smallest cluster.  Weights, as measured on GB300
+        // with 2^27 values without a gate (copy rate: 238 us): three stages
+        // against four 296 and 263 us at H = 2048, a single group against two
+        // 290 and 266 us at H = 6144; 36 clusters of 4 fit the 152 SMs.
         int best = 0;
-        for (int c = 1; c <= kSwMaxCluster; c *= 2) {
-            SandwichPlan q{};
-            if (!try_plan(q, H, ntens, backward, c))
-                continue;
-            const int busy = q.cols * q.groups * q.per_sm; // columns in work on an SM
-            if (busy > best) {
-                best = busy;
-                p = q;
+        for (int c = 1; c <= (H > 2048 ? kSwMaxCluster : 1); c *= 2)
+            for (int g = kSwMaxTile; g >= 1; --g) {
+                SandwichPlan q{};
+                if (!try_plan(q, H, ntens, true, c, g))
+                    continue;
+                int score = q.cols * q.groups * q.per_sm;
+                score = score > 6144 ? 6144 : score;
+                if (q.stages < 4)
+                    score = score * 89 / 100;
+                if (q.groups * q.per_sm == 1)
+                    score = score * 93 / 100;
+                score = c == 4 ? score * 93 / 100 : c == 2 ? score * 98 / 100 : score;
+                if (score > best) {
+                    best = score;
+                    p = q;
+                }
             }
-            if (H <= 2048 || best >= 12 * 512)
-                break;
-        }
     }
     const uint32_t tile = (uint32_t)p.groups;
     uint32_t ctas = (rows + tile - 1) / tile; // clusters, where a row has one
-    const uint32_t most = (uint32_t)kSMsStep * p.per_sm / p.cluster;
+    const uint32_t most = p.cluster == 4 ? kSwClustersOf4 : (uint32_t)kSMsStep * p.per_sm / p.cluster;
     if (ctas > most)
         ctas = most;
     p.rows_per_cta = ctas ? (rows + ctas - 1) / ctas : 0;
@@ -648,9 +698,8 @@ SandwichPlan sandwich_plan(int H, uint32_t rows, int ntens, bool backward)
 }
 
 template <class P>
-static cudaError_t launch_rows(void (*kern)(P), const P &p, const SandwichPlan &plan, cudaStream_t stream)
+static cudaError_t launch_rows(void (*kern)(P), const P &p, const SandwichPlan &plan, int threads, cudaStream_t stream)
 {
-    const int threads = 32 * (plan.groups * plan.W + 1);
     cudaError_t e = ensure_smem_attr((const void *)kern, plan.smem);
     if (e != cudaSuccess)
         return e;
@@ -673,25 +722,33 @@ static cudaError_t launch_rows(void (*kern)(P), const P &p, const SandwichPlan &
 cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
 {
     const bool g = p.L.ntens == 3;
+    const int threads = 32 * (plan.groups * plan.W + 1);
     if (plan.vpt == 1)
-        return g ? launch_rows(sandwich_fwd_kernel<1, true, kSwFwdThreads>, p, plan, stream)
-                 : launch_rows(sandwich_fwd_kernel<1, false, kSwFwdThreads>, p, plan, stream);
+        return g ? launch_rows(sandwich_fwd_kernel<1, true, kSwFwdThreads>, p, plan, threads, stream)
+                 : launch_rows(sandwich_fwd_kernel<1, false, kSwFwdThreads>, p, plan, threads, stream);
     if (plan.W <= 12)
-        return g ? launch_rows(sandwich_fwd_kernel<2, true, kSwFwdThreads>, p, plan, stream)
-                 : launch_rows(sandwich_fwd_kernel<2, false, kSwFwdThreads>, p, plan, stream);
-    return g ? launch_rows(sandwich_fwd_kernel<2, true, kSwWideThreads>, p, plan, stream)
-             : launch_rows(sandwich_fwd_kernel<2, false, kSwWideThreads>, p, plan, stream);
+        return g ? launch_rows(sandwich_fwd_kernel<2, true, kSwFwdThreads>, p, plan, threads, stream)
+                 : launch_rows(sandwich_fwd_kernel<2, false, kSwFwdThreads>, p, plan, threads, stream);
+    return g ? launch_rows(sandwich_fwd_kernel<2, true, kSwWideThreads>, p, plan, threads, stream)
+             : launch_rows(sandwich_fwd_kernel<2, false, kSwWideThreads>, p, plan, threads, stream);
 }
 
 template <int GATE>
 static cudaError_t launch_bwd_gate(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
 {
-    if (plan.stages < 2 || plan.W > 12) // a row is held while the next one is read
+    if (plan.stages < 2 || plan.groups * plan.W > kSwBwdWarps) // a row is held while the next one is read
         return cudaErrorInvalidValue;
+    const int threads = kSwBwdThreads;
+    const int rw = row_warps(plan.W * plan.cluster);
     if (plan.cluster > 1)
-        return launch_rows(sandwich_bwd_kernel<2, GATE, true>, p, plan, stream);
-    return plan.vpt == 1 ? launch_rows(sandwich_bwd_kernel<1, GATE, false>, p, plan, stream)
-                         : launch_rows(sandwich_bwd_kernel<2, GATE, false>, p, plan, stream);
+        return rw == 8    ? launch_rows(sandwich_bwd_kernel<2, GATE, true, 8>, p, plan, threads, stream)
+               : rw == 16 ? launch_rows(sandwich_bwd_kernel<2, GATE, true, 16>, p, plan, threads, stream)
+                          : launch_rows(sandwich_bwd_kernel<2, GATE, true, 32>, p, plan, threads, stream);
+    if (plan.W == 1)
+        return plan.vpt == 1 ? launch_rows(sandwich_bwd_kernel<1, GATE, false, 1>, p, plan, threads, stream)
+                             : launch_rows(sandwich_bwd_kernel<2, GATE, false, 1>, p, plan, threads, stream);
+    return rw == 8 ? launch_rows(sandwich_bwd_kernel<2, GATE, false, 8>, p, plan, threads, stream)
+                   : launch_rows(sandwich_bwd_kernel<2, GATE, false, 16>, p, plan, threads, stream);
 }
 
 cudaError_t launch_sandwich_bwd(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
