@@ -261,8 +261,10 @@ cudaError_t launch_grad_final(const double *partials, int n, float *norm, cudaSt
 }
 
 template cudaError_t launch_grad_sumsq<kGradFewTensors>(const GradParams<kGradFewTensors> &, int, cudaStream_t);
+template cudaError_t launch_grad_sumsq<kGradSomeTensors>(const GradParams<kGradSomeTensors> &, int, cudaStream_t);
 template cudaError_t launch_grad_sumsq<kGradMaxTensors>(const GradParams<kGradMaxTensors> &, int, cudaStream_t);
 template cudaError_t launch_grad_clip<kGradFewTensors>(const GradParams<kGradFewTensors> &, int, bool, cudaStream_t);
+template cudaError_t launch_grad_clip<kGradSomeTensors>(const GradParams<kGradSomeTensors> &, int, bool, cudaStream_t);
 template cudaError_t launch_grad_clip<kGradMaxTensors>(const GradParams<kGradMaxTensors> &, int, bool, cudaStream_t);
 
 } // namespace cake

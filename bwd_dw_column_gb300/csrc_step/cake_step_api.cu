@@ -369,11 +369,11 @@ cake_status grads(const void *const *data, const int64_t *counts, const int32_t 
     if ((st = check_workspace(workspace, workspace_bytes, cake_grad_norm_workspace_size(n))) != CAKE_OK)
         return st;
     double *partials = static_cast<double *>(workspace);
-    return cuda_status(n <= kGradFewTensors
-                           ? run_grads<kGradFewTensors>(data, counts, dtypes, outs, out_dtypes, n, clip, max_norm, eps,
-                                                        norm, partials, cu(stream))
-                           : run_grads<kGradMaxTensors>(data, counts, dtypes, outs, out_dtypes, n, clip, max_norm, eps,
-                                                        norm, partials, cu(stream)));
+    // the fewer parameters a launch carries, the sooner it starts
+    const auto run = n <= kGradFewTensors    ? run_grads<kGradFewTensors>
+                     : n <= kGradSomeTensors ? run_grads<kGradSomeTensors>
+                                             : run_grads<kGradMaxTensors>;
+    return cuda_status(run(data, counts, dtypes, outs, out_dtypes, n, clip, max_norm, eps, norm, partials, cu(stream)));
 }
 
 } // namespace

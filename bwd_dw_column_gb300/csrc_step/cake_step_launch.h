@@ -75,6 +75,7 @@ cudaError_t launch_sandwich_reduce(const SandwichReduceParams &p, cudaStream_t s
 constexpr int kGradChunk = 8192;
 // Tensors one launch takes: they travel in the launch parameters (32 KB).
 constexpr int kGradMaxTensors = 1000;
+constexpr int kGradSomeTensors = 256;
 constexpr int kGradFewTensors = 32;
 constexpr int kGradThreads = 256;
 constexpr int kGradCtas = 152 * 4;

@@ -24,13 +24,14 @@ on ``stream``, where its outputs and workspace are allocated too.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from array import array
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (CAKE_BF16, CAKE_FP32, _check, _P, _rows_of, _same_rows, _Shape, _Tensor, _tensor, _w_dtype,
-               load_library)
+from . import CAKE_BF16, CAKE_FP32, CAKE_OK, CakeError, load_library
 
 __all__ = [
     "cake_sandwich_fwd", "cake_sandwich_bwd", "cake_sandwich_bwd_workspace_size", "cake_sandwich_norm",
@@ -44,7 +45,7 @@ _vp, _i64, _f32, _int, _size = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, 
 
 def _bind(lib):
     """Declare the operators' C signatures on the library handle."""
-    T, S = _P(_Tensor), _P(_Shape)
+    T = S = _vp  # shapes and tensors are passed as packed bytes (see _three)
     for name, res, args in (
         ("cake_sandwich_fwd", _int, [S, T, T, _vp, _int, _vp, _int, _vp, T, _f32, _f32, T, T, _vp, _vp, _vp]),
         ("cake_sandwich_bwd_workspace_size", _size, [S]),
@@ -95,30 +96,72 @@ class _On:
 def _on(stream, *tensors):
     """Context of a call: every tensor (None: left out) on one CUDA device, which becomes
     the current one, with `stream` (None: its current stream) the current stream."""
-    dev = -1
+    dev = -2
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("every tensor must be on a CUDA device (no CPU path)")
         d = t.get_device()
-        if dev < 0:
+        if d != dev:
+            if d < 0:
+                raise ValueError("every tensor must be on a CUDA device (no CPU path)")
+            if dev != -2:
+                raise ValueError("every tensor must be on the same device")
             dev = d
-        elif d != dev:
-            raise ValueError("every tensor must be on the same device")
-    if stream is not None and stream.device.index != dev:
+    if stream is None:
+        if torch.cuda.current_device() == dev:
+            return _here
+    elif stream.device.index != dev:
         raise ValueError("the stream belongs to another device than the tensors")
-    if stream is None and torch.cuda.current_device() == dev:
-        return _here
     return _On(dev, stream)
 
 
 def _current() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    """The current device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
-def _ref(t):
-    return None if t is None else ctypes.byref(_tensor(t))
+# ------------------------------------------------------------------- marshalling
+
+# cake_shape and cake_tensor are three int64 each.  Packed bytes cost a third
+# of a ctypes structure, which counts where a call takes microseconds.
+_three = struct.Struct("=qqq").pack
+
+
+def _check(status: int, what: str):
+    if status != CAKE_OK:
+        raise CakeError(status, what)
+
+
+def _rows(t):
+    """(T, nh, H) of a [T, H] or [T, nh, H] tensor."""
+    if t.dim() == 2:
+        T, H = t.shape
+        return T, 1, H
+    if t.dim() == 3:
+        return tuple(t.shape)
+    raise ValueError(f"expected a [T, H] or [T, nh, H] tensor, got shape {tuple(t.shape)}")
+
+
+def _ref(t, shape, what):
+    """A BF16 activation of the given shape as a packed cake_tensor (None: NULL)."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"activations are BF16, got {t.dtype}")
+    st = t.stride()
+    if st[-1] != 1 and t.numel():
+        raise ValueError("the hidden dimension must be contiguous")
+    return _three(t.data_ptr(), st[0], st[1] if len(st) == 3 else 0)
+
+
+def _dtype(w):
+    if w.dtype is torch.bfloat16:
+        return CAKE_BF16
+    if w.dtype is torch.float32:
+        return CAKE_FP32
+    raise TypeError(f"weight is BF16 or FP32, got {w.dtype}")
 
 
 def _weight(w, H, what):
@@ -127,18 +170,24 @@ def _weight(w, H, what):
     return w if w.is_contiguous() else w.contiguous()
 
 
-def _rows_f32(t, shape, what):
-    if t.dtype != torch.float32 or t.numel() != shape.tokens * shape.heads or not t.is_contiguous():
+def _rows_f32(t, rows, what):
+    if t.dtype is not torch.float32 or t.numel() != rows or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous FP32 tensor of T*nh elements")
-    return t
+    return t.data_ptr()
+
+
+def _like(z):
+    return torch.empty_like(z) if z.is_contiguous() else torch.empty(z.shape, dtype=z.dtype, device=z.device)
 
 
 def _workspace(workspace, size, device):
+    """(tensor that keeps it alive, address, bytes)"""
     if workspace is None:
-        return torch.empty(max(size, 256), dtype=torch.uint8, device=device)
+        workspace = torch.empty(size or 256, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), size
     if not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # ---------------------------------------------------------------- sandwich norm
@@ -171,36 +220,36 @@ def cake_sandwich_fwd(z: torch.Tensor, x: torch.Tensor, w_post: torch.Tensor, w_
     """
     lib = load_library()
     with _on(stream, z, x, w_post, w_pre, gate, y, h_new, rstd_post, rstd_pre):
-        T, nh, H, _, _ = _rows_of(z)
-        _same_rows(z, x, "x")
+        T, nh, H = _rows(z)
+        size, rows = z.shape, T * nh
         w_post, w_pre = _weight(w_post, H, "w_post"), _weight(w_pre, H, "w_pre")
         g_row, g_elem = _gate(gate, z)
-        shape = _Shape(T, nh, H)
         if y is None:
-            y = torch.empty(z.shape, dtype=torch.bfloat16, device=z.device)
+            y = _like(z)
         if h_new is None:
-            h_new = torch.empty(z.shape, dtype=torch.bfloat16, device=z.device)
+            h_new = _like(z)
         if rstd_post is None:
-            rstd_post = torch.empty(T * nh, dtype=torch.float32, device=z.device)
+            rstd_post = torch.empty(rows, dtype=torch.float32, device=z.device)
         if rstd_pre is None:
-            rstd_pre = torch.empty(T * nh, dtype=torch.float32, device=z.device)
-        _same_rows(z, y, "y")
-        _same_rows(z, h_new, "h_new")
-        _rows_f32(rstd_post, shape, "rstd_post")
-        _rows_f32(rstd_pre, shape, "rstd_pre")
-        st = lib.cake_sandwich_fwd(ctypes.byref(shape), _ref(z), _ref(x), w_post.data_ptr(), _w_dtype(w_post),
-                                   w_pre.data_ptr(), _w_dtype(w_pre), g_row.data_ptr() if g_row is not None else None,
-                                   _ref(g_elem), scale, eps, _ref(y), _ref(h_new), rstd_post.data_ptr(),
-                                   rstd_pre.data_ptr(), _current())
+            rstd_pre = torch.empty(rows, dtype=torch.float32, device=z.device)
+        st = lib.cake_sandwich_fwd(_three(T, nh, H), _ref(z, size, "z"), _ref(x, size, "x"), w_post.data_ptr(),
+                                   _dtype(w_post), w_pre.data_ptr(), _dtype(w_pre),
+                                   None if g_row is None else g_row.data_ptr(), _ref(g_elem, size, "gate"), scale, eps,
+                                   _ref(y, size, "y"), _ref(h_new, size, "h_new"),
+                                   _rows_f32(rstd_post, rows, "rstd_post"), _rows_f32(rstd_pre, rows, "rstd_pre"),
+                                   _current())
         _check(st, "cake_sandwich_fwd")
     return y, h_new, rstd_post, rstd_pre
 
 
+@functools.lru_cache(maxsize=256)
+def _sandwich_bwd_bytes(T, nh, H):
+    return int(load_library().cake_sandwich_bwd_workspace_size(_three(T, nh, H)))
+
+
 def cake_sandwich_bwd_workspace_size(x_or_shape) -> int:
     """Workspace bytes the backward needs for this row set ([T, H] / [T, nh, H] tensor or (T, nh, H))."""
-    lib = load_library()
-    shape = _Shape(*(_rows_of(x_or_shape)[:3] if isinstance(x_or_shape, torch.Tensor) else x_or_shape))
-    return int(lib.cake_sandwich_bwd_workspace_size(ctypes.byref(shape)))
+    return _sandwich_bwd_bytes(*(_rows(x_or_shape) if isinstance(x_or_shape, torch.Tensor) else x_or_shape))
 
 
 def cake_sandwich_bwd(dy: torch.Tensor, h_new: torch.Tensor, z: torch.Tensor, rstd_post: torch.Tensor,
@@ -219,43 +268,40 @@ def cake_sandwich_bwd(dy: torch.Tensor, h_new: torch.Tensor, z: torch.Tensor, rs
     lib = load_library()
     with _on(stream, dy, h_new, z, rstd_post, rstd_pre, w_post, w_pre, dh, gate, workspace, dx, dz, dw_post, dw_pre,
              dgate):
-        T, nh, H, _, _ = _rows_of(z)
-        for t, what in ((dy, "dy"), (h_new, "h_new"), (dh, "dh"), (dx, "dx"), (dz, "dz")):
-            if t is not None:
-                _same_rows(z, t, what)
+        T, nh, H = _rows(z)
+        size, rows = z.shape, T * nh
         w_post, w_pre = _weight(w_post, H, "w_post"), _weight(w_pre, H, "w_pre")
         g_row, g_elem = _gate(gate, z)
-        shape = _Shape(T, nh, H)
-        _rows_f32(rstd_post, shape, "rstd_post")
-        _rows_f32(rstd_pre, shape, "rstd_pre")
         dev = z.device
         if dx is None:
-            dx = torch.empty(z.shape, dtype=torch.bfloat16, device=dev)
+            dx = _like(z)
         if dz is None:
-            dz = torch.empty(z.shape, dtype=torch.bfloat16, device=dev)
+            dz = _like(z)
         if dw_post is None:
             dw_post = torch.empty(H, dtype=torch.float32, device=dev)
         if dw_pre is None:
             dw_pre = torch.empty(H, dtype=torch.float32, device=dev)
         for t, what in ((dw_post, "dw_post"), (dw_pre, "dw_pre")):
-            if t.dtype != torch.float32 or t.numel() != H or not t.is_contiguous():
+            if t.dtype is not torch.float32 or t.numel() != H or not t.is_contiguous():
                 raise ValueError(f"{what} must be a contiguous FP32 tensor of H elements")
         if gate is None or not need_dgate:
             if dgate is not None:
                 raise ValueError("dgate is given, but no gradient of a gate is asked for")
         elif dgate is None:
             dgate = torch.empty(gate.shape, dtype=gate.dtype, device=dev)
-        elif dgate.shape != gate.shape or (g_row is not None and (dgate.dtype != torch.float32 or
+        elif dgate.shape != gate.shape or (g_row is not None and (dgate.dtype is not torch.float32 or
                                                                   not dgate.is_contiguous())):
             raise ValueError("dgate must have the gate's shape (and be contiguous FP32 for a value per row)")
-        workspace = _workspace(workspace, lib.cake_sandwich_bwd_workspace_size(ctypes.byref(shape)), dev)
-        st = lib.cake_sandwich_bwd(ctypes.byref(shape), _ref(dy), _ref(dh), _ref(h_new), _ref(z), rstd_post.data_ptr(),
-                                   rstd_pre.data_ptr(), w_post.data_ptr(), _w_dtype(w_post), w_pre.data_ptr(),
-                                   _w_dtype(w_pre), g_row.data_ptr() if g_row is not None else None, _ref(g_elem),
-                                   scale, _ref(dx), _ref(dz), dw_post.data_ptr(), dw_pre.data_ptr(),
+        workspace, ws, ws_bytes = _workspace(workspace, _sandwich_bwd_bytes(T, nh, H), dev)
+        st = lib.cake_sandwich_bwd(_three(T, nh, H), _ref(dy, size, "dy"), _ref(dh, size, "dh"),
+                                   _ref(h_new, size, "h_new"), _ref(z, size, "z"),
+                                   _rows_f32(rstd_post, rows, "rstd_post"), _rows_f32(rstd_pre, rows, "rstd_pre"),
+                                   w_post.data_ptr(), _dtype(w_post), w_pre.data_ptr(), _dtype(w_pre),
+                                   None if g_row is None else g_row.data_ptr(), _ref(g_elem, size, "gate"), scale,
+                                   _ref(dx, size, "dx"), _ref(dz, size, "dz"), dw_post.data_ptr(), dw_pre.data_ptr(),
                                    dgate.data_ptr() if g_row is not None and dgate is not None else None,
-                                   _ref(dgate) if g_elem is not None else None, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _current())
+                                   _ref(dgate, size, "dgate") if g_elem is not None else None, ws, ws_bytes,
+                                   _current())
         _check(st, "cake_sandwich_bwd")
     return dx, dz, dw_post, dw_pre, dgate
 
@@ -295,8 +341,6 @@ def cake_sandwich_norm(z: torch.Tensor, x: torch.Tensor, w_post: torch.Tensor, w
 
 def _dense(t: torch.Tensor) -> bool:
     """Whether the tensor's values fill one block of memory, in any order of its dimensions."""
-    if t.is_contiguous():
-        return True
     want = 1
     for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
         if stride != want:
@@ -305,27 +349,26 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
+_GRAD_DTYPES = {torch.bfloat16: CAKE_BF16, torch.float32: CAKE_FP32}
+
+
 def _tensors(grads, what):
-    """The tensors of a list (None: left out) as the ABI's arrays (pointers, counts, dtypes)."""
-    ptrs, counts, types = array("Q"), array("q"), array("i")
+    """The tensors as the ABI's arrays (pointers, counts, dtypes)."""
+    try:
+        types = array("i", [_GRAD_DTYPES[t.dtype] for t in grads])
+    except KeyError as e:
+        raise TypeError(f"{what} are BF16 or FP32, got {e.args[0]}") from None
     for t in grads:
-        if t.dtype is torch.bfloat16:
-            types.append(CAKE_BF16)
-        elif t.dtype is torch.float32:
-            types.append(CAKE_FP32)
-        else:
-            raise TypeError(f"{what} are BF16 or FP32, got {t.dtype}")
-        if not _dense(t):
+        if not t.is_contiguous() and not _dense(t):
             raise ValueError(f"{what} must fill one block of memory each (strides {t.stride()} of {tuple(t.shape)})")
-        ptrs.append(t.data_ptr())
-        counts.append(t.numel())
-    return ptrs, counts, types
+    return array("Q", [t.data_ptr() for t in grads]), array("q", [t.numel() for t in grads]), types
 
 
 def _addr(a):
     return a.buffer_info()[0] if len(a) else None
 
 
+@functools.lru_cache(maxsize=64)
 def cake_grad_norm_workspace_size(n: int) -> int:
     """Workspace bytes of a norm over (or clipping of) n tensors."""
     return int(load_library().cake_grad_norm_workspace_size(int(n)))
@@ -342,8 +385,8 @@ def _grad_call(grads, outs, clip, max_norm, eps, norm, workspace, stream):
             norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
         elif norm.dtype != torch.float32 or norm.numel() != 1:
             raise ValueError("norm must be an FP32 tensor of one element")
-        workspace = _workspace(workspace, lib.cake_grad_norm_workspace_size(n), norm.device)
-        ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), _current())
+        workspace, ws_at, ws_bytes = _workspace(workspace, cake_grad_norm_workspace_size(n), norm.device)
+        ws = (ws_at, ws_bytes, _current())
         if not clip:
             st = lib.cake_grad_norm(_addr(ptrs), _addr(counts), _addr(types), n, norm.data_ptr(), *ws)
             _check(st, "cake_grad_norm")
@@ -428,11 +471,13 @@ def cake_embedding_fwd(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.
         elif y.shape != (*ids.shape, H):
             raise ValueError(f"y has shape {tuple(y.shape)}, expected {(*ids.shape, H)}")
         st = lib.cake_embedding_fwd(ids.data_ptr(), int(ids.dtype is torch.int64), T, table.data_ptr(),
-                                    _w_dtype(table), V, H, table.stride(0), scale, _ref(y if y.dim() == 2 else y.view(T, H)), _current())
+                                    _dtype(table), V, H, table.stride(0), scale,
+                                    _ref(y if y.dim() == 2 else y.view(T, H), (T, H), "y"), _current())
         _check(st, "cake_embedding_fwd")
     return y
 
 
+@functools.lru_cache(maxsize=256)
 def cake_embedding_bwd_workspace_size(tokens: int, vocab: int, hidden: int) -> int:
     """Workspace bytes of an embedding's gradient."""
     return int(load_library().cake_embedding_bwd_workspace_size(int(tokens), int(vocab), int(hidden)))
@@ -464,11 +509,10 @@ def cake_embedding_bwd(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: f
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(vocab, H)}")
         if padding_idx is not None and not 0 <= padding_idx < vocab:
             raise ValueError(f"padding_idx {padding_idx} is outside the table")
-        workspace = _workspace(workspace, lib.cake_embedding_bwd_workspace_size(T, vocab, H), dy.device)
-        st = lib.cake_embedding_bwd(_ref(rows), ids.data_ptr(), int(ids.dtype is torch.int64), T, vocab, H, scale,
-                                    -1 if padding_idx is None else padding_idx, out.data_ptr(), _w_dtype(out),
-                                    out.stride(0), int(bool(accumulate)), workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), _current())
+        workspace, ws, ws_bytes = _workspace(workspace, cake_embedding_bwd_workspace_size(T, vocab, H), dy.device)
+        st = lib.cake_embedding_bwd(_ref(rows, (T, H), "dy"), ids.data_ptr(), int(ids.dtype is torch.int64), T, vocab, H, scale,
+                                    -1 if padding_idx is None else padding_idx, out.data_ptr(), _dtype(out),
+                                    out.stride(0), int(bool(accumulate)), ws, ws_bytes, _current())
         _check(st, "cake_embedding_bwd")
     return out
 
