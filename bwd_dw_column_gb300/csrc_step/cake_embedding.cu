@@ -21,6 +21,7 @@ namespace cake {
 __device__ int g_step_status;
 
 constexpr int kStatusInvalid = 1; // == CAKE_ERR_INVALID
+constexpr int kStatusTimeout = 5; // == CAKE_ERR_TIMEOUT
 
 __device__ __forceinline__ int64_t load_id(const void *ids, int i64, uint32_t t)
 {
@@ -31,7 +32,8 @@ __device__ __forceinline__ int64_t load_id(const void *ids, int i64, uint32_t t)
 
 constexpr int kEmbedThreads = 256;
 
-// One warp per 32 x 4 vectors of a row.
+// A warp takes 128 vectors (2 KB of output) of a row.
+template <bool F32>
 __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const __grid_constant__ EmbedFwdParams p)
 {
     const int lane = threadIdx.x & 31;
@@ -45,35 +47,43 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const __grid_c
         const bool live = id >= 0 && id < p.vocab;
         if (id >= p.vocab && v0 == 0)
             set_status(p.status, kStatusInvalid);
-        uint4 out[4];
+        uint4 raw[4][F32 ? 2 : 1];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int v = v0 + 32 * k;
-            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < (F32 ? 2 : 1); ++i)
+                raw[k][i] = make_uint4(0, 0, 0, 0);
             if (live && v < p.nvec) {
-                if (p.table_f32) {
-                    const float4 *s =
-                        reinterpret_cast<const float4 *>(static_cast<const float *>(p.table) + id * p.table_stride) +
-                        2 * v;
-                    const float4 a = __ldg(s), b = __ldg(s + 1);
-                    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-                    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+                if (F32) {
+                    const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const float *>(p.table) +
+                                                                     id * p.table_stride) + 2 * v;
+                    raw[k][0] = __ldg(s);
+                    raw[k][F32 ? 1 : 0] = __ldg(s + 1);
                 } else {
-                    unpack8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.table) +
-                                                                  id * p.table_stride) +
-                                  v),
-                            f);
+                    raw[k][0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.table) +
+                                                                      id * p.table_stride) + v);
                 }
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    f[q] = __fmul_rn(f[q], p.scale);
             }
-            out[k] = pack8(f);
         }
+        uint4 *y = reinterpret_cast<uint4 *>(p.y + (int64_t)t * p.y_stride);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k) {
+            float f[8];
+            if (F32) {
+                const uint4 a = raw[k][0], b = raw[k][F32 ? 1 : 0];
+                f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z);
+                f[3] = __uint_as_float(a.w), f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y);
+                f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
+            } else {
+                unpack8(raw[k][0], f);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                f[q] = live ? __fmul_rn(f[q], p.scale) : 0.f;
             if (v0 + 32 * k < p.nvec)
-                __stcs(reinterpret_cast<uint4 *>(p.y + (int64_t)t * p.y_stride) + v0 + 32 * k, out[k]);
+                __stcs(y + v0 + 32 * k, pack8(f));
+        }
     }
 }
 
@@ -92,7 +102,196 @@ __device__ __forceinline__ uint64_t make_pair(const SortParams &p, uint32_t t)
     const int64_t id = load_id(p.ids, p.ids_i64, t);
     const bool live = id >= 0 && id < (int64_t)p.vocab && id != p.padding_idx;
     const uint32_t key = live ? (uint32_t)id : p.vocab; // tokens without a gradient sort last
+    if (id >= (int64_t)p.vocab)
+        set_status(p.status, kStatusInvalid);
     return ((uint64_t)key << 32) | t;
+}
+
+// Sets the keys' bits in the bitmap of ids with a token.  A bit that is set
+// already (a common id's) costs a load only; all loads go out together.
+template <int N>
+__device__ __forceinline__ void mark_present(const SortParams &p, const uint32_t (&key)[N])
+{
+    uint32_t w[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        w[j] = key[j] < p.vocab ? __ldcg(p.present + (key[j] >> 5)) : 0xffffffffu;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (!((w[j] >> (key[j] & 31)) & 1u))
+            atomicOr(p.present + (key[j] >> 5), 1u << (key[j] & 31));
+}
+
+// Ranks a warp's 32 x N keys among those of the warp with the same digit, in
+// order (key j of lane l is the warp's key 32 j + l), and leaves the counts of
+// its digits in cnt, which is zero before.  Equal digits of the 32 keys of a
+// step find each other by a ballot per bit (GB300: with match.any the sort of
+// 65536 keys took 49 us).  Keys that are not `in` count for nothing.
+template <int N>
+__device__ __forceinline__ void rank_keys(const uint64_t (&key)[N], const bool (&in)[N], int shift, int bits,
+                                          uint32_t *cnt, uint32_t (&rank)[N])
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t same[N], dig[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        dig[j] = (uint32_t)(key[j] >> (32 + shift)) & ((1u << bits) - 1);
+        same[j] = __ballot_sync(0xffffffffu, in[j]);
+    }
+    for (int b = 0; b < bits; ++b)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const bool one = (dig[j] >> b) & 1u;
+            const uint32_t ones = __ballot_sync(0xffffffffu, one);
+            same[j] &= one ? ones : ~ones;
+        }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const uint32_t below = __popc(same[j] & ((1u << lane) - 1));
+        uint32_t old = 0;
+        if (in[j])
+            old = cnt[dig[j]];
+        rank[j] = old + below;
+        __syncwarp();
+        if (in[j] && below == 0)
+            cnt[dig[j]] = old + __popc(same[j]);
+        __syncwarp();
+    }
+}
+
+// One cluster sorts up to 8192 keys a CTA (PER a thread) in shared memory, in
+// one launch: in every pass each CTA ranks its keys, tells the others its
+// digits' counts, and puts its keys into the shared memory of the CTA where
+// they belong.  Scattered stores and atomics take an SM a cycle or two each,
+// so the keys are spread over as many CTAs as a cluster may have.
+//
+// The bitmap is complete after the first pass's barrier; a flag says so and
+// the dependent kernel may start then, to zero rows while the sort goes on.
+constexpr int kClusterWarps = kClusterThreads / 32;
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v)
+{
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+template <int PER>
+struct ClusterSortSmem {
+    uint64_t keys[2][PER * kClusterThreads];
+    uint32_t cnt[kClusterWarps][1 << kSortMaxBits];
+    uint32_t tot[2][kMaxSortCluster][1 << kSortMaxBits]; // by pass parity: every CTA's counts
+    uint32_t base[1 << kSortMaxBits];
+    uint32_t scan[8];
+};
+
+template <int PER>
+__global__ void __launch_bounds__(kClusterThreads, 1) embed_cluster_sort_kernel(const __grid_constant__ SortParams p)
+{
+    constexpr uint32_t kKeys = PER * kClusterThreads; // of a CTA
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    ClusterSortSmem<PER> &m = *reinterpret_cast<ClusterSortSmem<PER> *>(smem_raw);
+    const int bins = 1 << p.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t C = gridDim.x, rank_c = cluster_ctarank();
+    const uint32_t first = rank_c * kKeys + warp * 32 * PER + lane; // key j: first + 32 j
+    if (p.present && p.zero_present)
+        for (uint32_t i = blockIdx.x * kClusterThreads + threadIdx.x; i < (p.vocab + 31) / 32;
+             i += C * kClusterThreads)
+            p.present[i] = 0;
+    if (rank_c == 0 && threadIdx.x == 0)
+        *p.ready = 0;
+    const bool mark = p.present != nullptr;
+    uint64_t key[PER];
+    {
+        uint32_t k32[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const uint32_t t = first + 32 * j;
+            key[j] = t < p.tokens ? make_pair(p, t) : ~0ull; // past the end: sorts last
+            k32[j] = (uint32_t)(key[j] >> 32);
+        }
+        cluster_sync_all(); // the bitmap is zero
+        if (mark)
+            mark_present<PER>(p, k32);
+    }
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * p.bits;
+        for (int i = lane; i < bins; i += 32)
+            m.cnt[warp][i] = 0;
+        __syncwarp();
+        bool in[PER];
+        uint32_t rank[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            in[j] = true;
+        rank_keys<PER>(key, in, shift, p.bits, m.cnt[warp], rank);
+        __syncthreads();
+        // each warp's first place within the CTA's keys of a digit, and their count to every CTA
+        if (threadIdx.x < bins) {
+            uint32_t at = 0;
+#pragma unroll 8
+            for (int w = 0; w < kClusterWarps; ++w) {
+                const uint32_t c = m.cnt[w][threadIdx.x];
+                m.cnt[w][threadIdx.x] = at;
+                at += c;
+            }
+            const uint32_t to = smem_addr(&m.tot[pass & 1][rank_c][threadIdx.x]);
+            for (uint32_t c = 0; c < C; ++c)
+                st_cluster_u32(map_to_rank(to, c), at);
+        }
+        cluster_sync_all();
+        if (pass == 0) {
+            if (rank_c == 0 && threadIdx.x == 0) {
+                __threadfence();
+                atomicExch(p.ready, 1u);
+            }
+            pdl_launch_dependents();
+        }
+        // a digit's first place of this CTA: all smaller digits, and its own in earlier CTAs
+        uint32_t all = 0, before = 0;
+        if (threadIdx.x < bins)
+            for (uint32_t c = 0; c < C; ++c) {
+                const uint32_t v = m.tot[pass & 1][c][threadIdx.x];
+                all += v;
+                before += c < rank_c ? v : 0;
+            }
+        if (warp < 8) {
+            uint32_t incl = all;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                incl += lane >= o ? v : 0;
+            }
+            if (lane == 31)
+                m.scan[warp] = incl;
+            before += incl - all;
+        }
+        __syncthreads();
+        if (threadIdx.x < bins) {
+            for (int w = 0; w < warp; ++w)
+                before += m.scan[w];
+            m.base[threadIdx.x] = before;
+        }
+        __syncthreads();
+        // to the CTA and place where it belongs
+        const uint32_t out = smem_addr(m.keys[pass & 1]);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const uint32_t d = (uint32_t)(key[j] >> (32 + shift)) & (bins - 1);
+            const uint32_t at = m.base[d] + m.cnt[warp][d] + rank[j];
+            st_cluster_u64(map_to_rank(out + 8 * (at % kKeys), at / kKeys), key[j]);
+        }
+        cluster_sync_all();
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            key[j] = m.keys[pass & 1][warp * 32 * PER + 32 * j + lane];
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        if (first + 32 * j < p.tokens)
+            p.pairs[0][first + 32 * j] = key[j];
 }
 
 __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const __grid_constant__ SortParams p)
@@ -103,16 +302,19 @@ __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const __grid_
         h[i] = 0;
     __syncthreads();
     const uint32_t lo = blockIdx.x * p.tile_keys, hi = min(p.tokens, lo + p.tile_keys);
-    for (uint32_t t = lo + threadIdx.x; t < hi; t += kSortThreads) {
-        const uint64_t pr = make_pair(p, t);
-        const uint32_t key = (uint32_t)(pr >> 32);
-        if (key < p.vocab) {
-            if (!((__ldcg(p.present + (key >> 5)) >> (key & 31)) & 1u)) // a common id is set once
-                atomicOr(p.present + (key >> 5), 1u << (key & 31));
-        } else if (load_id(p.ids, p.ids_i64, t) >= (int64_t)p.vocab) {
-            set_status(p.status, kStatusInvalid);
+    for (uint32_t t0 = lo; t0 < hi; t0 += kSortBlock) {
+        uint32_t key[kSortPerThread];
+#pragma unroll
+        for (int j = 0; j < kSortPerThread; ++j) {
+            const uint32_t t = t0 + j * kSortThreads + threadIdx.x;
+            key[j] = t < hi ? (uint32_t)(make_pair(p, t) >> 32) : 0xffffffffu;
         }
-        atomicAdd(&h[key & (bins - 1)], 1u);
+        if (p.present)
+            mark_present<kSortPerThread>(p, key);
+#pragma unroll
+        for (int j = 0; j < kSortPerThread; ++j)
+            if (key[j] != 0xffffffffu)
+                atomicAdd(&h[key[j] & (bins - 1)], 1u);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < bins; i += kSortThreads)
@@ -131,14 +333,27 @@ __global__ void __launch_bounds__(kSortThreads)
     const uint32_t *hist = p.hist + (size_t)pass * p.tiles * bins;
     uint32_t *next_hist = pass + 1 < p.passes ? p.hist + (size_t)(pass + 1) * p.tiles * bins : nullptr;
 
-    // bins <= kSortThreads: thread d owns digit d
+    // Thread (g, d) sums digit d over every (kSortThreads / bins)-th tile, then
+    // thread d < bins over the g.
+    const int groups = kSortThreads / bins, g = threadIdx.x / bins, gd = threadIdx.x - g * bins;
+    {
+        uint32_t part = 0, part_before = 0;
+#pragma unroll 8
+        for (int t = g; t < p.tiles; t += groups) {
+            const uint32_t c = __ldcg(hist + (size_t)t * bins + gd);
+            part += c;
+            part_before += t < (int)blockIdx.x ? c : 0;
+        }
+        cnt[0][threadIdx.x] = part; // (kWarps rows of 256: two of them serve here)
+        cnt[1][threadIdx.x] = part_before;
+    }
+    __syncthreads();
     uint32_t before = 0, all = 0;
     const int d = threadIdx.x;
     if (d < bins)
-        for (int t = 0; t < p.tiles; ++t) {
-            const uint32_t c = __ldcg(hist + (size_t)t * bins + d);
-            all += c;
-            before += t < (int)blockIdx.x ? c : 0;
+        for (int k = 0; k < groups; ++k) {
+            all += cnt[0][k * bins + d];
+            before += cnt[1][k * bins + d];
         }
     scan[d] = all;
     __syncthreads();
@@ -151,33 +366,23 @@ __global__ void __launch_bounds__(kSortThreads)
     if (d < bins)
         base[d] = scan[d] - all + before;
 
+    __syncthreads();
     const uint32_t lo = blockIdx.x * p.tile_keys, hi = min(p.tokens, lo + p.tile_keys);
     for (uint32_t b0 = lo; b0 < hi; b0 += kSortBlock) {
         for (int i = threadIdx.x; i < kWarps * bins; i += kSortThreads)
             cnt[i / bins][i % bins] = 0;
         __syncthreads();
-        // a warp's keys are contiguous and taken in order; equal digits of
-        // the 32 keys of a step find each other by match
+        // a warp's keys are contiguous and taken in order
         uint64_t key[kSortPerThread];
         uint32_t rank[kSortPerThread];
+        bool in[kSortPerThread];
 #pragma unroll
         for (int j = 0; j < kSortPerThread; ++j) {
             const uint32_t t = b0 + warp * 32 * kSortPerThread + j * 32 + lane;
-            const bool in = t < hi;
-            key[j] = in ? (src ? __ldcg(src + t) : make_pair(p, t)) : ~0ull;
-            // keys past the end get a digit of their own and are not counted
-            const uint32_t dig = in ? (uint32_t)(key[j] >> (32 + shift)) & (bins - 1) : (uint32_t)bins;
-            const uint32_t same = __match_any_sync(0xffffffffu, dig);
-            const uint32_t below = __popc(same & ((1u << lane) - 1));
-            uint32_t old = 0;
-            if (in)
-                old = cnt[warp][dig];
-            rank[j] = old + below;
-            __syncwarp();
-            if (in && below == 0)
-                cnt[warp][dig] = old + __popc(same);
-            __syncwarp();
+            in[j] = t < hi;
+            key[j] = in[j] ? (src ? __ldcg(src + t) : make_pair(p, t)) : ~0ull;
         }
+        rank_keys<kSortPerThread>(key, in, shift, p.bits, cnt[warp], rank);
         __syncthreads();
         if (d < bins) {
             uint32_t at = base[d];
@@ -271,14 +476,27 @@ __device__ void fill_rows(const SegmentParams &p, uint32_t part, uint32_t parts)
 
 __global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid_constant__ SegmentParams p)
 {
-    const uint32_t sums = (uint32_t)p.windows * p.slices;
-    if (blockIdx.x >= sums) {
-        fill_rows(p, blockIdx.x - sums, p.fill_ctas);
+    if (blockIdx.x < (uint32_t)p.fill_ctas) {
+        if (p.ready) {
+            // the bitmap is complete, the sort perhaps not yet
+            const uint64_t t0 = globaltimer_ns();
+            while (ld_acquire_gpu(p.ready) == 0)
+                if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                    if (threadIdx.x == 0)
+                        set_status(p.status, kStatusTimeout);
+                    return;
+                }
+        } else {
+            pdl_wait();
+        }
+        fill_rows(p, blockIdx.x, p.fill_ctas);
         return;
     }
+    pdl_wait();
+    const uint32_t block = blockIdx.x - (uint32_t)p.fill_ctas;
     __shared__ uint32_t ids[kSegMaxWindow + kOverrun + 2], tok[kSegMaxWindow + kOverrun + 2];
     __shared__ int limits[2];
-    const uint32_t w = blockIdx.x / p.slices, slice = blockIdx.x - w * p.slices;
+    const uint32_t w = block / p.slices, slice = block - w * p.slices;
     const uint32_t lo = w * p.window;
     const uint32_t W = min((uint32_t)p.window, p.tokens - lo); // positions of this window
     const uint32_t ext = min(p.tokens - lo, (uint32_t)p.window + kOverrun + 1); // and those looked at
@@ -386,27 +604,57 @@ __global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid
 // which such a run starts adds the following windows' pieces in order.
 __global__ void __launch_bounds__(kSegThreads) embed_join_kernel(const __grid_constant__ SegmentParams p)
 {
+    __shared__ int last;
+    pdl_wait();
     const uint32_t w = blockIdx.x / p.slices, slice = blockIdx.x - w * p.slices;
     if (!(__ldcg(p.meta + 2 * w) & kMetaTrail))
         return;
     const uint32_t id = __ldcg(p.meta + 2 * w + 1);
+    if (id >= p.vocab)
+        return;
+    // the run's pieces are those of windows w + 1 .. w + n
+    uint32_t n = 0;
+    for (;; n += kSegThreads) {
+        if (threadIdx.x == 0)
+            last = kSegThreads;
+        __syncthreads();
+        const uint32_t u = w + 1 + n + threadIdx.x;
+        if (u >= (uint32_t)p.windows || !(__ldcg(p.meta + 2 * u) & kMetaLeadOn))
+            atomicMin(&last, (int)threadIdx.x);
+        __syncthreads();
+        const int l = last;
+        __syncthreads();
+        if (l < kSegThreads) {
+            n += l + 1;
+            break;
+        }
+    }
     const int H = 8 * p.nvec;
     const int col = (int)slice * kSegCols + 8 * (int)threadIdx.x;
-    if (col >= H || id >= p.vocab)
+    if (col >= H)
         return;
-    const float *t = p.partials + ((size_t)w * 2 + 1) * H + col;
-    float s[8];
+    const float4 *t = reinterpret_cast<const float4 *>(p.partials + ((size_t)w * 2 + 1) * H + col);
+    float4 a = __ldcg(t), b = __ldcg(t + 1);
+    float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const float4 *piece = reinterpret_cast<const float4 *>(p.partials + (size_t)(w + 1) * 2 * H + col);
+    const size_t step = (size_t)2 * H / 4;
+    for (uint32_t u = 0; u < n; u += 4) {
+        float4 v[4][2];
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-        s[q] = __ldcg(t + q);
-    for (uint32_t u = w + 1; u < (uint32_t)p.windows; ++u) {
-        const uint32_t f = __ldcg(p.meta + 2 * u);
-        const float *a = p.partials + (size_t)u * 2 * H + col;
+        for (int k = 0; k < 4; ++k)
+            if (u + k < n) {
+                v[k][0] = __ldcg(piece + (size_t)(u + k) * step);
+                v[k][1] = __ldcg(piece + (size_t)(u + k) * step + 1);
+            }
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            s[q] = __fadd_rn(s[q], __ldcg(a + q));
-        if (!(f & kMetaLeadOn))
-            break;
+        for (int k = 0; k < 4; ++k)
+            if (u + k < n) {
+                const float f[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                                    v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    s[q] = __fadd_rn(s[q], f[q]);
+            }
     }
     store_row8(p, id, col, s);
 }
@@ -416,10 +664,52 @@ __global__ void __launch_bounds__(kSegThreads) embed_join_kernel(const __grid_co
 cudaError_t launch_embed_fwd(const EmbedFwdParams &p, cudaStream_t stream)
 {
     const uint64_t items = (uint64_t)p.tokens * ((p.nvec + 127) / 128);
+    // an item a warp: CTAs that come and go keep more rows on their way than
+    // resident ones in a loop (GB300, T = 65536, H = 5120: 144 against 164 us)
     const uint64_t want = (items + kEmbedThreads / 32 - 1) / (kEmbedThreads / 32);
-    const int ctas = (int)(want < 152 * 8 * 8 ? want : 152 * 8 * 8);
-    embed_fwd_kernel<<<ctas, kEmbedThreads, 0, stream>>>(p);
+    const int ctas = (int)(want < (1u << 30) ? want : (1u << 30));
+    if (p.table_f32)
+        embed_fwd_kernel<true><<<ctas, kEmbedThreads, 0, stream>>>(p);
+    else
+        embed_fwd_kernel<false><<<ctas, kEmbedThreads, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+cudaError_t ensure_smem_attr(const void *kernel, size_t smem);
+
+template <int PER>
+static cudaError_t launch_cluster_sort(const SortParams &p, int ctas, cudaStream_t stream)
+{
+    const void *kern = (const void *)embed_cluster_sort_kernel<PER>;
+    cudaError_t e = ensure_smem_attr(kern, sizeof(ClusterSortSmem<PER>));
+    if (e == cudaSuccess && ctas > 8)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kClusterThreads);
+    cfg.dynamicSmemBytes = sizeof(ClusterSortSmem<PER>);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, embed_cluster_sort_kernel<PER>, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+cudaError_t launch_embed_cluster_sort(const SortParams &p, int ctas, cudaStream_t stream)
+{
+    const uint32_t per = (p.tokens + ctas * kClusterThreads - 1) / (ctas * kClusterThreads);
+    return per <= 1   ? launch_cluster_sort<1>(p, ctas, stream)
+           : per <= 2 ? launch_cluster_sort<2>(p, ctas, stream)
+           : per <= 4 ? launch_cluster_sort<4>(p, ctas, stream)
+           : per <= 8 ? launch_cluster_sort<8>(p, ctas, stream)
+                      : cudaErrorInvalidValue;
 }
 
 cudaError_t launch_embed_sort(const SortParams &p, uint64_t **sorted, cudaStream_t stream)
@@ -435,16 +725,29 @@ cudaError_t launch_embed_sort(const SortParams &p, uint64_t **sorted, cudaStream
     return cudaGetLastError();
 }
 
+static cudaError_t launch_dependent(void (*kern)(SegmentParams), const SegmentParams &p, int ctas, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kSegThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 cudaError_t launch_embed_segments(const SegmentParams &p, cudaStream_t stream)
 {
-    embed_segment_kernel<<<p.windows * p.slices + p.fill_ctas, kSegThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(embed_segment_kernel, p, p.windows * p.slices + p.fill_ctas, stream);
 }
 
 cudaError_t launch_embed_join(const SegmentParams &p, cudaStream_t stream)
 {
-    embed_join_kernel<<<p.windows * p.slices, kSegThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(embed_join_kernel, p, p.windows * p.slices, stream);
 }
 
 // Device address of the status word, looked up once per device.

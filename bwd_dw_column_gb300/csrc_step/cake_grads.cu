@@ -44,21 +44,35 @@ __device__ __forceinline__ float load_one(const void *src, int64_t i, bool f32)
                : __uint_as_float((uint32_t)static_cast<const uint16_t *>(src)[i] << 16);
 }
 
-// This thread's values of a chunk: 4 groups of 8, group u at value
-// u * 8 * kGradThreads + 8 * thread of the chunk; missing ones are zero.
+// This thread's values of a chunk; missing ones are zero.  A whole aligned
+// chunk comes in 16-byte loads: 4 groups of 8 BF16 values, group u at value
+// 8 (u * kGradThreads + thread), or 8 groups of 4 FP32 values, group u at
+// 4 (u * kGradThreads + thread).  QUADS: BF16 values in 8 groups of 4 as well,
+// so that FP32 outputs are written in whole lines.
 // (Plain loads: clipping in place writes what it has read.)
+template <bool QUADS>
 __device__ __forceinline__ void load_chunk(const GradDesc &d, int64_t first, float (&v)[kPerThread])
 {
     const bool f32 = d.flags & kGradSrcF32;
     const int64_t left = d.count - first;
     if ((d.flags & kGradVector) && left >= kGradChunk) {
-        if (f32) {
+        if (QUADS && !f32 && (d.flags & kGradDstF32)) {
+            const uint2 *s = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(d.src) + first);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint2 a = s[u * kGradThreads + threadIdx.x];
+                v[u * 4] = bf16lo(a.x);
+                v[u * 4 + 1] = bf16hi(a.x);
+                v[u * 4 + 2] = bf16lo(a.y);
+                v[u * 4 + 3] = bf16hi(a.y);
+            }
+        } else if (f32) {
             const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(d.src) + first);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float4 a = s[u * 2 * kGradThreads + k * kGradThreads + threadIdx.x];
+                    const float4 a = s[(u * 2 + k) * kGradThreads + threadIdx.x];
                     v[u * 8 + k * 4 + 0] = a.x;
                     v[u * 8 + k * 4 + 1] = a.y;
                     v[u * 8 + k * 4 + 2] = a.z;
@@ -127,7 +141,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const __grid_c
         i = find_tensor(p, c, i);
         const GradDesc &d = p.t[i];
         float v[kPerThread];
-        load_chunk(d, (int64_t)(c - d.chunk0) * kGradChunk, v);
+        load_chunk<false>(d, (int64_t)(c - d.chunk0) * kGradChunk, v);
         acc += chunk_sumsq(v);
     }
     acc = cta_sum(acc);
@@ -176,31 +190,30 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
         const GradDesc &d = p.t[i];
         const int64_t first = (int64_t)(c - d.chunk0) * kGradChunk;
         float v[kPerThread];
-        load_chunk(d, first, v);
+        load_chunk<true>(d, first, v);
         const bool f32 = d.flags & kGradSrcF32, o32 = d.flags & kGradDstF32;
         if ((d.flags & kGradVector) && d.count - first >= kGradChunk) {
-            // v[u * 8 ...]: 8 consecutive values of a BF16 source; two groups of 4 of an FP32 one
+            if (o32) { // 8 groups of 4, from either type
+                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(d.dst) + first);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                float w[8];
+                for (int u = 0; u < 8; ++u)
+                    o[u * kGradThreads + threadIdx.x] =
+                        make_float4(__fmul_rn(v[4 * u], coef), __fmul_rn(v[4 * u + 1], coef),
+                                    __fmul_rn(v[4 * u + 2], coef), __fmul_rn(v[4 * u + 3], coef));
+            } else if (f32) {
+                uint2 *o = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(d.dst) + first);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    w[k] = __fmul_rn(v[u * 8 + k], coef);
-                if (o32) {
-                    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(d.dst) + first);
+                for (int u = 0; u < 8; ++u)
+                    o[u * kGradThreads + threadIdx.x] =
+                        make_uint2(pack_bf16(__fmul_rn(v[4 * u], coef), __fmul_rn(v[4 * u + 1], coef)),
+                                   pack_bf16(__fmul_rn(v[4 * u + 2], coef), __fmul_rn(v[4 * u + 3], coef)));
+            } else {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int at = f32 ? u * 2 * kGradThreads + k * kGradThreads + threadIdx.x
-                                           : (u * kGradThreads + threadIdx.x) * 2 + k;
-                        o[at] = make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-                    }
-                } else if (f32) {
-                    uint2 *o = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(d.dst) + first);
+                for (int u = 0; u < 4; ++u) {
+                    float w[8];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        o[u * 2 * kGradThreads + k * kGradThreads + threadIdx.x] =
-                            make_uint2(pack_bf16(w[4 * k], w[4 * k + 1]), pack_bf16(w[4 * k + 2], w[4 * k + 3]));
-                } else {
+                    for (int k = 0; k < 8; ++k)
+                        w[k] = __fmul_rn(v[u * 8 + k], coef);
                     reinterpret_cast<uint4 *>(static_cast<uint16_t *>(d.dst) + first)[u * kGradThreads + threadIdx.x] =
                         pack8(w);
                 }

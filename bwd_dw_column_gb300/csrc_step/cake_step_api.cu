@@ -434,6 +434,7 @@ cake_status check_embedding(const void *ids, int ids_int64, int64_t tokens, cons
 // Sizes of a gradient call; they depend on the shape alone.
 struct EmbedPlan {
     int bits, passes, tiles, window, windows, slices;
+    int cluster; // CTAs of the one-launch sort; 0: a launch per pass
     uint32_t tile_keys;
     size_t present_bytes, hist_bytes, pairs_bytes, part_bytes, meta_bytes, total;
 };
@@ -446,6 +447,10 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int64_t H)
         ++key_bits;
     e.passes = (key_bits + kSortMaxBits - 1) / kSortMaxBits;
     e.bits = (key_bits + e.passes - 1) / e.passes;
+    e.cluster = 0;
+    if (T <= kClusterSortKeys)
+        for (e.cluster = 1; e.cluster < kMaxSortCluster && (int64_t)e.cluster * kClusterThreads < T;)
+            e.cluster *= 2;
     const int64_t per = ((T + kSortMaxTiles - 1) / kSortMaxTiles + kSortBlock - 1) / kSortBlock * kSortBlock;
     e.tile_keys = (uint32_t)per;
     e.tiles = (int)((T + per - 1) / per);
@@ -454,8 +459,8 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int64_t H)
     while (e.window > 32 && ((T + e.window - 1) / e.window) * e.slices < 152 * 8)
         e.window /= 2;
     e.windows = (int)((T + e.window - 1) / e.window);
-    e.present_bytes = align256(((size_t)V + 31) / 32 * 4);
-    e.hist_bytes = align256((size_t)e.passes * e.tiles * ((size_t)4 << e.bits));
+    e.present_bytes = 256 + align256(((size_t)V + 31) / 32 * 4); // a flag, then the bitmap
+    e.hist_bytes = e.cluster ? 0 : align256((size_t)e.passes * e.tiles * ((size_t)4 << e.bits));
     e.pairs_bytes = align256((size_t)T * 8);
     e.part_bytes = align256((size_t)e.windows * 2 * H * 4);
     e.meta_bytes = align256((size_t)e.windows * 8);
@@ -533,15 +538,20 @@ extern "C" cake_status cake_embedding_bwd(const cake_tensor *dy, const void *ids
     q.tiles = e.tiles;
     q.passes = e.passes;
     q.bits = e.bits;
-    q.present = reinterpret_cast<uint32_t *>(ws);
+    q.ready = reinterpret_cast<uint32_t *>(ws);
+    q.present = q.ready + 64;
     q.hist = reinterpret_cast<uint32_t *>(ws + e.present_bytes);
     uint8_t *at = ws + e.present_bytes + e.hist_bytes;
     q.pairs[0] = reinterpret_cast<uint64_t *>(at);
     q.pairs[1] = reinterpret_cast<uint64_t *>(at + e.pairs_bytes);
-    cudaError_t r = cudaMemsetAsync(ws, 0, e.present_bytes + e.hist_bytes, s);
-    uint64_t *sorted = nullptr;
+    // a small bitmap is zeroed by the sort itself
+    q.zero_present = e.cluster && (accumulate || e.present_bytes <= (size_t)32768 * e.cluster);
+    if (accumulate)
+        q.present = nullptr; // no row is to be zeroed
+    uint64_t *sorted = q.pairs[0];
+    cudaError_t r = q.zero_present ? cudaSuccess : cudaMemsetAsync(ws, 0, e.present_bytes + e.hist_bytes, s);
     if (r == cudaSuccess)
-        r = launch_embed_sort(q, &sorted, s);
+        r = e.cluster ? launch_embed_cluster_sort(q, e.cluster, s) : launch_embed_sort(q, &sorted, s);
     if (r != cudaSuccess)
         return CAKE_ERR_CUDA;
     SegmentParams g{};
@@ -560,7 +570,9 @@ extern "C" cake_status cake_embedding_bwd(const cake_tensor *dy, const void *ids
     g.dtable_stride = dtable_stride;
     g.accumulate = accumulate != 0;
     g.present = q.present;
-    g.fill_ctas = accumulate ? 0 : (int)std::min<int64_t>((vocab + 3) / 4, 152 * 16);
+    g.fill_ctas = accumulate ? 0 : (int)std::min<int64_t>((vocab + 3) / 4, 1 << 20);
+    g.ready = e.cluster && !accumulate ? q.ready : nullptr;
+    g.status = q.status;
     g.partials = reinterpret_cast<float *>(at + 2 * e.pairs_bytes);
     g.meta = reinterpret_cast<uint32_t *>(at + 2 * e.pairs_bytes + e.part_bytes);
     r = launch_embed_segments(g, s);

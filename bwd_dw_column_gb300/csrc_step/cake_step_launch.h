@@ -129,7 +129,9 @@ constexpr int kSortPerThread = 8;
 constexpr int kSortBlock = kSortThreads * kSortPerThread; // keys ranked together
 constexpr int kSortMaxTiles = 304;
 constexpr int kSortMaxBits = 8;                            // bits of a pass
-constexpr int kSortMaxPasses = 4;
+constexpr int kClusterThreads = 1024;                      // of each CTA of the one-launch sort
+constexpr int kMaxSortCluster = 16;
+constexpr int64_t kClusterSortKeys = 8 * kClusterThreads * kMaxSortCluster;
 
 struct SortParams {
     const void *ids;
@@ -143,7 +145,9 @@ struct SortParams {
     int bits;              // of each pass
     uint64_t *pairs[2];    // (key << 32) | token, ping-pong
     uint32_t *hist;        // [passes][tiles][1 << bits], zero before the first pass
-    uint32_t *present;     // bitmap of ids with a token, zero before the first pass
+    uint32_t *present;     // bitmap of ids with a token, zero before the first pass (nullptr: not wanted)
+    int zero_present;      // one-launch sort: zero the bitmap itself
+    uint32_t *ready;       // one-launch sort: set to 1 once the bitmap is complete
     int *status;
 };
 
@@ -162,12 +166,15 @@ struct SegmentParams {
     int64_t dtable_stride;
     int accumulate;
     const uint32_t *present;
-    int fill_ctas;         // CTAs after the sums' that zero the rows without a token
+    int fill_ctas;         // CTAs before the sums' that zero the rows without a token
+    const uint32_t *ready; // those start at this flag; nullptr: after the sort
+    int *status;
     float *partials;       // [windows][2][H]: sums of the leading and the trailing piece
     uint32_t *meta;        // [windows][2]: flags and the trailing piece's id
 };
 
 cudaError_t launch_embed_fwd(const EmbedFwdParams &p, cudaStream_t stream);
+cudaError_t launch_embed_cluster_sort(const SortParams &p, int ctas, cudaStream_t stream);
 cudaError_t launch_embed_sort(const SortParams &p, uint64_t **sorted, cudaStream_t stream);
 cudaError_t launch_embed_segments(const SegmentParams &p, cudaStream_t stream);
 cudaError_t launch_embed_join(const SegmentParams &p, cudaStream_t stream);
