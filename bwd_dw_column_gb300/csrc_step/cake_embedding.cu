@@ -422,38 +422,52 @@ constexpr int kSegThreads = 128;                // 8 columns a thread
 constexpr int kSegCols = 8 * kSegThreads;
 constexpr int kSegMaxWindow = 128;
 constexpr int kOverrun = 32;
-constexpr int kSegBatch = 8;                    // rows in flight
 // meta[w][0]
 constexpr uint32_t kMetaLead = 1;   // the window starts with a piece of an earlier window's run: partial 0
 constexpr uint32_t kMetaLeadOn = 2; // ... that goes on in the next window
 constexpr uint32_t kMetaTrail = 4;  // the window's last run goes on in the next window: partial 1
 
-__device__ __forceinline__ void store_row8(const SegmentParams &p, uint32_t id, int col, const float (&s)[8])
+// Eight values of row id of dtable as they were before.
+__device__ __forceinline__ void load_row8(const SegmentParams &p, uint32_t id, int col, uint4 (&a)[2])
+{
+    if (p.dtable_f32) {
+        const uint4 *o = reinterpret_cast<const uint4 *>(static_cast<const float *>(p.dtable) +
+                                                         (int64_t)id * p.dtable_stride + col);
+        a[0] = o[0];
+        a[1] = o[1];
+    } else {
+        a[0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.dtable) +
+                                                (int64_t)id * p.dtable_stride + col);
+    }
+}
+
+// Row id of dtable: scale * s [+ what it was].
+template <bool ACC>
+__device__ __forceinline__ void store_row8(const SegmentParams &p, uint32_t id, int col, const float (&s)[8],
+                                           const uint4 (&was)[2])
 {
     float v[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
         v[q] = __fmul_rn(s[q], p.scale);
     if (p.dtable_f32) {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.dtable) + (int64_t)id * p.dtable_stride + col);
-        if (p.accumulate) {
-            const float4 a = o[0], b = o[1];
-            v[0] = __fadd_rn(v[0], a.x), v[1] = __fadd_rn(v[1], a.y), v[2] = __fadd_rn(v[2], a.z);
-            v[3] = __fadd_rn(v[3], a.w), v[4] = __fadd_rn(v[4], b.x), v[5] = __fadd_rn(v[5], b.y);
-            v[6] = __fadd_rn(v[6], b.z), v[7] = __fadd_rn(v[7], b.w);
+        if (ACC) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = __fadd_rn(v[q], __uint_as_float(word(was[q >> 2], q & 3)));
         }
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.dtable) + (int64_t)id * p.dtable_stride + col);
         o[0] = make_float4(v[0], v[1], v[2], v[3]);
         o[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dtable) + (int64_t)id * p.dtable_stride + col);
-        if (p.accumulate) {
+        if (ACC) {
             float a[8];
-            unpack8(*o, a);
+            unpack8(was[0], a);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
                 v[q] = __fadd_rn(v[q], a[q]);
         }
-        *o = pack8(v);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dtable) + (int64_t)id * p.dtable_stride + col) = pack8(v);
     }
 }
 
@@ -474,8 +488,13 @@ __device__ void fill_rows(const SegmentParams &p, uint32_t part, uint32_t parts)
     }
 }
 
+// ACC: adds to dtable.  The rows that it adds to are loaded together with the
+// rows of dy, half as many at a time (GB300, T = 65536, H = 4096: a load at
+// each run's end instead took 172 us).
+template <bool ACC>
 __global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid_constant__ SegmentParams p)
 {
+    constexpr int kSegBatch = ACC ? 4 : 8; // rows in flight
     if (blockIdx.x < (uint32_t)p.fill_ctas) {
         if (p.ready) {
             // the bitmap is complete, the sort perhaps not yet
@@ -561,12 +580,16 @@ __global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     float *lead_part = p.partials + ((size_t)w * 2) * 8 * p.nvec + col, *trail_part = lead_part + 8 * p.nvec;
     for (uint32_t b = first; b < end; b += kSegBatch) {
-        uint4 r[kSegBatch];
+        uint4 r[kSegBatch], was[kSegBatch][2];
 #pragma unroll
         for (int k = 0; k < kSegBatch; ++k) {
-            r[k] = make_uint4(0, 0, 0, 0);
-            if (b + k < end && ids[1 + b + k] < p.vocab)
-                r[k] = __ldcs(reinterpret_cast<const uint4 *>(p.dy + (int64_t)tok[1 + b + k] * p.dy_stride + col));
+            r[k] = was[k][0] = was[k][1] = make_uint4(0, 0, 0, 0);
+            const uint32_t i = b + k;
+            if (i < end && ids[1 + i] < p.vocab) {
+                r[k] = __ldcs(reinterpret_cast<const uint4 *>(p.dy + (int64_t)tok[1 + i] * p.dy_stride + col));
+                if (ACC && (i + 1 == end || ids[2 + i] != ids[1 + i]))
+                    load_row8(p, ids[1 + i], col, was[k]);
+            }
         }
 #pragma unroll
         for (int k = 0; k < kSegBatch; ++k) {
@@ -589,7 +612,7 @@ __global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid
                         o[0] = make_float4(s[0], s[1], s[2], s[3]);
                         o[1] = make_float4(s[4], s[5], s[6], s[7]);
                     } else {
-                        store_row8(p, id, col, s);
+                        store_row8<ACC>(p, id, col, s, was[k]);
                     }
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
@@ -656,7 +679,13 @@ __global__ void __launch_bounds__(kSegThreads) embed_join_kernel(const __grid_co
                     s[q] = __fadd_rn(s[q], f[q]);
             }
     }
-    store_row8(p, id, col, s);
+    uint4 was[2] = {};
+    if (p.accumulate) {
+        load_row8(p, id, col, was);
+        store_row8<true>(p, id, col, s, was);
+    } else {
+        store_row8<false>(p, id, col, s, was);
+    }
 }
 
 // ------------------------------------------------------------------ launch
@@ -742,7 +771,8 @@ static cudaError_t launch_dependent(void (*kern)(SegmentParams), const SegmentPa
 
 cudaError_t launch_embed_segments(const SegmentParams &p, cudaStream_t stream)
 {
-    return launch_dependent(embed_segment_kernel, p, p.windows * p.slices + p.fill_ctas, stream);
+    return launch_dependent(p.accumulate ? embed_segment_kernel<true> : embed_segment_kernel<false>, p,
+                            p.windows * p.slices + p.fill_ctas, stream);
 }
 
 cudaError_t launch_embed_join(const SegmentParams &p, cudaStream_t stream)
