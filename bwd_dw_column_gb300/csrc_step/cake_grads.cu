@@ -24,10 +24,10 @@ namespace cake {
 constexpr int kGradWarps = kGradThreads / 32;
 constexpr int kPerThread = kGradChunk / kGradThreads; // 32 values
 
+// The last of tensors [lo, hi] whose first chunk is <= chunk.
 template <int N>
-__device__ __forceinline__ int find_tensor(const GradParams<N> &p, uint32_t chunk, int from)
+__device__ __forceinline__ int find_tensor(const GradParams<N> &p, uint32_t chunk, int lo, int hi)
 {
-    int lo = from, hi = p.n - 1; // the last tensor whose first chunk is <= chunk
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (p.t[mid].chunk0 <= chunk)
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const __grid_c
     double acc = 0.0;
     int i = 0;
     for (uint32_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
-        i = find_tensor(p, c, i);
+        i = find_tensor(p, c, i, p.n - 1);
         const GradDesc &d = p.t[i];
         float v[kPerThread];
         load_chunk<false>(d, (int64_t)(c - d.chunk0) * kGradChunk, v);
@@ -184,9 +184,11 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
     const float coef = q >= 1.0 ? 1.0f : (float)q;
     if (p.in_place && coef == 1.0f)
         return;
-    int i = 0;
-    for (uint32_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
-        i = find_tensor(p, c, i);
+    // last chunks first: L2 still holds what the sum has read last
+    int i = p.n - 1;
+    for (uint32_t k = blockIdx.x; k < p.chunks; k += gridDim.x) {
+        const uint32_t c = p.chunks - 1 - k;
+        i = find_tensor(p, c, 0, i);
         const GradDesc &d = p.t[i];
         const int64_t first = (int64_t)(c - d.chunk0) * kGradChunk;
         float v[kPerThread];

@@ -78,7 +78,7 @@ constexpr int kGradMaxTensors = 1000;
 constexpr int kGradSomeTensors = 256;
 constexpr int kGradFewTensors = 32;
 constexpr int kGradThreads = 256;
-constexpr int kGradCtas = 152 * 4;
+constexpr int kGradCtas = 152 * 8;
 
 struct GradDesc {
     const void *src;

@@ -96,17 +96,15 @@ class _On:
 def _on(stream, *tensors):
     """Context of a call: every tensor (None: left out) on one CUDA device, which becomes
     the current one, with `stream` (None: its current stream) the current stream."""
-    dev = -2
-    for t in tensors:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d != dev:
-            if d < 0:
-                raise ValueError("every tensor must be on a CUDA device (no CPU path)")
-            if dev != -2:
-                raise ValueError("every tensor must be on the same device")
-            dev = d
+    return _on_devices(stream, {t.get_device() for t in tensors if t is not None})
+
+
+def _on_devices(stream, devices):
+    if -1 in devices:
+        raise ValueError("every tensor must be on a CUDA device (no CPU path)")
+    if len(devices) != 1:
+        raise ValueError("every tensor must be on the same device")
+    dev, = devices
     if stream is None:
         if torch.cuda.current_device() == dev:
             return _here
@@ -350,6 +348,7 @@ def _dense(t: torch.Tensor) -> bool:
 
 
 _GRAD_DTYPES = {torch.bfloat16: CAKE_BF16, torch.float32: CAKE_FP32}
+_T = torch.Tensor  # its methods, mapped over lists of hundreds of tensors
 
 
 def _tensors(grads, what):
@@ -358,10 +357,20 @@ def _tensors(grads, what):
         types = array("i", [_GRAD_DTYPES[t.dtype] for t in grads])
     except KeyError as e:
         raise TypeError(f"{what} are BF16 or FP32, got {e.args[0]}") from None
-    for t in grads:
-        if not t.is_contiguous() and not _dense(t):
-            raise ValueError(f"{what} must fill one block of memory each (strides {t.stride()} of {tuple(t.shape)})")
-    return array("Q", [t.data_ptr() for t in grads]), array("q", [t.numel() for t in grads]), types
+    if not all(map(_T.is_contiguous, grads)):
+        for t in grads:
+            if not _dense(t):
+                raise ValueError(
+                    f"{what} must fill one block of memory each (strides {t.stride()} of {tuple(t.shape)})")
+    return array("Q", map(_T.data_ptr, grads)), array("q", map(_T.numel, grads)), types
+
+
+def _same_layouts(grads, outs):
+    if [o.shape for o in outs] != [g.shape for g in grads]:
+        return False
+    if all(map(_T.is_contiguous, grads)) and all(map(_T.is_contiguous, outs)):
+        return True
+    return all(o.stride() == g.stride() or (o.is_contiguous() and g.is_contiguous()) for g, o in zip(grads, outs))
 
 
 def _addr(a):
@@ -376,29 +385,32 @@ def cake_grad_norm_workspace_size(n: int) -> int:
 
 def _grad_call(grads, outs, clip, max_norm, eps, norm, workspace, stream):
     lib = load_library()
-    with _on(stream, *grads, *(outs or ()), norm, workspace):
+    if not grads and norm is None:
+        raise ValueError("no gradients: give the norm's tensor")
+    devices = set(map(_T.get_device, grads))
+    devices.update(t.get_device() for t in (norm, workspace) if t is not None)
+    if outs is not None:
+        devices.update(map(_T.get_device, outs))
+    with _on_devices(stream, devices):
         ptrs, counts, types = _tensors(grads, "gradients")
-        n = len(ptrs)
-        if not grads and norm is None:
-            raise ValueError("no gradients: give the norm's tensor")
+        n = len(grads)
         if norm is None:
             norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
-        elif norm.dtype != torch.float32 or norm.numel() != 1:
+        elif norm.dtype is not torch.float32 or norm.numel() != 1:
             raise ValueError("norm must be an FP32 tensor of one element")
-        workspace, ws_at, ws_bytes = _workspace(workspace, cake_grad_norm_workspace_size(n), norm.device)
-        ws = (ws_at, ws_bytes, _current())
+        workspace, ws, ws_bytes = _workspace(workspace, cake_grad_norm_workspace_size(n), norm.device)
         if not clip:
-            st = lib.cake_grad_norm(_addr(ptrs), _addr(counts), _addr(types), n, norm.data_ptr(), *ws)
+            st = lib.cake_grad_norm(_addr(ptrs), _addr(counts), _addr(types), n, norm.data_ptr(), ws, ws_bytes,
+                                    _current())
             _check(st, "cake_grad_norm")
             return norm
-        optrs = otypes = None
-        if outs is not None:
-            for g, o in zip(grads, outs):
-                if o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
-                    raise ValueError("an output must have its gradient's shape and order of dimensions")
+        optrs = otypes = ()
+        if outs:
+            if not _same_layouts(grads, outs):
+                raise ValueError("an output must have its gradient's shape and order of dimensions")
             optrs, _, otypes = _tensors(outs, "outputs")
-        st = lib.cake_grad_clip(_addr(ptrs), _addr(counts), _addr(types), _addr(optrs) if outs else None,
-                                _addr(otypes) if outs else None, n, max_norm, eps, norm.data_ptr(), *ws)
+        st = lib.cake_grad_clip(_addr(ptrs), _addr(counts), _addr(types), _addr(optrs), _addr(otypes), n, max_norm,
+                                eps, norm.data_ptr(), ws, ws_bytes, _current())
         _check(st, "cake_grad_clip")
         return norm
 

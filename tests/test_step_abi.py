@@ -100,6 +100,12 @@ def test_sandwich_bwd_refusals(cake):
     assert cake.cake_sandwich_bwd_workspace_size((4, 1, 64)) > 0
 
 
+def test_every_width_has_a_backward_plan(cake):
+    for H in range(8, 8193, 8):
+        for T in (1, 151, 100_000):
+            assert cake.cake_sandwich_bwd_workspace_size((T, 1, H)) >= 16 * H, (T, H)
+
+
 def grads(cake, ptrs, counts, types, outs=None, otypes=None, max_norm=1.0, eps=1e-6, norm=A, ws=A, n_ws=1 << 30,
           clip=True):
     n = len(ptrs)

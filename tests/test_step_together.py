@@ -1,0 +1,123 @@
+"""The training-step operators used together, as a training loop uses them:
+embedding -> two blocks, each followed by a sandwich norm -> gradients ->
+clipping.  Every operator is held to FP64 in its own test; here the autograd
+functions' run must give the bits of the same run written out with the entry
+points, eagerly and replayed from a CUDA graph, and a few optimizer steps have
+to run."""
+import pytest
+import torch
+
+DEV = torch.device("cuda:0") if torch.cuda.is_available() else None
+BF16 = torch.bfloat16
+pytestmark = pytest.mark.gpu
+V, H, T = 500, 640, 300
+PAD = 7
+
+
+@pytest.fixture(scope="module")
+def cake():
+    import __graft_entry__
+    __graft_entry__.build()
+    import bwd_dw_column_gb300 as cake
+    yield cake
+    assert cake.cake_rmsnorm_device_status() == 0
+
+
+def make():
+    g = torch.Generator().manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    params = {"table": r(V, H).mul(0.1), "w1": r(H, H).div(H ** 0.5).to(BF16), "w2": r(H, H).div(H ** 0.5).to(BF16),
+              "post1": 1 + 0.1 * r(H), "pre1": (1 + 0.1 * r(H)).to(BF16), "post2": (1 + 0.1 * r(H)).to(BF16),
+              "pre2": 1 + 0.1 * r(H), "gate": torch.sigmoid(r(T))}
+    ids = torch.randint(0, V, (T,), generator=g)
+    ids[::9], ids[5] = PAD, -1
+    return {k: v.to(DEV).requires_grad_() for k, v in params.items()}, ids.to(DEV), r(T, H).to(BF16).to(DEV)
+
+
+def forward(cake, p, ids):
+    x0 = cake.cake_embedding(ids, p["table"], 2.0, padding_idx=PAD)
+    z1 = x0 @ p["w1"]
+    y1, h1 = cake.cake_sandwich_norm(z1, x0, p["post1"], p["pre1"], 1e-6, p["gate"], 0.5)
+    z2 = y1 @ p["w2"]
+    return cake.cake_sandwich_norm(z2, h1, p["post2"], p["pre2"])
+
+
+def written_out(cake, p, ids, dy):
+    p = {k: v.detach() for k, v in p.items()}
+    x0 = cake.cake_embedding_fwd(ids, p["table"], 2.0)
+    z1 = x0 @ p["w1"]
+    y1, h1, a1, b1 = cake.cake_sandwich_fwd(z1, x0, p["post1"], p["pre1"], 1e-6, p["gate"], 0.5)
+    z2 = y1 @ p["w2"]
+    y2, h2, a2, b2 = cake.cake_sandwich_fwd(z2, h1, p["post2"], p["pre2"])
+    dh1, dz2, dpost2, dpre2, _ = cake.cake_sandwich_bwd(dy, h2, z2, a2, b2, p["post2"], p["pre2"])
+    dy1 = dz2 @ p["w2"].t()
+    dx0, dz1, dpost1, dpre1, dgate = cake.cake_sandwich_bwd(dy1, h1, z1, a1, b1, p["post1"], p["pre1"], dh1, p["gate"],
+                                                            0.5)
+    dx0 = dx0 + dz1 @ p["w1"].t()
+    return y2, {"table": cake.cake_embedding_bwd(dx0, ids, V, 2.0, PAD), "w1": x0.t() @ dz1, "w2": y1.t() @ dz2,
+                "post1": dpost1, "pre1": dpre1.to(BF16), "post2": dpost2.to(BF16), "pre2": dpre2, "gate": dgate}
+
+
+def test_autograd_run_gives_the_written_out_bits(cake):
+    p, ids, dy = make()
+    y, _ = forward(cake, p, ids)
+    y.backward(dy)
+    y2, want = written_out(cake, p, ids, dy)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2)
+    for k, v in p.items():
+        assert v.grad.dtype == v.dtype and torch.equal(v.grad, want[k]), k
+    assert not p["table"].grad[PAD].any()
+    # clipping the run's gradients, in place and into FP32 buffers
+    grads = [v.grad for v in p.values()]
+    into = [torch.empty(g.shape, dtype=torch.float32, device=DEV) for g in grads]
+    norm = float(cake.cake_grad_norm(grads))
+    assert norm > 0
+    n1 = cake.cake_clip_grad_norm(grads, norm / 2, out=into)
+    n2 = cake.cake_clip_grad_norm(grads, norm / 2)
+    assert float(n1) == float(n2) == norm
+    for g, o in zip(grads, into):
+        assert torch.equal(g, o.to(g.dtype))
+
+
+def test_step_in_a_graph(cake):
+    p, ids, dy = make()
+    opt = torch.optim.SGD(list(p.values()), lr=0.05)
+
+    def step():
+        opt.zero_grad(set_to_none=True)
+        y, _ = forward(cake, p, ids)
+        y.backward(dy)
+        norm = cake.cake_clip_grad_norm([v.grad for v in p.values()], 1.0)
+        opt.step()
+        return norm
+
+    start = {k: v.detach().clone() for k, v in p.items()}
+    eager = [float(step()) for _ in range(4)]
+    after = {k: v.detach().clone() for k, v in p.items()}
+    assert all(n > 0 for n in eager)
+
+    def reset():
+        with torch.no_grad():
+            for k, v in p.items():
+                v.copy_(start[k])
+
+    # no eager graph of these leaves is alive any more, and the warm-up runs on the capturing side
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    reset()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm = step()
+    reset()
+    replayed = []
+    for _ in range(4):
+        graph.replay()
+        replayed.append(float(norm))
+    torch.cuda.synchronize()
+    assert replayed == eager
+    for k, v in p.items():
+        assert torch.equal(v, after[k]), k
