@@ -656,8 +656,11 @@ __global__ void __launch_bounds__(kSegThreads) embed_join_kernel(const __grid_co
     const int col = (int)slice * kSegCols + 8 * (int)threadIdx.x;
     if (col >= H)
         return;
+    uint4 was[2] = {};
+    if (p.accumulate)
+        load_row8(p, id, col, was);
     const float4 *t = reinterpret_cast<const float4 *>(p.partials + ((size_t)w * 2 + 1) * H + col);
-    float4 a = __ldcg(t), b = __ldcg(t + 1);
+    const float4 a = __ldcg(t), b = __ldcg(t + 1);
     float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     const float4 *piece = reinterpret_cast<const float4 *>(p.partials + (size_t)(w + 1) * 2 * H + col);
     const size_t step = (size_t)2 * H / 4;
@@ -679,13 +682,10 @@ __global__ void __launch_bounds__(kSegThreads) embed_join_kernel(const __grid_co
                     s[q] = __fadd_rn(s[q], f[q]);
             }
     }
-    uint4 was[2] = {};
-    if (p.accumulate) {
-        load_row8(p, id, col, was);
+    if (p.accumulate)
         store_row8<true>(p, id, col, s, was);
-    } else {
+    else
         store_row8<false>(p, id, col, s, was);
-    }
 }
 
 // ------------------------------------------------------------------ launch

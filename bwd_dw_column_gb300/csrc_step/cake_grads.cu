@@ -8,7 +8,8 @@
 // of kGradChunk values; CTA b takes chunks b, b + ctas, ...  Two kernels: the
 // first leaves a partial sum of squares per CTA, the second adds the partials
 // up (every CTA does, in the same order, so that no third launch and no wait
-// between CTAs is needed) and scales.  Both orders depend on the shapes alone.
+// between CTAs is needed) and scales.  Short lists of small tensors take one
+// CTA and one launch.  All orders depend on the shapes alone.
 //
 // Sums: a thread adds the squares of the 32 values that it has of a chunk in
 // FP32, and the sum to its FP64 accumulator.  An FP32 sum outside
@@ -98,20 +99,42 @@ __device__ __forceinline__ void load_chunk(const GradDesc &d, int64_t first, flo
     }
 }
 
-__device__ __forceinline__ double chunk_sumsq(const float (&v)[kPerThread])
+__device__ __forceinline__ void store_one(const GradDesc &d, int64_t i, float v)
+{
+    if (d.flags & kGradDstF32)
+        static_cast<float *>(d.dst)[i] = v;
+    else
+        static_cast<uint16_t *>(d.dst)[i] = (uint16_t)pack_bf16(v, 0.f);
+}
+
+// min(1, max_norm / (norm + eps)) that keeps a NaN
+__device__ __forceinline__ float clip_coef(float max_norm, double norm, float eps)
+{
+    const double q = (double)max_norm / (norm + (double)eps);
+    return q >= 1.0 ? 1.0f : (float)q;
+}
+
+template <int K>
+__device__ __forceinline__ double values_sumsq(const float (&v)[K])
 {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k)
+    for (int k = 0; k < K; ++k)
         s[k & 3] = __fmaf_rn(v[k], v[k], s[k & 3]);
     const float t = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
     if (t >= 0x1p-60f && t <= 0x1p80f)
         return (double)t;
-    double e = 0.0; // small, zero, huge or not finite
-#pragma unroll 1
-    for (int k = 0; k < kPerThread; ++k)
-        e = fma((double)v[k], (double)v[k], e);
-    return e;
+    uint32_t any = 0; // zero, tiny, huge or not finite
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        any |= __float_as_uint(v[k]) & 0x7fffffffu;
+    if (any == 0)
+        return 0.0;
+    double e[2] = {0.0, 0.0};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        e[k & 1] = fma((double)v[k], (double)v[k], e[k & 1]);
+    return e[0] + e[1];
 }
 
 // The sum over the CTA in a fixed order, in thread 0.
@@ -142,7 +165,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const __grid_c
         const GradDesc &d = p.t[i];
         float v[kPerThread];
         load_chunk<false>(d, (int64_t)(c - d.chunk0) * kGradChunk, v);
-        acc += chunk_sumsq(v);
+        acc += values_sumsq(v);
     }
     acc = cta_sum(acc);
     if (threadIdx.x == 0)
@@ -150,18 +173,13 @@ __global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const __grid_c
     pdl_launch_dependents();
 }
 
-// Every thread gets the sum of all partials, in an order that is the same in every CTA.
+// The sum of all partials in thread 0, in an order that is the same in every CTA.
 __device__ __forceinline__ double all_partials(const double *partials, int n)
 {
     double v = 0.0;
     for (int i = threadIdx.x; i < n; i += kGradThreads)
         v += __ldcg(partials + i);
-    __shared__ double total;
-    v = cta_sum(v);
-    if (threadIdx.x == 0)
-        total = v;
-    __syncthreads();
-    return total;
+    return cta_sum(v);
 }
 
 __global__ void __launch_bounds__(kGradThreads) grad_final_kernel(const double *partials, int n, float *norm)
@@ -176,12 +194,17 @@ template <int N>
 __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_constant__ GradParams<N> p)
 {
     pdl_wait();
-    const double norm = sqrt(all_partials(p.partials, p.npartials));
-    if (p.norm && blockIdx.x == 0 && threadIdx.x == 0)
-        *p.norm = (float)norm;
-    // min(1, q) that keeps a NaN
-    const double q = (double)p.max_norm / (norm + (double)p.eps);
-    const float coef = q >= 1.0 ? 1.0f : (float)q;
+    // one thread takes the root and the quotient: FP64 is slow
+    __shared__ float shared_coef;
+    const double sum = all_partials(p.partials, p.npartials);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(sum);
+        if (p.norm && blockIdx.x == 0)
+            *p.norm = (float)norm;
+        shared_coef = clip_coef(p.max_norm, norm, p.eps);
+    }
+    __syncthreads();
+    const float coef = shared_coef;
     if (p.in_place && coef == 1.0f)
         return;
     // last chunks first: L2 still holds what the sum has read last
@@ -224,14 +247,72 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
 #pragma unroll
             for (int k = 0; k < kPerThread; ++k) {
                 const int64_t at = first + k * kGradThreads + threadIdx.x;
-                if (at < d.count) {
-                    const float w = __fmul_rn(v[k], coef);
-                    if (o32)
-                        static_cast<float *>(d.dst)[at] = w;
-                    else
-                        static_cast<uint16_t *>(d.dst)[at] = (uint16_t)pack_bf16(w, 0.f);
-                }
+                if (at < d.count)
+                    store_one(d, at, __fmul_rn(v[k], coef));
             }
+        }
+    }
+}
+
+// All of a short list in one CTA and one launch: a warp takes pieces of
+// kGradPiece values, first for the sum, then (clip) again for the scaling.
+__global__ void __launch_bounds__(kGradOneThreads)
+    grad_one_kernel(const __grid_constant__ GradParams<kGradFewTensors> p, int clip)
+{
+    constexpr int kWarps = kGradOneThreads / 32, kPer = kGradPiece / 32;
+    __shared__ double part[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    double acc = 0.0;
+    for (uint32_t c = warp; c < p.chunks; c += kWarps) {
+        const GradDesc &d = p.t[find_tensor(p, c, 0, p.n - 1)];
+        const int64_t first = (int64_t)(c - d.chunk0) * kGradPiece;
+        float v[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int64_t i = first + 32 * k + lane;
+            v[k] = i < d.count ? load_one(d.src, i, d.flags & kGradSrcF32) : 0.f;
+        }
+        acc += values_sumsq(v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (lane == 0)
+        part[warp] = acc;
+    __syncthreads();
+    // the rest of FP64 is one warp's: an SM does two such operations a cycle
+    __shared__ float shared_coef;
+    if (warp == 0) {
+        acc = part[lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            acc += __shfl_xor_sync(0xffffffffu, acc, o);
+        if (lane == 0) {
+            const double norm = sqrt(acc);
+            *p.norm = (float)norm;
+            shared_coef = clip ? clip_coef(p.max_norm, norm, p.eps) : 1.0f;
+        }
+    }
+    if (!clip)
+        return;
+    __syncthreads();
+    const float coef = shared_coef;
+    if (p.in_place && coef == 1.0f)
+        return;
+    for (uint32_t c = warp; c < p.chunks; c += kWarps) {
+        const GradDesc &d = p.t[find_tensor(p, c, 0, p.n - 1)];
+        const int64_t first = (int64_t)(c - d.chunk0) * kGradPiece;
+        float v[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int64_t i = first + 32 * k + lane;
+            v[k] = i < d.count ? load_one(d.src, i, d.flags & kGradSrcF32) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int64_t i = first + 32 * k + lane;
+            if (i < d.count)
+                store_one(d, i, __fmul_rn(v[k], coef));
         }
     }
 }
@@ -273,6 +354,12 @@ cudaError_t launch_grad_final(const double *partials, int n, float *norm, cudaSt
     const cudaLaunchConfig_t cfg = dependent_config(1, &attr, true, stream);
     cudaError_t e = cudaLaunchKernelEx(&cfg, grad_final_kernel, partials, n, norm);
     return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+cudaError_t launch_grad_one(const GradParams<kGradFewTensors> &p, bool clip, cudaStream_t stream)
+{
+    grad_one_kernel<<<1, kGradOneThreads, 0, stream>>>(p, clip);
+    return cudaGetLastError();
 }
 
 template cudaError_t launch_grad_sumsq<kGradFewTensors>(const GradParams<kGradFewTensors> &, int, cudaStream_t);

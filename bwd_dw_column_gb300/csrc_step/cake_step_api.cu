@@ -292,7 +292,7 @@ int64_t grad_launches(int64_t n) { return n <= 0 ? 0 : (n + kGradMaxTensors - 1)
 // The launches' tensors [i0, i1) as parameters; returns the CTAs.
 template <int N>
 int fill_grads(GradParams<N> &p, const void *const *data, const int64_t *counts, const int32_t *dtypes,
-               void *const *outs, const int32_t *out_dtypes, int64_t i0, int64_t i1)
+               void *const *outs, const int32_t *out_dtypes, int64_t i0, int64_t i1, int most, int64_t chunk = kGradChunk)
 {
     uint64_t chunks = 0;
     int k = 0;
@@ -307,11 +307,11 @@ int fill_grads(GradParams<N> &p, const void *const *data, const int64_t *counts,
         const bool o32 = outs ? out_dtypes[i] == CAKE_FP32 : dtypes[i] == CAKE_FP32;
         d.flags = (dtypes[i] == CAKE_FP32 ? kGradSrcF32 : 0) | (o32 ? kGradDstF32 : 0) |
                   (aligned16(d.src) && aligned16(d.dst) ? kGradVector : 0);
-        chunks += (uint64_t)((counts[i] + kGradChunk - 1) / kGradChunk);
+        chunks += (uint64_t)((counts[i] + chunk - 1) / chunk);
     }
     p.n = k;
     p.chunks = (uint32_t)chunks;
-    return (int)std::min<uint64_t>(chunks, kGradCtas);
+    return (int)std::min<uint64_t>(chunks, most);
 }
 
 template <int N>
@@ -321,9 +321,22 @@ cudaError_t run_grads(const void *const *data, const int64_t *counts, const int3
 {
     // the parameters of a launch are too large for the stack of a small thread
     static thread_local GradParams<N> p;
+    if constexpr (N == kGradFewTensors) {
+        int64_t pieces = 0;
+        for (int64_t i = 0; i < n && pieces <= kGradOnePieces; ++i)
+            pieces += (counts[i] + kGradPiece - 1) / kGradPiece;
+        if (pieces > 0 && pieces <= kGradOnePieces) {
+            fill_grads(p, data, counts, dtypes, outs, out_dtypes, 0, n, 1, kGradPiece);
+            p.max_norm = max_norm;
+            p.eps = eps;
+            p.in_place = outs == nullptr;
+            p.norm = norm;
+            return launch_grad_one(p, clip, s);
+        }
+    }
     int total = 0;
     for (int64_t i0 = 0; i0 < n; i0 += N) {
-        const int ctas = fill_grads(p, data, counts, dtypes, outs, out_dtypes, i0, std::min(n, i0 + N));
+        const int ctas = fill_grads(p, data, counts, dtypes, outs, out_dtypes, i0, std::min(n, i0 + N), kGradCtas);
         if (ctas == 0)
             continue;
         p.partials = partials + total;
@@ -338,7 +351,7 @@ cudaError_t run_grads(const void *const *data, const int64_t *counts, const int3
         return launch_grad_final(partials, total, norm, s);
     bool first = true;
     for (int64_t i0 = 0; i0 < n; i0 += N) {
-        const int ctas = fill_grads(p, data, counts, dtypes, outs, out_dtypes, i0, std::min(n, i0 + N));
+        const int ctas = fill_grads(p, data, counts, dtypes, outs, out_dtypes, i0, std::min(n, i0 + N), kGradClipCtas);
         if (ctas == 0)
             continue;
         p.partials = partials;

@@ -78,13 +78,19 @@ constexpr int kGradMaxTensors = 1000;
 constexpr int kGradSomeTensors = 256;
 constexpr int kGradFewTensors = 32;
 constexpr int kGradThreads = 256;
-constexpr int kGradCtas = 152 * 8;
+constexpr int kGradCtas = 152 * 8;      // of the norm's launches, at most
+constexpr int kGradClipCtas = 152 * 48; // of the scaling's
+
+// A list of at most kGradFewTensors tensors in kGradOnePieces pieces runs in one CTA.
+constexpr int kGradPiece = 512;
+constexpr int kGradOneThreads = 1024;
+constexpr int kGradOnePieces = 64;
 
 struct GradDesc {
     const void *src;
     void *dst;
     int64_t count;
-    uint32_t chunk0;       // the tensor's first chunk in this launch
+    uint32_t chunk0;       // the tensor's first chunk (one CTA: piece) in this launch
     uint32_t flags;        // kGrad*
 };
 constexpr uint32_t kGradSrcF32 = 1, kGradDstF32 = 2, kGradVector = 4; // kGradVector: 16-byte accesses are aligned
@@ -105,6 +111,7 @@ template <int N>
 cudaError_t launch_grad_sumsq(const GradParams<N> &p, int ctas, cudaStream_t stream);
 template <int N>
 cudaError_t launch_grad_clip(const GradParams<N> &p, int ctas, bool after_norm, cudaStream_t stream);
+cudaError_t launch_grad_one(const GradParams<kGradFewTensors> &p, bool clip, cudaStream_t stream);
 cudaError_t launch_grad_final(const double *partials, int n, float *norm, cudaStream_t stream);
 
 // ---------------------------------------------------------------- embedding

@@ -27,6 +27,7 @@ import ctypes
 import functools
 import struct
 from array import array
+from operator import attrgetter, is_not
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -348,29 +349,23 @@ def _dense(t: torch.Tensor) -> bool:
 
 
 _GRAD_DTYPES = {torch.bfloat16: CAKE_BF16, torch.float32: CAKE_FP32}
-_T = torch.Tensor  # its methods, mapped over lists of hundreds of tensors
+_T = torch.Tensor  # its methods and attributes, mapped over lists of hundreds of tensors
+_dtype_of, _is_tensor = attrgetter("dtype"), functools.partial(is_not, None)
 
 
 def _tensors(grads, what):
-    """The tensors as the ABI's arrays (pointers, counts, dtypes)."""
+    """The tensors as the ABI's arrays (pointers, counts, dtypes), and whether all are contiguous."""
     try:
-        types = array("i", [_GRAD_DTYPES[t.dtype] for t in grads])
+        types = array("i", map(_GRAD_DTYPES.__getitem__, map(_dtype_of, grads)))
     except KeyError as e:
         raise TypeError(f"{what} are BF16 or FP32, got {e.args[0]}") from None
-    if not all(map(_T.is_contiguous, grads)):
+    plain = all(map(_T.is_contiguous, grads))
+    if not plain:
         for t in grads:
             if not _dense(t):
                 raise ValueError(
                     f"{what} must fill one block of memory each (strides {t.stride()} of {tuple(t.shape)})")
-    return array("Q", map(_T.data_ptr, grads)), array("q", map(_T.numel, grads)), types
-
-
-def _same_layouts(grads, outs):
-    if [o.shape for o in outs] != [g.shape for g in grads]:
-        return False
-    if all(map(_T.is_contiguous, grads)) and all(map(_T.is_contiguous, outs)):
-        return True
-    return all(o.stride() == g.stride() or (o.is_contiguous() and g.is_contiguous()) for g, o in zip(grads, outs))
+    return array("Q", map(_T.data_ptr, grads)), array("q", map(_T.numel, grads)), types, plain
 
 
 def _addr(a):
@@ -392,7 +387,7 @@ def _grad_call(grads, outs, clip, max_norm, eps, norm, workspace, stream):
     if outs is not None:
         devices.update(map(_T.get_device, outs))
     with _on_devices(stream, devices):
-        ptrs, counts, types = _tensors(grads, "gradients")
+        ptrs, counts, types, plain = _tensors(grads, "gradients")
         n = len(grads)
         if norm is None:
             norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
@@ -406,9 +401,11 @@ def _grad_call(grads, outs, clip, max_norm, eps, norm, workspace, stream):
             return norm
         optrs = otypes = ()
         if outs:
-            if not _same_layouts(grads, outs):
-                raise ValueError("an output must have its gradient's shape and order of dimensions")
-            optrs, _, otypes = _tensors(outs, "outputs")
+            optrs, ocounts, otypes, oplain = _tensors(outs, "outputs")
+            if ocounts != counts or not (plain and oplain or all(
+                    g.is_contiguous() and o.is_contiguous() or (g.shape == o.shape and g.stride() == o.stride())
+                    for g, o in zip(grads, outs))):
+                raise ValueError("an output must hold its gradient's values in the same order")
         st = lib.cake_grad_clip(_addr(ptrs), _addr(counts), _addr(types), _addr(optrs), _addr(otypes), n, max_norm,
                                 eps, norm.data_ptr(), ws, ws_bytes, _current())
         _check(st, "cake_grad_clip")
@@ -429,8 +426,8 @@ def cake_clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, *, 
                         workspace: torch.Tensor | None = None, stream=None):
     """Scale all gradients by min(1, max_norm / (norm + eps)); returns the norm before it.
 
-    In place, or into ``out`` (a tensor per gradient, same shape, BF16 or FP32:
-    for instance the optimizer's FP32 buffers).  The host waits for nothing: a
+    In place, or into ``out`` (a tensor per gradient, as many values in the same
+    order, BF16 or FP32: for instance the optimizer's FP32 buffers).  The host waits for nothing: a
     NaN or infinite norm is for the caller to look at, and makes the gradients
     NaN as the formula says.  No tensor may be given twice, nor share memory
     with another.
@@ -442,10 +439,12 @@ def cake_clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, *, 
         out = list(out)
         if len(out) != len(grads):
             raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
-        out = [o for g, o in zip(grads, out) if g is not None]
-        if any(o is None for o in out):
-            raise ValueError("an output is missing for a gradient")
-    grads = [g for g in grads if g is not None]
+    if not all(map(_is_tensor, grads)):
+        if out is not None:
+            out = [o for g, o in zip(grads, out) if g is not None]
+        grads = [g for g in grads if g is not None]
+    if out is not None and not all(map(_is_tensor, out)):
+        raise ValueError("an output is missing for a gradient")
     return _grad_call(grads, out, True, max_norm, eps, norm, workspace, stream)
 
 
