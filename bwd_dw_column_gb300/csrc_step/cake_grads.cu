@@ -107,10 +107,14 @@ __device__ __forceinline__ void store_one(const GradDesc &d, int64_t i, float v)
         static_cast<uint16_t *>(d.dst)[i] = (uint16_t)pack_bf16(v, 0.f);
 }
 
-// min(1, max_norm / (norm + eps)) that keeps a NaN
+// min(1, max_norm / (norm + eps)) that keeps a NaN; 1 where norm + eps is 0
+// (there is nothing to scale)
 __device__ __forceinline__ float clip_coef(float max_norm, double norm, float eps)
 {
-    const double q = (double)max_norm / (norm + (double)eps);
+    const double by = norm + (double)eps;
+    if (by == 0.0)
+        return 1.0f;
+    const double q = (double)max_norm / by;
     return q >= 1.0 ? 1.0f : (float)q;
 }
 

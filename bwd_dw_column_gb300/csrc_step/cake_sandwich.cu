@@ -642,8 +642,11 @@ static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int clust
         if (p.stages >= want || p.per_sm == 1)
             break;
     }
-    if (p.stages > kSwMaxStages)
-        p.stages = kSwMaxStages;
+    // three stages of the forward against four to eight, GB300, 2^27 values:
+    // H = 256 174 us against 192, H = 2560 180 against 187; the others the same
+    const int most = backward ? kSwMaxStages : 3;
+    if (p.stages > most)
+        p.stages = most;
     p.smem = fixed + (size_t)p.stages * stage;
     const size_t comb = fixed + (size_t)(backward ? p.groups : 0) * p.cols * 16;
     if (comb > p.smem)

@@ -1,7 +1,9 @@
 // cake_step_api.cu -- the C ABI of the training-step operators: argument
 // validation, workspace layout and dispatch to the launchers.  Host code only.
 #include <algorithm>
+#include <climits>
 #include <cmath>
+#include <cstdlib>
 #include <vector>
 
 #include <cuda_runtime.h>
@@ -101,7 +103,8 @@ extern "C" cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_ten
         return st;
     // a row is written after it is read: an output may be an input's view
     // exactly, and not straddle other rows of one
-    if (overlap(y, h_new, shape))
+    if (overlap(y, h_new, shape) || std::abs(reinterpret_cast<intptr_t>(rstd_post) -
+                                             reinterpret_cast<intptr_t>(rstd_pre)) < (intptr_t)(rows * sizeof(float)))
         return CAKE_ERR_INVALID;
     const cake_tensor *outs[2] = {y, h_new}, *ins[3] = {z, x, has(gate) ? gate : nullptr};
     for (const cake_tensor *o : outs)
@@ -158,8 +161,9 @@ extern "C" cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_ten
         return st;
     if ((st = check_sandwich(shape, w_post, w_post_dtype, w_pre, w_pre_dtype, gate_rows, gate, scale)) != CAKE_OK)
         return st;
-    if (!dw_post || !dw_pre || dw_post == dw_pre)
-        return CAKE_ERR_INVALID;
+    if (!dw_post || !dw_pre || std::abs(reinterpret_cast<intptr_t>(dw_post) - reinterpret_cast<intptr_t>(dw_pre)) <
+                                   (intptr_t)(shape->hidden * sizeof(float)))
+        return CAKE_ERR_INVALID; // missing, or one reaches into the other
     if (!aligned16(dw_post) || !aligned16(dw_pre))
         return CAKE_ERR_UNSUPPORTED;
     if ((dgate_rows && !gate_rows) || (has(dgate) && !has(gate)))
@@ -228,24 +232,32 @@ extern "C" cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_ten
 
 namespace {
 
+constexpr int64_t kGradMostTensors = 1000000;
+
 struct Range {
     uintptr_t lo, hi;
-    int64_t id; // tensor; an output's is -1 - tensor where it is not the input itself
+    int64_t id; // tensor; an output's is -1 - tensor where it is not the input itself; the norm's is INT64_MIN
 };
 
 // The tensors of a call, checked; `clip`: outputs too.
 cake_status check_grads(const void *const *data, const int64_t *counts, const int32_t *dtypes, void *const *outs,
-                        const int32_t *out_dtypes, int64_t n, bool clip)
+                        const int32_t *out_dtypes, int64_t n, bool clip, const float *norm)
 {
     if (n < 0 || (n > 0 && (!data || !counts || !dtypes)) || (outs == nullptr) != (out_dtypes == nullptr))
         return CAKE_ERR_INVALID;
+    if (n > kGradMostTensors)
+        return CAKE_ERR_UNSUPPORTED;
     std::vector<Range> written, read;
-    if (clip)
-        written.reserve((size_t)n);
+    if (clip) {
+        written.reserve((size_t)n + 1);
+        written.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, INT64_MIN});
+    }
+    uint64_t chunks = 0;
     for (int64_t i = 0; i < n; ++i) {
         if (counts[i] < 0 || !good_dtype(dtypes[i]) || (outs && !good_dtype(out_dtypes[i])))
             return CAKE_ERR_INVALID;
-        if (counts[i] >= (int64_t(1) << 44)) // 2^32 chunks are more than any memory holds
+        chunks += (uint64_t)(counts[i] / kGradChunk) + 1;
+        if (chunks >= (uint64_t(1) << 32)) // a launch counts its chunks in 32 bits
             return CAKE_ERR_UNSUPPORTED;
         if (counts[i] == 0)
             continue;
@@ -287,7 +299,10 @@ cake_status check_grads(const void *const *data, const int64_t *counts, const in
     return CAKE_OK;
 }
 
-int64_t grad_launches(int64_t n) { return n <= 0 ? 0 : (n + kGradMaxTensors - 1) / kGradMaxTensors; }
+int64_t grad_launches(int64_t n)
+{
+    return n <= 0 || n > kGradMostTensors ? 0 : (n + kGradMaxTensors - 1) / kGradMaxTensors;
+}
 
 // The launches' tensors [i0, i1) as parameters; returns the CTAs.
 template <int N>
@@ -372,10 +387,15 @@ cake_status grads(const void *const *data, const int64_t *counts, const int32_t 
                   const int32_t *out_dtypes, int64_t n, bool clip, float max_norm, float eps, float *norm,
                   void *workspace, size_t workspace_bytes, cake_stream_t stream)
 {
-    cake_status st = check_grads(data, counts, dtypes, outs, out_dtypes, n, clip);
+    cake_status st = check_rows_f32(norm);
     if (st != CAKE_OK)
         return st;
-    if ((st = check_rows_f32(norm)) != CAKE_OK)
+    try {
+        st = check_grads(data, counts, dtypes, outs, out_dtypes, n, clip, norm);
+    } catch (...) { // no host memory for the list
+        return CAKE_ERR_WORKSPACE;
+    }
+    if (st != CAKE_OK)
         return st;
     if (n == 0)
         return cuda_status(cudaMemsetAsync(norm, 0, sizeof(float), cu(stream)));

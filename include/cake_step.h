@@ -14,7 +14,8 @@
  * calls that are ordered on one stream.  Every result is bitwise reproducible
  * for equal inputs and shapes.  Waits inside the kernels (for staged copies,
  * and between the CTAs of a thread-block cluster) are bounded and report
- * through cake_rmsnorm_device_status().
+ * through cake_rmsnorm_device_status().  A first call on a device looks up
+ * addresses and sets kernel attributes: make it before any stream capture.
  */
 #ifndef CAKE_STEP_H
 #define CAKE_STEP_H
@@ -96,8 +97,9 @@ cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_tensor *dy, co
  * outs NULL (out_dtypes NULL too) clips in place, and then writes nothing
  * where coef is 1.  An output may be exactly its own input or share no memory
  * with any tensor of the call; inputs may share memory with each other only
- * where they are not written (CAKE_ERR_INVALID).  max_norm >= 0 (infinity is
- * allowed), eps >= 0.  n = 0: norm is 0.
+ * where they are not written (CAKE_ERR_INVALID), and norm lies in none of
+ * them.  max_norm >= 0 (infinity is allowed), eps >= 0; coef is 1 where
+ * norm + eps is 0.  n at most 1000000; n = 0: norm is 0.
  */
 size_t cake_grad_norm_workspace_size(int64_t n);
 

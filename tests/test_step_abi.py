@@ -53,7 +53,7 @@ def V(at, st=64, sh=0):
 
 
 def fwd(cake, shape=None, z=None, x=None, w1=A, d1=0, w2=A, d2=0, grow=None, gate=None, scale=1.0, eps=1e-6, y=None,
-        h=None, r1=A, r2=A):
+        h=None, r1=A, r2=A + MB):
     return cake.load_library().cake_sandwich_fwd(shape or S(4), z or V(A), x or V(A + MB), w1, d1, w2, d2, grow, gate,
                                                  scale, eps, y or V(A + 2 * MB), h or V(A + 3 * MB), r1, r2, None)
 
@@ -71,6 +71,7 @@ def test_sandwich_fwd_refusals(cake):
     assert fwd(cake, r1=None) == INVALID and fwd(cake, r2=A + 2) == UNSUPPORTED
     assert fwd(cake, grow=A, gate=V(A + 5 * MB)) == INVALID
     assert fwd(cake, grow=A + 2) == UNSUPPORTED and fwd(cake, gate=V(A + 5 * MB + 8)) == UNSUPPORTED
+    assert fwd(cake, r2=A) == INVALID and fwd(cake, r2=A + 8) == INVALID  # rstd_pre reaches into rstd_post
     assert fwd(cake, y=V(A + 3 * MB)) == INVALID            # y and h_new are one
     assert fwd(cake, h=V(A + MB + 128)) == INVALID          # h_new straddles x's rows
     assert fwd(cake, S(4, 2), z=V(A, 128, 64), x=V(A + MB, 128, 64), y=V(A + 2 * MB, 64, 64)) == INVALID  # rows overlap
@@ -87,6 +88,7 @@ def bwd(cake, shape=None, dy=None, dh=None, h=None, z=None, r1=A, r2=A, w1=A, w2
 def test_sandwich_bwd_refusals(cake):
     assert bwd(cake, S(4, 1, 12)) == UNSUPPORTED
     assert bwd(cake, dwo=None) == INVALID and bwd(cake, dwr=A) == INVALID and bwd(cake, dwo=A + 4) == UNSUPPORTED
+    assert bwd(cake, dwr=A + 128) == INVALID                # dw_pre reaches into dw_post
     assert bwd(cake, dgr=A) == INVALID and bwd(cake, dg=V(A + 5 * MB)) == INVALID   # a gradient of no gate
     assert bwd(cake, grow=A, dgr=A + 2) == UNSUPPORTED
     assert bwd(cake, dx=V(A)) == INVALID and bwd(cake, dz=V(A + 2 * MB)) == INVALID  # in place
@@ -106,7 +108,7 @@ def test_every_width_has_a_backward_plan(cake):
             assert cake.cake_sandwich_bwd_workspace_size((T, 1, H)) >= 16 * H, (T, H)
 
 
-def grads(cake, ptrs, counts, types, outs=None, otypes=None, max_norm=1.0, eps=1e-6, norm=A, ws=A, n_ws=1 << 30,
+def grads(cake, ptrs, counts, types, outs=None, otypes=None, max_norm=1.0, eps=1e-6, norm=A // 2, ws=A, n_ws=1 << 30,
           clip=True):
     n = len(ptrs)
     arr = lambda t, v: (t * max(n, 1))(*v)  # noqa: E731
@@ -140,7 +142,14 @@ def test_grad_refusals(cake):
     assert grads(cake, [A], [4], [0], ws=None) == WORKSPACE and grads(cake, [A], [4], [0], n_ws=8) == WORKSPACE
     assert grads(cake, [A], [4], [0], ws=A + 8) == UNSUPPORTED
     assert grads(cake, [A], [4], [0], norm=None, clip=False) == INVALID
-    assert grads(cake, [A], [1 << 44], [0], clip=False) == UNSUPPORTED
+    assert grads(cake, [A], [1 << 46], [0], clip=False) == UNSUPPORTED
+    assert grads(cake, [A] * 4000, [1 << 34] * 4000, [0] * 4000, clip=False) == UNSUPPORTED  # 2^32 chunks and more
+    for at in (B, B + 8, B + 12):  # the norm lies in an output
+        assert grads(cake, [A], [8], [0], outs=[B], otypes=[0], norm=at) == INVALID
+    assert grads(cake, [A], [8], [0], norm=A + 4) == INVALID
+    lib = cake.load_library()
+    assert lib.cake_grad_norm(A, A, A, 1 << 60, A, A, 1 << 30, None) == UNSUPPORTED  # nothing of the lists is read
+    assert lib.cake_grad_norm_workspace_size(1 << 60) == 0
     assert cake.cake_grad_norm_workspace_size(0) == 0
     assert cake.cake_grad_norm_workspace_size(5000) > cake.cake_grad_norm_workspace_size(1) > 0
 

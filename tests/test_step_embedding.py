@@ -137,6 +137,28 @@ def test_runs_across_windows(cake, seed):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [1024, 1025, 16_384, 16_385, 32_769, 65_537, 131_072, 131_073, 200_000])
+def test_both_sorts(cake, T):
+    # one cluster of 1 to 16 CTAs with 1 to 8 keys a thread up to 131072 tokens, a launch per pass beyond
+    dy = torch.randn(T, 8, generator=gen(T)).to(BF16).to(DEV)
+    ids = make_ids("log", T, 3000, 1)
+    ids[::13] = -1
+    check_bwd(cake, dy, ids.to(DEV), 3000, 0.5)
+    check_bwd(cake, dy, ids.int().to(DEV), 3000, 0.5, 17, torch.randn(3000, 8, generator=gen(1)).to(DEV), True)
+    ids[3] = 1 << 30
+    check_bwd(cake, dy, ids.to(DEV), 3000)
+    assert cake.cake_rmsnorm_device_status(clear=True) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [1, 2, 31, 32, 33, 255, 256, 65_535, 65_536, 300_001, 5_000_000])
+def test_table_sizes(cake, V):
+    # digits of a pass, and bitmaps zeroed by the sort or before it
+    dy = torch.randn(700, 16, generator=gen(V)).to(BF16).to(DEV)
+    check_bwd(cake, dy, make_ids("uniform", 700, V).to(DEV), V)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_padding_types_and_adding(cake, dtype, accumulate):

@@ -133,6 +133,8 @@ def test_zeros_and_not_finite(cake):
         t.zero_()
     assert float(cake.cake_grad_norm(z)) == 0.0
     assert float(cake.cake_clip_grad_norm(z, 1.0)) == 0.0 and not any(t.any() for t in z)
+    cake.cake_clip_grad_norm(z, 0.0, eps=0.0)  # nothing to scale, and no 0 / 0
+    assert not any(t.any() for t in z)
     g = make([9000, 100], device=DEV)
     g[0][8500] = float("inf")
     assert float(cake.cake_grad_norm(g)) == math.inf

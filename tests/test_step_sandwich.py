@@ -275,6 +275,32 @@ def test_broadcast_gate_gradient(cake):
 
 
 @pytest.mark.gpu
+def test_rows_beyond_2_to_31_values(cake):
+    # the last rows of a tensor of 2.2e9 values come out as they do by themselves
+    T, H, n = 270_000, 8192, 5
+    c = case(n, H, "row", device=DEV)
+    big = {k: torch.zeros(T, H, dtype=torch.bfloat16, device=DEV) for k in ("z", "x", "dy", "dh")}
+    for k, v in big.items():
+        v[-n:] = c[k]
+    gate = torch.zeros(T, device=DEV)
+    gate[-n:] = c["gate"]
+    w = (c["w_post"], c["w_pre"])
+    got = cake.cake_sandwich_fwd(big["z"], big["x"], *w, EPS, gate, 0.5, y=big["z"].clone(), h_new=big["x"].clone())
+    want = cake.cake_sandwich_fwd(c["z"], c["x"], *w, EPS, c["gate"], 0.5)
+    for a, b in zip(got, want):
+        assert torch.equal(a[-n:], b)
+    del want
+    y, h, r1, r2 = got
+    dx, dz, dwo, dwr, dg = cake.cake_sandwich_bwd(big["dy"], h, big["z"], r1, r2, *w, big["dh"], gate, 0.5, dx=y)
+    small = cake.cake_sandwich_bwd(c["dy"], h[-n:], c["z"], r1[-n:], r2[-n:], *w, c["dh"], c["gate"], 0.5)
+    for a, b in zip((dx, dz, dg), (small[0], small[1], small[4])):
+        assert torch.equal(a[-n:], b)
+    # all other rows are zero, so the column sums are these rows' alone, added in another order
+    ref_sums = ref.sandwich_bwd(c["dy"], h[-n:], c["z"], r1[-n:], r2[-n:], *w, c["dh"], c["gate"], 0.5)
+    assert ref.excess(dwo, *ref_sums["dw_post"]) <= 1 and ref.excess(dwr, *ref_sums["dw_pre"]) <= 1
+
+
+@pytest.mark.gpu
 def test_two_graphs_on_two_streams(cake):
     """Captured calls keep their own workspaces: two graphs replayed at once give what each gives alone."""
     cases = [case(3000, 1536, "row", device=DEV, seed=s) for s in (1, 2)]
