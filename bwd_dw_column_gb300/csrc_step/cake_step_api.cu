@@ -488,6 +488,8 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int64_t H)
     e.tile_keys = (uint32_t)per;
     e.tiles = (int)((T + per - 1) / per);
     e.slices = (int)((H + 1023) / 1024);
+    // long windows (T = 65536, H = 4096 added: 188 us with 128 positions, 193
+    // with 64), shorter ones where that leaves SMs without work
     e.window = 128;
     while (e.window > 32 && ((T + e.window - 1) / e.window) * e.slices < 152 * 8)
         e.window /= 2;

@@ -78,8 +78,11 @@ constexpr int kGradMaxTensors = 1000;
 constexpr int kGradSomeTensors = 256;
 constexpr int kGradFewTensors = 32;
 constexpr int kGradThreads = 256;
-constexpr int kGradCtas = 152 * 8;      // of the norm's launches, at most
-constexpr int kGradClipCtas = 152 * 48; // of the scaling's
+// CTAs of the norm's launches, at most (each leaves a partial), and of the
+// scaling's: GB300, 0.65 G BF16 values into FP32 812 us with 8 an SM in both,
+// 793 us with 48 of the scaling's.
+constexpr int kGradCtas = 152 * 8;
+constexpr int kGradClipCtas = 152 * 48;
 
 // A list of at most kGradFewTensors tensors in kGradOnePieces pieces runs in one CTA.
 constexpr int kGradPiece = 512;
