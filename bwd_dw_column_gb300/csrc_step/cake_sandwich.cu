@@ -320,6 +320,12 @@ __device__ __forceinline__ float warp_sum3(float v0, float v1, float v2, int lan
     return r;
 }
 
+// mbar_wait with one answer for the whole warp: its lanes go on, or give up, together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
+}
+
 // GATE: 0 none, 1 a value per row, 2 a value per element.  CL: rows span a
 // cluster.  RW: row_warps of the layout.
 //
@@ -411,8 +417,8 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
     for (uint32_t j = 0; j <= ntiles && !abort; ++j) {
         float mine = 0.f;
         if (j < ntiles) {
-            abort = !mbar_wait(smem_addr(&m.s.full[st1]), ph1, p.wait_ns);
-            if (r0 + j * tile + gid < r_end && !abort) { // uniform across the group
+            abort = !warp_wait(smem_addr(&m.s.full[st1]), ph1, p.wait_ns);
+            if (r0 + j * tile + gid < r_end && !abort) { // uniform across the warp
                 const float2 rn = both(m.scalars[st1 * kSwMaxTile + gid].y);
                 float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f);
 #pragma unroll
@@ -473,7 +479,7 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
             if (r < r_end) {
                 float t3 = own;
                 if (joined) {
-                    if (!mbar_wait(smem_addr(m.sums + kSwSlots * gid + (i & 3)), (i >> 2) & 1, p.wait_ns))
+                    if (!warp_wait(smem_addr(m.sums + kSwSlots * gid + (i & 3)), (i >> 2) & 1, p.wait_ns))
                         abort = true;
                     // eight lanes to a sum
                     const float *from = red + (i & 3) * 4 * RW;
