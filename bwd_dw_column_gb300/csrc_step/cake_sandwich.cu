@@ -27,7 +27,7 @@ cudaError_t ensure_smem_attr(const void *kernel, size_t smem);
 
 constexpr int kSMsStep = 152;
 constexpr int kSwMaxStages = 16;
-constexpr int kSwMaxTile = 12;            // rows of a stage, at most
+constexpr int kSwMaxTile = 15;            // rows of a stage, at most
 constexpr int kSwSlots = 4;               // backward: rows whose partial sums may be in use
 constexpr int kSwMaxJoined = 6;           // groups whose rows span several warps, at most
 constexpr int kSwMaxRowWarps = 32;        // warps of a row over its cluster, at most
@@ -347,9 +347,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
 // a barrier of its own, hold the rows that may be in use, also where sums
 // reach one CTA of a cluster later than another.
 constexpr int kSwBwdWarps = 12;     // consumer warps; four more hold the producer
+constexpr int kSwBwdManyWarps = 15; // ... or fifteen at 128 registers, and the producer
 constexpr int kSwBwdThreads = 32 * (kSwBwdWarps + 4);
+static_assert(kSwBwdThreads == 32 * (kSwBwdManyWarps + 1), "both forms launch 16 warps");
 
-template <int VPT, int GATE, bool CL, int RW>
+// MANY: 15 consumer warps instead of 12, for rows of 5 or 7 warps, of which 12
+// leave two or five without work, and for rows of at most 256 columns, whose
+// sums take half the registers (GB300, 2^27 values: H = 2560 272 us against 307,
+// 5120 282 against 322, 7168 292 against 328, 256 265 against 283).
+template <int VPT, int GATE, bool CL, int RW, bool MANY = false>
 __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -372,16 +378,19 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
         cluster_sync_all(); // every CTA's barriers and slots exist before a remote access
     // Registers: 16 warps start with 128 each; the last four give 72 up, and
     // the twelve consumer warps take 24 more (12 x 152 + 4 x 56 = 16 x 128).
-    if (warp >= kSwBwdWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == kSwBwdWarps)
+    constexpr int kProducer = MANY ? kSwBwdManyWarps : kSwBwdWarps;
+    if (warp >= kProducer) {
+        if (!MANY)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == kProducer)
             sw_produce(m, L, p.in, p.rstd_post, p.rstd_pre, p.gate_rows, v0, nvec, r0, r_end, p.status, p.wait_ns);
         __syncwarp();
         if (CL)
             cluster_sync_all();
         return;
     }
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    if (!MANY)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     if (warp >= L.groups * L.W) { // no row for this warp
         if (CL)
             cluster_sync_all();
@@ -635,7 +644,8 @@ static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int clust
     p.vpt = H <= 256 ? 1 : 2;
     p.W = (nvec + 32 * p.vpt - 1) / (32 * p.vpt);
     p.groups = groups;
-    if (p.groups * p.W > (backward ? kSwBwdWarps : 16))
+    const bool many = p.vpt == 1 || ((p.W == 5 || p.W == 7) && cluster <= 2);
+    if (p.groups * p.W > (!backward ? 16 : many ? kSwBwdManyWarps : kSwBwdWarps))
         return false;
     // CTAs per SM: the backward's takes all registers, 28 of the forward's warps fit
     p.per_sm = backward ? 1 : 28 / (p.groups * p.W + 1) >= 2 ? 2 : 1;
@@ -747,10 +757,20 @@ cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, const SandwichPlan &
 template <int GATE>
 static cudaError_t launch_bwd_gate(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
 {
-    if (plan.stages < 2 || plan.groups * plan.W > kSwBwdWarps) // a row is held while the next one is read
+    if (plan.stages < 2) // a row is held while the next one is read
         return cudaErrorInvalidValue;
     const int threads = kSwBwdThreads;
     const int rw = row_warps(plan.W * plan.cluster);
+    if (plan.groups * plan.W > kSwBwdWarps) {
+        if (plan.groups * plan.W > kSwBwdManyWarps)
+            return cudaErrorInvalidValue;
+        if (plan.vpt == 1)
+            return launch_rows(sandwich_bwd_kernel<1, GATE, false, 1, true>, p, plan, threads, stream);
+        if (rw != (plan.cluster > 1 ? 16 : 8))
+            return cudaErrorInvalidValue;
+        return plan.cluster > 1 ? launch_rows(sandwich_bwd_kernel<2, GATE, true, 16, true>, p, plan, threads, stream)
+                                : launch_rows(sandwich_bwd_kernel<2, GATE, false, 8, true>, p, plan, threads, stream);
+    }
     if (plan.cluster > 1)
         return rw == 8    ? launch_rows(sandwich_bwd_kernel<2, GATE, true, 8>, p, plan, threads, stream)
                : rw == 16 ? launch_rows(sandwich_bwd_kernel<2, GATE, true, 16>, p, plan, threads, stream)
