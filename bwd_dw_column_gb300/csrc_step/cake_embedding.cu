@@ -632,6 +632,28 @@ __global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid
     }
 }
 
+// Adds the first n of N pieces, `step` apart, in order.
+template <int N>
+__device__ __forceinline__ void add_pieces(const float4 *piece, size_t step, uint32_t n, float (&s)[8])
+{
+    float4 v[N][2];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if ((uint32_t)k < n) {
+            v[k][0] = __ldcg(piece + (size_t)k * step);
+            v[k][1] = __ldcg(piece + (size_t)k * step + 1);
+        }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if ((uint32_t)k < n) {
+            const float f[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                                v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                s[q] = __fadd_rn(s[q], f[q]);
+        }
+}
+
 // Joins the partials of the runs that were cut: the CTA of the window in
 // which such a run starts adds the following windows' pieces in order.
 __global__ void __launch_bounds__(kSegThreads) embed_join_kernel(const __grid_constant__ SegmentParams p)
@@ -673,24 +695,11 @@ __global__ void __launch_bounds__(kSegThreads) embed_join_kernel(const __grid_co
     float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     const float4 *piece = reinterpret_cast<const float4 *>(p.partials + (size_t)(w + 1) * 2 * H + col);
     const size_t step = (size_t)2 * H / 4;
-    for (uint32_t u = 0; u < n; u += 4) {
-        float4 v[4][2];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (u + k < n) {
-                v[k][0] = __ldcg(piece + (size_t)(u + k) * step);
-                v[k][1] = __ldcg(piece + (size_t)(u + k) * step + 1);
-            }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (u + k < n) {
-                const float f[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
-                                    v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    s[q] = __fadd_rn(s[q], f[q]);
-            }
-    }
+    uint32_t u = 0;
+    for (; u + 8 <= n; u += 8) // a run over many windows: eight pieces on their way
+        add_pieces<8>(piece + (size_t)u * step, step, 8, s);
+    for (; u < n; u += 4)
+        add_pieces<4>(piece + (size_t)u * step, step, n - u, s);
     if (p.accumulate)
         store_row8<true>(p, id, col, s, was);
     else

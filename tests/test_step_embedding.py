@@ -177,6 +177,27 @@ def test_padding_types_and_adding(cake, dtype, accumulate):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_of_tokens_that_do_not_count(cake, bad):
+    # what stands in the rows of padding and of missing tokens is not looked at
+    T, H, V = 900, 136, 40
+    dy = torch.randn(T, H, generator=gen(11)).to(BF16).to(DEV)
+    ids = make_ids("log", T, V).to(DEV)
+    ids[::5], ids[1::7] = 9, -3
+    out = (ids == 9) | (ids < 0)
+    want = cake.cake_embedding_bwd(dy, ids, V, padding_idx=9)
+    dy[out] = bad
+    got = cake.cake_embedding_bwd(dy, ids, V, padding_idx=9)
+    assert torch.equal(got, want) and bool(torch.isfinite(got).all())
+    # and where they count, they stay in their row
+    hit = int(ids[~out][0])
+    dy[out] = 0
+    dy[(ids == hit).nonzero()[0], 5] = bad
+    got = cake.cake_embedding_bwd(dy, ids, V, padding_idx=9)
+    assert not bool(torch.isfinite(got[hit, 5])) and int((~torch.isfinite(got)).sum()) == 1
+
+
+@pytest.mark.gpu
 def test_all_tokens_are_padding(cake):
     dy = torch.randn(700, 64, generator=gen(7)).to(BF16).to(DEV)
     for ids in (torch.full((700,), 4), torch.full((700,), -1)):

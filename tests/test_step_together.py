@@ -121,3 +121,46 @@ def test_step_in_a_graph(cake):
     assert replayed == eager
     for k, v in p.items():
         assert torch.equal(v, after[k]), k
+
+
+def test_given_streams_and_host_threads(cake):
+    """Calls of several host threads, each on a stream of its own, give what each gives alone."""
+    import threading
+
+    def work(seed, stream):
+        g = torch.Generator().manual_seed(seed)
+        with torch.cuda.stream(stream):
+            ids = torch.randint(0, V, (2000 + seed,), generator=g).to(DEV)
+            rows = [torch.randn(2000 + seed, H, generator=g).to(BF16).to(DEV) for _ in range(3)]
+            w = torch.ones(H, device=DEV)
+        stream.synchronize()
+        got = []
+        for _ in range(6):
+            _, h, a, b = cake.cake_sandwich_fwd(rows[0], rows[1], w, w, stream=stream)
+            _, dz, dwo, _, _ = cake.cake_sandwich_bwd(rows[2], h, rows[0], a, b, w, w, stream=stream)
+            table = cake.cake_embedding_bwd(dz, ids, V, stream=stream)
+            norm = cake.cake_grad_norm([table, dwo, dz], stream=stream)
+            y = cake.cake_embedding_fwd(ids, table, stream=stream)
+            with torch.cuda.stream(stream):
+                got.append([t.clone() for t in (dz, dwo, table, y)] + [norm])
+                cake.cake_clip_grad_norm([table, dwo], 1e-3, stream=stream)
+                got[-1] += [table, dwo]
+        stream.synchronize()
+        return got
+
+    alone = [work(s, torch.cuda.Stream()) for s in range(3)]
+    streams, out = [torch.cuda.Stream() for _ in range(3)], [None] * 3
+
+    def run(s):
+        out[s] = work(s, streams[s])
+
+    threads = [threading.Thread(target=run, args=(s,)) for s in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for a, b in zip(alone, out):
+        for i in range(6):
+            for x, y in zip(a[0], b[i]):
+                assert torch.equal(x, y)
