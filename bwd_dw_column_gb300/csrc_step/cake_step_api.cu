@@ -40,6 +40,41 @@ cake_status check_rows_f32(const void *p)
     return (reinterpret_cast<uintptr_t>(p) & 3u) ? CAKE_ERR_UNSUPPORTED : CAKE_OK;
 }
 
+// Memory of a call's tensors: what it writes shares none with anything else.
+struct Memory {
+    uintptr_t lo, hi;
+};
+
+Memory memory(const void *p, uint64_t bytes)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, p ? lo + (uintptr_t)bytes : lo};
+}
+
+Memory memory(const cake_tensor *t, const cake_shape *s)
+{
+    if (!has(t))
+        return {0, 0};
+    const auto e = extent(t, s);
+    return {e.first, e.second};
+}
+
+bool meet(const Memory &a, const Memory &b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
+
+// Whether one of the `nw` written ranges meets another one or a range that is read.
+bool any_meet(const Memory *written, int nw, const Memory *read, int nr)
+{
+    for (int i = 0; i < nw; ++i) {
+        for (int k = 0; k < i; ++k)
+            if (meet(written[i], written[k]))
+                return true;
+        for (int k = 0; k < nr; ++k)
+            if (meet(written[i], read[k]))
+                return true;
+    }
+    return false;
+}
+
 // The weights and the gate of a sandwich norm.
 cake_status check_sandwich(const cake_shape *shape, const void *w_post, cake_dtype post_dtype, const void *w_pre,
                            cake_dtype pre_dtype, const float *gate_rows, const cake_tensor *gate, float scale)
@@ -101,10 +136,14 @@ extern "C" cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_ten
         (st = check_out_tensor(y, shape)) != CAKE_OK || (st = check_out_tensor(h_new, shape)) != CAKE_OK ||
         (st = check_rows_f32(rstd_post)) != CAKE_OK || (st = check_rows_f32(rstd_pre)) != CAKE_OK)
         return st;
-    // a row is written after it is read: an output may be an input's view
-    // exactly, and not straddle other rows of one
-    if (overlap(y, h_new, shape) || std::abs(reinterpret_cast<intptr_t>(rstd_post) -
-                                             reinterpret_cast<intptr_t>(rstd_pre)) < (intptr_t)(rows * sizeof(float)))
+    // a row is written after it is read: y and h_new may be an input's view
+    // exactly, and not straddle other rows of one; nothing else is shared
+    const uint64_t rb = (uint64_t)rows * 4, wb = (uint64_t)shape->hidden;
+    const Memory written[4] = {memory(rstd_post, rb), memory(rstd_pre, rb), memory(y, shape), memory(h_new, shape)};
+    const Memory lists[3] = {memory(gate_rows, rb), memory(w_post, wb * (w_post_dtype == CAKE_FP32 ? 4 : 2)),
+                             memory(w_pre, wb * (w_pre_dtype == CAKE_FP32 ? 4 : 2))};
+    const Memory rows_in[3] = {memory(z, shape), memory(x, shape), memory(gate, shape)};
+    if (any_meet(written, 4, lists, 3) || any_meet(written, 2, rows_in, 3))
         return CAKE_ERR_INVALID;
     const cake_tensor *outs[2] = {y, h_new}, *ins[3] = {z, x, has(gate) ? gate : nullptr};
     for (const cake_tensor *o : outs)
@@ -182,19 +221,22 @@ extern "C" cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_ten
         (st = check_rows_f32(rstd_post)) != CAKE_OK || (st = check_rows_f32(rstd_pre)) != CAKE_OK ||
         (dgate_rows && (st = check_rows_f32(dgate_rows)) != CAKE_OK))
         return st;
-    // outputs are written while later rows of the inputs are still being read
-    const cake_tensor *outs[3] = {dx, dz, has(dgate) ? dgate : nullptr};
-    const cake_tensor *ins[5] = {dy, h_new, z, has(dh) ? dh : nullptr, has(gate) ? gate : nullptr};
-    for (int o = 0; o < 3; ++o) {
-        for (const cake_tensor *i : ins)
-            if (overlap(outs[o], i, shape))
-                return CAKE_ERR_INVALID;
-        for (int q = 0; q < o; ++q)
-            if (overlap(outs[o], outs[q], shape))
-                return CAKE_ERR_INVALID;
-    }
-    if ((st = check_workspace(workspace, workspace_bytes, cake_sandwich_bwd_workspace_size(shape))) != CAKE_OK)
+    const size_t need = cake_sandwich_bwd_workspace_size(shape);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != CAKE_OK)
         return st;
+    // outputs are written while later rows of the inputs are still being read
+    const uint64_t rb = (uint64_t)rows * 4, wb = (uint64_t)H;
+    const Memory written[7] = {memory(dx, shape),       memory(dz, shape),     memory(dgate, shape),
+                               memory(dgate_rows, rb),  memory(dw_post, wb * 4), memory(dw_pre, wb * 4),
+                               memory(workspace, need)};
+    const Memory read[10] = {memory(dy, shape),    memory(h_new, shape),
+                             memory(z, shape),     memory(dh, shape),
+                             memory(gate, shape),  memory(gate_rows, rb),
+                             memory(rstd_post, rb), memory(rstd_pre, rb),
+                             memory(w_post, wb * (w_post_dtype == CAKE_FP32 ? 4 : 2)),
+                             memory(w_pre, wb * (w_pre_dtype == CAKE_FP32 ? 4 : 2))};
+    if (any_meet(written, 7, read, 10))
+        return CAKE_ERR_INVALID;
     SandwichBwdParams p{};
     p.in[0] = make_view(h_new, shape);
     p.in[1] = make_view(z, shape);
@@ -241,7 +283,7 @@ struct Range {
 
 // The tensors of a call, checked; `clip`: outputs too.
 cake_status check_grads(const void *const *data, const int64_t *counts, const int32_t *dtypes, void *const *outs,
-                        const int32_t *out_dtypes, int64_t n, bool clip, const float *norm)
+                        const int32_t *out_dtypes, int64_t n, bool clip, const float *norm, const Memory &scratch)
 {
     if (n < 0 || (n > 0 && (!data || !counts || !dtypes)) || (outs == nullptr) != (out_dtypes == nullptr))
         return CAKE_ERR_INVALID;
@@ -281,6 +323,12 @@ cake_status check_grads(const void *const *data, const int64_t *counts, const in
         written.push_back({o, o + osize * (uintptr_t)counts[i], o == a && osize == size ? i : -1 - i});
         read.push_back(in);
     }
+    if (meet(scratch, memory(norm, 4)))
+        return CAKE_ERR_INVALID;
+    for (int64_t i = 0; i < n; ++i)
+        if (meet(scratch, memory(data[i], (uint64_t)counts[i] * (dtypes[i] == CAKE_FP32 ? 4 : 2))) ||
+            (outs && meet(scratch, memory(outs[i], (uint64_t)counts[i] * (out_dtypes[i] == CAKE_FP32 ? 4 : 2)))))
+            return CAKE_ERR_INVALID;
     // written ranges share memory with no other range but their own input
     const auto by_lo = [](const Range &x, const Range &y) { return x.lo < y.lo; };
     std::sort(written.begin(), written.end(), by_lo);
@@ -390,8 +438,11 @@ cake_status grads(const void *const *data, const int64_t *counts, const int32_t 
     cake_status st = check_rows_f32(norm);
     if (st != CAKE_OK)
         return st;
+    const size_t need = cake_grad_norm_workspace_size(n);
+    if (n > 0 && (st = check_workspace(workspace, workspace_bytes, need)) != CAKE_OK)
+        return st;
     try {
-        st = check_grads(data, counts, dtypes, outs, out_dtypes, n, clip, norm);
+        st = check_grads(data, counts, dtypes, outs, out_dtypes, n, clip, norm, memory(workspace, need));
     } catch (...) { // no host memory for the list
         return CAKE_ERR_WORKSPACE;
     }
@@ -399,8 +450,6 @@ cake_status grads(const void *const *data, const int64_t *counts, const int32_t 
         return st;
     if (n == 0)
         return cuda_status(cudaMemsetAsync(norm, 0, sizeof(float), cu(stream)));
-    if ((st = check_workspace(workspace, workspace_bytes, cake_grad_norm_workspace_size(n))) != CAKE_OK)
-        return st;
     double *partials = static_cast<double *>(workspace);
     // the fewer parameters a launch carries, the sooner it starts
     const auto run = n <= kGradFewTensors    ? run_grads<kGradFewTensors>
@@ -437,6 +486,11 @@ extern "C" cake_status cake_grad_clip(void *const *data, const int64_t *counts, 
 
 namespace {
 
+Memory table_memory(const void *table, int dtype, int64_t vocab, int64_t hidden, int64_t stride)
+{
+    return memory(table, ((uint64_t)(vocab - 1) * (uint64_t)stride + (uint64_t)hidden) * (dtype == CAKE_FP32 ? 4 : 2));
+}
+
 cake_status check_embedding(const void *ids, int ids_int64, int64_t tokens, const void *table, int dtype,
                             int64_t vocab, int64_t hidden, int64_t stride, float scale, const cake_tensor *rows,
                             bool rows_out)
@@ -457,11 +511,10 @@ cake_status check_embedding(const void *ids, int ids_int64, int64_t tokens, cons
     cake_status st = rows_out ? check_out_tensor(rows, &shape) : check_tensor(rows, &shape);
     if (st != CAKE_OK)
         return st;
-    // the rows and the table share no memory
-    const auto e = extent(rows, &shape);
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(table);
-    const uintptr_t hi = lo + (uintptr_t)((vocab - 1) * stride + hidden) * (dtype == CAKE_FP32 ? 4 : 2);
-    return e.first < hi && lo < e.second ? CAKE_ERR_INVALID : CAKE_OK;
+    // what is written, the rows or the table, shares memory with nothing else
+    const Memory r = memory(rows, &shape), t = table_memory(table, dtype, vocab, hidden, stride);
+    const Memory i = memory(ids, (uint64_t)tokens * (ids_int64 ? 8 : 4));
+    return meet(r, t) || meet(i, rows_out ? r : t) ? CAKE_ERR_INVALID : CAKE_OK;
 }
 
 // Sizes of a gradient call; they depend on the shape alone.
@@ -560,6 +613,12 @@ extern "C" cake_status cake_embedding_bwd(const cake_tensor *dy, const void *ids
     const EmbedPlan e = embed_plan(tokens, vocab, hidden);
     if ((st = check_workspace(workspace, workspace_bytes, e.total)) != CAKE_OK)
         return st;
+    const cake_shape shape{tokens, 1, hidden};
+    const Memory scratch = memory(workspace, e.total);
+    const Memory others[3] = {memory(dy, &shape), memory(ids, (uint64_t)tokens * (ids_int64 ? 8 : 4)),
+                              table_memory(dtable, dtable_dtype, vocab, hidden, dtable_stride)};
+    if (any_meet(&scratch, 1, others, 3))
+        return CAKE_ERR_INVALID;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     SortParams q{};
     if (step_status_ptr(&q.status) != cudaSuccess)

@@ -10,12 +10,13 @@
  * they are additions of this library.
  *
  * Workspaces here hold nothing between calls: they need no initialisation
- * (and none after an error), must be 256-byte aligned, and may be shared by
- * calls that are ordered on one stream.  Every result is bitwise reproducible
- * for equal inputs and shapes.  Waits inside the kernels (for staged copies,
- * and between the CTAs of a thread-block cluster) are bounded and report
- * through cake_rmsnorm_device_status().  A first call on a device looks up
- * addresses and sets kernel attributes: make it before any stream capture.
+ * (and none after an error), must be 256-byte aligned, share no memory with
+ * the call's tensors, and may be shared by calls that are ordered on one
+ * stream.  Every result is bitwise reproducible for equal inputs and shapes.
+ * Waits inside the kernels (for staged copies, and between the CTAs of a
+ * thread-block cluster) are bounded and report through
+ * cake_rmsnorm_device_status().  A first call on a device looks up addresses
+ * and sets kernel attributes: make it before any stream capture.
  */
 #ifndef CAKE_STEP_H
 #define CAKE_STEP_H
@@ -52,8 +53,8 @@ extern "C" {
  * multiplies as it is given: an activation before it is the caller's.
  * Shapes, strides, alignment and sharing of memory as for cake_rmsnorm_fwd
  * and cake_rmsnorm_bwd: an output of the forward may be exactly an input view
- * (h_new in place of x), no output of the backward may share memory with any
- * other tensor of the call.  w_post and w_pre have a dtype each.
+ * (y or h_new in place of z, x or gate), and nothing else that a call writes
+ * may share memory with any other tensor of it.  w_post and w_pre have a dtype each.
  */
 cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_tensor *z, const cake_tensor *x,
                               const void *w_post, cake_dtype w_post_dtype, const void *w_pre,
@@ -123,7 +124,8 @@ cake_status cake_grad_clip(void *const *data, const int64_t *counts, const int32
  * CAKE_ERR_INVALID.  padding_idx (-1: none): that id adds nothing to dtable.
  * table, dtable: [vocab, H] BF16 or FP32, row strides in elements, 16-byte
  * aligned rows; y, dy: BF16 rows [T, H].  H a multiple of 8, at most
- * CAKE_MAX_HIDDEN; T and vocab below 2^31.
+ * CAKE_MAX_HIDDEN; T and vocab below 2^31.  What is written shares memory with
+ * no other tensor of the call.
  *
  * The gradient sorts the tokens by id (stably) and sums each id's rows in
  * FP32 in an order that depends on the ids alone, so it is bitwise

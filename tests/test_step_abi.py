@@ -187,6 +187,62 @@ def test_embedding_bwd_refusals(cake):
     assert 0 < small < large
 
 
+@pytest.mark.parametrize("shift", [0, 16, -16])
+def test_written_memory_is_shared_with_nothing(cake, shift):
+    """Every pair of a written tensor and another one that meet is refused (but forward rows in place)."""
+    far = [(20 + k) * MB for k in range(16)]
+    # 4 rows of 64 values: 512 bytes a tensor, 16 bytes a list of rows, 128 or 256 a weight
+    at = dict(zip(("z", "x", "gate", "y", "h", "w1", "w2", "r1", "r2", "dy", "dh", "dgr", "dwo", "dwr", "grow", "ws"), far))
+
+    def forward(row_gate, **moved):
+        a = {**at, **moved}
+        gate = {"grow": a["grow"]} if row_gate else {"gate": V(a["gate"])}
+        return fwd(cake, z=V(a["z"]), x=V(a["x"]), y=V(a["y"]), h=V(a["h"]), w1=a["w1"], w2=a["w2"], r1=a["r1"],
+                   r2=a["r2"], **gate)
+
+    def meets(place):  # where a tensor of more than 16 bytes starts that reaches into the one at `place`
+        return place + min(shift, 0)
+
+    for out in ("r1", "r2"):
+        for other in ("z", "x", "y", "h", "w1", "w2"):
+            assert forward(True, **{out: at[other] + max(shift, 0)}) == INVALID, (out, other)
+        assert forward(True, **{out: at["grow"] + (4 if shift else 0)}) == INVALID
+        assert forward(False, **{out: at["gate"] + max(shift, 0)}) == INVALID
+    for out in ("y", "h"):
+        for other in ("w1", "w2", "grow"):
+            assert forward(True, **{out: meets(at[other])}) == INVALID, (out, other)
+
+    names = ("dx", "dz", "dwo", "dwr", "dgr")
+
+    def backward(**moved):
+        a = {**at, "dx": 40 * MB, "dz": 41 * MB, **moved}
+        return bwd(cake, dy=V(a["dy"]), dh=V(a["dh"]), h=V(a["h"]), z=V(a["z"]), r1=a["r1"], r2=a["r2"], w1=a["w1"],
+                   w2=a["w2"], grow=a["grow"], dx=V(a["dx"]), dz=V(a["dz"]), dwo=a["dwo"], dwr=a["dwr"], dgr=a["dgr"],
+                   ws=a["ws"])
+
+    places = {**at, "dx": 40 * MB, "dz": 41 * MB}
+    for out in names:
+        for other in ("dy", "dh", "h", "z", "r1", "r2", "w1", "w2", "grow", "dx", "dz", "dwo", "dwr", "dgr", "ws"):
+            if out != other:
+                to = places[other] if out == "dgr" else meets(places[other])
+                assert backward(**{out: to}) == INVALID, (out, other)
+    for other in ("dy", "dh", "h", "z", "r1", "r2", "w1", "w2", "grow"):
+        assert backward(ws=places[other]) == INVALID, other
+
+
+def test_scratch_and_ids_are_shared_with_nothing(cake):
+    B, C = A + MB, A + 2 * MB
+    for n in (100, 1 << 18):
+        assert grads(cake, [B], [n], [1], ws=B + 256) == INVALID
+        assert grads(cake, [B], [n], [1], ws=B, clip=False) == INVALID
+    assert grads(cake, [A], [4], [0], outs=[B], otypes=[1], ws=B) == INVALID
+    assert grads(cake, [A], [4], [0], norm=C + 64, ws=C) == INVALID
+    assert efwd(cake, ids=A + 2 * MB + 8) == INVALID and efwd(cake, ids=A + 2 * MB - 8) == INVALID
+    assert ebwd(cake, ids=A + MB + 8, ws=32 * MB) == INVALID and ebwd(cake, ids=A + MB - 8, ws=32 * MB) == INVALID
+    for place in (A, A + MB, A + 2 * MB):  # ids, dtable, dy
+        assert ebwd(cake, ws=place) == INVALID
+
+
 def test_python_refusals_without_a_gpu(cake):
     z = torch.zeros(4, 64, dtype=torch.bfloat16)
     w = torch.ones(64)
