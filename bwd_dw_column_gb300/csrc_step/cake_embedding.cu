@@ -13,9 +13,9 @@
 // the ids alone, and every row of dtable has one writer.
 //
 // HBM bounds the lookup and, where there are many tokens or rows, the gradient
-// (GB300: T = 65536, H = 5120 lookup 143 us; the whole gradient of 131072 x 2048
-// from 8192 tokens 165 us, 6.7 TB/s; 65536 tokens added at H = 4096 186 us, of
-// which the sort is 21 us and the join 10 us).
+// (GB300: T = 65536, H = 5120 lookup 142 us; the whole gradient of 131072 x 2048
+// from 8192 tokens 162 us, 6.8 TB/s; 65536 tokens added at H = 4096 185 us, of
+// which the sort is 20 us and the join 12 us).
 #include <mutex>
 
 #include "../csrc/cake_device.cuh"
@@ -207,8 +207,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_cluster_sort_kernel(
         for (uint32_t i = blockIdx.x * kClusterThreads + threadIdx.x; i < (p.vocab + 31) / 32;
              i += C * kClusterThreads)
             p.present[i] = 0;
-    if (rank_c == 0 && threadIdx.x == 0)
-        *p.ready = 0;
+    if (rank_c == 0 && threadIdx.x == 0) {
+        p.ready[0] = 0;
+        p.ready[1] = 0; // the sums' count of cut runs
+    }
     const bool mark = p.present != nullptr;
     uint64_t key[PER];
     {
@@ -420,15 +422,13 @@ __global__ void __launch_bounds__(kSortThreads)
 // ----------------------------------------------------------------- segments
 //
 // CTA (window w, slice s) sums columns of the rows whose sorted positions are
-// in [w * window, (w + 1) * window).  Runs that end within kOverrun positions
-// after their window are finished by the window in which they start.  A run
-// that goes further is cut at the window boundaries: its first window leaves
-// a "trailing" partial, the windows that it fills one each, and the last a
+// in [w * window, (w + 1) * window).  Runs that end within `overrun` positions
+// after their window (at most a window) are finished by the window in which
+// they start.  A run that goes further is cut at the window boundaries: its
+// first window leaves a "trailing" partial and enters itself in the list of cut
+// runs, the windows that it fills leave a partial each, and the last a
 // "leading" one.
-constexpr int kSegThreads = 128;                // 8 columns a thread
-constexpr int kSegCols = 8 * kSegThreads;
-constexpr int kSegMaxWindow = 128;
-constexpr int kOverrun = 32;
+constexpr uint32_t kMostOverrun = 32;
 // meta[w][0]
 constexpr uint32_t kMetaLead = 1;   // the window starts with a piece of an earlier window's run: partial 0
 constexpr uint32_t kMetaLeadOn = 2; // ... that goes on in the next window
@@ -479,14 +479,14 @@ __device__ __forceinline__ void store_row8(const SegmentParams &p, uint32_t id, 
 }
 
 // Zeroes the rows of dtable whose id has no token: a warp per row.  (A CTA for
-// every four rows: 165 us for 131072 x 2048 FP32 values, against 174 and 216 us
+// every 32 KB: 165 us for 131072 x 2048 FP32 values, against 174 and 216 us
 // with 16 and 6 CTAs an SM in a loop.)
 __device__ void fill_rows(const SegmentParams &p, uint32_t part, uint32_t parts)
 {
     const int lane = threadIdx.x & 31;
-    const uint32_t warps = parts * (kSegThreads / 32);
+    const uint32_t warps = parts * (blockDim.x / 32);
     const int vecs = p.dtable_f32 ? 2 * p.nvec : p.nvec;
-    for (uint32_t v = part * (kSegThreads / 32) + (threadIdx.x >> 5); v < p.vocab; v += warps) {
+    for (uint32_t v = part * (blockDim.x / 32) + (threadIdx.x >> 5); v < p.vocab; v += warps) {
         if ((__ldcg(p.present + (v >> 5)) >> (v & 31)) & 1u)
             continue;
         uint4 *o = p.dtable_f32
@@ -501,7 +501,7 @@ __device__ void fill_rows(const SegmentParams &p, uint32_t part, uint32_t parts)
 // rows of dy, half as many at a time (GB300, T = 65536, H = 4096: a load at
 // each run's end instead took 172 us).
 template <bool ACC>
-__global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid_constant__ SegmentParams p)
+__global__ void __launch_bounds__(kSegMaxThreads) embed_segment_kernel(const __grid_constant__ SegmentParams p)
 {
     constexpr int kSegBatch = ACC ? 4 : 8; // rows in flight
     if (blockIdx.x < (uint32_t)p.fill_ctas) {
@@ -522,14 +522,15 @@ __global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid
     }
     pdl_wait();
     const uint32_t block = blockIdx.x - (uint32_t)p.fill_ctas;
-    __shared__ uint32_t ids[kSegMaxWindow + kOverrun + 2], tok[kSegMaxWindow + kOverrun + 2];
+    __shared__ uint32_t ids[kSegMaxWindow + kMostOverrun + 2], tok[kSegMaxWindow + kMostOverrun + 2];
     __shared__ int limits[2];
     const uint32_t w = block / p.slices, slice = block - w * p.slices;
     const uint32_t lo = w * p.window;
     const uint32_t W = min((uint32_t)p.window, p.tokens - lo); // positions of this window
-    const uint32_t ext = min(p.tokens - lo, (uint32_t)p.window + kOverrun + 1); // and those looked at
+    const uint32_t overrun = min((uint32_t)p.window, kMostOverrun);
+    const uint32_t ext = min(p.tokens - lo, (uint32_t)p.window + overrun + 1); // and those looked at
     // ids[1 + i], tok[1 + i]: position lo + i; ids[0]: the position before
-    for (uint32_t i = threadIdx.x; i < ext; i += kSegThreads) {
+    for (uint32_t i = threadIdx.x; i < ext; i += blockDim.x) {
         const uint64_t pr = __ldcg(p.pairs + lo + i);
         ids[1 + i] = (uint32_t)(pr >> 32);
         tok[1 + i] = (uint32_t)pr;
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid
     __syncthreads();
     // the leading run: positions equal to the one before the window
     // (limits[0]: its length within W); the trailing run's end (limits[1])
-    for (uint32_t i = threadIdx.x; i < ext; i += kSegThreads) {
+    for (uint32_t i = threadIdx.x; i < ext; i += blockDim.x) {
         if (i < W && ids[1 + i] != ids[0])
             atomicMin(&limits[0], (int)i);
         if (i >= W && ids[1 + i] != ids[W])
@@ -559,21 +560,21 @@ __global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid
     if (lead == W) {
         // one run of an earlier window fills this one; the window before has
         // finished it if it ends within the overrun
-        if (W > kOverrun || goes_on) {
+        if (W > overrun || goes_on) {
             first = 0;
             flags = kMetaLead;
-            if (goes_on && over <= kOverrun)
+            if (goes_on && over <= overrun)
                 end = W + over;
             else if (goes_on)
                 flags |= kMetaLeadOn;
             lead_end = end;
         }
     } else {
-        if (lead > kOverrun) {
+        if (lead > overrun) {
             first = 0;
             flags = kMetaLead;
         }
-        if (goes_on && over <= kOverrun)
+        if (goes_on && over <= overrun)
             end = W + over;
         else if (goes_on)
             flags |= kMetaTrail;
@@ -581,9 +582,11 @@ __global__ void __launch_bounds__(kSegThreads) embed_segment_kernel(const __grid
     if (slice == 0 && threadIdx.x == 0) {
         p.meta[2 * w] = flags;
         p.meta[2 * w + 1] = ids[W];
+        if ((flags & kMetaTrail) && ids[W] < p.vocab)
+            p.cut[atomicAdd(p.cuts, 1u)] = w; // (their order changes no result)
     }
 
-    const int col = (int)slice * kSegCols + 8 * (int)threadIdx.x;
+    const int col = 8 * ((int)(slice * blockDim.x) + (int)threadIdx.x);
     if (col >= 8 * p.nvec)
         return;
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -654,56 +657,85 @@ __device__ __forceinline__ void add_pieces(const float4 *piece, size_t step, uin
         }
 }
 
-// Joins the partials of the runs that were cut: the CTA of the window in
-// which such a run starts adds the following windows' pieces in order.
-__global__ void __launch_bounds__(kSegThreads) embed_join_kernel(const __grid_constant__ SegmentParams p)
+// Joins the partials of the cut runs: a CTA takes an eighth of a run's columns
+// (64 to 1024 of them), its G groups of L threads every G-th of the run's pieces
+// each, and the groups' sums are added in their order.  A common id's run has
+// hundreds of pieces where windows are short (GB300, ncu, T = 65536 with
+// frequencies of 1/k: H = 64 7 us, H = 512 17 us; with the pieces of a run one
+// after another 21 and 25 us).
+constexpr int kJoinThreads = 256;
+constexpr int kJoinCtas = 152 * 4;
+
+__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const __grid_constant__ SegmentParams p)
 {
     __shared__ int last;
+    __shared__ __align__(16) float part[8 * kJoinThreads]; // [G][8 L]
     pdl_wait();
-    const uint32_t w = blockIdx.x / p.slices, slice = blockIdx.x - w * p.slices;
-    if (!(__ldcg(p.meta + 2 * w) & kMetaTrail))
-        return;
-    const uint32_t id = __ldcg(p.meta + 2 * w + 1);
-    if (id >= p.vocab)
-        return;
-    // the run's pieces are those of windows w + 1 .. w + n
-    uint32_t n = 0;
-    for (;; n += kSegThreads) {
-        if (threadIdx.x == 0)
-            last = kSegThreads;
-        __syncthreads();
-        const uint32_t u = w + 1 + n + threadIdx.x;
-        if (u >= (uint32_t)p.windows || !(__ldcg(p.meta + 2 * u) & kMetaLeadOn))
-            atomicMin(&last, (int)threadIdx.x);
-        __syncthreads();
-        const int l = last;
-        __syncthreads();
-        if (l < kSegThreads) {
-            n += l + 1;
-            break;
-        }
-    }
+    const uint32_t L = (uint32_t)p.join_lanes, G = kJoinThreads / L, blocks = ((uint32_t)p.nvec + L - 1) / L;
+    const uint64_t items = (uint64_t)__ldcg(p.cuts) * blocks;
     const int H = 8 * p.nvec;
-    const int col = (int)slice * kSegCols + 8 * (int)threadIdx.x;
-    if (col >= H)
-        return;
-    uint4 was[2] = {};
-    if (p.accumulate)
-        load_row8(p, id, col, was);
-    const float4 *t = reinterpret_cast<const float4 *>(p.partials + ((size_t)w * 2 + 1) * H + col);
-    const float4 a = __ldcg(t), b = __ldcg(t + 1);
-    float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const float4 *piece = reinterpret_cast<const float4 *>(p.partials + (size_t)(w + 1) * 2 * H + col);
-    const size_t step = (size_t)2 * H / 4;
-    uint32_t u = 0;
-    for (; u + 8 <= n; u += 8) // a run over many windows: eight pieces on their way
-        add_pieces<8>(piece + (size_t)u * step, step, 8, s);
-    for (; u < n; u += 4)
-        add_pieces<4>(piece + (size_t)u * step, step, n - u, s);
-    if (p.accumulate)
-        store_row8<true>(p, id, col, s, was);
-    else
-        store_row8<false>(p, id, col, s, was);
+    const uint32_t g = threadIdx.x / L, c = threadIdx.x - g * L;
+    for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const uint32_t run = (uint32_t)(item / blocks), block = (uint32_t)(item - (uint64_t)run * blocks);
+        const uint32_t w = __ldcg(p.cut + run);
+        const uint32_t id = __ldcg(p.meta + 2 * w + 1);
+        // the run's pieces are those of windows w + 1 .. w + n
+        uint32_t n = 0;
+        for (;; n += 4 * kJoinThreads) {
+            if (threadIdx.x == 0)
+                last = 4 * kJoinThreads;
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t i = q * kJoinThreads + threadIdx.x, u = w + 1 + n + i;
+                if (u >= (uint32_t)p.windows || !(__ldcg(p.meta + 2 * u) & kMetaLeadOn))
+                    atomicMin(&last, (int)i);
+            }
+            __syncthreads();
+            const int l = last;
+            __syncthreads();
+            if (l < 4 * kJoinThreads) {
+                n += l + 1;
+                break;
+            }
+        }
+        const int col = 8 * (int)(L * block + c);
+        uint4 was[2] = {};
+        if (g == 0 && col < H && p.accumulate)
+            load_row8(p, id, col, was);
+        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (col < H) {
+            const size_t step = (size_t)2 * H / 4; // from window to window
+            if (g == 0) // the piece of window w itself
+                add_pieces<1>(reinterpret_cast<const float4 *>(p.partials + ((size_t)w * 2 + 1) * H + col), step, 1, s);
+            const float4 *piece =
+                reinterpret_cast<const float4 *>(p.partials + (size_t)(w + 1) * 2 * H + col) + (size_t)g * step;
+            const uint32_t m = g < n ? (n - g + G - 1) / G : 0;
+            for (uint32_t u = 0; u < m; u += 8)
+                add_pieces<8>(piece + (size_t)u * G * step, G * step, min(8u, m - u), s);
+        }
+        float4 *o = reinterpret_cast<float4 *>(part + 8 * threadIdx.x);
+        o[0] = make_float4(s[0], s[1], s[2], s[3]);
+        o[1] = make_float4(s[4], s[5], s[6], s[7]);
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < 8 * L; i += kJoinThreads) {
+            float t = part[i];
+            for (uint32_t k = 1; k < min(n, G); ++k)
+                t = __fadd_rn(t, part[8 * L * k + i]);
+            part[i] = t;
+        }
+        __syncthreads();
+        if (g == 0 && col < H) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                s[q] = part[8 * c + q];
+            if (p.accumulate)
+                store_row8<true>(p, id, col, s, was);
+            else
+                store_row8<false>(p, id, col, s, was);
+        }
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------------------------ launch
@@ -772,11 +804,12 @@ cudaError_t launch_embed_sort(const SortParams &p, uint64_t **sorted, cudaStream
     return cudaGetLastError();
 }
 
-static cudaError_t launch_dependent(void (*kern)(SegmentParams), const SegmentParams &p, int ctas, cudaStream_t stream)
+static cudaError_t launch_dependent(void (*kern)(SegmentParams), const SegmentParams &p, int ctas, int threads,
+                                    cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kSegThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -790,12 +823,17 @@ static cudaError_t launch_dependent(void (*kern)(SegmentParams), const SegmentPa
 cudaError_t launch_embed_segments(const SegmentParams &p, cudaStream_t stream)
 {
     return launch_dependent(p.accumulate ? embed_segment_kernel<true> : embed_segment_kernel<false>, p,
-                            p.windows * p.slices + p.fill_ctas, stream);
+                            p.windows * p.slices + p.fill_ctas, p.threads, stream);
 }
 
 cudaError_t launch_embed_join(const SegmentParams &p, cudaStream_t stream)
 {
-    return launch_dependent(embed_join_kernel, p, p.windows * p.slices, stream);
+    SegmentParams q = p;
+    q.join_lanes = 8;
+    while (q.join_lanes < 128 && 8 * q.join_lanes < p.nvec)
+        q.join_lanes *= 2;
+    const uint64_t most = (uint64_t)p.windows * ((p.nvec + q.join_lanes - 1) / q.join_lanes);
+    return launch_dependent(embed_join_kernel, q, most < kJoinCtas ? (int)most : kJoinCtas, kJoinThreads, stream);
 }
 
 // Device address of the status word, looked up once per device.

@@ -519,7 +519,7 @@ cake_status check_embedding(const void *ids, int ids_int64, int64_t tokens, cons
 
 // Sizes of a gradient call; they depend on the shape alone.
 struct EmbedPlan {
-    int bits, passes, tiles, window, windows, slices;
+    int bits, passes, tiles, window, windows, slices, threads;
     int cluster; // CTAs of the one-launch sort; 0: a launch per pass
     uint32_t tile_keys;
     size_t present_bytes, hist_bytes, pairs_bytes, part_bytes, meta_bytes, total;
@@ -540,18 +540,21 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int64_t H)
     const int64_t per = ((T + kSortMaxTiles - 1) / kSortMaxTiles + kSortBlock - 1) / kSortBlock * kSortBlock;
     e.tile_keys = (uint32_t)per;
     e.tiles = (int)((T + per - 1) / per);
-    e.slices = (int)((H + 1023) / 1024);
+    const int nvec = (int)(H / 8);
+    e.slices = (nvec + kSegMaxThreads - 1) / kSegMaxThreads;
+    e.threads = ((nvec + e.slices - 1) / e.slices + 31) / 32 * 32;
     // long windows (T = 65536, H = 4096 added: 188 us with 128 positions, 193
-    // with 64), shorter ones where that leaves SMs without work
-    e.window = 128;
-    while (e.window > 32 && ((T + e.window - 1) / e.window) * e.slices < 152 * 8)
+    // with 64), shorter ones where that leaves SMs without work (T = 4096,
+    // H = 1024 added: 32 us with at least 32 positions, 23 with at least 8)
+    e.window = kSegMaxWindow;
+    while (e.window > kSegMinWindow && ((T + e.window - 1) / e.window) * e.slices < 152 * 8)
         e.window /= 2;
     e.windows = (int)((T + e.window - 1) / e.window);
     e.present_bytes = 256 + align256(((size_t)V + 31) / 32 * 4); // a flag, then the bitmap
     e.hist_bytes = e.cluster ? 0 : align256((size_t)e.passes * e.tiles * ((size_t)4 << e.bits));
     e.pairs_bytes = align256((size_t)T * 8);
     e.part_bytes = align256((size_t)e.windows * 2 * H * 4);
-    e.meta_bytes = align256((size_t)e.windows * 8);
+    e.meta_bytes = align256((size_t)e.windows * 12);
     e.total = e.present_bytes + e.hist_bytes + 2 * e.pairs_bytes + e.part_bytes + e.meta_bytes;
     return e;
 }
@@ -655,6 +658,7 @@ extern "C" cake_status cake_embedding_bwd(const cake_tensor *dy, const void *ids
     g.window = e.window;
     g.windows = e.windows;
     g.slices = e.slices;
+    g.threads = e.threads;
     g.nvec = (int)(hidden / 8);
     g.dy = static_cast<const uint16_t *>(dy->data);
     g.dy_stride = dy->stride_token;
@@ -664,11 +668,14 @@ extern "C" cake_status cake_embedding_bwd(const cake_tensor *dy, const void *ids
     g.dtable_stride = dtable_stride;
     g.accumulate = accumulate != 0;
     g.present = q.present;
-    g.fill_ctas = accumulate ? 0 : (int)std::min<int64_t>((vocab + 3) / 4, 1 << 20);
+    const int64_t fill_rows = std::max<int64_t>(e.threads / 32, 32768 / (hidden * (int64_t)size));
+    g.fill_ctas = accumulate ? 0 : (int)std::min<int64_t>((vocab + fill_rows - 1) / fill_rows, 1 << 20);
     g.ready = e.cluster && !accumulate ? q.ready : nullptr;
     g.status = q.status;
     g.partials = reinterpret_cast<float *>(at + 2 * e.pairs_bytes);
     g.meta = reinterpret_cast<uint32_t *>(at + 2 * e.pairs_bytes + e.part_bytes);
+    g.cut = g.meta + 2 * (size_t)e.windows;
+    g.cuts = q.ready + 1;
     r = launch_embed_segments(g, s);
     if (r == cudaSuccess)
         r = launch_embed_join(g, s);

@@ -139,6 +139,9 @@ constexpr int kSortPerThread = 8;
 constexpr int kSortBlock = kSortThreads * kSortPerThread; // keys ranked together
 constexpr int kSortMaxTiles = 304;
 constexpr int kSortMaxBits = 8;                            // bits of a pass
+constexpr int kSegMaxThreads = 128;                        // of a CTA of the sums
+constexpr int kSegMaxWindow = 128;                         // sorted positions of such a CTA
+constexpr int kSegMinWindow = 8;
 constexpr int kClusterThreads = 1024;                      // of each CTA of the one-launch sort
 constexpr int kMaxSortCluster = 16;
 constexpr int64_t kClusterSortKeys = 8 * kClusterThreads * kMaxSortCluster;
@@ -157,7 +160,7 @@ struct SortParams {
     uint32_t *hist;        // [passes][tiles][1 << bits], zero before the first pass
     uint32_t *present;     // bitmap of ids with a token, zero before the first pass (nullptr: not wanted)
     int zero_present;      // one-launch sort: zero the bitmap itself
-    uint32_t *ready;       // one-launch sort: set to 1 once the bitmap is complete
+    uint32_t *ready;       // [0] one-launch sort: set to 1 once the bitmap is complete; [1] zero for the sums
     int *status;
 };
 
@@ -167,6 +170,7 @@ struct SegmentParams {
     uint32_t vocab;
     int window;            // sorted positions of a CTA
     int windows, slices;   // CTAs of the sums: windows x column slices
+    int threads;           // of such a CTA, 8 columns each
     int nvec;
     const uint16_t *dy;
     int64_t dy_stride;
@@ -181,6 +185,9 @@ struct SegmentParams {
     int *status;
     float *partials;       // [windows][2][H]: sums of the leading and the trailing piece
     uint32_t *meta;        // [windows][2]: flags and the trailing piece's id
+    uint32_t *cut;         // [windows]: the windows in which a cut run starts, *cuts of them
+    uint32_t *cuts;
+    int join_lanes;        // threads of the join over a piece's columns, 8 each
 };
 
 cudaError_t launch_embed_fwd(const EmbedFwdParams &p, cudaStream_t stream);

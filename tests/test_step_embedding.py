@@ -129,11 +129,41 @@ def test_gradient(cake, kind, T, H, V):
 @pytest.mark.gpu
 @pytest.mark.parametrize("seed", range(6))
 def test_runs_across_windows(cake, seed):
-    # enough tokens and columns for every window size (shapes choose 32, 64 or 128)
+    # enough tokens and columns for the longer windows (shapes choose 8 to 128)
     T, H = [(3000, 64), (40_000, 64), (90_000, 64), (160_000, 64), (50_000, 1032), (30_000, 2056)][seed]
     dy = torch.randn(T, H, generator=gen(seed)).to(BF16).to(DEV)
     ids = make_ids("runs", T, 100_000, seed)
     check_bwd(cake, dy, ids.to(DEV), 100_000, 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [(300, 64), (3000, 520), (9000, 1544), (25_000, 64), (25_000, 264), (6000, 4104)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_short_runs_across_short_windows(cake, T, H, accumulate):
+    # windows of 8 and 16 (of 32 with the widest rows), runs that end at, before and after their ends and overruns
+    lengths = [1, 2, 7, 8, 9, 10, 15, 16, 17, 18, 23, 24, 25, 31, 32, 33, 34, 40, 64, 65, 100]
+    g = gen(T + H)
+    order = torch.randperm(len(lengths), generator=g).tolist()
+    ids, k = [], 0
+    while len(ids) < T:
+        ids += [k] * lengths[order[k % len(order)]]
+        k += 1
+    ids = torch.tensor(ids[:T])[torch.randperm(T, generator=g)].to(DEV)
+    dy = torch.randn(T, H, generator=g).to(BF16).to(DEV)
+    base = torch.randn(k, H, generator=g).to(DEV) if accumulate else None
+    check_bwd(cake, dy, ids, k, 0.5, None, base, accumulate)
+    ids[ids == 3] = -1
+    check_bwd(cake, dy, ids, k, 0.5, k // 2, base, accumulate)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [(70_000, 64), (300_000, 8)])
+def test_one_id_has_most_tokens(cake, T, H):
+    # a cut run of thousands of pieces, more than a CTA looks at in one step
+    ids = make_ids("log", T, 500, 3)
+    ids[torch.rand(T, generator=gen(T)) < 0.9] = 250
+    dy = torch.randn(T, H, generator=gen(H)).to(BF16).to(DEV)
+    check_bwd(cake, dy, ids.to(DEV), 500, 1.0)
 
 
 @pytest.mark.gpu
