@@ -352,9 +352,9 @@ constexpr int kSwBwdThreads = 32 * (kSwBwdWarps + 4);
 static_assert(kSwBwdThreads == 32 * (kSwBwdManyWarps + 1), "both forms launch 16 warps");
 
 // MANY: 15 consumer warps instead of 12, for rows of 5 or 7 warps, of which 12
-// leave two or five without work, and for rows of at most 256 columns, whose
-// sums take half the registers (GB300, 2^27 values: H = 2560 272 us against 307,
-// 5120 282 against 322, 7168 292 against 328, 256 265 against 283).
+// leave two or five without work, and for threads of 8 columns, whose sums take
+// half the registers (GB300, 2^27 values: H = 2560 272 us against 307, 5120 282
+// against 322, 7168 292 against 328, 256 265 against 283).
 template <int VPT, int GATE, bool CL, int RW, bool MANY = false>
 __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p)
 {
@@ -641,7 +641,12 @@ static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int clust
     const int nvec = (H / 8 + cluster - 1) / cluster; // of a CTA
     p.cluster = cluster;
     p.cols = 8 * nvec;
-    p.vpt = H <= 256 ? 1 : 2;
+    // 16 columns a thread, but 8 where that leaves fewer lanes without work: rows
+    // of up to 256 columns, and the backward's of 520 to 768, on 3 warps instead
+    // of 2 (GB300, 2^27 values: H = 520 415 us against 495, 768 290 against 339;
+    // rows of 1032 to 1280 on 5 warps instead of 3: 354 to 291 against 349 to 289)
+    const int narrow = (nvec + 31) / 32;
+    p.vpt = narrow == 1 || (backward && cluster == 1 && narrow == 3) ? 1 : 2;
     p.W = (nvec + 32 * p.vpt - 1) / (32 * p.vpt);
     p.groups = groups;
     const bool many = p.vpt == 1 || ((p.W == 5 || p.W == 7) && cluster <= 2);
@@ -761,6 +766,11 @@ static cudaError_t launch_bwd_gate(const SandwichBwdParams &p, const SandwichPla
         return cudaErrorInvalidValue;
     const int threads = kSwBwdThreads;
     const int rw = row_warps(plan.W * plan.cluster);
+    if (plan.vpt == 1 && plan.W > 1) {
+        if (plan.groups * plan.W > kSwBwdManyWarps || plan.cluster > 1 || rw != 8)
+            return cudaErrorInvalidValue;
+        return launch_rows(sandwich_bwd_kernel<1, GATE, false, 8, true>, p, plan, threads, stream);
+    }
     if (plan.groups * plan.W > kSwBwdWarps) {
         if (plan.groups * plan.W > kSwBwdManyWarps)
             return cudaErrorInvalidValue;

@@ -154,6 +154,16 @@ def test_in_place_forward(cake):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H", [8, 256, 264, 512, 520, 640, 704, 768, 776, 1000, 1024, 1280, 2056, 2560, 3584, 4608])
+def test_row_widths(cake, H):
+    # a CTA's first, middle and last tiles of every layout of warps to rows
+    gate = ("none", "row", "elem")[H // 8 % 3]
+    c = case(2501 if H <= 256 else 1501, H, gate, device=DEV)
+    _, h, r1, r2 = check_fwd(cake, c, 0.5)
+    check_bwd(cake, c, 0.5, h=h, r=(r1, r2))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [4096, 20011])
 def test_many_rows(cake, T):
     c = case(T, 768, "row", device=DEV, offset=1.0)
