@@ -13,8 +13,8 @@
 // the ids alone, and every row of dtable has one writer.
 //
 // HBM bounds the lookup and, where there are many tokens or rows, the gradient
-// (GB300: T = 65536, H = 5120 lookup 142 us; the whole gradient of 131072 x 2048
-// from 8192 tokens 162 us, 6.8 TB/s; 65536 tokens added at H = 4096 185 us, of
+// (GB300: T = 65536, H = 5120 lookup 141 us; the whole gradient of 131072 x 2048
+// from 8192 tokens 160 us, 6.9 TB/s; 65536 tokens added at H = 4096 184 us, of
 // which the sort is 20 us and the join 12 us).
 #include <mutex>
 
@@ -41,6 +41,7 @@ constexpr int kEmbedThreads = 256;
 template <bool F32>
 __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const __grid_constant__ EmbedFwdParams p)
 {
+    pdl_wait();
     const int lane = threadIdx.x & 31;
     const uint32_t per_row = (uint32_t)((p.nvec + 127) / 128);
     const uint64_t items = (uint64_t)p.tokens * per_row;
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_cluster_sort_kernel(
     ClusterSortSmem<PER> &m = *reinterpret_cast<ClusterSortSmem<PER> *>(smem_raw);
     const int bins = 1 << p.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t C = gridDim.x, rank_c = cluster_ctarank();
+    pdl_wait();
     const uint32_t first = rank_c * kKeys + warp * 32 * PER + lane; // key j: first + 32 j
     if (p.present && p.zero_present)
         for (uint32_t i = blockIdx.x * kClusterThreads + threadIdx.x; i < (p.vocab + 31) / 32;
@@ -740,6 +742,24 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const __grid_c
 
 // ------------------------------------------------------------------ launch
 
+// A launch may start while the one before it in the stream drains; the kernels
+// wait for its end before they touch memory.
+template <class P>
+static cudaError_t launch_dependent(void (*kern)(P), const P &p, int ctas, int threads, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 cudaError_t launch_embed_fwd(const EmbedFwdParams &p, cudaStream_t stream)
 {
     const uint64_t items = (uint64_t)p.tokens * ((p.nvec + 127) / 128);
@@ -747,11 +767,8 @@ cudaError_t launch_embed_fwd(const EmbedFwdParams &p, cudaStream_t stream)
     // resident ones in a loop (GB300, T = 65536, H = 5120: 144 against 164 us)
     const uint64_t want = (items + kEmbedThreads / 32 - 1) / (kEmbedThreads / 32);
     const int ctas = (int)(want < (1u << 30) ? want : (1u << 30));
-    if (p.table_f32)
-        embed_fwd_kernel<true><<<ctas, kEmbedThreads, 0, stream>>>(p);
-    else
-        embed_fwd_kernel<false><<<ctas, kEmbedThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(p.table_f32 ? embed_fwd_kernel<true> : embed_fwd_kernel<false>, p, ctas, kEmbedThreads,
+                            stream);
 }
 
 cudaError_t ensure_smem_attr(const void *kernel, size_t smem);
@@ -770,13 +787,15 @@ static cudaError_t launch_cluster_sort(const SortParams &p, int ctas, cudaStream
     cfg.blockDim = dim3(kClusterThreads);
     cfg.dynamicSmemBytes = sizeof(ClusterSortSmem<PER>);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, embed_cluster_sort_kernel<PER>, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
@@ -802,22 +821,6 @@ cudaError_t launch_embed_sort(const SortParams &p, uint64_t **sorted, cudaStream
     }
     *sorted = p.pairs[(p.passes - 1) & 1];
     return cudaGetLastError();
-}
-
-static cudaError_t launch_dependent(void (*kern)(SegmentParams), const SegmentParams &p, int ctas, int threads,
-                                    cudaStream_t stream)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
-    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 cudaError_t launch_embed_segments(const SegmentParams &p, cudaStream_t stream)

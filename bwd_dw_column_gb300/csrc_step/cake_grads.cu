@@ -19,7 +19,7 @@
 // below 2^-149 against a sum of 2^-60 or more.
 //
 // HBM bounds both kernels: a norm reads once, clipping reads twice beyond L2
-// and writes once (GB300: the norm of 3.1 G FP32 values 1.69 ms, 7.4 TB/s; 0.65 G
+// and writes once (GB300: the norm of 3.1 G FP32 values 1.66 ms, 7.5 TB/s; 0.65 G
 // BF16 values clipped into FP32 0.79 ms, 6.6 TB/s with the second read).
 #include "../csrc/cake_device.cuh"
 #include "cake_step_launch.h"
@@ -166,6 +166,7 @@ __device__ __forceinline__ double cta_sum(double v)
 template <int N>
 __global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const __grid_constant__ GradParams<N> p)
 {
+    pdl_wait();
     double acc = 0.0;
     int i = 0;
     for (uint32_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(kGradOneThreads)
     constexpr int kWarps = kGradOneThreads / 32, kPer = kGradPiece / 32;
     __shared__ double part[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
     double acc = 0.0;
     for (uint32_t c = warp; c < p.chunks; c += kWarps) {
         const GradDesc &d = p.t[find_tensor(p, c, 0, p.n - 1)];
@@ -327,31 +329,34 @@ __global__ void __launch_bounds__(kGradOneThreads)
 
 // ------------------------------------------------------------------ launch
 
-template <int N>
-cudaError_t launch_grad_sumsq(const GradParams<N> &p, int ctas, cudaStream_t stream)
-{
-    grad_sumsq_kernel<N><<<ctas, kGradThreads, 0, stream>>>(p);
-    return cudaGetLastError();
-}
-
-static cudaLaunchConfig_t dependent_config(int ctas, cudaLaunchAttribute *attr, bool dependent, cudaStream_t stream)
+// A launch that may start while the one before it in the stream drains.
+static cudaLaunchConfig_t dependent_config(int ctas, int threads, cudaLaunchAttribute *attr, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kGradThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = stream;
     attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr->val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = dependent ? 1 : 0;
+    cfg.numAttrs = 1;
     return cfg;
 }
 
 template <int N>
-cudaError_t launch_grad_clip(const GradParams<N> &p, int ctas, bool after_norm, cudaStream_t stream)
+cudaError_t launch_grad_sumsq(const GradParams<N> &p, int ctas, cudaStream_t stream)
 {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = dependent_config(ctas, &attr, after_norm, stream);
+    const cudaLaunchConfig_t cfg = dependent_config(ctas, kGradThreads, &attr, stream);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, grad_sumsq_kernel<N>, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int N>
+cudaError_t launch_grad_clip(const GradParams<N> &p, int ctas, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = dependent_config(ctas, kGradThreads, &attr, stream);
     cudaError_t e = cudaLaunchKernelEx(&cfg, grad_clip_kernel<N>, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
@@ -359,22 +364,24 @@ cudaError_t launch_grad_clip(const GradParams<N> &p, int ctas, bool after_norm, 
 cudaError_t launch_grad_final(const double *partials, int n, float *norm, cudaStream_t stream)
 {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = dependent_config(1, &attr, true, stream);
+    const cudaLaunchConfig_t cfg = dependent_config(1, kGradThreads, &attr, stream);
     cudaError_t e = cudaLaunchKernelEx(&cfg, grad_final_kernel, partials, n, norm);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 cudaError_t launch_grad_one(const GradParams<kGradFewTensors> &p, bool clip, cudaStream_t stream)
 {
-    grad_one_kernel<<<1, kGradOneThreads, 0, stream>>>(p, clip);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = dependent_config(1, kGradOneThreads, &attr, stream);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, grad_one_kernel, p, (int)clip);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 template cudaError_t launch_grad_sumsq<kGradFewTensors>(const GradParams<kGradFewTensors> &, int, cudaStream_t);
 template cudaError_t launch_grad_sumsq<kGradSomeTensors>(const GradParams<kGradSomeTensors> &, int, cudaStream_t);
 template cudaError_t launch_grad_sumsq<kGradMaxTensors>(const GradParams<kGradMaxTensors> &, int, cudaStream_t);
-template cudaError_t launch_grad_clip<kGradFewTensors>(const GradParams<kGradFewTensors> &, int, bool, cudaStream_t);
-template cudaError_t launch_grad_clip<kGradSomeTensors>(const GradParams<kGradSomeTensors> &, int, bool, cudaStream_t);
-template cudaError_t launch_grad_clip<kGradMaxTensors>(const GradParams<kGradMaxTensors> &, int, bool, cudaStream_t);
+template cudaError_t launch_grad_clip<kGradFewTensors>(const GradParams<kGradFewTensors> &, int, cudaStream_t);
+template cudaError_t launch_grad_clip<kGradSomeTensors>(const GradParams<kGradSomeTensors> &, int, cudaStream_t);
+template cudaError_t launch_grad_clip<kGradMaxTensors>(const GradParams<kGradMaxTensors> &, int, cudaStream_t);
 
 } // namespace cake

@@ -16,8 +16,8 @@
 // Both kernels stream rows through shared memory as the RMSNorm kernels do
 // (a producer warp with bulk copies, row groups of W warps as consumers,
 // bounded waits).  HBM bounds the forward (GB300, T = 16384, H = 6144, a gate a
-// row: 126 us, 0.94 of the copy rate); the backward is held by its warps'
-// instruction latencies a little below that (T = 65536, H = 4096: 531 us, 0.90).
+// row: 124 us, 0.96 of the copy rate); the backward is held by its warps'
+// instruction latencies a little below that (T = 65536, H = 4096: 530 us, 0.90).
 #include "../csrc/cake_rows.cuh"
 #include "cake_step_launch.h"
 
@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_fwd_kernel(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t r0 = blockIdx.x * L.rows_per_cta, r_end = min(L.rows, r0 + L.rows_per_cta);
     init_ring(m.s, RL);
+    pdl_wait();
     if (warp == L.groups * L.W) {
         sw_produce(m, L, p.in, nullptr, nullptr, p.gate_rows, 0, nvec, r0, r_end, p.status, p.wait_ns);
         return;
@@ -376,6 +377,7 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
     init_ring(m.s, RL);
     if (CL)
         cluster_sync_all(); // every CTA's barriers and slots exist before a remote access
+    pdl_wait();
     // Registers: 16 warps start with 128 each; the last four give 72 up, and
     // the twelve consumer warps take 24 more (12 x 152 + 4 x 56 = 16 x 128).
     constexpr int kProducer = MANY ? kSwBwdManyWarps : kSwBwdWarps;
@@ -734,13 +736,16 @@ static cudaError_t launch_rows(void (*kern)(P), const P &p, const SandwichPlan &
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = plan.smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)plan.cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    // started while the launch before it drains (GB300: 2 to 4 us less a call where calls follow one another)
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)plan.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = plan.cluster > 1 ? 1 : 0;
+    cfg.numAttrs = plan.cluster > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }

@@ -423,7 +423,7 @@ cudaError_t run_grads(const void *const *data, const int64_t *counts, const int3
         p.eps = eps;
         p.in_place = outs == nullptr;
         p.norm = first ? norm : nullptr;
-        cudaError_t e = launch_grad_clip(p, ctas, first, s);
+        cudaError_t e = launch_grad_clip(p, ctas, s);
         if (e != cudaSuccess)
             return e;
         first = false;

@@ -113,7 +113,7 @@ struct GradParams {
 template <int N>
 cudaError_t launch_grad_sumsq(const GradParams<N> &p, int ctas, cudaStream_t stream);
 template <int N>
-cudaError_t launch_grad_clip(const GradParams<N> &p, int ctas, bool after_norm, cudaStream_t stream);
+cudaError_t launch_grad_clip(const GradParams<N> &p, int ctas, cudaStream_t stream);
 cudaError_t launch_grad_one(const GradParams<kGradFewTensors> &p, bool clip, cudaStream_t stream);
 cudaError_t launch_grad_final(const double *partials, int n, float *norm, cudaStream_t stream);
 

@@ -164,3 +164,76 @@ def test_given_streams_and_host_threads(cake):
         for i in range(6):
             for x, y in zip(a[0], b[i]):
                 assert torch.equal(x, y)
+
+
+def _calls(cake, seed):
+    """Inputs, and a call of every operator that reads them and returns what it wrote."""
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g).to(BF16).to(DEV)  # noqa: E731
+    big, table_rows, n = 5_000_000, 700, 3000
+    ins = {"z": r(n, H), "x": r(n, H), "dy": r(n, H), "table": r(table_rows, H).float(),
+           "ids": torch.randint(0, table_rows, (n,), generator=g).to(DEV),
+           "far": torch.randint(0, big, (n,), generator=g).to(DEV)}
+    w = torch.ones(H, device=DEV)
+    small = torch.full((n, 8), 0.5, dtype=BF16, device=DEV)
+    _, h, a, b = cake.cake_sandwich_fwd(ins["z"], ins["x"], w, w)
+
+    def clip(t):
+        out = torch.empty(t.shape, dtype=torch.float32, device=DEV)
+        return cake.cake_clip_grad_norm([t], 1.0, out=[out]), out
+
+    return ins, {
+        "fwd": ("z", lambda i: cake.cake_sandwich_fwd(i["z"], i["x"], w, w)),
+        "bwd": ("dy", lambda i: cake.cake_sandwich_bwd(i["dy"], h, i["z"], a, b, w, w)[:4]),
+        "norm": ("x", lambda i: (cake.cake_grad_norm([i["x"], i["z"]]),)),
+        "short": ("table", lambda i: (cake.cake_grad_norm([i["table"][:9]]),)),
+        "clip": ("x", lambda i: clip(i["x"])),
+        "clip short": ("z", lambda i: clip(i["z"][:20])),
+        "lookup": ("ids", lambda i: (cake.cake_embedding_fwd(i["ids"], i["table"]),)),
+        "gradient": ("dy", lambda i: (cake.cake_embedding_bwd(i["dy"], i["ids"], table_rows),)),
+        "gradient, many rows": ("far", lambda i: (cake.cake_embedding_bwd(small, i["far"], big),)),
+    }
+
+
+@pytest.mark.parametrize("name", ["fwd", "bwd", "norm", "short", "clip", "clip short", "lookup", "gradient",
+                                  "gradient, many rows"])
+def test_waits_for_the_work_before(cake, name):
+    """A call right behind the kernel, copy or fill that writes its input reads what that has written, eagerly and in
+    a graph, and its outputs are whole for the work behind it."""
+    ins, calls = _calls(cake, 11)
+    key, call = calls[name]
+    other = _calls(cake, 12)[0][key]
+    zero, slow = torch.zeros_like(other), torch.randn(4096, 4096, device=DEV)
+    want = {}
+    for k, src in (("a", ins[key].clone()), ("b", other), ("zero", zero)):
+        ins[key].copy_(src)
+        torch.cuda.synchronize()
+        want[k] = src, [t.clone() for t in call(ins)]
+        torch.cuda.synchronize()
+
+    def run():
+        got = []
+        for k in ("a", "b", "zero", "b", "a"):
+            slow @ slow  # work that the writer of the input waits behind
+            if k == "zero":
+                ins[key].zero_()
+            else:
+                ins[key].copy_(want[k][0])
+            got.append((k, [t.clone() for t in call(ins)]))
+            ins[key].copy_(want["a"][0])  # and one behind the call, over what it has read
+        return got
+
+    def check(got):
+        torch.cuda.synchronize()
+        for k, ts in got:
+            for t, w in zip(ts, want[k][1]):
+                assert torch.equal(t, w) or (torch.equal(t.isnan(), w.isnan()) and torch.equal(t.nan_to_num(), w.nan_to_num()))
+
+    for _ in range(3):
+        check(run())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(2):
+        graph.replay()
+        check(got)
