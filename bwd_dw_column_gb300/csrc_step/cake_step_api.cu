@@ -299,7 +299,7 @@ cake_status check_grads(const void *const *data, const int64_t *counts, const in
         if (counts[i] < 0 || !good_dtype(dtypes[i]) || (outs && !good_dtype(out_dtypes[i])))
             return CAKE_ERR_INVALID;
         chunks += (uint64_t)(counts[i] / kGradChunk) + 1;
-        if (chunks >= (uint64_t(1) << 32)) // a launch counts its chunks in 32 bits
+        if (chunks >= (uint64_t(1) << 31)) // a launch counts its chunks in 32 bits
             return CAKE_ERR_UNSUPPORTED;
         if (counts[i] == 0)
             continue;
