@@ -663,12 +663,12 @@ __device__ __forceinline__ void add_pieces(const float4 *piece, size_t step, uin
 // (64 to 1024 of them), its G groups of L threads every G-th of the run's pieces
 // each, and the groups' sums are added in their order.  A common id's run has
 // hundreds of pieces where windows are short (GB300, ncu, T = 65536 with
-// frequencies of 1/k: H = 64 7 us, H = 512 17 us; with the pieces of a run one
+// frequencies of 1/k: H = 64 7 us, H = 512 11 us; with the pieces of a run one
 // after another 21 and 25 us).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtas = 152 * 4;
 
-__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const __grid_constant__ SegmentParams p)
+__global__ void __launch_bounds__(kJoinThreads, 4) embed_join_kernel(const __grid_constant__ SegmentParams p)
 {
     __shared__ int last;
     __shared__ __align__(16) float part[8 * kJoinThreads]; // [G][8 L]
@@ -713,8 +713,10 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const __grid_c
             const float4 *piece =
                 reinterpret_cast<const float4 *>(p.partials + (size_t)(w + 1) * 2 * H + col) + (size_t)g * step;
             const uint32_t m = g < n ? (n - g + G - 1) / G : 0;
-            for (uint32_t u = 0; u < m; u += 8)
-                add_pieces<8>(piece + (size_t)u * G * step, G * step, min(8u, m - u), s);
+            // four at a time and four CTAs an SM (H = 512: 52 us in all, 56 with eight
+            // at a time, which leave room for two CTAs)
+            for (uint32_t u = 0; u < m; u += 4)
+                add_pieces<4>(piece + (size_t)u * G * step, G * step, min(4u, m - u), s);
         }
         float4 *o = reinterpret_cast<float4 *>(part + 8 * threadIdx.x);
         o[0] = make_float4(s[0], s[1], s[2], s[3]);
