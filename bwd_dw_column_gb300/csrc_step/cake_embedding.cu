@@ -113,19 +113,19 @@ __device__ __forceinline__ uint64_t make_pair(const SortParams &p, uint32_t t)
     return ((uint64_t)key << 32) | t;
 }
 
-// Sets the keys' bits in the bitmap of ids with a token.  A bit that is set
-// already (a common id's) costs a load only; all loads go out together.
+// Sets the keys' bits in the bitmap of ids with a token: one lane for the equal
+// keys of a step, and none for a bit that is set already (a common id's).
 template <int N>
 __device__ __forceinline__ void mark_present(const SortParams &p, const uint32_t (&key)[N])
 {
-    uint32_t w[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-        w[j] = key[j] < p.vocab ? __ldcg(p.present + (key[j] >> 5)) : 0xffffffffu;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (!((w[j] >> (key[j] & 31)) & 1u))
-            atomicOr(p.present + (key[j] >> 5), 1u << (key[j] & 31));
+    for (int j = 0; j < N; ++j) {
+        const bool one = (__match_any_sync(0xffffffffu, key[j]) & ((1u << (threadIdx.x & 31)) - 1)) == 0;
+        uint32_t *w = p.present + (key[j] >> 5);
+        const uint32_t bit = 1u << (key[j] & 31);
+        if (one && key[j] < p.vocab && !(__ldcg(w) & bit))
+            atomicOr(w, bit);
+    }
 }
 
 // Ranks a warp's 32 x N keys among those of the warp with the same digit, in
@@ -480,22 +480,31 @@ __device__ __forceinline__ void store_row8(const SegmentParams &p, uint32_t id, 
     }
 }
 
-// Zeroes the rows of dtable whose id has no token: a warp per row.  (A CTA for
-// every 32 KB: 165 us for 131072 x 2048 FP32 values, against 174 and 216 us
-// with 16 and 6 CTAs an SM in a loop.)
+// Zeroes the rows of dtable whose id has no token: a warp takes as many rows as
+// make 8 KB, 32 at most.  (Warps that come and go: 165 us for 131072 x 2048 FP32
+// values, against 174 and 216 us with 16 and 6 CTAs an SM in a loop.)
 __device__ void fill_rows(const SegmentParams &p, uint32_t part, uint32_t parts)
 {
-    const int lane = threadIdx.x & 31;
-    const uint32_t warps = parts * (blockDim.x / 32);
-    const int vecs = p.dtable_f32 ? 2 * p.nvec : p.nvec;
-    for (uint32_t v = part * (blockDim.x / 32) + (threadIdx.x >> 5); v < p.vocab; v += warps) {
-        if ((__ldcg(p.present + (v >> 5)) >> (v & 31)) & 1u)
-            continue;
-        uint4 *o = p.dtable_f32
-                       ? reinterpret_cast<uint4 *>(static_cast<float *>(p.dtable) + (int64_t)v * p.dtable_stride)
-                       : reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dtable) + (int64_t)v * p.dtable_stride);
-        for (int i = lane; i < vecs; i += 32)
-            __stcs(o + i, make_uint4(0, 0, 0, 0));
+    const uint32_t lane = threadIdx.x & 31, R = (uint32_t)p.fill_rows;
+    const uint64_t step = (uint64_t)parts * (blockDim.x / 32) * R;
+    const uint32_t vecs = p.dtable_f32 ? 2 * p.nvec : p.nvec;
+    const int64_t stride = p.dtable_stride * (p.dtable_f32 ? 4 : 2);
+    for (uint64_t v0 = ((uint64_t)part * (blockDim.x / 32) + (threadIdx.x >> 5)) * R; v0 < p.vocab; v0 += step) {
+        const uint32_t has = __ldcg(p.present + (v0 >> 5)) >> (v0 & 31); // (R rows lie in one word)
+        const uint32_t n = min((uint64_t)R, p.vocab - v0);
+        uint8_t *row0 = static_cast<uint8_t *>(p.dtable) + (int64_t)v0 * stride;
+        if (vecs >= 32) {
+            for (uint32_t r = 0; r < n; ++r)
+                if (!((has >> r) & 1u))
+                    for (uint32_t i = lane; i < vecs; i += 32)
+                        __stcs(reinterpret_cast<uint4 *>(row0 + r * stride) + i, make_uint4(0, 0, 0, 0));
+        } else {
+            for (uint32_t i = lane; i < n * vecs; i += 32) {
+                const uint32_t r = i / vecs;
+                if (!((has >> r) & 1u))
+                    __stcs(reinterpret_cast<uint4 *>(row0 + r * stride) + (i - r * vecs), make_uint4(0, 0, 0, 0));
+            }
+        }
     }
 }
 

@@ -668,8 +668,11 @@ extern "C" cake_status cake_embedding_bwd(const cake_tensor *dy, const void *ids
     g.dtable_stride = dtable_stride;
     g.accumulate = accumulate != 0;
     g.present = q.present;
-    const int64_t fill_rows = std::max<int64_t>(e.threads / 32, 32768 / (hidden * (int64_t)size));
-    g.fill_ctas = accumulate ? 0 : (int)std::min<int64_t>((vocab + fill_rows - 1) / fill_rows, 1 << 20);
+    g.fill_rows = 1;
+    while (g.fill_rows < 32 && g.fill_rows * 2 * hidden * (int64_t)size <= 8192)
+        g.fill_rows *= 2;
+    const int64_t fill = g.fill_rows * (e.threads / 32);
+    g.fill_ctas = accumulate ? 0 : (int)std::min<int64_t>((vocab + fill - 1) / fill, 1 << 20);
     g.ready = e.cluster && !accumulate ? q.ready : nullptr;
     g.status = q.status;
     g.partials = reinterpret_cast<float *>(at + 2 * e.pairs_bytes);

@@ -181,6 +181,7 @@ struct SegmentParams {
     int accumulate;
     const uint32_t *present;
     int fill_ctas;         // CTAs before the sums' that zero the rows without a token
+    int fill_rows;         // rows that a warp of those takes at a time: a power of two, at most 32
     const uint32_t *ready; // those start at this flag; nullptr: after the sort
     int *status;
     float *partials;       // [windows][2][H]: sums of the leading and the trailing piece
