@@ -237,3 +237,82 @@ def test_waits_for_the_work_before(cake, name):
     for _ in range(2):
         graph.replay()
         check(got)
+
+
+@pytest.mark.parametrize("name", ["fwd", "bwd", "norm", "short", "clip", "clip short", "lookup", "gradient",
+                                  "gradient, many rows"])
+def test_waits_for_another_stream(cake, name):
+    """A call behind a wait for another stream, which writes its input late, reads what that has written; work of
+    the other stream behind the call does not reach it."""
+    ins, calls = _calls(cake, 21)
+    key, call = calls[name]
+    other = _calls(cake, 22)[0][key]
+    slow, side = torch.randn(4096, 4096, device=DEV), torch.cuda.Stream()
+    want = {}
+    for k, src in (("a", ins[key].clone()), ("b", other)):
+        ins[key].copy_(src)
+        torch.cuda.synchronize()
+        want[k] = src, [t.clone() for t in call(ins)]
+        torch.cuda.synchronize()
+    spot = torch.zeros(8, device=DEV)
+
+    def run():
+        main, got, made = torch.cuda.current_stream(), [], []
+        for k in ("a", "b", "a"):
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                made.append(slow @ slow)
+                ins[key].copy_(want[k][0])
+            spot.add_(1)  # a short kernel of this stream before the wait
+            main.wait_stream(side)
+            got.append((k, call(ins)))
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                ins[key].copy_(want["b" if k == "a" else "a"][0])
+        main.wait_stream(side)
+        return got, made
+
+    def check(got):
+        torch.cuda.synchronize()
+        for k, ts in got:
+            for t, w in zip(ts, want[k][1]):
+                assert torch.equal(t, w)
+
+    for _ in range(3):
+        check(run()[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, made = run()
+    for _ in range(2):
+        graph.replay()
+        check(got)
+
+
+@pytest.mark.parametrize("rows", [300, 40_000])
+def test_behind_the_norms_own_kernels(cake, rows):
+    """The norm's backward, whose gradients the step's operators take up at once."""
+    g = torch.Generator().manual_seed(rows)
+    x, dy, z = (torch.randn(rows, H, generator=g).to(BF16).to(DEV) for _ in range(3))
+    w = (1 + 0.1 * torch.randn(H, generator=g)).to(DEV)
+    ids = torch.randint(0, 900, (rows,), generator=g).to(DEV)
+    _, h, a, b = cake.cake_sandwich_fwd(z, x, w, w)
+
+    def run(wait):
+        pause = torch.cuda.synchronize if wait else lambda: None
+        _, rstd = cake.cake_rmsnorm_fwd(x, w, 1e-6)
+        dx, dw = cake.cake_rmsnorm_bwd(dy, x, rstd, w, deterministic=True)[:2]
+        pause()
+        norm = cake.cake_grad_norm([dw, dx])
+        pause()
+        dx2, dz, *_ = cake.cake_sandwich_bwd(dx, h, z, a, b, w, w)
+        pause()
+        table = cake.cake_embedding_bwd(dx2, ids, 900)
+        pause()
+        _, rstd2 = cake.cake_rmsnorm_fwd(dz, w, 1e-6)
+        torch.cuda.synchronize()
+        return dx, dw, norm, dx2, dz, table, rstd2
+
+    want = run(True)
+    for _ in range(5):
+        for got, w_ in zip(run(False), want):
+            assert torch.equal(got, w_)
