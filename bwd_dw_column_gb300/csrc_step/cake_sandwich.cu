@@ -353,10 +353,13 @@ constexpr int kSwBwdThreads = 32 * (kSwBwdWarps + 4);
 static_assert(kSwBwdThreads == 32 * (kSwBwdManyWarps + 1), "both forms launch 16 warps");
 
 // MANY: 15 consumer warps instead of 12, for rows of 5 or 7 warps, of which 12
-// leave two or five without work, and for threads of 8 columns, whose sums take
-// half the registers (GB300, 2^27 values: H = 2560 272 us against 307, 5120 282
+// leave two or five without work, and for threads of 8 or 12 columns, whose sums
+// take fewer registers (GB300, 2^27 values: H = 2560 272 us against 307, 5120 282
 // against 322, 7168 292 against 328, 256 265 against 283).
-template <int VPT, int GATE, bool CL, int RW, bool MANY = false>
+//
+// HALF: a thread takes 4 columns more, the half vectors behind the row's first
+// 32 W vectors: 12 columns a thread.
+template <int VPT, int GATE, bool CL, int RW, bool MANY = false, bool HALF = false>
 __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __grid_constant__ SandwichBwdParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -408,10 +411,39 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
         sw.wsm = m.w[1];
         stage_weight(sw, RL, static_cast<const uint8_t *>(p.w_pre) + v0 * (p.pre_f32 ? 32 : 16), p.pre_f32);
     }
-    auto weight = [&](int which, int v, float2(&w2)[4]) { sw_weight(m.w[which], nvec, v, w2); };
-    float2 hi1[VPT][4], lo1[VPT][4], hi2[VPT][4], lo2[VPT][4]; // dw_post, dw_pre
+    // Piece k of the thread's columns is vector k * vstride + gtid, or half
+    // vector gtid behind all of those: index(k) counts in vectors or halves.
+    constexpr int K = VPT + HALF;
+    auto is_half = [](int k) { return HALF && k == VPT; };
+    auto index = [&](int k) { return is_half(k) ? 2 * VPT * vstride + gtid : k * vstride + gtid; };
+    auto inside = [&](int k, int v) { return v < (is_half(k) ? 2 * nvec : nvec); };
+    auto at = [&](const uint4 *row, int k, int v) { // the piece's address
+        return is_half(k) ? reinterpret_cast<const uint4 *>(reinterpret_cast<const uint2 *>(row) + v) : row + v;
+    };
+    auto load = [&](const uint4 *from, int k) {
+        if (!is_half(k))
+            return *from;
+        const uint2 a = *reinterpret_cast<const uint2 *>(from);
+        return make_uint4(a.x, a.y, 0, 0);
+    };
+    auto store = [&](uint4 *row, int k, int v, const uint32_t(&o)[4]) {
+        if (is_half(k))
+            __stcs(reinterpret_cast<uint2 *>(row) + v, make_uint2(o[0], o[1]));
+        else
+            __stcs(row + v, make_uint4(o[0], o[1], o[2], o[3]));
+    };
+    auto weight = [&](int which, int k, int v, float2(&w2)[4]) {
+        if (is_half(k)) {
+            const float4 a = reinterpret_cast<const float4 *>(m.w[which])[(v & 1) * nvec + (v >> 1)];
+            w2[0] = make_float2(a.x, a.y);
+            w2[1] = make_float2(a.z, a.w);
+        } else {
+            sw_weight(m.w[which], nvec, v, w2);
+        }
+    };
+    float2 hi1[K][4], lo1[K][4], hi2[K][4], lo2[K][4]; // dw_post, dw_pre
 #pragma unroll
-    for (int k = 0; k < VPT; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             hi1[k][q] = lo1[k][q] = hi2[k][q] = lo2[k][q] = both(0.f);
@@ -433,21 +465,23 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
                 const float2 rn = both(m.scalars[st1 * kSwMaxTile + gid].y);
                 float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f);
 #pragma unroll
-                for (int k = 0; k < VPT; ++k) {
-                    const int v = k * vstride + gtid;
-                    if (v < nvec) {
-                        const uint4 *row = gbase + st1 * sbytes + v;
-                        const uint4 h = row[0], z = row[tb], d = row[2 * tb];
+                for (int k = 0; k < K; ++k) {
+                    const int v = index(k);
+                    if (inside(k, v)) {
+                        const uint4 *row = at(gbase + st1 * sbytes, k, v);
+                        const uint4 h = load(row, k), z = load(row + tb, k), d = load(row + 2 * tb, k);
                         uint4 g = make_uint4(0, 0, 0, 0), e = make_uint4(0, 0, 0, 0);
                         if (GATE == 2)
-                            g = row[3 * tb];
+                            g = load(row + 3 * tb, k);
                         if (has_dh)
-                            e = row[dh_off];
+                            e = load(row + dh_off, k);
                         float2 w1[4], w2[4];
-                        weight(0, v, w1);
-                        weight(1, v, w2);
+                        weight(0, k, v, w1);
+                        weight(1, k, v, w2);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
+                            if (is_half(k) && q >= 2)
+                                continue;
                             const float2 hq = bf2(word(h, q)), dq = bf2(word(d, q));
                             const float2 a = mul2(dq, w2[q]);
                             const float2 bz =
@@ -523,22 +557,24 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
                 uint4 *dx = out_row(p.dx, r, L.nh) + vo, *dz = out_row(p.dz, r, L.nh) + vo;
                 uint4 *dg = GATE == 2 && p.dgate.base ? out_row(p.dgate, r, L.nh) + vo : nullptr;
 #pragma unroll
-                for (int k = 0; k < VPT; ++k) {
-                    const int v = k * vstride + gtid;
-                    if (v < nvec && !abort) {
-                        const uint4 *row = gbase + st2 * sbytes + v;
-                        const uint4 h = row[0], z = row[tb], d = row[2 * tb];
+                for (int k = 0; k < K; ++k) {
+                    const int v = index(k);
+                    if (inside(k, v) && !abort) {
+                        const uint4 *row = at(gbase + st2 * sbytes, k, v);
+                        const uint4 h = load(row, k), z = load(row + tb, k), d = load(row + 2 * tb, k);
                         uint4 g = make_uint4(0, 0, 0, 0), e = make_uint4(0, 0, 0, 0);
                         if (GATE == 2)
-                            g = row[3 * tb];
+                            g = load(row + 3 * tb, k);
                         if (has_dh)
-                            e = row[dh_off];
+                            e = load(row + dh_off, k);
                         float2 w1[4], w2[4];
-                        weight(0, v, w1);
-                        weight(1, v, w2);
+                        weight(0, k, v, w1);
+                        weight(1, k, v, w2);
                         uint32_t ox[4], oz[4], og[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
+                            if (is_half(k) && q >= 2)
+                                continue;
                             const float2 zq = bf2(word(z, q));
                             const float2 a = mul2(bf2(word(d, q)), w2[q]);
                             const float2 t = fma2(nk2, bf2(word(h, q)), fma2(rn, a, bf2(word(e, q))));
@@ -550,10 +586,10 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
                                 og[q] = pack2(mul2(mul2(st, zq), w1[q]));
                             kahan2(hi1[k][q], lo1[k][q], mt, zq);
                         }
-                        __stcs(dx + v, make_uint4(ox[0], ox[1], ox[2], ox[3]));
-                        __stcs(dz + v, make_uint4(oz[0], oz[1], oz[2], oz[3]));
+                        store(dx, k, v, ox);
+                        store(dz, k, v, oz);
                         if (GATE == 2 && dg)
-                            __stcs(dg + v, make_uint4(og[0], og[1], og[2], og[3]));
+                            store(dg, k, v, og);
                     }
                 }
             }
@@ -573,14 +609,16 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
     float4 *comb = reinterpret_cast<float4 *>(m.s.ring);
     consumer_sync(RL);
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int v = k * vstride + gtid;
-        if (v < nvec)
+    for (int k = 0; k < K; ++k) {
+        const int v = index(k), pair = is_half(k) ? 2 * v : 4 * v;
+        if (inside(k, v))
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                comb[(size_t)(2 * gid) * nslot + 4 * v + q] =
+                if (is_half(k) && q >= 2)
+                    continue;
+                comb[(size_t)(2 * gid) * nslot + pair + q] =
                     make_float4(hi1[k][q].x, lo1[k][q].x, hi1[k][q].y, lo1[k][q].y);
-                comb[(size_t)(2 * gid + 1) * nslot + 4 * v + q] =
+                comb[(size_t)(2 * gid + 1) * nslot + pair + q] =
                     make_float4(hi2[k][q].x, lo2[k][q].x, hi2[k][q].y, lo2[k][q].y);
             }
     }
@@ -643,13 +681,13 @@ static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int clust
     const int nvec = (H / 8 + cluster - 1) / cluster; // of a CTA
     p.cluster = cluster;
     p.cols = 8 * nvec;
-    // 16 columns a thread, but 8 where that leaves fewer lanes without work: rows
-    // of up to 256 columns, and the backward's of 520 to 768, on 3 warps instead
-    // of 2 (GB300, 2^27 values: H = 520 415 us against 495, 768 290 against 339;
-    // rows of 1032 to 1280 on 5 warps instead of 3: 354 to 291 against 349 to 289)
-    const int narrow = (nvec + 31) / 32;
-    p.vpt = narrow == 1 || (backward && cluster == 1 && narrow == 3) ? 1 : 2;
-    p.W = (nvec + 32 * p.vpt - 1) / (32 * p.vpt);
+    // 8 columns a thread up to 256, 16 beyond; the backward of rows of one CTA
+    // takes 12 where they leave fewer lanes without work (GB300, 2^27 values:
+    // H = 264 321 us against 444, 384 253 against 310, 640 330 against 404, 1032 283
+    // against 348, 1152 261 against 317, 1664 279 against 313; the copy takes 238)
+    p.half = backward && H <= 2048 && nvec > 32 && (nvec + 47) / 48 * 48 < (nvec + 63) / 64 * 64;
+    p.vpt = nvec <= 32 || p.half ? 1 : 2;
+    p.W = p.half ? (nvec + 47) / 48 : (nvec + 32 * p.vpt - 1) / (32 * p.vpt);
     p.groups = groups;
     const bool many = p.vpt == 1 || ((p.W == 5 || p.W == 7) && cluster <= 2);
     if (p.groups * p.W > (!backward ? 16 : many ? kSwBwdManyWarps : kSwBwdWarps))
@@ -771,10 +809,11 @@ static cudaError_t launch_bwd_gate(const SandwichBwdParams &p, const SandwichPla
         return cudaErrorInvalidValue;
     const int threads = kSwBwdThreads;
     const int rw = row_warps(plan.W * plan.cluster);
-    if (plan.vpt == 1 && plan.W > 1) {
-        if (plan.groups * plan.W > kSwBwdManyWarps || plan.cluster > 1 || rw != 8)
+    if (plan.half) {
+        if (plan.groups * plan.W > kSwBwdManyWarps || plan.cluster > 1 || (plan.W > 1 && rw != 8))
             return cudaErrorInvalidValue;
-        return launch_rows(sandwich_bwd_kernel<1, GATE, false, 8, true>, p, plan, threads, stream);
+        return plan.W == 1 ? launch_rows(sandwich_bwd_kernel<1, GATE, false, 1, true, true>, p, plan, threads, stream)
+                           : launch_rows(sandwich_bwd_kernel<1, GATE, false, 8, true, true>, p, plan, threads, stream);
     }
     if (plan.groups * plan.W > kSwBwdWarps) {
         if (plan.groups * plan.W > kSwBwdManyWarps)

@@ -18,6 +18,7 @@ namespace cake {
 // clusters) share the rows.
 struct SandwichPlan {
     int cluster, cols, vpt, W, groups, stages, per_sm, parts;
+    bool half; // backward: a thread takes 4 columns more than 8 vpt
     uint32_t rows_per_cta;
     size_t smem;
 };

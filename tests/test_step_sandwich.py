@@ -154,7 +154,8 @@ def test_in_place_forward(cake):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("H", [8, 256, 264, 512, 520, 640, 704, 768, 776, 1000, 1024, 1280, 2056, 2560, 3584, 4608])
+@pytest.mark.parametrize("H", [8, 256, 264, 320, 384, 392, 512, 520, 640, 704, 768, 776, 1000, 1024, 1032, 1096, 1152, 1280, 1544,
+                               1664, 1920, 2056, 2560, 3584, 4608])
 def test_row_widths(cake, H):
     # a CTA's first, middle and last tiles of every layout of warps to rows
     gate = ("none", "row", "elem")[H // 8 % 3]
