@@ -29,7 +29,7 @@ constexpr int kSMsStep = 152;
 constexpr int kSwMaxStages = 16;
 constexpr int kSwMaxTile = 15;            // rows of a stage, at most
 constexpr int kSwSlots = 4;               // backward: rows whose partial sums may be in use
-constexpr int kSwMaxJoined = 6;           // groups whose rows span several warps, at most
+constexpr int kSwMaxJoined = 7;           // groups whose rows span several warps, at most
 constexpr int kSwMaxRowWarps = 32;        // warps of a row over its cluster, at most
 constexpr int kSwMaxCluster = 4;
 constexpr int kSwClustersOf4 = 36;        // that a GB300 holds at a time
