@@ -352,10 +352,11 @@ constexpr int kSwBwdManyWarps = 15; // ... or fifteen at 128 registers, and the 
 constexpr int kSwBwdThreads = 32 * (kSwBwdWarps + 4);
 static_assert(kSwBwdThreads == 32 * (kSwBwdManyWarps + 1), "both forms launch 16 warps");
 
-// MANY: 15 consumer warps instead of 12, for rows of 5 or 7 warps, of which 12
-// leave two or five without work, and for threads of 8 or 12 columns, whose sums
-// take fewer registers (GB300, 2^27 values: H = 2560 272 us against 307, 5120 282
-// against 322, 7168 292 against 328, 256 265 against 283).
+// MANY: up to 15 consumer warps instead of 12, for rows of 2, 5 or 7 warps, of
+// which 12 hold fewer, and for threads of 8 or 12 columns, whose sums take fewer
+// registers (GB300, 2^27 values: H = 2560 272 us against 307, 5120 282 against
+// 322, 7168 292 against 328, 256 265 against 283; 1024 with an element gate 338
+// against 349).
 //
 // HALF: a thread takes 4 columns more, the half vectors behind the row's first
 // 32 W vectors: 12 columns a thread.
@@ -689,7 +690,7 @@ static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int clust
     p.vpt = nvec <= 32 || p.half ? 1 : 2;
     p.W = p.half ? (nvec + 47) / 48 : (nvec + 32 * p.vpt - 1) / (32 * p.vpt);
     p.groups = groups;
-    const bool many = p.vpt == 1 || ((p.W == 5 || p.W == 7) && cluster <= 2);
+    const bool many = p.vpt == 1 || ((p.W == 2 || p.W == 5 || p.W == 7) && cluster <= 2);
     if (p.groups * p.W > (!backward ? 16 : many ? kSwBwdManyWarps : kSwBwdWarps))
         return false;
     // CTAs per SM: the backward's takes all registers, 28 of the forward's warps fit
@@ -732,8 +733,10 @@ SandwichPlan sandwich_plan(int H, uint32_t rows, int ntens, bool backward)
         // The most columns in work on an SM, up to the 6144 that keep HBM
         // busy; of equals the smallest cluster.  Weights, as measured on GB300
         // with 2^27 values without a gate (copy rate: 238 us): three stages
-        // against four 296 and 263 us at H = 2048, a single group against two
-        // 290 and 266 us at H = 6144; 36 clusters of 4 fit the 152 SMs.
+        // against four 296 and 263 us at H = 2048 (with an element gate seven
+        // groups of three against six of four 381 and 368 us at H = 840), a single
+        // group against two 290 and 266 us at H = 6144; 36 clusters of 4 fit the
+        // 152 SMs.
         int best = 0;
         for (int c = 1; c <= (H > 2048 ? kSwMaxCluster : 1); c *= 2)
             for (int g = kSwMaxTile; g >= 1; --g) {
@@ -743,10 +746,10 @@ SandwichPlan sandwich_plan(int H, uint32_t rows, int ntens, bool backward)
                 int score = q.cols * q.groups * q.per_sm;
                 score = score > 6144 ? 6144 : score;
                 if (q.stages < 4)
-                    score = score * 89 / 100;
+                    score = score * 85 / 100;
                 if (q.groups * q.per_sm == 1)
                     score = score * 93 / 100;
-                score = c == 4 ? score * 93 / 100 : c == 2 ? score * 98 / 100 : score;
+                score = c == 4 ? score * 93 / 100 : c == 2 ? score * 97 / 100 : score;
                 if (score > best) {
                     best = score;
                     p = q;
