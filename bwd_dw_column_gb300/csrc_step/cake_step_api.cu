@@ -325,10 +325,13 @@ cake_status check_grads(const void *const *data, const int64_t *counts, const in
     }
     if (meet(scratch, memory(norm, 4)))
         return CAKE_ERR_INVALID;
-    for (int64_t i = 0; i < n; ++i)
-        if (meet(scratch, memory(data[i], (uint64_t)counts[i] * (dtypes[i] == CAKE_FP32 ? 4 : 2))) ||
+    // (of clipping, the norm is among the written ranges below)
+    for (int64_t i = 0; i < n; ++i) {
+        const Memory in = memory(data[i], (uint64_t)counts[i] * (dtypes[i] == CAKE_FP32 ? 4 : 2));
+        if (meet(scratch, in) || (!clip && meet(memory(norm, 4), in)) ||
             (outs && meet(scratch, memory(outs[i], (uint64_t)counts[i] * (out_dtypes[i] == CAKE_FP32 ? 4 : 2)))))
             return CAKE_ERR_INVALID;
+    }
     // written ranges share memory with no other range but their own input
     const auto by_lo = [](const Range &x, const Range &y) { return x.lo < y.lo; };
     std::sort(written.begin(), written.end(), by_lo);

@@ -88,7 +88,7 @@ cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_tensor *dy, co
  * n tensors: data[i] is a device pointer (aligned to its element size) to
  * counts[i] contiguous values of dtypes[i]; BF16 and FP32 may be mixed.  The
  * arrays themselves are HOST memory, read before the call returns.  norm: one
- * FP32 device value.  Squares whose FP32 sum would overflow or vanish are
+ * FP32 device value, in none of the tensors (CAKE_ERR_INVALID).  Squares whose FP32 sum would overflow or vanish are
  * summed again in FP64, so norm is right to FP32 rounding over the whole
  * range of the types.  A NaN or infinity gives a NaN or infinite norm, and
  * clipping then follows the formula (infinite: coef is 0, and infinity * 0 is
@@ -98,8 +98,7 @@ cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_tensor *dy, co
  * outs NULL (out_dtypes NULL too) clips in place, and then writes nothing
  * where coef is 1.  An output may be exactly its own input or share no memory
  * with any tensor of the call; inputs may share memory with each other only
- * where they are not written (CAKE_ERR_INVALID), and norm lies in none of
- * them.  max_norm >= 0 (infinity is allowed), eps >= 0; coef is 1 where
+ * where they are not written (CAKE_ERR_INVALID).  max_norm >= 0 (infinity is allowed), eps >= 0; coef is 1 where
  * norm + eps is 0.  n at most 1000000; n = 0: norm is 0.
  */
 size_t cake_grad_norm_workspace_size(int64_t n);

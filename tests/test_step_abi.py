@@ -243,6 +243,16 @@ def test_scratch_and_ids_are_shared_with_nothing(cake):
         assert ebwd(cake, ws=place) == INVALID
 
 
+@pytest.mark.parametrize("clip", [False, True])
+@pytest.mark.parametrize("count,dtype", [(8, 0), (8, 1), (1 << 18, 0), (1, 1)])
+def test_the_norm_lies_in_no_gradient(cake, count, dtype, clip):
+    """A norm inside a tensor that the call reads would overwrite some of its values."""
+    B = A + MB
+    size = 4 if dtype else 2
+    for at in sorted({B, B + max(0, (count * size // 2) // 4 * 4), B + max(0, count * size - 4)}):
+        assert grads(cake, [A + 2 * MB, B], [4, count], [0, dtype], norm=at, ws=16 * MB, clip=clip) == INVALID, at
+
+
 def test_python_refusals_without_a_gpu(cake):
     z = torch.zeros(4, 64, dtype=torch.bfloat16)
     w = torch.ones(64)
