@@ -465,7 +465,7 @@ def cake_rmsnorm_plan_occupancy(shape, backward=True, has_extra=False, determini
 
 def cake_rmsnorm_device_status(clear: bool = True) -> int:
     """The kernels' device status word (0; 5 after a bounded wait ran out; 1 after an embedding
-    met an id outside its table).  Synchronises."""
+    met an id outside its table and no wait ran out).  Synchronises."""
     lib = load_library()
     code = ctypes.c_int(0)
     _check(lib.cake_rmsnorm_device_status(ctypes.byref(code), int(bool(clear))), "cake_rmsnorm_device_status")

@@ -18,7 +18,7 @@
 // which the sort is 20 us and the join 9 us).
 #include <mutex>
 
-#include "../csrc/cake_device.cuh"
+#include "cake_step_device.cuh"
 #include "cake_step_launch.h"
 
 namespace cake {
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const __grid_c
         const int64_t id = load_id(p.ids, p.ids_i64, t);
         const bool live = id >= 0 && id < p.vocab;
         if (id >= p.vocab && v0 == 0)
-            set_status(p.status, kStatusInvalid);
+            raise_status(p.status, kStatusInvalid);
         uint4 raw[4][F32 ? 2 : 1];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -109,7 +109,7 @@ __device__ __forceinline__ uint64_t make_pair(const SortParams &p, uint32_t t)
     const bool live = id >= 0 && id < (int64_t)p.vocab && id != p.padding_idx;
     const uint32_t key = live ? (uint32_t)id : p.vocab; // tokens without a gradient sort last
     if (id >= (int64_t)p.vocab)
-        set_status(p.status, kStatusInvalid);
+        raise_status(p.status, kStatusInvalid);
     return ((uint64_t)key << 32) | t;
 }
 
@@ -520,9 +520,9 @@ __global__ void __launch_bounds__(kSegMaxThreads) embed_segment_kernel(const __g
             // the bitmap is complete, the sort perhaps not yet
             const uint64_t t0 = globaltimer_ns();
             while (ld_acquire_gpu(p.ready) == 0)
-                if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                if (globaltimer_ns() - t0 > p.wait_ns) {
                     if (threadIdx.x == 0)
-                        set_status(p.status, kStatusTimeout);
+                        raise_status(p.status, kStatusTimeout);
                     return;
                 }
         } else {

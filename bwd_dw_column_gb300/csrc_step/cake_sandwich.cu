@@ -19,6 +19,7 @@
 // row: 124 us, 0.96 of the copy rate); the backward is held by its warps'
 // instruction latencies a little below that (T = 65536, H = 4096: 530 us, 0.90).
 #include "../csrc/cake_rows.cuh"
+#include "cake_step_device.cuh"
 #include "cake_step_launch.h"
 
 namespace cake {
@@ -115,7 +116,7 @@ __device__ __forceinline__ uint4 *out_row(const RowView &v, uint32_t r, uint32_t
 template <int NT>
 __device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout &L, const RowView (&in)[NT],
                                            const float *sc0, const float *sc1, const float *sc2, int v0, int nvec,
-                                           uint32_t r0, uint32_t r_end, int *status, uint64_t wait_ns)
+                                           uint32_t r0, uint32_t r_end, int *status, uint64_t wait_ns, int withhold)
 {
     const uint32_t lane = threadIdx.x & 31;
     const uint64_t pol = policy_evict_first();
@@ -132,13 +133,15 @@ __device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout
         }
         return v;
     };
+    // tests of the waits: bytes of the first stage that never come
+    const uint32_t missing = withhold == 1 || (withhold == 2 && blockIdx.x == 0) ? 16 : 0;
     float4 next = scalars(r0);
     uint32_t st = 0, ph = 0, it = 0;
     for (uint32_t row0 = r0; row0 < r_end; row0 += tile, ++it) {
         if (it >= (uint32_t)L.stages &&
             !__all_sync(0xffffffffu, mbar_wait(smem_addr(&m.s.empty[st]), ph ^ 1u, wait_ns))) {
             if (lane == 0)
-                set_status(status, kStatusTimeout);
+                raise_status(status, kStatusTimeout);
             break;
         }
         const uint32_t n = min(tile, r_end - row0);
@@ -147,7 +150,7 @@ __device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout
             m.scalars[st * kSwMaxTile + lane] = next;
         __syncwarp();
         if (lane == 0)
-            mbar_arrive_expect_tx(bar, (uint32_t)L.ntens * n * row_bytes);
+            mbar_arrive_expect_tx(bar, (uint32_t)L.ntens * n * row_bytes + (it == 0 ? missing : 0));
         __syncwarp();
         const uint32_t dst0 = smem_addr(m.s.ring) + st * m.s.stage_bytes;
 #pragma unroll
@@ -173,7 +176,7 @@ __device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout
     const uint32_t first = it > (uint32_t)L.stages ? it - L.stages : 0;
     for (uint32_t j = first; j < it; ++j)
         if (!mbar_wait(smem_addr(&m.s.full[j % L.stages]), (j / L.stages) & 1, wait_ns) && lane == 0)
-            set_status(status, kStatusTimeout);
+            raise_status(status, kStatusTimeout);
 }
 
 // ------------------------------------------------------------------ forward
@@ -194,7 +197,8 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_fwd_kernel(const __grid_c
     init_ring(m.s, RL);
     pdl_wait();
     if (warp == L.groups * L.W) {
-        sw_produce(m, L, p.in, nullptr, nullptr, p.gate_rows, 0, nvec, r0, r_end, p.status, p.wait_ns);
+        sw_produce(m, L, p.in, nullptr, nullptr, p.gate_rows, 0, nvec, r0, r_end, p.status, p.wait_ns,
+                   p.withhold);
         return;
     }
     const int gid = warp / L.W, wig = warp - gid * L.W, gtid = wig * 32 + lane, vstride = 32 * L.W;
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_fwd_kernel(const __grid_c
         }
     }
     if (abort && lane == 0)
-        set_status(p.status, kStatusTimeout);
+        raise_status(p.status, kStatusTimeout);
 }
 
 // ----------------------------------------------------------------- backward
@@ -389,7 +393,8 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
         if (!MANY)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kProducer)
-            sw_produce(m, L, p.in, p.rstd_post, p.rstd_pre, p.gate_rows, v0, nvec, r0, r_end, p.status, p.wait_ns);
+            sw_produce(m, L, p.in, p.rstd_post, p.rstd_pre, p.gate_rows, v0, nvec, r0, r_end, p.status, p.wait_ns,
+                       p.withhold);
         __syncwarp();
         if (CL)
             cluster_sync_all();
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
         own = mine;
     }
     if (abort && lane == 0)
-        set_status(p.status, kStatusTimeout);
+        raise_status(p.status, kStatusTimeout);
 
     // The CTA partial: the groups' sums in group order, through the drained
     // ring ([group][w][4 nvec] float4 (hi, lo, hi, lo) of a column pair).

@@ -8,13 +8,20 @@
 
 #include <cuda_runtime.h>
 
-#include "../../include/cake_step.h"
+#include "../../include/cake_step_test.h"
 #include "cake_check.h"
 #include "cake_step_launch.h"
 
 using namespace cake;
 
 namespace {
+
+// The limit of the kernels' waits, and what never comes (cake_step_wait_test).
+struct Waits {
+    uint64_t ns = kWaitLimitNs;
+    int withhold = 0;
+};
+thread_local Waits t_waits;
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
@@ -114,6 +121,15 @@ SandwichLayout sandwich_layout(const SandwichPlan &plan, const cake_shape *shape
 
 } // namespace
 
+extern "C" cake_status cake_step_wait_test(uint32_t wait_limit_us, int withhold)
+{
+    if (wait_limit_us > 1000000 || withhold < 0 || withhold > 2 || (wait_limit_us == 0 && withhold))
+        return CAKE_ERR_INVALID;
+    t_waits.ns = wait_limit_us ? (uint64_t)wait_limit_us * 1000u : kWaitLimitNs;
+    t_waits.withhold = withhold;
+    return CAKE_OK;
+}
+
 // ------------------------------------------------------------ sandwich norm
 
 extern "C" cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_tensor *z, const cake_tensor *x,
@@ -167,7 +183,8 @@ extern "C" cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_ten
     p.pre_f32 = w_pre_dtype == CAKE_FP32;
     p.rstd_post = rstd_post;
     p.rstd_pre = rstd_pre;
-    p.wait_ns = kWaitLimitNs;
+    p.wait_ns = t_waits.ns;
+    p.withhold = t_waits.withhold;
     if (step_status_ptr(&p.status) != cudaSuccess)
         return CAKE_ERR_CUDA;
     return cuda_status(launch_sandwich_fwd(p, plan, cu(stream)));
@@ -263,7 +280,8 @@ extern "C" cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_ten
     p.post_f32 = w_post_dtype == CAKE_FP32;
     p.pre_f32 = w_pre_dtype == CAKE_FP32;
     p.partials = static_cast<float2 *>(workspace);
-    p.wait_ns = kWaitLimitNs;
+    p.wait_ns = t_waits.ns;
+    p.withhold = t_waits.withhold;
     if (step_status_ptr(&p.status) != cudaSuccess || launch_sandwich_bwd(p, plan, cu(stream)) != cudaSuccess)
         return CAKE_ERR_CUDA;
     SandwichReduceParams rp{p.partials, plan.parts, H, {dw_post, dw_pre}};
@@ -650,6 +668,8 @@ extern "C" cake_status cake_embedding_bwd(const cake_tensor *dy, const void *ids
         q.present = nullptr; // no row is to be zeroed
     uint64_t *sorted = q.pairs[0];
     cudaError_t r = q.zero_present ? cudaSuccess : cudaMemsetAsync(ws, 0, e.present_bytes + e.hist_bytes, s);
+    if (r == cudaSuccess && t_waits.withhold)
+        r = cudaMemsetAsync(q.ready + 2, 0, 4, s);
     if (r == cudaSuccess)
         r = e.cluster ? launch_embed_cluster_sort(q, e.cluster, s) : launch_embed_sort(q, &sorted, s);
     if (r != cudaSuccess)
@@ -676,7 +696,8 @@ extern "C" cake_status cake_embedding_bwd(const cake_tensor *dy, const void *ids
         g.fill_rows *= 2;
     const int64_t fill = g.fill_rows * (e.threads / 32);
     g.fill_ctas = accumulate ? 0 : (int)std::min<int64_t>((vocab + fill - 1) / fill, 1 << 20);
-    g.ready = e.cluster && !accumulate ? q.ready : nullptr;
+    g.ready = e.cluster && !accumulate ? q.ready + (t_waits.withhold == 1 ? 2 : 0) : nullptr;
+    g.wait_ns = t_waits.ns;
     g.status = q.status;
     g.partials = reinterpret_cast<float *>(at + 2 * e.pairs_bytes);
     g.meta = reinterpret_cast<uint32_t *>(at + 2 * e.pairs_bytes + e.part_bytes);

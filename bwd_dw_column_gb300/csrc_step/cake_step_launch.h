@@ -40,6 +40,7 @@ struct SandwichFwdParams {
     float *rstd_post, *rstd_pre;
     int *status;
     uint64_t wait_ns;
+    int withhold;          // see cake_step_wait_test
 };
 
 struct SandwichBwdParams {
@@ -57,6 +58,7 @@ struct SandwichBwdParams {
     float2 *partials;      // [2][parts][H] (hi, lo): dw_post's, then dw_pre's
     int *status;
     uint64_t wait_ns;
+    int withhold;          // see cake_step_wait_test
 };
 
 struct SandwichReduceParams {
@@ -161,7 +163,8 @@ struct SortParams {
     uint32_t *hist;        // [passes][tiles][1 << bits], zero before the first pass
     uint32_t *present;     // bitmap of ids with a token, zero before the first pass (nullptr: not wanted)
     int zero_present;      // one-launch sort: zero the bitmap itself
-    uint32_t *ready;       // [0] one-launch sort: set to 1 once the bitmap is complete; [1] zero for the sums
+    uint32_t *ready;       // [0] one-launch sort: set to 1 once the bitmap is complete; [1] zero for the sums;
+                           // [2] tests of the waits: stays 0
     int *status;
 };
 
@@ -184,6 +187,7 @@ struct SegmentParams {
     int fill_ctas;         // CTAs before the sums' that zero the rows without a token
     int fill_rows;         // rows that a warp of those takes at a time: a power of two, at most 32
     const uint32_t *ready; // those start at this flag; nullptr: after the sort
+    uint64_t wait_ns;
     int *status;
     float *partials;       // [windows][2][H]: sums of the leading and the trailing piece
     uint32_t *meta;        // [windows][2]: flags and the trailing piece's id

@@ -38,7 +38,7 @@ __all__ = [
     "cake_sandwich_fwd", "cake_sandwich_bwd", "cake_sandwich_bwd_workspace_size", "cake_sandwich_norm",
     "CakeSandwichFunction", "cake_grad_norm", "cake_clip_grad_norm", "cake_grad_norm_workspace_size",
     "cake_embedding_fwd", "cake_embedding_bwd", "cake_embedding_bwd_workspace_size", "cake_embedding",
-    "CakeEmbeddingFunction",
+    "CakeEmbeddingFunction", "cake_step_wait_test",
 ]
 
 _vp, _i64, _f32, _int, _size = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int, ctypes.c_size_t
@@ -59,6 +59,7 @@ def _bind(lib):
         ("cake_embedding_bwd_workspace_size", _size, [_i64, _i64, _i64]),
         ("cake_embedding_bwd", _int, [T, _vp, _int, _i64, _i64, _i64, _f32, _i64, _vp, _int, _i64, _int, _vp, _size,
                                       _vp]),
+        ("cake_step_wait_test", _int, [ctypes.c_uint32, _int]),
     ):
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
@@ -117,6 +118,12 @@ def _on_devices(stream, devices):
 def _current() -> int:
     """The current device's current stream."""
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def cake_step_wait_test(wait_limit_us: int = 0, withhold: int = 0):
+    """Tests of the kernels' bounded waits: the limit of the waits of the calls that this host thread makes from now
+    on, and what never comes to them (see ``include/cake_step_test.h``); no arguments: the ordinary limit again."""
+    _check(load_library().cake_step_wait_test(wait_limit_us, withhold), "cake_step_wait_test")
 
 
 # ------------------------------------------------------------------- marshalling

@@ -350,8 +350,8 @@ const char *cake_status_str(cake_status status);
 /*
  * Read the device status word that kernels set when a bounded wait runs out
  * (CAKE_OK or CAKE_ERR_TIMEOUT; CAKE_ERR_INVALID after an embedding of
- * cake_step.h met an id outside its table) on the current device; clear != 0
- * resets it.
+ * cake_step.h met an id outside its table, unless a wait ran out as well) on
+ * the current device; clear != 0 resets it.
  * Synchronises the device.  Returns CAKE_ERR_CUDA if the read itself fails.
  */
 cake_status cake_rmsnorm_device_status(int *code, int clear);
