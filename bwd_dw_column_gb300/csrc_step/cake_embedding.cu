@@ -517,14 +517,18 @@ __global__ void __launch_bounds__(kSegMaxThreads) embed_segment_kernel(const __g
     constexpr int kSegBatch = ACC ? 4 : 8; // rows in flight
     if (blockIdx.x < (uint32_t)p.fill_ctas) {
         if (p.ready) {
-            // the bitmap is complete, the sort perhaps not yet
-            const uint64_t t0 = globaltimer_ns();
-            while (ld_acquire_gpu(p.ready) == 0)
-                if (globaltimer_ns() - t0 > p.wait_ns) {
-                    if (threadIdx.x == 0)
-                        raise_status(p.status, kStatusTimeout);
-                    return;
-                }
+            // the bitmap is complete, the sort perhaps not yet; one thread waits and
+            // answers for the CTA, so that no row is left out without a report
+            int late = 0;
+            if (threadIdx.x == 0) {
+                const uint64_t t0 = globaltimer_ns();
+                while (ld_acquire_gpu(p.ready) == 0 && !late)
+                    late = globaltimer_ns() - t0 > p.wait_ns;
+                if (late)
+                    raise_status(p.status, kStatusTimeout);
+            }
+            if (__syncthreads_or(late))
+                return;
         } else {
             pdl_wait();
         }

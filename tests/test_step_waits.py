@@ -113,3 +113,42 @@ def test_a_zeroing_flag_that_nothing_sets(cake, T, H, V):
     has[ids] = True
     assert torch.equal(out[has], want[has]) and bool((out[~has] == 7).all())  # the sums do not wait for the flag
     assert torch.equal(cake.cake_embedding_bwd(dy, ids, V, out=out), want)
+
+
+@pytest.mark.gpu
+def test_a_zeroing_cta_goes_on_or_gives_up_as_a_whole(cake):
+    """A flag that a copy of the host sets at about the time at which the limit runs out: a CTA zeroes all of its 8
+    rows (4 warps of 2 rows of 8 KB) or none, and no row is left without a report."""
+    T, H, V, limit = 300, 1024, 16_000, 1500
+    g = torch.Generator().manual_seed(T)
+    ids = torch.randint(0, V, (T,), generator=g).to(DEV)
+    dy = torch.randn(T, H, generator=g).to(BF16).to(DEV)
+    want = cake.cake_embedding_bwd(dy, ids, V)
+    has = torch.zeros(V, dtype=torch.bool, device=DEV)
+    has[ids] = True
+    out = torch.empty(V, H, device=DEV)
+    ws = torch.zeros(cake.cake_embedding_bwd_workspace_size(T, V, H), dtype=torch.uint8, device=DEV)
+    flag, one, side = ws[8:12].view(torch.int32), torch.ones(1, dtype=torch.int32).pin_memory(), torch.cuda.Stream()
+    may, calls = ~has.view(-1, 8), {"whole": 0, "none": 0, "some": 0}
+    try:
+        for k in range(240):
+            out.fill_(7)
+            torch.cuda.synchronize()
+            with waits(cake, limit, 1):
+                cake.cake_embedding_bwd(dy, ids, V, out=out, workspace=ws)
+            until = time.perf_counter() + 1e-6 * (limit - 60 + k % 120)
+            while time.perf_counter() < until:
+                pass
+            with torch.cuda.stream(side):
+                flag.copy_(one, non_blocking=True)
+            status = cake.cake_rmsnorm_device_status(clear=True)
+            kept = (out == 7).all(1) & ~has
+            assert torch.equal(out[~kept], want[~kept])  # a row is whole or untouched
+            assert status == (TIMEOUT if bool(kept.any()) else 0)
+            gave_up = kept.view(-1, 8)
+            assert torch.equal(gave_up, gave_up.any(1, keepdim=True) & may)
+            calls["none" if torch.equal(gave_up, may) else "some" if status else "whole"] += 1
+    finally:
+        cake.cake_rmsnorm_device_status(clear=True)
+    assert torch.equal(cake.cake_embedding_bwd(dy, ids, V, out=out), want)
+    print("\nrows zeroed:", calls)
