@@ -253,12 +253,9 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_cluster_sort_kernel(
                 st_cluster_u32(map_to_rank(to, c), at);
         }
         cluster_sync_all();
-        if (pass == 0) {
-            if (rank_c == 0 && threadIdx.x == 0) {
-                __threadfence();
-                atomicExch(p.ready, 1u);
-            }
-            pdl_launch_dependents();
+        if (pass == 0 && rank_c == 0 && threadIdx.x == 0) {
+            __threadfence();
+            atomicExch(p.ready, 1u);
         }
         // a digit's first place of this CTA: all smaller digits, and its own in earlier CTAs
         uint32_t all = 0, before = 0;
@@ -280,6 +277,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_cluster_sort_kernel(
             before += incl - all;
         }
         __syncthreads();
+        // only now: a launch that starts earlier could meet the flag and the bitmap
+        // of the workspace's last call
+        if (pass == 0)
+            pdl_launch_dependents();
         if (threadIdx.x < bins) {
             for (int w = 0; w < warp; ++w)
                 before += m.scan[w];

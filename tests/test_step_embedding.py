@@ -282,6 +282,28 @@ def test_the_same_bits_every_time_and_in_graphs(cake):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H,V", [(1, 64, 3000), (700, 256, 20_000), (1024, 1024, 8000), (3000, 128, 50_000),
+                                   (140_000, 8, 9000)])
+def test_a_workspace_holds_nothing_between_calls(cake, T, H, V):
+    """Calls one after another in one workspace, whose flags, bitmap and lists are those of other ids' calls."""
+    sets = [(make_ids("uniform", T, V, s).to(DEV), torch.randn(T, H, generator=gen(s)).to(BF16).to(DEV))
+            for s in range(3)]
+    want = [cake.cake_embedding_bwd(dy, ids, V) for ids, dy in sets]
+    base = torch.randn(V, H, generator=gen(9)).to(DEV)
+    added = [cake.cake_embedding_bwd(dy, ids, V, out=base.clone(), accumulate=True) for ids, dy in sets]
+    ws = torch.full((cake.cake_embedding_bwd_workspace_size(T, V, H),), 0xff, dtype=torch.uint8, device=DEV)
+    outs = [torch.empty(V, H, device=DEV) for _ in range(6)]
+    for _ in range(20):
+        for k, o in enumerate(outs):  # nothing waits between the calls
+            ids, dy = sets[k % 3]
+            cake.cake_embedding_bwd(dy, ids, V, out=o.copy_(base) if k == 4 else o.fill_(5), accumulate=k == 4,
+                                    workspace=ws)
+        torch.cuda.synchronize()
+        for k, o in enumerate(outs):
+            assert torch.equal(o, added[k % 3] if k == 4 else want[k % 3]), k
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_autograd(cake, dtype):
     V, H = 300, 192
