@@ -331,6 +331,35 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
 }
 
+// warp_wait for a phase that other CTAs of the cluster complete: it acquires
+// their writes at the cluster's scope.
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    bool ok = try_wait_cluster(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t i = 1; !ok; ++i) {
+            ok = try_wait_cluster(bar, parity);
+            if (!ok && (i & 3u) == 0 && globaltimer_ns() - t0 > limit_ns)
+                break;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 // GATE: 0 none, 1 a value per row, 2 a value per element.  CL: rows span a
 // cluster.  RW: row_warps of the layout.
 //
@@ -530,7 +559,9 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
             if (r < r_end) {
                 float t3 = own;
                 if (joined) {
-                    if (!warp_wait(smem_addr(m.sums + kSwSlots * gid + (i & 3)), (i >> 2) & 1, p.wait_ns))
+                    const uint32_t bar = smem_addr(m.sums + kSwSlots * gid + (i & 3));
+                    if (!(CL ? warp_wait_cluster(bar, (i >> 2) & 1, p.wait_ns)
+                             : warp_wait(bar, (i >> 2) & 1, p.wait_ns)))
                         abort = true;
                     // eight lanes to a sum
                     const float *from = red + (i & 3) * 4 * RW;

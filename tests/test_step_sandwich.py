@@ -165,6 +165,21 @@ def test_row_widths(cake, H):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H", [3080, 4104, 5120, 6144, 7168, 8192])
+@pytest.mark.parametrize("gate", ["none", "row", "elem"])
+def test_many_rows_over_clusters(cake, H, gate):
+    # rows split over 2 and 4 CTAs: 9 tiles of a cluster and more, so that the ring, and the four slots and
+    # barriers of the sums that cross between its CTAs, come round several times
+    c = case(2999, H, gate, device=DEV, w=[(torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32)][H // 8 % 2])
+    _, h, r1, r2 = check_fwd(cake, c, 0.5)
+    a = check_bwd(cake, c, 0.5, h=h, r=(r1, r2))
+    for _ in range(3):
+        b = check_bwd(cake, c, 0.5, h=h, r=(r1, r2))
+        for s, t in zip(a, b):
+            assert s is None and t is None or torch.equal(s, t)  # bit for bit
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [4096, 20011])
 def test_many_rows(cake, T):
     c = case(T, 768, "row", device=DEV, offset=1.0)
