@@ -31,7 +31,7 @@ constexpr int kSwMaxStages = 16;
 constexpr int kSwMaxTile = 15;            // rows of a stage, at most
 constexpr int kSwSlots = 4;               // backward: rows whose partial sums may be in use
 constexpr int kSwMaxJoined = 7;           // groups whose rows span several warps, at most
-constexpr int kSwMaxRowWarps = 32;        // warps of a row over its cluster, at most
+constexpr int kSwMaxRowWarps = 16;        // warps of a row over its cluster, at most
 constexpr int kSwMaxCluster = 4;
 constexpr int kSwClustersOf4 = 36;        // that a GB300 holds at a time
 // Shared memory before the weights: the ring's barriers (256 bytes), the row
@@ -41,9 +41,9 @@ constexpr int kSwRedBytes = 4096;
 constexpr int kSwScalarsAt = kSwRed + kSwRedBytes;
 constexpr int kSwFixed = (kSwScalarsAt + kSwMaxStages * kSwMaxTile * 16 + 127) / 128 * 128;
 
-// Room for the warps of a row in a slot of partial sums: 8, 16 or 32; 1: rows
-// of one warp, which need no slots.
-__host__ __device__ constexpr int row_warps(int n) { return n == 1 ? 1 : n <= 8 ? 8 : n <= 16 ? 16 : 32; }
+// Room for the warps of a row in a slot of partial sums: 8 or 16; 1: rows of
+// one warp, which need no slots.
+__host__ __device__ constexpr int row_warps(int n) { return n == 1 ? 1 : n <= 8 ? 8 : 16; }
 
 struct SwSmem {
     Smem s;               // barriers, reduction slots, flag, ring
@@ -567,12 +567,9 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
                     const float *from = red + (i & 3) * 4 * RW;
                     if (RW == 8) {
                         t3 = from[lane];
-                    } else if (RW == 16) {
+                    } else {
                         const float2 a = reinterpret_cast<const float2 *>(from)[lane];
                         t3 = __fadd_rn(a.x, a.y);
-                    } else {
-                        const float4 a = reinterpret_cast<const float4 *>(from)[lane];
-                        t3 = __fadd_rn(__fadd_rn(a.x, a.y), __fadd_rn(a.z, a.w));
                     }
 #pragma unroll
                     for (int o = 4; o > 0; o >>= 1)
@@ -729,6 +726,8 @@ static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int clust
     const bool many = p.vpt == 1 || ((p.W == 2 || p.W == 5 || p.W == 7) && cluster <= 2);
     if (p.groups * p.W > (!backward ? 16 : many ? kSwBwdManyWarps : kSwBwdWarps))
         return false;
+    if (backward && cluster == 1 && p.W > 8) // (a cluster of 2 leaves fewer warps without work)
+        return false;
     // CTAs per SM: the backward's takes all registers, 28 of the forward's warps fit
     p.per_sm = backward ? 1 : 28 / (p.groups * p.W + 1) >= 2 ? 2 : 1;
     const size_t fixed = (size_t)kSwFixed + 2 * weight_smem_bytes(p.cols);
@@ -841,38 +840,46 @@ cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, const SandwichPlan &
              : launch_rows(sandwich_fwd_kernel<2, false, kSwWideThreads>, p, plan, threads, stream);
 }
 
+SandwichBuild sandwich_build(const SandwichPlan &plan)
+{
+    SandwichBuild b;
+    b.vpt = plan.vpt;
+    b.rw = row_warps(plan.W * plan.cluster);
+    b.cl = plan.cluster > 1;
+    b.many = plan.vpt == 1 || plan.groups * plan.W > kSwBwdWarps;
+    b.half = plan.half;
+    return b;
+}
+
+template <int GATE, int VPT, bool CL, int RW, bool MANY, bool HALF>
+static bool launch_build(const SandwichBuild &b, const SandwichBwdParams &p, const SandwichPlan &plan,
+                         cudaStream_t stream, cudaError_t &e)
+{
+    if (b.vpt != VPT || b.cl != CL || b.rw != RW || b.many != MANY || b.half != HALF)
+        return false;
+    e = launch_rows(sandwich_bwd_kernel<VPT, GATE, CL, RW, MANY, HALF>, p, plan, kSwBwdThreads, stream);
+    return true;
+}
+
+// The builds that some width's plan takes.
 template <int GATE>
 static cudaError_t launch_bwd_gate(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)
 {
-    if (plan.stages < 2) // a row is held while the next one is read
+    // (a row is held while the next one is read: two stages)
+    if (plan.stages < 2 || plan.groups * plan.W > kSwBwdManyWarps)
         return cudaErrorInvalidValue;
-    const int threads = kSwBwdThreads;
-    const int rw = row_warps(plan.W * plan.cluster);
-    if (plan.half) {
-        if (plan.groups * plan.W > kSwBwdManyWarps || plan.cluster > 1 || (plan.W > 1 && rw != 8))
-            return cudaErrorInvalidValue;
-        return plan.W == 1 ? launch_rows(sandwich_bwd_kernel<1, GATE, false, 1, true, true>, p, plan, threads, stream)
-                           : launch_rows(sandwich_bwd_kernel<1, GATE, false, 8, true, true>, p, plan, threads, stream);
-    }
-    if (plan.groups * plan.W > kSwBwdWarps) {
-        if (plan.groups * plan.W > kSwBwdManyWarps)
-            return cudaErrorInvalidValue;
-        if (plan.vpt == 1)
-            return launch_rows(sandwich_bwd_kernel<1, GATE, false, 1, true>, p, plan, threads, stream);
-        if (rw != (plan.cluster > 1 ? 16 : 8))
-            return cudaErrorInvalidValue;
-        return plan.cluster > 1 ? launch_rows(sandwich_bwd_kernel<2, GATE, true, 16, true>, p, plan, threads, stream)
-                                : launch_rows(sandwich_bwd_kernel<2, GATE, false, 8, true>, p, plan, threads, stream);
-    }
-    if (plan.cluster > 1)
-        return rw == 8    ? launch_rows(sandwich_bwd_kernel<2, GATE, true, 8>, p, plan, threads, stream)
-               : rw == 16 ? launch_rows(sandwich_bwd_kernel<2, GATE, true, 16>, p, plan, threads, stream)
-                          : launch_rows(sandwich_bwd_kernel<2, GATE, true, 32>, p, plan, threads, stream);
-    if (plan.W == 1)
-        return plan.vpt == 1 ? launch_rows(sandwich_bwd_kernel<1, GATE, false, 1>, p, plan, threads, stream)
-                             : launch_rows(sandwich_bwd_kernel<2, GATE, false, 1>, p, plan, threads, stream);
-    return rw == 8 ? launch_rows(sandwich_bwd_kernel<2, GATE, false, 8>, p, plan, threads, stream)
-                   : launch_rows(sandwich_bwd_kernel<2, GATE, false, 16>, p, plan, threads, stream);
+    const SandwichBuild b = sandwich_build(plan);
+    cudaError_t e = cudaErrorInvalidValue; // no such build
+    (void)(launch_build<GATE, 1, false, 1, true, false>(b, p, plan, stream, e) ||
+           launch_build<GATE, 1, false, 1, true, true>(b, p, plan, stream, e) ||
+           launch_build<GATE, 1, false, 8, true, true>(b, p, plan, stream, e) ||
+           launch_build<GATE, 2, false, 1, false, false>(b, p, plan, stream, e) ||
+           launch_build<GATE, 2, false, 8, false, false>(b, p, plan, stream, e) ||
+           launch_build<GATE, 2, false, 8, true, false>(b, p, plan, stream, e) ||
+           launch_build<GATE, 2, true, 8, false, false>(b, p, plan, stream, e) ||
+           launch_build<GATE, 2, true, 16, false, false>(b, p, plan, stream, e) ||
+           launch_build<GATE, 2, true, 16, true, false>(b, p, plan, stream, e));
+    return e;
 }
 
 cudaError_t launch_sandwich_bwd(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream)

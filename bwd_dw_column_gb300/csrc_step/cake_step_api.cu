@@ -190,6 +190,22 @@ extern "C" cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_ten
     return cuda_status(launch_sandwich_fwd(p, plan, cu(stream)));
 }
 
+extern "C" cake_status cake_sandwich_bwd_plan(const cake_shape *shape, int tensors, int plan[9])
+{
+    uint32_t rows = 0;
+    cake_status st = check_shape(shape, &rows);
+    if (st != CAKE_OK)
+        return st;
+    if (!plan || rows == 0 || tensors < 3 || tensors > 5)
+        return CAKE_ERR_INVALID;
+    const SandwichPlan p = sandwich_plan((int)shape->hidden, rows, tensors, true);
+    const SandwichBuild b = sandwich_build(p);
+    const int got[9] = {b.vpt,     b.cl,     b.rw,     b.many, b.half,
+                        p.cluster, p.groups, p.stages, (int)((p.rows_per_cta + p.groups - 1) / p.groups)};
+    std::copy(got, got + 9, plan);
+    return CAKE_OK;
+}
+
 extern "C" size_t cake_sandwich_bwd_workspace_size(const cake_shape *shape)
 {
     uint32_t rows = 0;

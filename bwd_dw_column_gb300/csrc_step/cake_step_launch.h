@@ -67,6 +67,13 @@ struct SandwichReduceParams {
     float *dw[2];           // dw_post, dw_pre
 };
 
+// The build of the backward kernel that a plan takes: see sandwich_bwd_kernel.
+struct SandwichBuild {
+    int vpt, rw;
+    bool cl, many, half;
+};
+
+SandwichBuild sandwich_build(const SandwichPlan &plan);
 SandwichPlan sandwich_plan(int H, uint32_t rows, int ntens, bool backward);
 cudaError_t launch_sandwich_fwd(const SandwichFwdParams &p, const SandwichPlan &plan, cudaStream_t stream);
 cudaError_t launch_sandwich_bwd(const SandwichBwdParams &p, const SandwichPlan &plan, cudaStream_t stream);

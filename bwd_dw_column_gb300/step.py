@@ -60,6 +60,7 @@ def _bind(lib):
         ("cake_embedding_bwd", _int, [T, _vp, _int, _i64, _i64, _i64, _f32, _i64, _vp, _int, _i64, _int, _vp, _size,
                                       _vp]),
         ("cake_step_wait_test", _int, [ctypes.c_uint32, _int]),
+        ("cake_sandwich_bwd_plan", _int, [S, _int, ctypes.POINTER(_int)]),
     ):
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args

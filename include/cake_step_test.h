@@ -1,6 +1,6 @@
 /*
- * cake_step_test.h -- an entry point for tests of the training-step operators'
- * bounded waits; no program needs it.
+ * cake_step_test.h -- entry points for tests of the training-step operators'
+ * bounded waits and launch plans; no program needs them.
  */
 #ifndef CAKE_STEP_TEST_H
 #define CAKE_STEP_TEST_H
@@ -25,6 +25,16 @@ extern "C" {
  * return, and cake_rmsnorm_device_status() gives CAKE_ERR_TIMEOUT.
  */
 cake_status cake_step_wait_test(uint32_t wait_limit_us, int withhold);
+
+/*
+ * The plan of cake_sandwich_bwd for a shape and a number of staged tensors (3,
+ * and one more each for an element gate and dh).  plan: the kernel's build
+ * (16-byte vectors of a thread, whether rows span a cluster, room for a row's
+ * warps, whether more than 12 consumer warps run, whether a thread takes half
+ * a vector more), then CTAs of a cluster, rows of a stage, stages, and stages'
+ * worth of rows of the largest CTA or cluster.  Host only.
+ */
+cake_status cake_sandwich_bwd_plan(const cake_shape *shape, int tensors, int plan[9]);
 
 #ifdef __cplusplus
 }

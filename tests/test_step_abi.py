@@ -5,6 +5,7 @@ launch.  No call here reaches a kernel."""
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -106,6 +107,39 @@ def test_every_width_has_a_backward_plan(cake):
     for H in range(8, 8193, 8):
         for T in (1, 151, 100_000):
             assert cake.cake_sandwich_bwd_workspace_size((T, 1, H)) >= 16 * H, (T, H)
+
+
+def plan(cake, T, H, tensors):
+    got = (ctypes.c_int * 9)()
+    assert cake.load_library().cake_sandwich_bwd_plan(S(T, 1, H), tensors, got) == 0
+    return tuple(got)
+
+
+def test_every_build_of_the_backward_is_reached(cake):
+    """The library holds the kernels that some width takes, for each gate, and no others."""
+    names = subprocess.run(["nm", "-C", cake.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    held = set(re.findall(r"cake::sandwich_bwd_kernel<(\d+), (\d+), (\w+), (\d+), (\w+), (\w+)>", names))
+    flag = ("false", "true")
+    taken = set()
+    for gate in (0, 1, 2):
+        for H in range(8, 8193, 8):
+            for dh in (0, 1):
+                vpt, cl, rw, many, half = plan(cake, 100_000, H, 3 + (gate == 2) + dh)[:5]
+                taken.add((str(vpt), str(gate), flag[cl], str(rw), flag[many], flag[half]))
+    assert held and held == taken, (sorted(held - taken), sorted(taken - held))
+
+
+@pytest.mark.parametrize("tensors", [4, 5])
+def test_the_tested_cluster_shapes_come_round_several_times(cake, tensors):
+    for H in (4104, 5120, 6144, 7168, 8192):  # (3080 columns stay on one CTA)
+        cluster, _, stages, tiles = plan(cake, 2999, H, tensors)[5:]
+        assert cluster > 1 and tiles >= 9 and tiles >= 2 * stages, H
+
+
+def test_plan_refusals(cake):
+    got, call = (ctypes.c_int * 9)(), cake.load_library().cake_sandwich_bwd_plan
+    assert call(S(4), 2, got) == INVALID and call(S(4), 6, got) == INVALID and call(S(0), 3, got) == INVALID
+    assert call(S(4), 3, None) == INVALID and call(S(4, 1, 60), 3, got) == UNSUPPORTED
 
 
 def grads(cake, ptrs, counts, types, outs=None, otypes=None, max_norm=1.0, eps=1e-6, norm=A // 2, ws=A, n_ws=1 << 30,
