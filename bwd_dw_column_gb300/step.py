@@ -19,7 +19,9 @@ Every result is bitwise reproducible for equal inputs and shapes.  Workspaces
 hold nothing between calls; without one from the caller a call takes it from
 torch's allocator, so calls on several streams and in several captured graphs
 never share one.  A call runs on the tensors' device, on its current stream or
-on ``stream``, where its outputs and workspace are allocated too.
+on ``stream``, where its outputs and workspace are allocated too.  Tensors that a caller gives
+to be written count as changed in place for autograd, as with torch's own
+in-place operations: a backward pass that has saved one raises.
 """
 from __future__ import annotations
 
@@ -31,6 +33,7 @@ from operator import attrgetter, is_not
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import CAKE_BF16, CAKE_FP32, CAKE_OK, CakeError, load_library
 
@@ -139,6 +142,11 @@ def _check(status: int, what: str):
         raise CakeError(status, what)
 
 
+def _given(*tensors):
+    """The tensors among a call's outputs that the caller has given."""
+    return [t for t in tensors if t is not None]
+
+
 def _rows(t):
     """(T, nh, H) of a [T, H] or [T, nh, H] tensor."""
     if t.dim() == 2:
@@ -231,6 +239,7 @@ def cake_sandwich_fwd(z: torch.Tensor, x: torch.Tensor, w_post: torch.Tensor, w_
         size, rows = z.shape, T * nh
         w_post, w_pre = _weight(w_post, H, "w_post"), _weight(w_pre, H, "w_pre")
         g_row, g_elem = _gate(gate, z)
+        given = _given(y, h_new, rstd_post, rstd_pre)
         if y is None:
             y = _like(z)
         if h_new is None:
@@ -246,6 +255,8 @@ def cake_sandwich_fwd(z: torch.Tensor, x: torch.Tensor, w_post: torch.Tensor, w_
                                    _rows_f32(rstd_post, rows, "rstd_post"), _rows_f32(rstd_pre, rows, "rstd_pre"),
                                    _current())
         _check(st, "cake_sandwich_fwd")
+        if given:
+            increment_version(given)
     return y, h_new, rstd_post, rstd_pre
 
 
@@ -280,6 +291,7 @@ def cake_sandwich_bwd(dy: torch.Tensor, h_new: torch.Tensor, z: torch.Tensor, rs
         w_post, w_pre = _weight(w_post, H, "w_post"), _weight(w_pre, H, "w_pre")
         g_row, g_elem = _gate(gate, z)
         dev = z.device
+        given = _given(dx, dz, dw_post, dw_pre, dgate)
         if dx is None:
             dx = _like(z)
         if dz is None:
@@ -310,6 +322,8 @@ def cake_sandwich_bwd(dy: torch.Tensor, h_new: torch.Tensor, z: torch.Tensor, rs
                                    _ref(dgate, size, "dgate") if g_elem is not None else None, ws, ws_bytes,
                                    _current())
         _check(st, "cake_sandwich_bwd")
+        if given:
+            increment_version(given)
     return dx, dz, dw_post, dw_pre, dgate
 
 
@@ -397,6 +411,7 @@ def _grad_call(grads, outs, clip, max_norm, eps, norm, workspace, stream):
     with _on_devices(stream, devices):
         ptrs, counts, types, plain = _tensors(grads, "gradients")
         n = len(grads)
+        given = _given(norm)
         if norm is None:
             norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
         elif norm.dtype is not torch.float32 or norm.numel() != 1:
@@ -406,6 +421,8 @@ def _grad_call(grads, outs, clip, max_norm, eps, norm, workspace, stream):
             st = lib.cake_grad_norm(_addr(ptrs), _addr(counts), _addr(types), n, norm.data_ptr(), ws, ws_bytes,
                                     _current())
             _check(st, "cake_grad_norm")
+            if given:
+                increment_version(given)
             return norm
         optrs = otypes = ()
         if outs:
@@ -417,6 +434,7 @@ def _grad_call(grads, outs, clip, max_norm, eps, norm, workspace, stream):
         st = lib.cake_grad_clip(_addr(ptrs), _addr(counts), _addr(types), _addr(optrs), _addr(otypes), n, max_norm,
                                 eps, norm.data_ptr(), ws, ws_bytes, _current())
         _check(st, "cake_grad_clip")
+        increment_version(given + (grads if outs is None else outs))
         return norm
 
 
@@ -485,6 +503,7 @@ def cake_embedding_fwd(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.
         ids = _ids(ids)
         V, H = _table(table, "table")
         T = ids.numel()
+        given = _given(y)
         if y is None:
             y = torch.empty((*ids.shape, H), dtype=torch.bfloat16, device=table.device)
         elif y.shape != (*ids.shape, H):
@@ -493,6 +512,8 @@ def cake_embedding_fwd(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.
                                     _dtype(table), V, H, table.stride(0), scale,
                                     _ref(y if y.dim() == 2 else y.view(T, H), (T, H), "y"), _current())
         _check(st, "cake_embedding_fwd")
+        if given:
+            increment_version(given)
     return y
 
 
@@ -520,6 +541,7 @@ def cake_embedding_bwd(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: f
         if dy.shape[:-1] != ids.shape:
             raise ValueError(f"dy has shape {tuple(dy.shape)}, expected {(*ids.shape, H)}")
         rows = dy if dy.dim() == 2 else dy.reshape(T, H)
+        given = _given(out)
         if out is None:
             if accumulate:
                 raise ValueError("accumulate needs the table that is added to")
@@ -533,6 +555,8 @@ def cake_embedding_bwd(dy: torch.Tensor, ids: torch.Tensor, vocab: int, scale: f
                                     -1 if padding_idx is None else padding_idx, out.data_ptr(), _dtype(out),
                                     out.stride(0), int(bool(accumulate)), ws, ws_bytes, _current())
         _check(st, "cake_embedding_bwd")
+        if given:
+            increment_version(given)
     return out
 
 

@@ -316,3 +316,54 @@ def test_behind_the_norms_own_kernels(cake, rows):
     for _ in range(5):
         for got, w_ in zip(run(False), want):
             assert torch.equal(got, w_)
+
+
+def test_tensors_that_a_call_writes_count_as_changed(cake):
+    """A backward pass that has saved what a call overwrites raises, as after torch's own in-place operations."""
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g).to(BF16).to(DEV)  # noqa: E731
+    n, w = 40, torch.ones(H, device=DEV)
+    f32 = lambda *s: torch.zeros(*s, device=DEV)  # noqa: E731
+    z, x, dy, gate = r(n, H), r(n, H), r(n, H), torch.ones(n, device=DEV)
+    ids = torch.randint(0, V, (n,), generator=g).to(DEV)
+    table, base = r(V, H), r(V, H)
+    _, h, a, b = cake.cake_sandwich_fwd(z, x, w, w)
+    calls = [
+        (lambda o: cake.cake_sandwich_fwd(z, x, w, w, **o), {"y": r(n, H), "h_new": r(n, H), "rstd_post": f32(n),
+                                                            "rstd_pre": f32(n)}),
+        (lambda o: cake.cake_sandwich_bwd(dy, h, z, a, b, w, w, None, gate, **o),
+         {"dx": r(n, H), "dz": r(n, H), "dw_post": f32(H), "dw_pre": f32(H), "dgate": f32(n)}),
+        (lambda o: cake.cake_grad_norm([z, x], **o), {"norm": f32(1)}),
+        (lambda o: cake.cake_clip_grad_norm([z, x], 1.0, out=list(o.values())[1:], norm=o["norm"]),
+         {"norm": f32(1), "a": f32(n, H), "b": f32(n, H)}),
+        (lambda o: cake.cake_clip_grad_norm([None, *o.values()], 1.0), {"a": r(n, H), "b": f32(7)}),
+        (lambda o: cake.cake_clip_grad_norm(o["a"], 1e9), {"a": r(3)}),
+        (lambda o: cake.cake_embedding_fwd(ids, table, **o), {"y": r(n, H)}),
+        (lambda o: cake.cake_embedding_bwd(dy, ids, V, **o), {"out": r(V, H)}),
+        (lambda o: cake.cake_embedding_bwd(dy, ids, V, accumulate=True, **o), {"out": base}),
+    ]
+    read = (z, x, dy, gate, ids, table, h, a, b, w)
+    before = [t._version for t in read]
+    for call, outs in calls:
+        was = {k: t._version for k, t in outs.items()}
+        call(outs)
+        assert all(t._version > was[k] for k, t in outs.items()), outs.keys()
+    assert [t._version for t in read] == before
+
+    leaf = r(n, H).requires_grad_()
+    stream = leaf * 2
+    kept = stream.sin()  # saves the stream for its gradient
+    cake.cake_sandwich_fwd(z, stream.detach(), w, w, h_new=stream.detach())
+    with pytest.raises(RuntimeError, match="inplace"):
+        kept.sum().backward()
+    leaf = r(n, H).requires_grad_()
+    grad = leaf * 2
+    kept = grad.sin()
+    cake.cake_clip_grad_norm([grad.detach()], 1e-3)
+    with pytest.raises(RuntimeError, match="inplace"):
+        kept.sum().backward()
+
+    with torch.inference_mode():  # such tensors have no count, in or out of the mode
+        t = torch.ones(9, device=DEV)
+        cake.cake_clip_grad_norm([t], 0.5)
+    assert abs(float(cake.cake_clip_grad_norm([t], 0.25)) - 0.5) < 1e-5
