@@ -219,3 +219,29 @@ def test_more_than_2_to_31_values(cake):
     cake.cake_clip_grad_norm([g], 6.5, eps=0.0)
     torch.cuda.synchronize()
     assert [float(g[i]) for i in (0, 1 << 31, n - 1, 1, n - 2)] == [2.0, 6.0, 1.5, 0.0, 0.0]
+
+
+@pytest.mark.gpu
+def test_one_workspace_and_given_norms(cake):
+    """Calls of one launch, of many tensors and of several launches, in one workspace that holds garbage."""
+    lists = [make([5, 70], device=DEV), make([100_003, 77], device=DEV), make([64 + i % 300 for i in range(2100)],
+                                                                              device=DEV)]
+    want = [float(cake.cake_grad_norm(g)) for g in lists]
+    ws = torch.full((cake.cake_grad_norm_workspace_size(2100),), 0xff, dtype=torch.uint8, device=DEV)
+    norms = torch.full((3, 1), 7.0, device=DEV)
+    for clip in (False, True):
+        for _ in range(3):
+            for g, n in zip(lists, norms):
+                outs = [torch.empty_like(t) for t in g]
+                got = (cake.cake_clip_grad_norm(g, 0.5, out=outs, norm=n, workspace=ws) if clip else
+                       cake.cake_grad_norm(g, norm=n, workspace=ws))
+                assert got is n
+            assert norms.flatten().tolist() == want
+    with pytest.raises(cake.CakeError):
+        cake.cake_grad_norm(lists[2], workspace=ws[:64])
+    with pytest.raises(ValueError):
+        cake.cake_grad_norm(lists[0], norm=torch.zeros(2, device=DEV))
+    with pytest.raises(ValueError):
+        cake.cake_grad_norm(lists[0], norm=torch.zeros(1, dtype=torch.float64, device=DEV))
+    with pytest.raises(cake.CakeError):  # the norm in a gradient
+        cake.cake_grad_norm(lists[1], norm=lists[1][1][4:5])

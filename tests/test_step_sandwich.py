@@ -368,3 +368,85 @@ def test_given_stream(cake):
     s.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", ["row", "elem"])
+@pytest.mark.parametrize("T,nh,H", [(40, None, 640), (9, 4, 264), (300, None, 5120)])
+def test_given_outputs(cake, T, nh, H, gate):
+    """Every output in a tensor of the caller's, rows strided where they may be, gives the bits of a new one."""
+    c = case(T, H, gate, nh=nh, device=DEV)
+    args = (c["w_post"], c["w_pre"], EPS, c["gate"], 0.5)
+    want = cake.cake_sandwich_fwd(c["z"], c["x"], *args)
+    lead = c["z"].shape[:-1]
+    rstd = [torch.full(lead, 7.0, device=DEV) for _ in range(2)]
+    got = cake.cake_sandwich_fwd(c["z"], c["x"], *args, rstd_post=rstd[0], rstd_pre=rstd[1])
+    assert got[2] is rstd[0] and got[3] is rstd[1]
+    for a, b in zip(got, want):
+        assert torch.equal(a.flatten(), b.flatten())
+    _, h, r1, r2 = got
+    back = (c["dy"], h, c["z"], r1, r2, c["w_post"], c["w_pre"], c["dh"], c["gate"], 0.5)
+    want = check_bwd(cake, c, 0.5, h=h, r=(r1, r2))
+    buf = torch.full((*lead, H + 24), 7.0, dtype=torch.bfloat16, device=DEV)
+    dgate = buf[..., 16:16 + H] if gate == "elem" else torch.full(lead, 7.0, device=DEV)
+    dw = torch.full((2, H), 7.0, device=DEV)
+    got = cake.cake_sandwich_bwd(*back, dgate=dgate, dw_post=dw[0], dw_pre=dw[1])
+    assert got[4] is dgate and got[2].data_ptr() == dw.data_ptr()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    if gate == "elem":
+        assert bool((buf[..., :16] == 7).all()) and bool((buf[..., 16 + H:] == 7).all())
+    # the gate's gradient left out
+    got = cake.cake_sandwich_bwd(*back, need_dgate=False)
+    assert got[4] is None
+    for a, b in zip(got[:4], want):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        cake.cake_sandwich_bwd(*back, need_dgate=False, dgate=dgate)
+    with pytest.raises(ValueError):
+        cake.cake_sandwich_bwd(*back, dgate=dgate[:-1])
+    with pytest.raises((ValueError, TypeError)):
+        cake.cake_sandwich_bwd(*back, dgate=dgate.double())
+    with pytest.raises(ValueError):
+        cake.cake_sandwich_bwd(*back[:8], None, 0.5, dgate=dgate)
+    with pytest.raises(ValueError):
+        cake.cake_sandwich_bwd(*back, dw_pre=dw[0, :-1])
+    with pytest.raises(ValueError):
+        cake.cake_sandwich_fwd(c["z"], c["x"], *args, rstd_post=rstd[0].flatten()[1:])
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_ordered_calls(cake):
+    """Calls of several widths, gates and row counts one after another in one workspace that holds garbage."""
+    cases = [case(T, H, gate, device=DEV) for T, H, gate in
+             [(700, 1536, "none"), (1, 64, "row"), (300, 5120, "elem"), (2000, 264, "row"), (64, 8192, "none")]]
+    calls, want, size = [], [], 0
+    for c in cases:
+        _, h, r1, r2 = cake.cake_sandwich_fwd(c["z"], c["x"], c["w_post"], c["w_pre"], EPS, c["gate"], 0.5)
+        calls.append((c["dy"], h, c["z"], r1, r2, c["w_post"], c["w_pre"], c["dh"], c["gate"], 0.5))
+        want.append(check_bwd(cake, c, 0.5, h=h, r=(r1, r2)))
+        size = max(size, cake.cake_sandwich_bwd_workspace_size(c["z"]))
+    ws = torch.full((size,), 0xff, dtype=torch.uint8, device=DEV)
+    for _ in range(3):
+        got = [cake.cake_sandwich_bwd(*a, workspace=ws) for a in calls]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for a, b in zip(g, w):
+                assert a is None and b is None or torch.equal(a, b)
+    with pytest.raises(cake.CakeError):
+        cake.cake_sandwich_bwd(*calls[2], workspace=ws[:1024])
+    with pytest.raises(cake.CakeError):
+        cake.cake_sandwich_bwd(*calls[0], workspace=ws[8:])
+    with pytest.raises(ValueError):
+        cake.cake_sandwich_bwd(*calls[0], workspace=ws[::2])
+
+
+@pytest.mark.gpu
+def test_a_gate_without_a_gradient(cake):
+    for gate in ("row", "elem"):
+        c = case(33, 520, gate, device=DEV)
+        z = c["z"].clone().requires_grad_()
+        y, h = cake.cake_sandwich_norm(z, c["x"], c["w_post"], c["w_pre"], EPS, c["gate"], 0.5)
+        torch.autograd.backward([y, h], [c["dy"], c["dh"]])
+        want = check_bwd(cake, c, 0.5)
+        assert torch.equal(z.grad, want[1]) and c["gate"].grad is None
