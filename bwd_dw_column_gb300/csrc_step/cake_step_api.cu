@@ -48,25 +48,37 @@ cake_status check_rows_f32(const void *p)
 }
 
 // Memory of a call's tensors: what it writes shares none with anything else.
+// Equally spaced rows: `row` bytes every `step` bytes; step 0: all of [lo, hi).
 struct Memory {
-    uintptr_t lo, hi;
+    uintptr_t lo, hi, step, row;
 };
 
 Memory memory(const void *p, uint64_t bytes)
 {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, p ? lo + (uintptr_t)bytes : lo};
+    return {lo, p ? lo + (uintptr_t)bytes : lo, 0, 0};
 }
 
 Memory memory(const cake_tensor *t, const cake_shape *s)
 {
     if (!has(t))
-        return {0, 0};
+        return {0, 0, 0, 0};
     const auto e = extent(t, s);
-    return {e.first, e.second};
+    const RowView v = make_view(t, s);
+    return {e.first, e.second, v.uniform ? (uintptr_t)(2 * v.row_stride) : 0, (uintptr_t)(2 * s->hidden)};
 }
 
-bool meet(const Memory &a, const Memory &b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
+// (Rows of unlike spacing count as the whole of what they span.)
+bool meet(const Memory &a, const Memory &b)
+{
+    if (!(a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi))
+        return false;
+    if (a.step == 0 || a.step != b.step)
+        return true;
+    // columns of one buffer: where b's rows lie after a's, within a row of the buffer
+    const uintptr_t off = b.lo >= a.lo ? (b.lo - a.lo) % a.step : (a.step - (a.lo - b.lo) % a.step) % a.step;
+    return off < a.row || off + b.row > a.step;
+}
 
 // Whether one of the `nw` written ranges meets another one or a range that is read.
 bool any_meet(const Memory *written, int nw, const Memory *read, int nr)
@@ -130,6 +142,11 @@ extern "C" cake_status cake_step_wait_test(uint32_t wait_limit_us, int withhold)
     return CAKE_OK;
 }
 
+extern "C" int cake_step_rows_meet(const cake_shape *shape, const cake_tensor *a, const cake_tensor *b)
+{
+    return meet(memory(a, shape), memory(b, shape));
+}
+
 // ------------------------------------------------------------ sandwich norm
 
 extern "C" cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_tensor *z, const cake_tensor *x,
@@ -164,7 +181,7 @@ extern "C" cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_ten
     const cake_tensor *outs[2] = {y, h_new}, *ins[3] = {z, x, has(gate) ? gate : nullptr};
     for (const cake_tensor *o : outs)
         for (const cake_tensor *i : ins)
-            if (i && overlap(o, i, shape) && !same_view(o, i, shape))
+            if (i && meet(memory(o, shape), memory(i, shape)) && !same_view(o, i, shape))
                 return CAKE_ERR_INVALID;
     SandwichFwdParams p{};
     const SandwichPlan plan = sandwich_plan((int)shape->hidden, rows, has(gate) ? 3 : 2, false);

@@ -64,6 +64,7 @@ def _bind(lib):
                                       _vp]),
         ("cake_step_wait_test", _int, [ctypes.c_uint32, _int]),
         ("cake_sandwich_bwd_plan", _int, [S, _int, ctypes.POINTER(_int)]),
+        ("cake_step_rows_meet", _int, [S, T, T]),
     ):
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args

@@ -54,7 +54,9 @@ extern "C" {
  * Shapes, strides, alignment and sharing of memory as for cake_rmsnorm_fwd
  * and cake_rmsnorm_bwd: an output of the forward may be exactly an input view
  * (y or h_new in place of z, x or gate), and nothing else that a call writes
- * may share memory with any other tensor of it.  w_post and w_pre have a dtype each.
+ * may share memory with any other tensor of it.  (Tensors that are columns of
+ * one buffer share none; they are told apart where their rows are equally
+ * spaced, and alike.)  w_post and w_pre have a dtype each.
  */
 cake_status cake_sandwich_fwd(const cake_shape *shape, const cake_tensor *z, const cake_tensor *x,
                               const void *w_post, cake_dtype w_post_dtype, const void *w_pre,

@@ -36,6 +36,9 @@ cake_status cake_step_wait_test(uint32_t wait_limit_us, int withhold);
  */
 cake_status cake_sandwich_bwd_plan(const cake_shape *shape, int tensors, int plan[9]);
 
+/* Whether the calls take two tensors of a shape to share memory.  Host only. */
+int cake_step_rows_meet(const cake_shape *shape, const cake_tensor *a, const cake_tensor *b);
+
 #ifdef __cplusplus
 }
 #endif

@@ -4,6 +4,7 @@ count on, and arguments outside the documented ranges are refused before any
 launch.  No call here reaches a kernel."""
 import ctypes
 import os
+import random
 import re
 import subprocess
 
@@ -262,6 +263,32 @@ def test_written_memory_is_shared_with_nothing(cake, shift):
                 assert backward(**{out: to}) == INVALID, (out, other)
     for other in ("dy", "dh", "h", "z", "r1", "r2", "w1", "w2", "grow"):
         assert backward(ws=places[other]) == INVALID, other
+
+
+def test_columns_of_one_buffer_share_nothing(cake):
+    """Rows that interleave: taken to meet exactly where bytes of them do."""
+    T, H, B = 4, 64, 64 * MB
+    rng, seen = random.Random(0), set()
+
+    def meet(a, b, nh=1):
+        return bool(cake.load_library().cake_step_rows_meet(S(T, nh, H), V(*a), V(*b)))
+
+    def rows(at, st, sh, nh):
+        return [at + 2 * (t * st + k * sh) for t in range(T) for k in range(nh)]
+
+    for _ in range(4000):
+        nh, sh = rng.choice([1, 2, 3]), 8 * rng.randint(8, 28)
+        a = (B, nh * sh, sh)
+        b = (B + 16 * rng.randint(-300, 300), nh * sh, sh)
+        want = any(abs(p - q) < 2 * H for p in rows(*a, nh) for q in rows(*b, nh))
+        got = meet(a, b, nh)
+        inner = 0 < abs(b[0] - a[0]) < 2 * T * nh * sh - 4 * H  # (past the ends, extents alone decide)
+        assert got == want or (got and not inner), (a, b, nh)
+        seen.add((nh > 1, got))
+    assert len(seen) == 4
+    # rows of unlike strides, and heads that are not equally spaced, are taken as all that they span
+    assert meet((B, 128, 0), (B + 128, 256, 0)) and not meet((B, 128, 0), (B + 1024, 256, 0))
+    assert meet((B, 512, 128), (B + 128, 512, 128), 2)
 
 
 def test_scratch_and_ids_are_shared_with_nothing(cake):

@@ -450,3 +450,33 @@ def test_a_gate_without_a_gradient(cake):
         torch.autograd.backward([y, h], [c["dy"], c["dh"]])
         want = check_bwd(cake, c, 0.5)
         assert torch.equal(z.grad, want[1]) and c["gate"].grad is None
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("nh", [None, 3])
+def test_tensors_in_columns_of_one_buffer(cake, nh):
+    T, H = 33, 320
+    c = case(T, H, "elem", nh=nh, device=DEV)
+    args = (c["w_post"], c["w_pre"], EPS, c["gate"], 0.5)
+    want = cake.cake_sandwich_fwd(c["z"], c["x"], *args)
+    back = check_bwd(cake, c, 0.5, h=want[1], r=want[2:])
+    lead = c["z"].shape[:-1]
+    buf = torch.full((*lead, 2 * H), 7.0, dtype=torch.bfloat16, device=DEV)
+    y, h = buf.chunk(2, dim=-1)
+    got = cake.cake_sandwich_fwd(c["z"], c["x"], *args, y=y, h_new=h)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    y.copy_(c["z"]), h.copy_(c["x"])  # and in place
+    got = cake.cake_sandwich_fwd(y, h, *args, y=y, h_new=h)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    wide = torch.full((*lead, 4 * H), 7.0, dtype=torch.bfloat16, device=DEV)
+    dy, dx, dz, dg = wide.chunk(4, dim=-1)
+    dy.copy_(c["dy"])
+    got = cake.cake_sandwich_bwd(dy, want[1], c["z"], *want[2:], c["w_post"], c["w_pre"], c["dh"], c["gate"], 0.5,
+                                 dx=dx, dz=dz, dgate=dg)
+    for a, b in zip(got, back):
+        assert torch.equal(a, b)
+    assert torch.equal(dy, c["dy"])
+    with pytest.raises(cake.CakeError):
+        cake.cake_sandwich_fwd(c["z"], c["x"], *args, y=buf[..., :H], h_new=buf[..., H - 8:2 * H - 8])
