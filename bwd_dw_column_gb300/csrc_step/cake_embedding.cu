@@ -18,12 +18,14 @@
 // which the sort is 20 us and the join 9 us).
 #include <mutex>
 
-#include "cake_step_device.cuh"
+#include "../csrc/cake_device.cuh"
 #include "cake_step_launch.h"
 
 namespace cake {
 
-__device__ int g_step_status;
+// A word for each code, so that an id outside its table (whose outputs are
+// defined) never hides a wait that ran out (whose outputs are not).
+__device__ int g_step_status[2]; // timeouts, ids outside their table
 
 constexpr int kStatusInvalid = 1; // == CAKE_ERR_INVALID
 constexpr int kStatusTimeout = 5; // == CAKE_ERR_TIMEOUT
@@ -52,7 +54,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const __grid_c
         const int64_t id = load_id(p.ids, p.ids_i64, t);
         const bool live = id >= 0 && id < p.vocab;
         if (id >= p.vocab && v0 == 0)
-            raise_status(p.status, kStatusInvalid);
+            set_status(p.status + 1, kStatusInvalid);
         uint4 raw[4][F32 ? 2 : 1];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -109,7 +111,7 @@ __device__ __forceinline__ uint64_t make_pair(const SortParams &p, uint32_t t)
     const bool live = id >= 0 && id < (int64_t)p.vocab && id != p.padding_idx;
     const uint32_t key = live ? (uint32_t)id : p.vocab; // tokens without a gradient sort last
     if (id >= (int64_t)p.vocab)
-        raise_status(p.status, kStatusInvalid);
+        set_status(p.status + 1, kStatusInvalid);
     return ((uint64_t)key << 32) | t;
 }
 
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(kSegMaxThreads) embed_segment_kernel(const __g
                 while (ld_acquire_gpu(p.ready) == 0 && !late)
                     late = globaltimer_ns() - t0 > p.wait_ns;
                 if (late)
-                    raise_status(p.status, kStatusTimeout);
+                    set_status(p.status, kStatusTimeout);
             }
             if (__syncthreads_or(late))
                 return;
@@ -878,11 +880,13 @@ cudaError_t step_status_ptr(int **out)
 
 cudaError_t step_status(int *code, int clear)
 {
-    cudaError_t e = cudaMemcpyFromSymbol(code, g_step_status, sizeof(int));
+    int words[2] = {};
+    cudaError_t e = cudaMemcpyFromSymbol(words, g_step_status, sizeof(words));
     if (e == cudaSuccess && clear) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbol(g_step_status, &zero, sizeof(int));
+        const int zero[2] = {};
+        e = cudaMemcpyToSymbol(g_step_status, zero, sizeof(zero));
     }
+    *code = words[0] ? words[0] : words[1];
     return e;
 }
 

@@ -19,7 +19,6 @@
 // row: 124 us, 0.96 of the copy rate); the backward is held by its warps'
 // instruction latencies a little below that (T = 65536, H = 4096: 530 us, 0.90).
 #include "../csrc/cake_rows.cuh"
-#include "cake_step_device.cuh"
 #include "cake_step_launch.h"
 
 namespace cake {
@@ -133,15 +132,17 @@ __device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout
         }
         return v;
     };
-    // tests of the waits: bytes of the first stage that never come
-    const uint32_t missing = withhold == 1 || (withhold == 2 && blockIdx.x == 0) ? 16 : 0;
+    // tests of the waits: 16 bytes of the first stage that never come
+    if (lane == 0 && (withhold == 1 || (withhold == 2 && blockIdx.x == 0)))
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], 16;" ::"r"(smem_addr(&m.s.full[0]))
+                     : "memory");
     float4 next = scalars(r0);
     uint32_t st = 0, ph = 0, it = 0;
     for (uint32_t row0 = r0; row0 < r_end; row0 += tile, ++it) {
         if (it >= (uint32_t)L.stages &&
             !__all_sync(0xffffffffu, mbar_wait(smem_addr(&m.s.empty[st]), ph ^ 1u, wait_ns))) {
             if (lane == 0)
-                raise_status(status, kStatusTimeout);
+                set_status(status, kStatusTimeout);
             break;
         }
         const uint32_t n = min(tile, r_end - row0);
@@ -150,7 +151,7 @@ __device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout
             m.scalars[st * kSwMaxTile + lane] = next;
         __syncwarp();
         if (lane == 0)
-            mbar_arrive_expect_tx(bar, (uint32_t)L.ntens * n * row_bytes + (it == 0 ? missing : 0));
+            mbar_arrive_expect_tx(bar, (uint32_t)L.ntens * n * row_bytes);
         __syncwarp();
         const uint32_t dst0 = smem_addr(m.s.ring) + st * m.s.stage_bytes;
 #pragma unroll
@@ -176,7 +177,7 @@ __device__ __forceinline__ void sw_produce(const SwSmem &m, const SandwichLayout
     const uint32_t first = it > (uint32_t)L.stages ? it - L.stages : 0;
     for (uint32_t j = first; j < it; ++j)
         if (!mbar_wait(smem_addr(&m.s.full[j % L.stages]), (j / L.stages) & 1, wait_ns) && lane == 0)
-            raise_status(status, kStatusTimeout);
+            set_status(status, kStatusTimeout);
 }
 
 // ------------------------------------------------------------------ forward
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1) sandwich_fwd_kernel(const __grid_c
         }
     }
     if (abort && lane == 0)
-        raise_status(p.status, kStatusTimeout);
+        set_status(p.status, kStatusTimeout);
 }
 
 // ----------------------------------------------------------------- backward
@@ -331,8 +332,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
 }
 
-// warp_wait for a phase that other CTAs of the cluster complete: it acquires
-// their writes at the cluster's scope.
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -346,6 +345,8 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
+// warp_wait for a phase that other CTAs of the cluster complete: it acquires
+// their writes at the cluster's scope.
 __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns)
 {
     bool ok = try_wait_cluster(bar, parity);
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(kSwBwdThreads, 1) sandwich_bwd_kernel(const __
         own = mine;
     }
     if (abort && lane == 0)
-        raise_status(p.status, kStatusTimeout);
+        set_status(p.status, kStatusTimeout);
 
     // The CTA partial: the groups' sums in group order, through the drained
     // ring ([group][w][4 nvec] float4 (hi, lo, hi, lo) of a column pair).

@@ -210,6 +210,6 @@ cudaError_t launch_embed_segments(const SegmentParams &p, cudaStream_t stream);
 cudaError_t launch_embed_join(const SegmentParams &p, cudaStream_t stream);
 
 cudaError_t step_status(int *code, int clear);
-cudaError_t step_status_ptr(int **out);
+cudaError_t step_status_ptr(int **out); // two words: waits that ran out, ids outside their table
 
 } // namespace cake
