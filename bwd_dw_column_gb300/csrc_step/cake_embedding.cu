@@ -14,8 +14,8 @@
 //
 // HBM bounds the lookup and, where there are many tokens or rows, the gradient
 // (GB300: T = 65536, H = 5120 lookup 140 us; the whole gradient of 131072 x 2048
-// from 8192 tokens 159 us, 6.9 TB/s; 65536 tokens added at H = 4096 181 us, of
-// which the sort is 20 us and the join 9 us).
+// from 8192 tokens 159 us, 7.0 TB/s; 65536 tokens added at H = 4096 179 to 185
+// us, of which the sort is 20 us and the join 9 us).
 #include <mutex>
 
 #include "../csrc/cake_device.cuh"

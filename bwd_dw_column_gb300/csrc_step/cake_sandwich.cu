@@ -17,7 +17,7 @@
 // (a producer warp with bulk copies, row groups of W warps as consumers,
 // bounded waits).  HBM bounds the forward (GB300, T = 16384, H = 6144, a gate a
 // row: 124 us, 0.96 of the copy rate); the backward is held by its warps'
-// instruction latencies a little below that (T = 65536, H = 4096: 530 us, 0.90).
+// instruction latencies a little below that (T = 65536, H = 4096: 533 us, 0.89).
 #include "../csrc/cake_rows.cuh"
 #include "cake_step_launch.h"
 
@@ -718,7 +718,7 @@ static bool try_plan(SandwichPlan &p, int H, int ntens, bool backward, int clust
     p.cols = 8 * nvec;
     // 8 columns a thread up to 256, 16 beyond; the backward of rows of one CTA
     // takes 12 where they leave fewer lanes without work (GB300, 2^27 values:
-    // H = 264 321 us against 444, 384 253 against 310, 640 330 against 404, 1032 283
+    // H = 264 321 us against 444, 384 253 against 310, 640 321 against 404, 1032 283
     // against 348, 1152 261 against 317, 1664 279 against 313; the copy takes 238)
     p.half = backward && H <= 2048 && nvec > 32 && (nvec + 47) / 48 * 48 < (nvec + 63) / 64 * 64;
     p.vpt = nvec <= 32 || p.half ? 1 : 2;

@@ -13,9 +13,10 @@
  * (and none after an error), must be 256-byte aligned, share no memory with
  * the call's tensors, and may be shared by calls that are ordered on one
  * stream.  Every result is bitwise reproducible for equal inputs and shapes.
- * Waits inside the kernels (for staged copies, and between the CTAs of a
- * thread-block cluster) are bounded and report through
- * cake_rmsnorm_device_status().  A first call on a device looks up addresses
+ * Waits inside the kernels (for staged copies, for a row's sums, and for the
+ * flag that the embedding gradient's zeroing starts at) are bounded and report
+ * through cake_rmsnorm_device_status(); the CTAs of a thread-block cluster meet
+ * at hardware barriers besides, which every thread reaches.  A first call on a device looks up addresses
  * and sets kernel attributes: make it before any stream capture.
  */
 #ifndef CAKE_STEP_H
@@ -91,8 +92,8 @@ cake_status cake_sandwich_bwd(const cake_shape *shape, const cake_tensor *dy, co
  * counts[i] contiguous values of dtypes[i]; BF16 and FP32 may be mixed.  The
  * arrays themselves are HOST memory, read before the call returns.  norm: one
  * FP32 device value, in none of the tensors (CAKE_ERR_INVALID).  Squares whose FP32 sum would overflow or vanish are
- * summed again in FP64, so norm is right to FP32 rounding over the whole
- * range of the types.  A NaN or infinity gives a NaN or infinite norm, and
+ * summed again in FP64, so norm is within 6 half-steps of FP32 (2^-24 of the
+ * value each) over the whole range of the types.  A NaN or infinity gives a NaN or infinite norm, and
  * clipping then follows the formula (infinite: coef is 0, and infinity * 0 is
  * NaN; NaN: everything becomes NaN).
  *
