@@ -16,7 +16,9 @@ Entry points (same names as the C ABI):
 * ``cake_rmsnorm_bwd_select`` (the window table's choice; host only);
 * ``cake_rmsnorm_device_status``, ``cake_status_str``;
 * the training-step operators around the norm (sandwich norm, gradient norm
-  and clipping, embedding): the module ``step``, whose names are here too.
+  and clipping, embedding): the module ``step``, whose names are here too;
+* a block's operators between the norms (gated feed-forward block, per-head
+  norm with rotary positions, dropout): the module ``block``, likewise.
 
 Names follow the pages' Python facade (PR #8208 page, description:
 forward / backward / workspace entry points taking ``deterministic``, default
@@ -127,6 +129,7 @@ def load_library(path: str = LIB_PATH):
         lib.cake_rmsnorm_device_status.restype = ctypes.c_int
         lib.cake_rmsnorm_device_status.argtypes = [_P(ctypes.c_int), ctypes.c_int]
         step._bind(lib)
+        block._bind(lib)
         _lib = lib
         return lib
 
@@ -485,3 +488,9 @@ from . import step  # noqa: E402
 from .step import *  # noqa: E402,F401,F403
 
 __all__ += step.__all__
+
+# a block's operators between the norms
+from . import block  # noqa: E402
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += block.__all__

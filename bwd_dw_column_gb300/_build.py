@@ -1,6 +1,6 @@
 """Build ``libcake_rmsnorm.so`` in-tree with nvcc for sm_103a.
 
-Each ``csrc/*.cu`` and ``csrc_step/*.cu`` file compiles in its own nvcc process (in parallel), then
+Each ``.cu`` file of ``csrc``, ``csrc_step`` and ``csrc_block`` compiles in its own nvcc process (in parallel), then
 nvcc links them into one shared library next to this file.  The CUDA runtime
 is linked statically, so the library needs only the driver at run time.
 """
@@ -15,6 +15,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 CSRC_STEP = os.path.join(HERE, "csrc_step")  # the training-step operators around the norm
+CSRC_BLOCK = os.path.join(HERE, "csrc_block")  # a block's operators between the norms
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libcake_rmsnorm.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
@@ -31,12 +32,12 @@ def _nvcc() -> str:
 
 
 def sources():
-    return sorted(os.path.join(d, f) for d in (CSRC, CSRC_STEP) for f in os.listdir(d) if f.endswith(".cu"))
+    return sorted(os.path.join(d, f) for d in (CSRC, CSRC_STEP, CSRC_BLOCK) for f in os.listdir(d) if f.endswith(".cu"))
 
 
 def _inputs():
     files = sources()
-    for d in (CSRC, CSRC_STEP, INCLUDE):
+    for d in (CSRC, CSRC_STEP, CSRC_BLOCK, INCLUDE):
         files += [os.path.join(d, f) for f in os.listdir(d) if f.endswith((".cuh", ".h"))]
     files.append(os.path.abspath(__file__))
     return files

@@ -1,0 +1,604 @@
+"""A training block's operators between the norms: Python binding and autograd.
+
+Three groups of operators that run between the RMSNorm and the sandwich norm,
+each in hand-written kernels behind the C ABI of ``include/cake_block.h``
+(formulas and conventions there).  They have no counterpart in the pages; they
+are additions of this library.
+
+* Gated feed-forward block -- both projections, the activation and the product
+  in one tensor-core kernel, and its gradients: ``cake_gated_fwd``,
+  ``cake_gated_bwd`` and the differentiable ``cake_gated``;
+* per-head norm of queries and keys with rotary positions of several axes:
+  ``cake_rotary_table``, ``cake_rotary_fwd``, ``cake_rotary_bwd`` and the
+  differentiable ``cake_rotary``;
+* dropout from a counter-based generator, whose mask is never stored, alone and
+  with the residual addition and the norm after it: ``cake_dropout_fwd``,
+  ``cake_dropout_bwd``, ``cake_dropout_norm_fwd``, ``cake_dropout_norm_bwd`` and
+  the differentiable ``cake_dropout`` and ``cake_dropout_norm``.
+
+Devices, streams, workspaces, given outputs and errors are as in the module
+``step``: a call runs on the tensors' device, on its current stream or on
+``stream``; without a workspace from the caller it takes one from torch's
+allocator; tensors that a caller gives to be written count as changed in place.
+Every result is bitwise reproducible for equal inputs and shapes.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import math
+import struct
+
+import torch
+from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
+
+from . import load_library
+from .step import (_check, _current, _dtype, _given, _like, _on, _ref, _rows, _rows_f32, _three, _weight,
+                   _workspace)
+
+__all__ = [
+    "cake_gated_fwd", "cake_gated_bwd", "cake_gated_bwd_workspace_size", "cake_gated", "CakeGatedFunction",
+    "cake_rotary_table", "cake_rotary_fwd", "cake_rotary_bwd", "cake_rotary_bwd_workspace_size", "cake_rotary",
+    "CakeRotaryFunction", "cake_dropout_fwd", "cake_dropout_bwd", "cake_dropout", "CakeDropoutFunction",
+    "cake_dropout_norm_fwd", "cake_dropout_norm_bwd", "cake_dropout_norm_bwd_workspace_size", "cake_dropout_norm",
+    "CakeDropoutNormFunction", "cake_block_wait_test",
+]
+
+_vp, _i64, _u64, _f32, _int, _size = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float, ctypes.c_int,
+                                      ctypes.c_size_t)
+
+
+def _bind(lib):
+    """Declare the operators' C signatures on the library handle."""
+    T = S = R = _vp  # shapes, tensors and rotations are passed as packed bytes
+    for name, res, args in (
+        ("cake_gated_fwd", _int, [_i64, _i64, _i64, T, T, T, _int, T, T, T, _vp]),
+        ("cake_gated_bwd_workspace_size", _size, [_i64, _i64, _i64]),
+        ("cake_gated_bwd", _int, [_i64, _i64, _i64, T, T, T, T, T, T, _int, T, T, T, _vp, _size, _vp]),
+        ("cake_rotary_fwd", _int, [_i64, _i64, _i64, _i64, T, T, R, _vp, _int, _vp, _int, _f32, T, T, _vp, _vp, _vp]),
+        ("cake_rotary_bwd_workspace_size", _size, [_i64, _i64, _i64, _i64]),
+        ("cake_rotary_bwd", _int, [_i64, _i64, _i64, _i64, T, T, R, T, T, _vp, _vp, _vp, _int, _vp, _int, T, T, _vp,
+                                   _vp, _vp, _size, _vp]),
+        ("cake_dropout", _int, [S, T, T, _f32, _u64, _u64, _vp, T, _vp]),
+        ("cake_dropout_norm_fwd", _int, [S, T, T, _vp, _int, _f32, _u64, _u64, _vp, _f32, T, T, _vp, _vp]),
+        ("cake_dropout_norm_bwd_workspace_size", _size, [S]),
+        ("cake_dropout_norm_bwd", _int, [S, T, T, T, _vp, _vp, _int, _f32, _u64, _u64, _vp, T, T, _vp, _vp, _size,
+                                         _vp]),
+        ("cake_block_wait_test", _int, [ctypes.c_uint32, _int]),
+    ):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = res, args
+
+
+def cake_block_wait_test(wait_limit_us: int = 0, withhold: int = 0):
+    """Tests of the kernels' bounded waits: the limit of the waits of the calls that this host thread makes from now
+    on, and whether a part of the first copies never comes (see ``include/cake_block_test.h``); no arguments: the
+    ordinary limit again."""
+    _check(load_library().cake_block_wait_test(wait_limit_us, withhold), "cake_block_wait_test")
+
+
+# ------------------------------------------------------------------------ gated
+
+_ACTS = {"silu": 0, "gelu": 1}
+
+
+def _act(act):
+    try:
+        return _ACTS[act]
+    except KeyError:
+        raise ValueError(f"act is 'silu' or 'gelu' (the tanh form), got {act!r}") from None
+
+
+def _matrix(t, rows, cols, what):
+    """A BF16 [rows, cols] matrix as a packed cake_tensor (None: NULL)."""
+    if t is None:
+        return None
+    if t.dim() != 2:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected a matrix")
+    return _ref(t, (rows, cols), what)
+
+
+def _new(rows, cols, like):
+    return torch.empty((rows, cols), dtype=torch.bfloat16, device=like.device)
+
+
+def cake_gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu", *, save: bool = True,
+                   h: torch.Tensor | None = None, g: torch.Tensor | None = None, u: torch.Tensor | None = None,
+                   stream=None):
+    """Forward: (h, g, u) with g = x w_gate^T, u = x w_up^T and h = act(g) * u.
+
+    x: BF16 [T, H]; w_gate, w_up: BF16 [F, H] (the two may be halves of one
+    matrix); H and F multiples of 8.  act: "silu" or "gelu" (the tanh form).
+    With ``save`` false g and u, which only the backward needs, are not written
+    and come back as None.
+    """
+    lib = load_library()
+    with _on(stream, x, w_gate, w_up, h, g, u):
+        if x.dim() != 2 or w_gate.dim() != 2:
+            raise ValueError(f"expected x [T, H] and w_gate [F, H], got {tuple(x.shape)} and {tuple(w_gate.shape)}")
+        (T, H), F = x.shape, w_gate.shape[0]
+        if not save and (g is not None or u is not None):
+            raise ValueError("g or u is given, but save is false")
+        given = _given(h, g, u)
+        if h is None:
+            h = _new(T, F, x)
+        if save:
+            g = _new(T, F, x) if g is None else g
+            u = _new(T, F, x) if u is None else u
+        st = lib.cake_gated_fwd(T, H, F, _matrix(x, T, H, "x"), _matrix(w_gate, F, H, "w_gate"),
+                                _matrix(w_up, F, H, "w_up"), _act(act), _matrix(h, T, F, "h"), _matrix(g, T, F, "g"),
+                                _matrix(u, T, F, "u"), _current())
+        _check(st, "cake_gated_fwd")
+        if given:
+            increment_version(given)
+    return h, g, u
+
+
+@functools.lru_cache(maxsize=256)
+def cake_gated_bwd_workspace_size(tokens: int, hidden: int, ffn: int) -> int:
+    """Workspace bytes of the gated block's backward."""
+    return int(load_library().cake_gated_bwd_workspace_size(int(tokens), int(hidden), int(ffn)))
+
+
+def cake_gated_bwd(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor, u: torch.Tensor, w_gate: torch.Tensor,
+                   w_up: torch.Tensor, act: str = "silu", *, need_dx: bool = True, need_dw: bool = True,
+                   workspace: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                   dw_gate: torch.Tensor | None = None, dw_up: torch.Tensor | None = None, stream=None):
+    """Backward: (dx, dw_gate, dw_up), BF16; None for what is not needed.
+
+    dh: gradient of h, BF16 [T, F]; g and u as the forward gave them.
+    """
+    lib = load_library()
+    with _on(stream, dh, x, g, u, w_gate, w_up, workspace, dx, dw_gate, dw_up):
+        if x.dim() != 2 or w_gate.dim() != 2:
+            raise ValueError(f"expected x [T, H] and w_gate [F, H], got {tuple(x.shape)} and {tuple(w_gate.shape)}")
+        (T, H), F = x.shape, w_gate.shape[0]
+        if (dx is not None and not need_dx) or ((dw_gate is not None or dw_up is not None) and not need_dw):
+            raise ValueError("an output is given for a gradient that is not asked for")
+        given = _given(dx, dw_gate, dw_up)
+        if need_dx and dx is None:
+            dx = _new(T, H, x)
+        if need_dw:
+            dw_gate = _new(F, H, x) if dw_gate is None else dw_gate
+            dw_up = _new(F, H, x) if dw_up is None else dw_up
+        workspace, ws, ws_bytes = _workspace(workspace, cake_gated_bwd_workspace_size(T, H, F), x.device)
+        st = lib.cake_gated_bwd(T, H, F, _matrix(dh, T, F, "dh"), _matrix(x, T, H, "x"), _matrix(g, T, F, "g"),
+                                _matrix(u, T, F, "u"), _matrix(w_gate, F, H, "w_gate"), _matrix(w_up, F, H, "w_up"),
+                                _act(act), _matrix(dx, T, H, "dx"), _matrix(dw_gate, F, H, "dw_gate"),
+                                _matrix(dw_up, F, H, "dw_up"), ws, ws_bytes, _current())
+        _check(st, "cake_gated_bwd")
+        if given:
+            increment_version(given)
+    return dx, dw_gate, dw_up
+
+
+class CakeGatedFunction(torch.autograd.Function):
+    """The gated block with the library's forward and backward: ``apply(x, w_gate, w_up, act)``."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, act="silu"):
+        rows = x.reshape(-1, x.shape[-1])
+        h, g, u = cake_gated_fwd(rows, w_gate, w_up, act)
+        ctx.save_for_backward(rows, g, u, w_gate, w_up)
+        ctx.act, ctx.size = act, x.shape
+        return h.view(*x.shape[:-1], h.shape[-1])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh):
+        x, g, u, w_gate, w_up = ctx.saved_tensors
+        dh = dh.to(torch.bfloat16).reshape(g.shape).contiguous()
+        dx, dwg, dwu = cake_gated_bwd(dh, x, g, u, w_gate, w_up, ctx.act, need_dx=ctx.needs_input_grad[0],
+                                      need_dw=ctx.needs_input_grad[1] or ctx.needs_input_grad[2])
+        return None if dx is None else dx.view(ctx.size), dwg, dwu, None
+
+
+def cake_gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu") -> torch.Tensor:
+    """Differentiable gated block: act(x w_gate^T) * (x w_up^T) of x [..., H]; see ``cake_gated_fwd``."""
+    if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
+        return CakeGatedFunction.apply(x, w_gate, w_up, act)
+    h, _, _ = cake_gated_fwd(x.reshape(-1, x.shape[-1]), w_gate, w_up, act, save=False)
+    return h.view(*x.shape[:-1], h.shape[-1])
+
+
+# ----------------------------------------------------------------------- rotary
+
+_STYLES = {"half": 0, "adjacent": 1}
+_rotation = struct.Struct("=qqQQQixxxxqqixxxx").pack  # cake_rotary
+
+
+def cake_rotary_table(sections, base: float = 10000.0, *, shared: bool = False, freqs=None, device="cuda"):
+    """(turns, axes) of a rotation: each pair's frequency and the axis whose position turns it.
+
+    sections: the number of pairs of each axis.  The i-th of an axis' n pairs
+    has the frequency base^(-i / n) radians a position, or with ``shared`` pair
+    j of all of them base^(-j / pairs); ``freqs`` gives every pair's frequency
+    instead.  turns: int64, the frequency's share of a turn in units of 2^-64
+    (modulo 2^64).
+    """
+    sections = [int(n) for n in sections]
+    pairs = sum(sections)
+    if freqs is None:
+        freqs = [base ** (-j / pairs) for j in range(pairs)] if shared else \
+            [base ** (-i / n) for n in sections for i in range(n)]
+    freqs = [float(f) for f in freqs]
+    if len(freqs) != pairs:
+        raise ValueError(f"{len(freqs)} frequencies for {pairs} pairs")
+    turns = []
+    for f in freqs:
+        if not math.isfinite(f):
+            raise ValueError(f"a frequency is {f}")
+        t = round(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64
+        turns.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+    axes = [a for a, n in enumerate(sections) for _ in range(n)]
+    return (torch.tensor(turns, dtype=torch.int64, device=device),
+            torch.tensor(axes, dtype=torch.int32, device=device))
+
+
+def _heads(t, what):
+    if t is not None and t.dim() != 3:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected [T, heads, D]")
+    return t
+
+
+def _packed_rotation(positions, turns, axes, style, T):
+    """(the packed cake_rotary, the tensors that it points into)."""
+    if style not in _STYLES:
+        raise ValueError(f"style is 'half' or 'adjacent', got {style!r}")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"positions are int32 or int64, got {positions.dtype}")
+    if positions.dim() not in (1, 2) or positions.shape[-1] != T:
+        raise ValueError(f"positions have shape {tuple(positions.shape)}, expected [{T}] or [axes, {T}]")
+    if turns.dtype is not torch.int64 or turns.dim() != 1:
+        raise TypeError("turns is an int64 tensor [pairs] (see cake_rotary_table)")
+    turns = turns.contiguous()
+    n_axes = positions.shape[0] if positions.dim() == 2 else 1
+    if axes is None:
+        if n_axes > 1:
+            raise ValueError("positions of several axes need each pair's axis")
+    else:
+        if axes.dtype is not torch.int32 or axes.shape != turns.shape:
+            raise ValueError("axes is an int32 tensor of turns' shape")
+        axes = axes.contiguous()
+    st = positions.stride()
+    packed = _rotation(turns.numel(), n_axes, turns.data_ptr(), 0 if axes is None else axes.data_ptr(),
+                       positions.data_ptr(), int(positions.dtype is torch.int64), st[0] if len(st) == 2 else 0, st[-1],
+                       _STYLES[style])
+    return packed, (turns, axes)
+
+
+def _norm_weights(k, w_q, w_k, D):
+    if k is not None and (w_q is None) != (w_k is None):
+        raise ValueError("queries and keys are normed both or neither: give w_q and w_k, or none")
+    if w_q is None:
+        return None, None
+    return _weight(w_q, D, "w_q"), None if k is None else _weight(w_k, D, "w_k")
+
+
+def _w(w):
+    """A weight's address and dtype (None: NULL)."""
+    return (None, 0) if w is None else (w.data_ptr(), _dtype(w))
+
+
+def cake_rotary_fwd(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns: torch.Tensor,
+                    axes: torch.Tensor | None = None, w_q: torch.Tensor | None = None,
+                    w_k: torch.Tensor | None = None, eps: float = 1e-6, *, style: str = "half",
+                    q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                    rstd_q: torch.Tensor | None = None, rstd_k: torch.Tensor | None = None, stream=None):
+    """Forward: (q_out, k_out, rstd_q, rstd_k): each head normed (with w_q, w_k), then rotated by its position.
+
+    q: BF16 [T, heads, D], k: BF16 [T, k_heads, D] or None, views with a
+    contiguous D (a multiple of 16, at most 512); positions: int32 or int64 [T]
+    or [axes, T]; turns, axes: see ``cake_rotary_table``.  The first 2 * pairs
+    columns are rotated, pair i being columns (i, pairs + i) in style "half"
+    and (2 i, 2 i + 1) in style "adjacent".  w_q, w_k: [D] BF16 or FP32; without
+    them there is no norm and rstd_q and rstd_k are None, else they are FP32
+    [T * heads].  q_out may be q itself and k_out k itself.
+    """
+    lib = load_library()
+    with _on(stream, q, k, positions, turns, axes, w_q, w_k, q_out, k_out, rstd_q, rstd_k):
+        T, nq, D = _heads(q, "q").shape
+        nk = 0 if k is None else _heads(k, "k").shape[1]
+        if k is None and (k_out is not None or rstd_k is not None):
+            raise ValueError("an output for keys is given without keys")
+        w_q, w_k = _norm_weights(k, w_q, w_k, D)
+        if w_q is None and (rstd_q is not None or rstd_k is not None):
+            raise ValueError("rstd is given, but there is no norm")
+        rotation, alive = _packed_rotation(positions, turns, axes, style, T)
+        given = _given(q_out, k_out, rstd_q, rstd_k)
+        if q_out is None:
+            q_out = _like(q)
+        if k is not None and k_out is None:
+            k_out = _like(k)
+        if w_q is not None:
+            if rstd_q is None:
+                rstd_q = torch.empty(T * nq, dtype=torch.float32, device=q.device)
+            if k is not None and rstd_k is None:
+                rstd_k = torch.empty(T * nk, dtype=torch.float32, device=q.device)
+        st = lib.cake_rotary_fwd(T, nq, nk, D, _ref(q, (T, nq, D), "q"), _ref(k, (T, nk, D), "k"), rotation, *_w(w_q),
+                                 *_w(w_k), eps, _ref(q_out, (T, nq, D), "q_out"), _ref(k_out, (T, nk, D), "k_out"),
+                                 None if rstd_q is None else _rows_f32(rstd_q, T * nq, "rstd_q"),
+                                 None if rstd_k is None else _rows_f32(rstd_k, T * nk, "rstd_k"), _current())
+        _check(st, "cake_rotary_fwd")
+        if given:
+            increment_version(given)
+    return q_out, k_out, rstd_q, rstd_k
+
+
+@functools.lru_cache(maxsize=256)
+def cake_rotary_bwd_workspace_size(tokens: int, q_heads: int, k_heads: int, hidden: int) -> int:
+    """Workspace bytes of the rotary backward with a norm (k_heads 0: no keys)."""
+    return int(load_library().cake_rotary_bwd_workspace_size(int(tokens), int(q_heads), int(k_heads), int(hidden)))
+
+
+def cake_rotary_bwd(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.Tensor, turns: torch.Tensor,
+                    axes: torch.Tensor | None = None, q: torch.Tensor | None = None, k: torch.Tensor | None = None,
+                    rstd_q: torch.Tensor | None = None, rstd_k: torch.Tensor | None = None,
+                    w_q: torch.Tensor | None = None, w_k: torch.Tensor | None = None, *, style: str = "half",
+                    workspace: torch.Tensor | None = None, dq_out: torch.Tensor | None = None,
+                    dk_out: torch.Tensor | None = None, dw_q: torch.Tensor | None = None,
+                    dw_k: torch.Tensor | None = None, stream=None):
+    """Backward: (dq_out, dk_out, dw_q, dw_k); dw_q and dw_k are FP32 [D], None without a norm.
+
+    dq, dk: gradients of the forward's q_out and k_out; q, k, rstd_q, rstd_k:
+    the forward's inputs and what it gave (with a norm only).  dq_out may be dq
+    itself and dk_out dk itself.
+    """
+    lib = load_library()
+    with _on(stream, dq, dk, positions, turns, axes, q, k, rstd_q, rstd_k, w_q, w_k, workspace, dq_out, dk_out, dw_q,
+             dw_k):
+        T, nq, D = _heads(dq, "dq").shape
+        nk = 0 if dk is None else _heads(dk, "dk").shape[1]
+        if dk is None and (dk_out is not None or dw_k is not None):
+            raise ValueError("an output for keys is given without keys")
+        w_q, w_k = _norm_weights(dk, w_q, w_k, D)
+        norm = w_q is not None
+        if norm and (q is None or rstd_q is None or (dk is not None and (k is None or rstd_k is None))):
+            raise ValueError("the norm's gradient needs the forward's inputs and rstd")
+        if not norm and (dw_q is not None or dw_k is not None):
+            raise ValueError("a weight's gradient is given, but there is no norm")
+        rotation, alive = _packed_rotation(positions, turns, axes, style, T)
+        given = _given(dq_out, dk_out, dw_q, dw_k)
+        if dq_out is None:
+            dq_out = _like(dq)
+        if dk is not None and dk_out is None:
+            dk_out = _like(dk)
+        if norm:
+            if dw_q is None:
+                dw_q = torch.empty(D, dtype=torch.float32, device=dq.device)
+            if dk is not None and dw_k is None:
+                dw_k = torch.empty(D, dtype=torch.float32, device=dq.device)
+            for t, what in ((dw_q, "dw_q"), (dw_k, "dw_k")):
+                if t is not None and (t.dtype is not torch.float32 or t.numel() != D or not t.is_contiguous()):
+                    raise ValueError(f"{what} must be a contiguous FP32 tensor of D elements")
+        size = cake_rotary_bwd_workspace_size(T, nq, nk, D) if norm else 0
+        workspace, ws, ws_bytes = _workspace(workspace, size, dq.device)
+        keys = norm and dk is not None
+        st = lib.cake_rotary_bwd(T, nq, nk, D, _ref(dq, (T, nq, D), "dq"), _ref(dk, (T, nk, D), "dk"), rotation,
+                                 _ref(q if norm else None, (T, nq, D), "q"), _ref(k if keys else None, (T, nk, D), "k"),
+                                 _rows_f32(rstd_q, T * nq, "rstd_q") if norm else None,
+                                 _rows_f32(rstd_k, T * nk, "rstd_k") if keys else None, *_w(w_q), *_w(w_k),
+                                 _ref(dq_out, (T, nq, D), "dq_out"), _ref(dk_out, (T, nk, D), "dk_out"),
+                                 dw_q.data_ptr() if norm else None, dw_k.data_ptr() if keys else None, ws, ws_bytes,
+                                 _current())
+        _check(st, "cake_rotary_bwd")
+        if given:
+            increment_version(given)
+    return dq_out, dk_out, dw_q, dw_k
+
+
+class CakeRotaryFunction(torch.autograd.Function):
+    """Normed and rotated queries and keys with the library's forward and backward:
+    ``apply(q, k, positions, turns, axes, w_q, w_k, eps, style)``."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, turns, axes=None, w_q=None, w_k=None, eps=1e-6, style="half"):
+        y, z, rq, rk = cake_rotary_fwd(q, k, positions, turns, axes, w_q, w_k, eps, style=style)
+        norm = w_q is not None
+        ctx.save_for_backward(positions, turns, axes, w_q, w_k, rq, rk, q if norm else None, k if norm else None)
+        ctx.style, ctx.sizes = style, (q.shape, None if k is None else k.shape)
+        ctx.set_materialize_grads(False)
+        return y, z
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        if dq is None and dk is None:
+            return (None,) * 9
+        positions, turns, axes, w_q, w_k, rq, rk, q, k = ctx.saved_tensors
+        grads = []
+        for d, size in zip((dq, dk), ctx.sizes):
+            if size is not None and d is None:
+                d = torch.zeros(size, dtype=torch.bfloat16, device=positions.device)
+            grads.append(None if size is None else d.to(torch.bfloat16).contiguous())
+        dq, dk, dwq, dwk = cake_rotary_bwd(*grads, positions, turns, axes, q, k, rq, rk, w_q, w_k, style=ctx.style)
+        return (dq, dk, None, None, None, None if w_q is None else dwq.to(w_q.dtype),
+                None if w_k is None or dwk is None else dwk.to(w_k.dtype), None, None)
+
+
+def cake_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns: torch.Tensor,
+                axes: torch.Tensor | None = None, w_q: torch.Tensor | None = None, w_k: torch.Tensor | None = None,
+                eps: float = 1e-6, style: str = "half"):
+    """Differentiable per-head norm and rotary positions: (q_out, k_out); see ``cake_rotary_fwd``."""
+    return CakeRotaryFunction.apply(q, k, positions, turns, axes, w_q, w_k, eps, style)
+
+
+# ---------------------------------------------------------------------- dropout
+
+def _random(seed):
+    """(host seed, address of a device seed and offset or None) of a number or an int64 tensor of two."""
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype is not torch.int64 or seed.numel() != 2 or not seed.is_contiguous():
+            raise ValueError("a seed on the device is a contiguous int64 tensor of two: the seed, and a number added to "
+                             "offset")
+        return 0, seed.data_ptr()
+    return int(seed), None
+
+
+def _on_device(seed):
+    return seed if isinstance(seed, torch.Tensor) else None
+
+
+def cake_dropout_fwd(x: torch.Tensor, p: float, seed, offset: int = 0, residual: torch.Tensor | None = None, *,
+                     y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = bf16(m * x [+ residual]), m 0 with probability p and else 1 over the share that is kept.
+
+    x, residual: BF16 [T, H] or [T, nh, H] views.  The mask goes by seed,
+    offset and an element's place alone and is never stored: calls with the
+    same ones drop the same elements, so give every use of a step an offset of
+    its own.  p counts in steps of 2^-16.  seed: a number, or an int64 tensor
+    of two on the device, the seed and a number that is added to offset, which
+    a captured graph reads anew at each replay.  y may be x or residual.
+    """
+    lib = load_library()
+    with _on(stream, x, residual, y, _on_device(seed)):
+        T, nh, H = _rows(x)
+        size = x.shape
+        host, rng = _random(seed)
+        given = _given(y)
+        if y is None:
+            y = _like(x)
+        st = lib.cake_dropout(_three(T, nh, H), _ref(x, size, "x"), _ref(residual, size, "residual"), p, host,
+                              int(offset), rng, _ref(y, size, "y"), _current())
+        _check(st, "cake_dropout")
+        if given:
+            increment_version(given)
+    return y
+
+
+def cake_dropout_bwd(dy: torch.Tensor, p: float, seed, offset: int = 0, *, dx: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """dx = bf16(m * dy): the gradient of ``cake_dropout_fwd``'s x (that of its residual is dy)."""
+    return cake_dropout_fwd(dy, p, seed, offset, y=dx, stream=stream)
+
+
+class CakeDropoutFunction(torch.autograd.Function):
+    """Dropout with an optional residual addition: ``apply(x, residual, p, seed, offset)``."""
+
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset=0):
+        ctx.save_for_backward(_on_device(seed))
+        ctx.p, ctx.seed, ctx.offset = p, None if isinstance(seed, torch.Tensor) else seed, offset
+        return cake_dropout_fwd(x, p, seed, offset, residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        seed, = ctx.saved_tensors
+        dy = dy.to(torch.bfloat16).contiguous()
+        dx = cake_dropout_bwd(dy, ctx.p, ctx.seed if seed is None else seed, ctx.offset) \
+            if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None, None
+
+
+def cake_dropout(x: torch.Tensor, p: float, seed, offset: int = 0,
+                 residual: torch.Tensor | None = None) -> torch.Tensor:
+    """Differentiable dropout, with an optional residual addition; see ``cake_dropout_fwd``."""
+    return CakeDropoutFunction.apply(x, residual, p, seed, offset)
+
+
+def cake_dropout_norm_fwd(x: torch.Tensor, residual: torch.Tensor, w: torch.Tensor, p: float, seed, offset: int = 0,
+                          eps: float = 1e-6, *, y: torch.Tensor | None = None, h_new: torch.Tensor | None = None,
+                          rstd: torch.Tensor | None = None, stream=None):
+    """Forward: (y, h_new, rstd): h_new = bf16(residual + m * x), y = norm(h_new) * w.
+
+    x: a block's output, residual: the residual stream, BF16 [T, H] or
+    [T, nh, H]; w: [H] BF16 or FP32; p, seed, offset: see ``cake_dropout_fwd``.
+    y and h_new may be x or residual themselves.
+    """
+    lib = load_library()
+    with _on(stream, x, residual, w, y, h_new, rstd, _on_device(seed)):
+        T, nh, H = _rows(x)
+        size, rows = x.shape, T * nh
+        w = _weight(w, H, "w")
+        host, rng = _random(seed)
+        given = _given(y, h_new, rstd)
+        if y is None:
+            y = _like(x)
+        if h_new is None:
+            h_new = _like(x)
+        if rstd is None:
+            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        st = lib.cake_dropout_norm_fwd(_three(T, nh, H), _ref(x, size, "x"), _ref(residual, size, "residual"),
+                                       w.data_ptr(), _dtype(w), p, host, int(offset), rng, eps, _ref(y, size, "y"),
+                                       _ref(h_new, size, "h_new"), _rows_f32(rstd, rows, "rstd"), _current())
+        _check(st, "cake_dropout_norm_fwd")
+        if given:
+            increment_version(given)
+    return y, h_new, rstd
+
+
+@functools.lru_cache(maxsize=256)
+def _dropout_norm_bwd_bytes(T, nh, H):
+    return int(load_library().cake_dropout_norm_bwd_workspace_size(_three(T, nh, H)))
+
+
+def cake_dropout_norm_bwd_workspace_size(x_or_shape) -> int:
+    """Workspace bytes the backward needs for this row set ([T, H] / [T, nh, H] tensor or (T, nh, H))."""
+    return _dropout_norm_bwd_bytes(*(_rows(x_or_shape) if isinstance(x_or_shape, torch.Tensor) else x_or_shape))
+
+
+def cake_dropout_norm_bwd(dy: torch.Tensor, h_new: torch.Tensor, rstd: torch.Tensor, w: torch.Tensor, p: float, seed,
+                          offset: int = 0, dh: torch.Tensor | None = None, *, workspace: torch.Tensor | None = None,
+                          dx: torch.Tensor | None = None, dresidual: torch.Tensor | None = None,
+                          dw: torch.Tensor | None = None, stream=None):
+    """Backward: (dresidual, dx, dw); dw is FP32 [H].
+
+    dy: gradient of y; dh: that reaching h_new directly, or None; h_new and rstd
+    as the forward gave them, p, seed and offset as it took them.
+    """
+    lib = load_library()
+    with _on(stream, dy, h_new, rstd, w, dh, workspace, dx, dresidual, dw, _on_device(seed)):
+        T, nh, H = _rows(dy)
+        size, rows = dy.shape, T * nh
+        w = _weight(w, H, "w")
+        host, rng = _random(seed)
+        given = _given(dx, dresidual, dw)
+        if dx is None:
+            dx = _like(dy)
+        if dresidual is None:
+            dresidual = _like(dy)
+        if dw is None:
+            dw = torch.empty(H, dtype=torch.float32, device=dy.device)
+        elif dw.dtype is not torch.float32 or dw.numel() != H or not dw.is_contiguous():
+            raise ValueError("dw must be a contiguous FP32 tensor of H elements")
+        workspace, ws, ws_bytes = _workspace(workspace, _dropout_norm_bwd_bytes(T, nh, H), dy.device)
+        st = lib.cake_dropout_norm_bwd(_three(T, nh, H), _ref(dy, size, "dy"), _ref(dh, size, "dh"),
+                                       _ref(h_new, size, "h_new"), _rows_f32(rstd, rows, "rstd"), w.data_ptr(),
+                                       _dtype(w), p, host, int(offset), rng, _ref(dx, size, "dx"),
+                                       _ref(dresidual, size, "dresidual"), dw.data_ptr(), ws, ws_bytes, _current())
+        _check(st, "cake_dropout_norm_bwd")
+        if given:
+            increment_version(given)
+    return dresidual, dx, dw
+
+
+class CakeDropoutNormFunction(torch.autograd.Function):
+    """(y, h_new) of dropout, residual addition and norm:
+    ``apply(x, residual, w, p, seed, offset, eps)``."""
+
+    @staticmethod
+    def forward(ctx, x, residual, w, p, seed, offset=0, eps=1e-6):
+        y, h, rstd = cake_dropout_norm_fwd(x, residual, w, p, seed, offset, eps)
+        ctx.save_for_backward(h, rstd, w, _on_device(seed))
+        ctx.p, ctx.seed, ctx.offset = p, None if isinstance(seed, torch.Tensor) else seed, offset
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh):
+        if dy is None and dh is None:
+            return (None,) * 7
+        h, rstd, w, seed = ctx.saved_tensors
+        dy = torch.zeros_like(h) if dy is None else dy.to(torch.bfloat16).contiguous()
+        dh = None if dh is None else dh.to(torch.bfloat16).contiguous()
+        dres, dx, dw = cake_dropout_norm_bwd(dy, h, rstd, w, ctx.p, ctx.seed if seed is None else seed, ctx.offset, dh)
+        return dx, dres, dw.to(w.dtype), None, None, None, None
+
+
+def cake_dropout_norm(x: torch.Tensor, residual: torch.Tensor, w: torch.Tensor, p: float, seed, offset: int = 0,
+                      eps: float = 1e-6):
+    """Differentiable dropout, residual addition and norm: (y, h_new); see ``cake_dropout_norm_fwd``."""
+    return CakeDropoutNormFunction.apply(x, residual, w, p, seed, offset, eps)

@@ -1,0 +1,468 @@
+// cake_dropout.cu -- dropout from a counter-based generator for sm_103a: alone,
+// with a residual addition, and with the residual addition and the RMSNorm
+// after it, forward and backward.
+//
+// The random bits of 8 neighbouring elements (a thread's 16-byte vector) are
+// one block of Philox4x32-10 (Salmon, Moraes, Dror, Shaw 2011): ten rounds of
+// two 32 x 32 -> 64 bit products.  Sixteen bits an element make that about 9
+// instructions an element; with 32 it would be twice as much.  Nothing of the
+// mask is stored or read, so HBM bounds every kernel here.
+#include "../csrc/cake_rows.cuh"
+#include "cake_block_launch.h"
+
+namespace cake {
+
+struct Philox {
+    uint32_t k0, k1, o0, o1;
+};
+
+__device__ __forceinline__ Philox philox_init(const DropoutRng &r)
+{
+    uint64_t seed = r.seed, off = r.offset;
+    if (r.rng) {
+        seed = r.rng[0];
+        off += r.rng[1];
+    }
+    return {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)off, (uint32_t)(off >> 32)};
+}
+
+// 16 bits for each of the 8 elements of vector b, lowest first.
+__device__ __forceinline__ uint4 philox(const Philox &s, uint64_t b)
+{
+    uint32_t x = (uint32_t)b, y = (uint32_t)(b >> 32), z = s.o0, w = s.o1, k0 = s.k0, k1 = s.k1;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t p0 = (uint64_t)x * 0xD2511F53u, p1 = (uint64_t)z * 0xCD9E8D57u;
+        x = (uint32_t)(p1 >> 32) ^ y ^ k0;
+        z = (uint32_t)(p0 >> 32) ^ w ^ k1;
+        y = (uint32_t)p1;
+        w = (uint32_t)p0;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return make_uint4(x, y, z, w);
+}
+
+// The factors of a pair of elements: 0 where dropped.
+__device__ __forceinline__ bool keep_lo(uint32_t bits, uint32_t cut) { return (bits & 0xffffu) >= cut; }
+__device__ __forceinline__ bool keep_hi(uint32_t bits, uint32_t cut) { return (bits >> 16) >= cut; }
+
+// scale * v where kept, 0 elsewhere.
+__device__ __forceinline__ float2 dropped(float2 v, uint32_t bits, uint32_t cut, float scale)
+{
+    return make_float2(keep_lo(bits, cut) ? __fmul_rn(v.x, scale) : 0.f,
+                       keep_hi(bits, cut) ? __fmul_rn(v.y, scale) : 0.f);
+}
+
+// -------------------------------------------------------------------- alone
+
+// A CTA takes 1024 neighbouring vectors at a time, four a thread.  Their rows
+// come from one 64-bit division for all of them and a 32-bit one for each.
+constexpr int kDropThreads = 256;
+constexpr int kDropPer = 4;
+constexpr uint32_t kDropVecs = kDropThreads * kDropPer;
+constexpr uint64_t kDropCtas = 1 << 20;
+
+template <bool RES>
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropoutParams p)
+{
+    pdl_wait();
+    const Philox key = philox_init(p.r);
+    for (uint64_t v0 = (uint64_t)blockIdx.x * kDropVecs; v0 < p.vecs; v0 += (uint64_t)gridDim.x * kDropVecs) {
+        const uint32_t row0 = (uint32_t)(v0 / p.nvec), rem = (uint32_t)(v0 - (uint64_t)row0 * p.nvec);
+        const uint32_t n = p.vecs - v0 < kDropVecs ? (uint32_t)(p.vecs - v0) : kDropVecs;
+        uint4 x[kDropPer], e[kDropPer];
+        uint32_t row[kDropPer], col[kDropPer];
+#pragma unroll
+        for (int k = 0; k < kDropPer; ++k) {
+            const uint32_t i = k * kDropThreads + threadIdx.x, at = rem + i, q = at / p.nvec;
+            row[k] = row0 + q;
+            col[k] = (at - q * p.nvec) * 8;
+            if (i < n) {
+                x[k] = __ldcs(reinterpret_cast<const uint4 *>(p.x.base + row_off(p.x, row[k], p.nh) + col[k]));
+                if (RES)
+                    e[k] = __ldcs(reinterpret_cast<const uint4 *>(p.residual.base +
+                                                                  row_off(p.residual, row[k], p.nh) + col[k]));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kDropPer; ++k) {
+            const uint32_t i = k * kDropThreads + threadIdx.x;
+            if (i >= n)
+                break;
+            const uint4 bits = philox(key, v0 + i);
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float2 v = dropped(bf2(word(x[k], q)), word(bits, q), p.r.cut, p.r.scale);
+                if (RES)
+                    v = add2(v, bf2(word(e[k], q)));
+                o[q] = pack2(v);
+            }
+            __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.y.base) + row_off(p.y, row[k], p.nh) + col[k]),
+                   make_uint4(o[0], o[1], o[2], o[3]));
+        }
+    }
+}
+
+// ------------------------------------------------------------ with the norm
+
+// Both kernels stream rows through shared memory as the RMSNorm kernels do (a
+// producer warp with bulk copies, row groups of W warps, bounded waits).
+constexpr int kDnThreads = 416;      // 12 consumer warps and the producer
+constexpr int kDnWideThreads = 544;  // 16: the forward's rows of more than 6144 columns
+
+template <int VPT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == kDnThreads ? 2 : 1)
+    dropout_norm_fwd_kernel(const __grid_constant__ DropoutNormParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const Layout &L = p.L;
+    const Smem s = carve_smem(smem_raw, L);
+    const Chunk c = cta_chunk(L);
+    const int W = L.warps_per_row, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    init_ring(s, L);
+    pdl_wait();
+    if (warp == L.groups * W) {
+        const RowView views[2] = {p.in[0], p.in[1]};
+        produce<2>(s, L, c, views, 2, p.status, p.wait_ns);
+        return;
+    }
+    const int gid = warp / W, wig = warp - gid * W, gtid = wig * 32 + lane, vstride = 32 * W, nvec = L.nvec;
+    const Philox key = philox_init(p.r);
+    stage_weight(s, L, p.w, p.w_f32);
+    bool abort = false;
+    uint32_t slot = 0, st = 0, ph = 0;
+    for (uint32_t it = 0; it < c.ntiles && !abort; ++it) {
+        const uint32_t r = c.r0 + it * c.tile_rows + gid;
+        uint4 bits[VPT]; // before the wait: they need no data
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+            bits[k] = philox(key, (uint64_t)r * nvec + k * vstride + gtid);
+        abort = !mbar_wait(smem_addr(&s.full[st]), ph, p.wait_ns);
+        if (r < c.r_end) { // uniform across the group
+            const uint8_t *stage = s.ring + st * s.stage_bytes + (size_t)gid * L.H * 2;
+            const uint4 *xs = reinterpret_cast<const uint4 *>(stage);
+            const uint4 *es = reinterpret_cast<const uint4 *>(stage + s.tens_bytes);
+            uint4 h[VPT];
+            float2 ss = make_float2(0.f, 0.f);
+            uint4 *hrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[1].base) + row_off(p.out[1], r, L.nh));
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = k * vstride + gtid;
+                h[k] = make_uint4(0, 0, 0, 0);
+                if (v < nvec) {
+                    const uint4 x = xs[v], e = es[v];
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        o[q] = pack2(add2(dropped(bf2(word(x, q)), word(bits[k], q), p.r.cut, p.r.scale),
+                                          bf2(word(e, q))));
+                        const float2 a = bf2(o[q]);
+                        ss = fma2(a, a, ss);
+                    }
+                    h[k] = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (!abort)
+                        __stcs(hrow + v, h[k]);
+                }
+            }
+            const float tot = group_sum(__fadd_rn(ss.x, ss.y), s, L, gid, wig, lane, slot++, abort);
+            const float rs = 1.0f / sqrtf(__fadd_rn(__fmul_rn(tot, L.inv_h), p.eps));
+            const float2 rs2 = make_float2(rs, rs);
+            uint4 *yrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[0].base) + row_off(p.out[0], r, L.nh));
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = k * vstride + gtid;
+                if (v < nvec && !abort) {
+                    float2 w2[4];
+                    weight_pairs(s, L, v, w2);
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        o[q] = pack2(mul2(mul2(bf2(word(h[k], q)), rs2), w2[q]));
+                    __stcs(yrow + v, make_uint4(o[0], o[1], o[2], o[3]));
+                }
+            }
+            if (gtid == 0 && !abort)
+                p.rstd_out[r] = rs;
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_addr(&s.empty[st]));
+        if (++st == (uint32_t)L.stages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+    if (abort && lane == 0)
+        set_status(p.status, kStatusTimeout);
+}
+
+// Kahan-compensated hi += a * b of column pairs; lo holds the part of the last
+// term that hi has not taken up.
+__device__ __forceinline__ void kahan_pair(float2 &hi, float2 &lo, float2 a, float2 b)
+{
+    const float2 y = fma2(a, b, lo);
+    const float2 t = add2(hi, y);
+    lo = add2(sub2(hi, t), y);
+    hi = t;
+}
+
+// A thread holds 8 VPT columns of the row and of the weight's gradient (Kahan
+// pairs).  The mask's bits are computed before the row's sum and kept as one
+// bit an element.
+template <int VPT, bool DH>
+__global__ void __launch_bounds__(kDnThreads, 1) dropout_norm_bwd_kernel(const __grid_constant__ DropoutNormParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const Layout &L = p.L;
+    const Smem s = carve_smem(smem_raw, L);
+    const Chunk c = cta_chunk(L);
+    const int W = L.warps_per_row, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    init_ring(s, L);
+    pdl_wait();
+    if (warp == L.groups * W) {
+        const RowView views[3] = {p.in[0], p.in[1], p.in[2]};
+        produce<3>(s, L, c, views, L.ntens, p.status, p.wait_ns);
+        return;
+    }
+    const int gid = warp / W, wig = warp - gid * W, gtid = wig * 32 + lane, vstride = 32 * W, nvec = L.nvec;
+    const Philox key = philox_init(p.r);
+    stage_weight(s, L, p.w, p.w_f32);
+    float2 hi[VPT][4], lo[VPT][4];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            hi[k][q] = lo[k][q] = make_float2(0.f, 0.f);
+    bool abort = false;
+    uint32_t slot = 0, st = 0, ph = 0;
+    for (uint32_t it = 0; it < c.ntiles && !abort; ++it) {
+        const uint32_t r = c.r0 + it * c.tile_rows + gid;
+        const float rs = r < c.r_end ? __ldg(p.rstd + r) : 0.f;
+        uint32_t keep = 0;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const uint4 b = philox(key, (uint64_t)r * nvec + k * vstride + gtid);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                keep |= ((uint32_t)keep_lo(word(b, q), p.r.cut) | (uint32_t)keep_hi(word(b, q), p.r.cut) << 1)
+                        << (8 * k + 2 * q);
+        }
+        abort = !mbar_wait(smem_addr(&s.full[st]), ph, p.wait_ns);
+        if (r < c.r_end) { // uniform across the group
+            const uint8_t *stage = s.ring + st * s.stage_bytes + (size_t)gid * L.H * 2;
+            const uint4 *hs = reinterpret_cast<const uint4 *>(stage);
+            const uint4 *ds = reinterpret_cast<const uint4 *>(stage + s.tens_bytes);
+            const uint4 *es = reinterpret_cast<const uint4 *>(stage + 2 * s.tens_bytes);
+            const float2 rs2 = make_float2(rs, rs);
+            uint4 h[VPT], d[VPT];
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = k * vstride + gtid;
+                h[k] = d[k] = make_uint4(0, 0, 0, 0);
+                if (v < nvec) {
+                    h[k] = hs[v];
+                    d[k] = ds[v];
+                    float2 w2[4];
+                    weight_pairs(s, L, v, w2);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 dq = bf2(word(d[k], q)), hh = mul2(bf2(word(h[k], q)), rs2);
+                        sum = fma2(mul2(dq, w2[q]), hh, sum);
+                        kahan_pair(hi[k][q], lo[k][q], dq, hh);
+                    }
+                }
+            }
+            const float tot = group_sum(__fadd_rn(sum.x, sum.y), s, L, gid, wig, lane, slot++, abort);
+            const float m = -__fmul_rn(tot, L.inv_h);
+            const float2 mean = make_float2(m, m);
+            uint4 *xrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[0].base) + row_off(p.out[0], r, L.nh));
+            uint4 *erow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[1].base) + row_off(p.out[1], r, L.nh));
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = k * vstride + gtid;
+                if (v < nvec && !abort) {
+                    uint4 e = make_uint4(0, 0, 0, 0);
+                    if (DH)
+                        e = es[v];
+                    float2 w2[4];
+                    weight_pairs(s, L, v, w2);
+                    uint32_t ox[4], oe[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 a = mul2(bf2(word(d[k], q)), w2[q]), hh = mul2(bf2(word(h[k], q)), rs2);
+                        float2 t = mul2(rs2, fma2(hh, mean, a));
+                        if (DH)
+                            t = add2(t, bf2(word(e, q)));
+                        oe[q] = pack2(t);
+                        const uint32_t b = keep >> (8 * k + 2 * q);
+                        ox[q] = pack2(make_float2(b & 1 ? __fmul_rn(t.x, p.r.scale) : 0.f,
+                                                  b & 2 ? __fmul_rn(t.y, p.r.scale) : 0.f));
+                    }
+                    __stcs(xrow + v, make_uint4(ox[0], ox[1], ox[2], ox[3]));
+                    __stcs(erow + v, make_uint4(oe[0], oe[1], oe[2], oe[3]));
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_addr(&s.empty[st]));
+        if (++st == (uint32_t)L.stages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+    if (abort && lane == 0)
+        set_status(p.status, kStatusTimeout);
+    // The CTA partial: the groups' sums in group order, through the drained
+    // ring ([group][4 nvec] float4 (hi, lo, hi, lo) of a column pair).
+    const int nct = L.groups * W * 32, nslot = 4 * nvec;
+    float4 *comb = reinterpret_cast<float4 *>(s.ring);
+    consumer_sync(L);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int v = k * vstride + gtid;
+        if (v < nvec)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                comb[(size_t)gid * nslot + 4 * v + q] = make_float4(hi[k][q].x, lo[k][q].x, hi[k][q].y, lo[k][q].y);
+    }
+    consumer_sync(L);
+    for (int i = threadIdx.x; i < nslot; i += nct) {
+        float4 a = comb[i];
+        for (int g = 1; g < L.groups; ++g) {
+            const float4 b = comb[(size_t)g * nslot + i];
+            comp_add(a.x, a.y, b.x);
+            a.y = __fadd_rn(a.y, b.y);
+            comp_add(a.z, a.w, b.z);
+            a.w = __fadd_rn(a.w, b.w);
+        }
+        reinterpret_cast<float4 *>(p.partials + (size_t)blockIdx.x * L.H)[i] = a;
+    }
+    pdl_launch_dependents();
+}
+
+// Column sums of the CTAs' partials in CTA order: a warp takes 32 columns and
+// every 16th CTA; the 16 sums of a column are then added in warp order.
+constexpr int kColumnWarps = 16;
+
+__global__ void __launch_bounds__(32 * kColumnWarps) column_sum_kernel(const __grid_constant__ ColumnSumParams p)
+{
+    __shared__ float2 part[kColumnWarps][32];
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, list = blockIdx.y;
+    const int j = blockIdx.x * 32 + lane;
+    float hi = 0.f, lo = 0.f;
+    if (j < p.H)
+        for (int q = warp; q < p.P[list]; q += kColumnWarps) {
+            const float2 v = __ldcg(p.partials[list] + (size_t)q * p.H + j);
+            comp_add(hi, lo, v.x);
+            lo = __fadd_rn(lo, v.y);
+        }
+    part[warp][lane] = make_float2(hi, lo);
+    __syncthreads();
+    if (warp == 0 && j < p.H) {
+        for (int w = 1; w < kColumnWarps; ++w) {
+            comp_add(hi, lo, part[w][lane].x);
+            lo = __fadd_rn(lo, part[w][lane].y);
+        }
+        p.out[list][j] = __fadd_rn(hi, lo);
+    }
+}
+
+// ------------------------------------------------------------------- launch
+
+// The shape of a CTA goes by H and the staged tensors alone, so the orders of
+// the sums do too.
+DropoutNormPlan dropout_norm_plan(int H, uint32_t rows, int ntens, bool backward)
+{
+    const int nvec = H / 8;
+    DropoutNormPlan p{};
+    int best = -1;
+    for (int vpt = 1; vpt <= (backward ? 4 : 2); ++vpt) {
+        const int W = (nvec + 32 * vpt - 1) / (32 * vpt);
+        const int most = !backward && vpt == 2 && W > 12 ? 16 : 12;
+        if (W > most)
+            continue;
+        const int groups = most / W;
+        // columns in work, those of a single row group counted less: its warps wait for one sum together
+        int score = groups * H > 6144 ? 6144 : groups * H;
+        if (groups == 1)
+            score = score * 8 / 10;
+        if (score > best) {
+            best = score;
+            p.vpt = vpt;
+            p.W = W;
+            p.groups = groups;
+        }
+    }
+    const size_t fixed = kMiscBytes + weight_smem_bytes(H), stage = (size_t)ntens * p.groups * H * 2;
+    int per_sm = !backward && p.groups * p.W <= 12 ? 2 : 1;
+    for (;; --per_sm) {
+        const size_t room = 228 * 1024 / per_sm - 1024;
+        p.stages = room > fixed ? (int)((room - fixed) / stage) : 0;
+        if (p.stages >= 2 || per_sm == 1)
+            break;
+    }
+    // no more than 3 stages in the forward, 6 in the backward, or what brings 48 KB on their way
+    int most = (int)((48 * 1024 + stage - 1) / stage);
+    most = most > (backward ? 6 : 3) ? most : backward ? 6 : 3;
+    most = most > 16 ? 16 : most;
+    if (p.stages > most)
+        p.stages = most;
+    // (the backward's column sums, 8 bytes a column of each group, pass through the ring of two stages or more)
+    p.smem = fixed + p.stages * stage;
+    const uint32_t tiles = (rows + p.groups - 1) / p.groups;
+    const uint32_t ctas = tiles < (uint32_t)(kSMsBlock * per_sm) ? tiles : kSMsBlock * per_sm;
+    p.rows_per_cta = ctas ? (rows + ctas - 1) / ctas : 0;
+    p.ctas = p.rows_per_cta ? (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta) : 0;
+    return p;
+}
+
+cudaError_t launch_dropout(const DropoutParams &p, cudaStream_t stream)
+{
+    const uint64_t want = (p.vecs + kDropVecs - 1) / kDropVecs;
+    const dim3 grid((unsigned)(want < kDropCtas ? want : kDropCtas));
+    return p.residual.base ? launch_after(dropout_kernel<true>, grid, kDropThreads, 0, stream, p)
+                           : launch_after(dropout_kernel<false>, grid, kDropThreads, 0, stream, p);
+}
+
+cudaError_t launch_dropout_norm_fwd(const DropoutNormParams &p, const DropoutNormPlan &plan, cudaStream_t stream)
+{
+    const int threads = 32 * (plan.groups * plan.W + 1);
+    const dim3 grid((unsigned)plan.ctas);
+    if (plan.vpt == 1)
+        return launch_after(dropout_norm_fwd_kernel<1, kDnThreads>, grid, threads, plan.smem, stream, p);
+    if (threads <= kDnThreads)
+        return launch_after(dropout_norm_fwd_kernel<2, kDnThreads>, grid, threads, plan.smem, stream, p);
+    return launch_after(dropout_norm_fwd_kernel<2, kDnWideThreads>, grid, threads, plan.smem, stream, p);
+}
+
+template <int VPT>
+static cudaError_t launch_dn_bwd(const DropoutNormParams &p, const DropoutNormPlan &plan, cudaStream_t stream)
+{
+    const int threads = 32 * (plan.groups * plan.W + 1);
+    const dim3 grid((unsigned)plan.ctas);
+    return p.L.ntens == 3 ? launch_after(dropout_norm_bwd_kernel<VPT, true>, grid, threads, plan.smem, stream, p)
+                          : launch_after(dropout_norm_bwd_kernel<VPT, false>, grid, threads, plan.smem, stream, p);
+}
+
+cudaError_t launch_dropout_norm_bwd(const DropoutNormParams &p, const DropoutNormPlan &plan, cudaStream_t stream)
+{
+    switch (plan.vpt) {
+    case 1: return launch_dn_bwd<1>(p, plan, stream);
+    case 2: return launch_dn_bwd<2>(p, plan, stream);
+    case 3: return launch_dn_bwd<3>(p, plan, stream);
+    default: return launch_dn_bwd<4>(p, plan, stream);
+    }
+}
+
+cudaError_t launch_column_sum(const ColumnSumParams &p, int lists, cudaStream_t stream)
+{
+    return launch_after(column_sum_kernel, dim3((unsigned)((p.H + 31) / 32), (unsigned)lists), 32 * kColumnWarps, 0,
+                        stream, p);
+}
+
+} // namespace cake
