@@ -375,7 +375,7 @@ extern "C" cake_status cake_rotary_fwd(int64_t tokens, int64_t q_heads, int64_t 
         l.w_f32 = dtype[i] == CAKE_FP32;
         l.rstd_out = rstd[i];
     }
-    rotary_plan(p, false);
+    rotary_plan(p);
     return cuda_status(launch_rotary(p, rotary->style == CAKE_ROTARY_ADJACENT, false, cu(stream)));
 }
 
@@ -390,7 +390,7 @@ extern "C" size_t cake_rotary_bwd_workspace_size(int64_t tokens, int64_t q_heads
     fill_rotary(p, &none, tokens, hidden);
     for (int i = 0; i < c.lists; ++i)
         p.l[i].heads = (uint32_t)c.shape[i].heads;
-    rotary_plan(p, true);
+    rotary_plan(p);
     return (size_t)(p.l[0].ctas + p.l[1].ctas) * hidden * sizeof(float2);
 }
 
@@ -472,7 +472,7 @@ extern "C" cake_status cake_rotary_bwd(int64_t tokens, int64_t q_heads, int64_t 
         }
     }
     const bool adjacent = rotary->style == CAKE_ROTARY_ADJACENT;
-    rotary_plan(p, norm);
+    rotary_plan(p);
     if (!norm) // a rotation's gradient is rotated back
         return cuda_status(launch_rotary(p, adjacent, true, cu(stream)));
     p.l[0].partials = static_cast<float2 *>(workspace);

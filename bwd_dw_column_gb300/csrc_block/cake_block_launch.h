@@ -74,9 +74,8 @@ struct RotaryList {
     float *rstd_out;        // forward
     const float *rstd;      // backward
     float2 *partials;       // backward: [ctas][D] (hi, lo)
-    uint32_t tokens_per_cta;
-    int splits;             // lane groups that share a token's heads
     int ctas;
+    uint32_t run, rounds;   // see RotaryWalk
 };
 
 struct RotaryParams {
@@ -92,7 +91,7 @@ struct RotaryParams {
     int *status;            // [1]: an axis outside its range
 };
 
-void rotary_plan(RotaryParams &p, bool sums); // sets tokens_per_cta, splits and ctas of both lists
+void rotary_plan(RotaryParams &p); // sets both lists' ctas
 cudaError_t launch_rotary(const RotaryParams &p, bool adjacent, bool inverse, cudaStream_t stream);
 cudaError_t launch_rotary_bwd(const RotaryParams &p, bool adjacent, cudaStream_t stream);
 
@@ -132,12 +131,11 @@ cudaError_t ensure_smem_attr(const void *kernel, size_t smem);
 
 // Launched while the launch before it drains: the kernels wait for that one
 // before they read anything.
-// (Dynamic shared memory up to 48 KB needs no attribute of the kernel.)
 template <class... P, class... A>
 inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                                 const A &...args)
 {
-    if (smem > 48 * 1024) {
+    if (smem > 0) {
         cudaError_t e = ensure_smem_attr((const void *)kern, smem);
         if (e != cudaSuccess)
             return e;

@@ -345,8 +345,10 @@ __global__ void __launch_bounds__(kDnThreads, 1) dropout_norm_bwd_kernel(const _
 }
 
 // Column sums of the CTAs' partials in CTA order: a warp takes 32 columns and
-// every 16th CTA; the 16 sums of a column are then added in warp order.
-constexpr int kColumnWarps = 16;
+// every 32nd CTA, with several of its loads on their way at once; the 32 sums
+// of a column are then added in warp order.
+constexpr int kColumnWarps = 32;
+constexpr int kColumnAhead = 8;
 
 __global__ void __launch_bounds__(32 * kColumnWarps) column_sum_kernel(const __grid_constant__ ColumnSumParams p)
 {
@@ -356,10 +358,18 @@ __global__ void __launch_bounds__(32 * kColumnWarps) column_sum_kernel(const __g
     const int j = blockIdx.x * 32 + lane;
     float hi = 0.f, lo = 0.f;
     if (j < p.H)
-        for (int q = warp; q < p.P[list]; q += kColumnWarps) {
-            const float2 v = __ldcg(p.partials[list] + (size_t)q * p.H + j);
-            comp_add(hi, lo, v.x);
-            lo = __fadd_rn(lo, v.y);
+        for (int q0 = warp; q0 < p.P[list]; q0 += kColumnAhead * kColumnWarps) {
+            float2 v[kColumnAhead];
+#pragma unroll
+            for (int i = 0; i < kColumnAhead; ++i) {
+                const int q = q0 + i * kColumnWarps;
+                v[i] = q < p.P[list] ? __ldcg(p.partials[list] + (size_t)q * p.H + j) : make_float2(0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kColumnAhead; ++i) {
+                comp_add(hi, lo, v[i].x);
+                lo = __fadd_rn(lo, v[i].y);
+            }
         }
     part[warp][lane] = make_float2(hi, lo);
     __syncthreads();

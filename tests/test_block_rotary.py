@@ -245,3 +245,23 @@ def test_gradients_against_differences(cake):
         e[j] = h
         want = (loss(v64, w64 + e) - loss(v64, w64 - e)) / (2 * h)
         assert abs(float(dw[j]) - want) <= 1e-5 * (1 + abs(want))
+
+
+def test_several_axes_with_few_lanes_and_uneven_shares(cake):
+    """More axes than a row has lanes, tokens that leave the last lane groups without one, steps that no share divides."""
+    g = torch.Generator().manual_seed(11)
+    for T, n, D, sections, style in ((6151, 3, 32, (4, 2, 1, 1), "half"), (4099, 17, 48, (8, 8, 8), "adjacent"),
+                                     (2051, 5, 16, (2, 3, 3), "half"), (997, 40, 112, (16, 8), "half")):
+        q, k = heads(g, T, n, D), heads(g, T, 1, D)
+        w = weights(g, D, True)
+        turns, axes = cake.cake_rotary_table(sections, 100.0, device=DEV)
+        pos = torch.randint(-50, 500, (len(sections), T), generator=g).to(DEV)
+        angle = ref.phases(pos, turns, axes)
+        y, z, rq, rk = cake.cake_rotary_fwd(q, k, pos, turns, axes, w, w, style=style)
+        dq, dk, dwq, dwk = cake.cake_rotary_bwd(y, z, pos, turns, axes, q, k, rq, rk, w, w, style=style)
+        for v, y_, rs, dv, dw in ((q, y, rq, dq, dwq), (k, z, rk, dk, dwk)):
+            want, allow, r64 = ref.rotary_fwd(v, angle, w, 1e-6, style)
+            check("y", y_, want, allow)
+            want, allow, dw64, edw = ref.rotary_bwd(y_, angle, v, rs, w, style)
+            check("dv", dv, want, allow)
+            check("dw", dw, dw64, edw)
