@@ -66,6 +66,7 @@ def _bind(lib):
         ("cake_dropout_norm_bwd", _int, [S, T, T, T, _vp, _vp, _int, _f32, _u64, _u64, _vp, T, T, _vp, _vp, _size,
                                          _vp]),
         ("cake_block_wait_test", _int, [ctypes.c_uint32, _int]),
+        ("cake_dropout_norm_plan", _int, [S, _int, _int, ctypes.POINTER(_i64)]),
     ):
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args

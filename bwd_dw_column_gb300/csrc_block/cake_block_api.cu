@@ -46,6 +46,7 @@ Layout rows_layout(const DropoutNormPlan &plan, const cake_shape *shape, uint32_
     L.rows_per_group = 1;
     L.lanes_per_row = 32;
     L.stages = plan.stages;
+    L.lo_bytes = plan.lo_bytes;
     L.ntens = ntens;
     L.rows = rows;
     L.nh = (uint32_t)shape->heads;
@@ -74,6 +75,20 @@ extern "C" cake_status cake_block_wait_test(uint32_t wait_limit_us, int withhold
     return CAKE_OK;
 }
 
+extern "C" cake_status cake_dropout_norm_plan(const cake_shape *shape, int tensors, int backward, int64_t plan[8])
+{
+    uint32_t rows = 0;
+    const cake_status st = check_shape(shape, &rows);
+    if (st != CAKE_OK)
+        return st;
+    if (!plan || rows == 0 || tensors < 2 || tensors > 3)
+        return CAKE_ERR_INVALID;
+    const DropoutNormPlan p = dropout_norm_plan((int)shape->hidden, rows, tensors, backward != 0);
+    const int64_t got[8] = {p.vpt, p.W, p.groups, p.stages, p.ctas, p.rows_per_cta, p.lo_bytes, (int64_t)p.smem};
+    std::copy(got, got + 8, plan);
+    return CAKE_OK;
+}
+
 extern "C" cake_status cake_dropout(const cake_shape *shape, const cake_tensor *x, const cake_tensor *residual, float p,
                                     uint64_t seed, uint64_t offset, const uint64_t *rng, const cake_tensor *y,
                                     cake_stream_t stream)
@@ -97,6 +112,7 @@ extern "C" cake_status cake_dropout(const cake_shape *shape, const cake_tensor *
     q.y = make_view(y, shape);
     q.nh = (uint32_t)shape->heads;
     q.nvec = (uint32_t)(shape->hidden / 8);
+    q.reciprocal = (uint32_t)(((uint64_t(1) << 31) + q.nvec - 1) / q.nvec);
     q.vecs = (uint64_t)rows * q.nvec;
     return cuda_status(launch_dropout(q, cu(stream)));
 }

@@ -25,11 +25,13 @@ struct DropoutParams {
     DropoutRng r;
     RowView x, residual, y; // residual.base == nullptr: none
     uint32_t nh, nvec;      // vectors of 8 elements of a row
+    uint32_t reciprocal;    // 2^31 / nvec, rounded up
     uint64_t vecs;          // of the whole tensor
 };
 
 struct DropoutNormPlan {
-    int vpt, W, groups, stages, ctas;
+    int vpt, W, groups, stages, per_sm, ctas;
+    int lo_bytes;           // backward: the threads' column sums
     uint32_t rows_per_cta;
     size_t smem;
 };

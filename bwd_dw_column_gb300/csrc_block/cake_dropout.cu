@@ -43,46 +43,63 @@ __device__ __forceinline__ uint4 philox(const Philox &s, uint64_t b)
     return make_uint4(x, y, z, w);
 }
 
-// The factors of a pair of elements: 0 where dropped.
-__device__ __forceinline__ bool keep_lo(uint32_t bits, uint32_t cut) { return (bits & 0xffffu) >= cut; }
-__device__ __forceinline__ bool keep_hi(uint32_t bits, uint32_t cut) { return (bits >> 16) >= cut; }
-
-// scale * v where kept, 0 elsewhere.
-__device__ __forceinline__ float2 dropped(float2 v, uint32_t bits, uint32_t cut, float scale)
+// The vector's bits, all zero where every element is dropped (cut = 65536).
+__device__ __forceinline__ uint4 random_bits(const DropoutRng &r, const Philox &s, uint64_t b)
 {
-    return make_float2(keep_lo(bits, cut) ? __fmul_rn(v.x, scale) : 0.f,
-                       keep_hi(bits, cut) ? __fmul_rn(v.y, scale) : 0.f);
+    return r.cut < 65536 ? philox(s, b) : make_uint4(0, 0, 0, 0);
 }
+
+// scale * v where kept, 0 elsewhere; `limit` is the cut in the upper half of a word.
+__device__ __forceinline__ float2 dropped(float2 v, uint32_t bits, uint32_t limit, float2 scale)
+{
+    v = mul2(v, scale);
+    return make_float2((bits << 16) >= limit ? v.x : 0.f, bits >= limit ? v.y : 0.f);
+}
+
+__device__ __forceinline__ uint32_t limit_of(const DropoutRng &r) { return r.cut < 65536 ? r.cut << 16 : 0xffffffffu; }
 
 // -------------------------------------------------------------------- alone
 
-// A CTA takes 1024 neighbouring vectors at a time, four a thread.  Their rows
-// come from one 64-bit division for all of them and a 32-bit one for each.
+// A CTA takes 1024 neighbouring vectors at a time, four a thread.  Rows that are
+// not one block of memory come from one division for all of them and a product
+// with a reciprocal for each.
 constexpr int kDropThreads = 256;
 constexpr int kDropPer = 4;
 constexpr uint32_t kDropVecs = kDropThreads * kDropPer;
 constexpr uint64_t kDropCtas = 1 << 20;
 
-template <bool RES>
+// Elements from v's base to vector `at` of the rows from row0 on; at < nvec + kDropVecs.
+__device__ __forceinline__ int64_t vec_off(const RowView &v, const DropoutParams &p, uint32_t row0, uint32_t at)
+{
+    const uint32_t q = __umulhi(2 * at, p.reciprocal); // at / nvec: exact below 2^31 / nvec
+    return row_off(v, row0 + q, p.nh) + (int64_t)((at - q * p.nvec) * 8);
+}
+
+template <bool RES, bool DENSE>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropoutParams p)
 {
     pdl_wait();
     const Philox key = philox_init(p.r);
+    const uint32_t limit = limit_of(p.r);
+    const float2 scale = make_float2(p.r.scale, p.r.scale);
     for (uint64_t v0 = (uint64_t)blockIdx.x * kDropVecs; v0 < p.vecs; v0 += (uint64_t)gridDim.x * kDropVecs) {
-        const uint32_t row0 = (uint32_t)(v0 / p.nvec), rem = (uint32_t)(v0 - (uint64_t)row0 * p.nvec);
+        uint32_t row0 = 0, rem = 0;
+        if (!DENSE) {
+            row0 = v0 >> 32 ? (uint32_t)(v0 / p.nvec) : (uint32_t)v0 / p.nvec;
+            rem = (uint32_t)(v0 - (uint64_t)row0 * p.nvec);
+        }
         const uint32_t n = p.vecs - v0 < kDropVecs ? (uint32_t)(p.vecs - v0) : kDropVecs;
+        auto off = [&](const RowView &v, uint32_t i) {
+            return DENSE ? (int64_t)(v0 + i) * 8 : vec_off(v, p, row0, rem + i);
+        };
         uint4 x[kDropPer], e[kDropPer];
-        uint32_t row[kDropPer], col[kDropPer];
 #pragma unroll
         for (int k = 0; k < kDropPer; ++k) {
-            const uint32_t i = k * kDropThreads + threadIdx.x, at = rem + i, q = at / p.nvec;
-            row[k] = row0 + q;
-            col[k] = (at - q * p.nvec) * 8;
+            const uint32_t i = k * kDropThreads + threadIdx.x;
             if (i < n) {
-                x[k] = __ldcs(reinterpret_cast<const uint4 *>(p.x.base + row_off(p.x, row[k], p.nh) + col[k]));
+                x[k] = __ldcs(reinterpret_cast<const uint4 *>(p.x.base + off(p.x, i)));
                 if (RES)
-                    e[k] = __ldcs(reinterpret_cast<const uint4 *>(p.residual.base +
-                                                                  row_off(p.residual, row[k], p.nh) + col[k]));
+                    e[k] = __ldcs(reinterpret_cast<const uint4 *>(p.residual.base + off(p.residual, i)));
             }
         }
 #pragma unroll
@@ -90,16 +107,16 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
             const uint32_t i = k * kDropThreads + threadIdx.x;
             if (i >= n)
                 break;
-            const uint4 bits = philox(key, v0 + i);
+            const uint4 bits = random_bits(p.r, key, v0 + i);
             uint32_t o[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float2 v = dropped(bf2(word(x[k], q)), word(bits, q), p.r.cut, p.r.scale);
+                float2 v = dropped(bf2(word(x[k], q)), word(bits, q), limit, scale);
                 if (RES)
                     v = add2(v, bf2(word(e[k], q)));
                 o[q] = pack2(v);
             }
-            __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.y.base) + row_off(p.y, row[k], p.nh) + col[k]),
+            __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.y.base) + off(p.y, i)),
                    make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
@@ -130,6 +147,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kDnThreads ? 2 : 1)
     }
     const int gid = warp / W, wig = warp - gid * W, gtid = wig * 32 + lane, vstride = 32 * W, nvec = L.nvec;
     const Philox key = philox_init(p.r);
+    const uint32_t limit = limit_of(p.r);
+    const float2 scale = make_float2(p.r.scale, p.r.scale);
     stage_weight(s, L, p.w, p.w_f32);
     bool abort = false;
     uint32_t slot = 0, st = 0, ph = 0;
@@ -138,7 +157,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kDnThreads ? 2 : 1)
         uint4 bits[VPT]; // before the wait: they need no data
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
-            bits[k] = philox(key, (uint64_t)r * nvec + k * vstride + gtid);
+            bits[k] = random_bits(p.r, key, (uint64_t)r * nvec + k * vstride + gtid);
         abort = !mbar_wait(smem_addr(&s.full[st]), ph, p.wait_ns);
         if (r < c.r_end) { // uniform across the group
             const uint8_t *stage = s.ring + st * s.stage_bytes + (size_t)gid * L.H * 2;
@@ -156,7 +175,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kDnThreads ? 2 : 1)
                     uint32_t o[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        o[q] = pack2(add2(dropped(bf2(word(x, q)), word(bits[k], q), p.r.cut, p.r.scale),
+                        o[q] = pack2(add2(dropped(bf2(word(x, q)), word(bits[k], q), limit, scale),
                                           bf2(word(e, q))));
                         const float2 a = bf2(o[q]);
                         ss = fma2(a, a, ss);
@@ -198,21 +217,28 @@ __global__ void __launch_bounds__(THREADS, THREADS == kDnThreads ? 2 : 1)
         set_status(p.status, kStatusTimeout);
 }
 
-// Kahan-compensated hi += a * b of column pairs; lo holds the part of the last
-// term that hi has not taken up.
-__device__ __forceinline__ void kahan_pair(float2 &hi, float2 &lo, float2 a, float2 b)
+// A thread holds 8 VPT columns of a row.  Its terms of dw are added over 16 rows
+// in registers and then to Kahan pairs in shared memory that only it uses.  With
+// h the row, a = dy w and S = sum of a h the gradient is
+//   t = dh + rstd a - rstd^3 (S / H) h,
+// so that the first pass needs no scaled copy of the row but for dw.
+constexpr int kDnBlock = 16;
+
+__device__ __forceinline__ void fold_columns(float4 *at, int step, float2 (&sum)[4])
 {
-    const float2 y = fma2(a, b, lo);
-    const float2 t = add2(hi, y);
-    lo = add2(sub2(hi, t), y);
-    hi = t;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float4 &v = at[q * step]; // two columns' sums, and what they have not taken up
+        const float2 hi = make_float2(v.x, v.y), y = add2(sum[q], make_float2(v.z, v.w)), t = add2(hi, y),
+                     lo = add2(sub2(hi, t), y);
+        v = make_float4(t.x, t.y, lo.x, lo.y);
+        sum[q] = make_float2(0.f, 0.f);
+    }
 }
 
-// A thread holds 8 VPT columns of the row and of the weight's gradient (Kahan
-// pairs).  The mask's bits are computed before the row's sum and kept as one
-// bit an element.
 template <int VPT, bool DH>
-__global__ void __launch_bounds__(kDnThreads, 1) dropout_norm_bwd_kernel(const __grid_constant__ DropoutNormParams p)
+__global__ void __launch_bounds__(kDnWideThreads, 1)
+    dropout_norm_bwd_kernel(const __grid_constant__ DropoutNormParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const Layout &L = p.L;
@@ -227,28 +253,29 @@ __global__ void __launch_bounds__(kDnThreads, 1) dropout_norm_bwd_kernel(const _
         return;
     }
     const int gid = warp / W, wig = warp - gid * W, gtid = wig * 32 + lane, vstride = 32 * W, nvec = L.nvec;
+    const int nct = L.groups * W * 32;
     const Philox key = philox_init(p.r);
+    const uint32_t limit = limit_of(p.r);
+    const float2 scale = make_float2(p.r.scale, p.r.scale);
     stage_weight(s, L, p.w, p.w_f32);
-    float2 hi[VPT][4], lo[VPT][4];
+    float4 *const sums = s.lo + threadIdx.x; // [VPT][4][consumer threads]
+    float2 acc[VPT][4];
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            hi[k][q] = lo[k][q] = make_float2(0.f, 0.f);
+        for (int q = 0; q < 4; ++q) {
+            acc[k][q] = make_float2(0.f, 0.f);
+            sums[(4 * k + q) * nct] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     bool abort = false;
     uint32_t slot = 0, st = 0, ph = 0;
     for (uint32_t it = 0; it < c.ntiles && !abort; ++it) {
         const uint32_t r = c.r0 + it * c.tile_rows + gid;
         const float rs = r < c.r_end ? __ldg(p.rstd + r) : 0.f;
-        uint32_t keep = 0;
+        uint4 bits[VPT]; // before the wait: they need no data
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const uint4 b = philox(key, (uint64_t)r * nvec + k * vstride + gtid);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                keep |= ((uint32_t)keep_lo(word(b, q), p.r.cut) | (uint32_t)keep_hi(word(b, q), p.r.cut) << 1)
-                        << (8 * k + 2 * q);
-        }
+        for (int k = 0; k < VPT; ++k)
+            bits[k] = random_bits(p.r, key, (uint64_t)r * nvec + k * vstride + gtid);
         abort = !mbar_wait(smem_addr(&s.full[st]), ph, p.wait_ns);
         if (r < c.r_end) { // uniform across the group
             const uint8_t *stage = s.ring + st * s.stage_bytes + (size_t)gid * L.H * 2;
@@ -256,34 +283,32 @@ __global__ void __launch_bounds__(kDnThreads, 1) dropout_norm_bwd_kernel(const _
             const uint4 *ds = reinterpret_cast<const uint4 *>(stage + s.tens_bytes);
             const uint4 *es = reinterpret_cast<const uint4 *>(stage + 2 * s.tens_bytes);
             const float2 rs2 = make_float2(rs, rs);
-            uint4 h[VPT], d[VPT];
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int v = k * vstride + gtid;
-                h[k] = d[k] = make_uint4(0, 0, 0, 0);
                 if (v < nvec) {
-                    h[k] = hs[v];
-                    d[k] = ds[v];
+                    const uint4 h = hs[v], d = ds[v];
                     float2 w2[4];
                     weight_pairs(s, L, v, w2);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float2 dq = bf2(word(d[k], q)), hh = mul2(bf2(word(h[k], q)), rs2);
-                        sum = fma2(mul2(dq, w2[q]), hh, sum);
-                        kahan_pair(hi[k][q], lo[k][q], dq, hh);
+                        const float2 dq = bf2(word(d, q)), hq = bf2(word(h, q));
+                        sum = fma2(mul2(dq, w2[q]), hq, sum);
+                        acc[k][q] = fma2(mul2(hq, rs2), dq, acc[k][q]);
                     }
                 }
             }
             const float tot = group_sum(__fadd_rn(sum.x, sum.y), s, L, gid, wig, lane, slot++, abort);
-            const float m = -__fmul_rn(tot, L.inv_h);
-            const float2 mean = make_float2(m, m);
+            const float m = -__fmul_rn(__fmul_rn(__fmul_rn(tot, L.inv_h), rs), __fmul_rn(rs, rs));
+            const float2 m2 = make_float2(m, m);
             uint4 *xrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[0].base) + row_off(p.out[0], r, L.nh));
             uint4 *erow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[1].base) + row_off(p.out[1], r, L.nh));
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int v = k * vstride + gtid;
                 if (v < nvec && !abort) {
+                    const uint4 h = hs[v], d = ds[v];
                     uint4 e = make_uint4(0, 0, 0, 0);
                     if (DH)
                         e = es[v];
@@ -292,14 +317,13 @@ __global__ void __launch_bounds__(kDnThreads, 1) dropout_norm_bwd_kernel(const _
                     uint32_t ox[4], oe[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float2 a = mul2(bf2(word(d[k], q)), w2[q]), hh = mul2(bf2(word(h[k], q)), rs2);
-                        float2 t = mul2(rs2, fma2(hh, mean, a));
+                        const float2 a = mul2(bf2(word(d, q)), w2[q]);
+                        float2 t = mul2(bf2(word(h, q)), m2);
+                        t = fma2(rs2, a, t);
                         if (DH)
                             t = add2(t, bf2(word(e, q)));
                         oe[q] = pack2(t);
-                        const uint32_t b = keep >> (8 * k + 2 * q);
-                        ox[q] = pack2(make_float2(b & 1 ? __fmul_rn(t.x, p.r.scale) : 0.f,
-                                                  b & 2 ? __fmul_rn(t.y, p.r.scale) : 0.f));
+                        ox[q] = pack2(dropped(t, word(bits[k], q), limit, scale));
                     }
                     __stcs(xrow + v, make_uint4(ox[0], ox[1], ox[2], ox[3]));
                     __stcs(erow + v, make_uint4(oe[0], oe[1], oe[2], oe[3]));
@@ -313,21 +337,28 @@ __global__ void __launch_bounds__(kDnThreads, 1) dropout_norm_bwd_kernel(const _
             st = 0;
             ph ^= 1u;
         }
+        if (it % kDnBlock == kDnBlock - 1)
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                fold_columns(sums + 4 * k * nct, nct, acc[k]);
     }
     if (abort && lane == 0)
         set_status(p.status, kStatusTimeout);
     // The CTA partial: the groups' sums in group order, through the drained
     // ring ([group][4 nvec] float4 (hi, lo, hi, lo) of a column pair).
-    const int nct = L.groups * W * 32, nslot = 4 * nvec;
+    const int nslot = 4 * nvec;
     float4 *comb = reinterpret_cast<float4 *>(s.ring);
     consumer_sync(L);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int v = k * vstride + gtid;
+        fold_columns(sums + 4 * k * nct, nct, acc[k]);
         if (v < nvec)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                comb[(size_t)gid * nslot + 4 * v + q] = make_float4(hi[k][q].x, lo[k][q].x, hi[k][q].y, lo[k][q].y);
+            for (int q = 0; q < 4; ++q) {
+                const float4 f = sums[(4 * k + q) * nct];
+                comb[(size_t)gid * nslot + 4 * v + q] = make_float4(f.x, f.z, f.y, f.w);
+            }
     }
     consumer_sync(L);
     for (int i = threadIdx.x; i < nslot; i += nct) {
@@ -384,36 +415,16 @@ __global__ void __launch_bounds__(32 * kColumnWarps) column_sum_kernel(const __g
 
 // ------------------------------------------------------------------- launch
 
-// The shape of a CTA goes by H and the staged tensors alone, so the orders of
-// the sums do too.
-DropoutNormPlan dropout_norm_plan(int H, uint32_t rows, int ntens, bool backward)
+// Shared memory of a plan's CTA for its vpt, W and groups; false: no two stages fit.
+static bool fit_plan(DropoutNormPlan &p, int H, int ntens, bool backward)
 {
-    const int nvec = H / 8;
-    DropoutNormPlan p{};
-    int best = -1;
-    for (int vpt = 1; vpt <= (backward ? 4 : 2); ++vpt) {
-        const int W = (nvec + 32 * vpt - 1) / (32 * vpt);
-        const int most = !backward && vpt == 2 && W > 12 ? 16 : 12;
-        if (W > most)
-            continue;
-        const int groups = most / W;
-        // columns in work, those of a single row group counted less: its warps wait for one sum together
-        int score = groups * H > 6144 ? 6144 : groups * H;
-        if (groups == 1)
-            score = score * 8 / 10;
-        if (score > best) {
-            best = score;
-            p.vpt = vpt;
-            p.W = W;
-            p.groups = groups;
-        }
-    }
-    const size_t fixed = kMiscBytes + weight_smem_bytes(H), stage = (size_t)ntens * p.groups * H * 2;
-    int per_sm = !backward && p.groups * p.W <= 12 ? 2 : 1;
-    for (;; --per_sm) {
-        const size_t room = 228 * 1024 / per_sm - 1024;
+    p.lo_bytes = backward ? p.vpt * 64 * p.groups * p.W * 32 : 0;
+    const size_t fixed = kMiscBytes + weight_smem_bytes(H) + p.lo_bytes, stage = (size_t)ntens * p.groups * H * 2;
+    p.per_sm = !backward && p.groups * p.W <= 12 ? 2 : 1;
+    for (;; --p.per_sm) {
+        const size_t room = 228 * 1024 / p.per_sm - 1024; // 1 KB of each CTA is the system's
         p.stages = room > fixed ? (int)((room - fixed) / stage) : 0;
-        if (p.stages >= 2 || per_sm == 1)
+        if (p.stages >= 2 || p.per_sm == 1)
             break;
     }
     // no more than 3 stages in the forward, 6 in the backward, or what brings 48 KB on their way
@@ -422,10 +433,43 @@ DropoutNormPlan dropout_norm_plan(int H, uint32_t rows, int ntens, bool backward
     most = most > 16 ? 16 : most;
     if (p.stages > most)
         p.stages = most;
-    // (the backward's column sums, 8 bytes a column of each group, pass through the ring of two stages or more)
-    p.smem = fixed + p.stages * stage;
-    const uint32_t tiles = (rows + p.groups - 1) / p.groups;
-    const uint32_t ctas = tiles < (uint32_t)(kSMsBlock * per_sm) ? tiles : kSMsBlock * per_sm;
+    size_t ring = p.stages * stage;
+    if (backward && ring < (size_t)p.groups * H * 8) // the groups' column sums pass through it
+        ring = (size_t)p.groups * H * 8;
+    p.smem = fixed + ring;
+    return p.stages >= 2 && p.smem <= 227 * 1024;
+}
+
+// The shape of a CTA goes by H and the staged tensors alone, so the orders of
+// the sums do too: the most columns in work up to the 6144 that keep HBM busy,
+// those of a single row group (whose warps wait for one sum together) and of
+// less than three stages counted less; of equals the fewest columns a thread.
+DropoutNormPlan dropout_norm_plan(int H, uint32_t rows, int ntens, bool backward)
+{
+    const int nvec = H / 8;
+    DropoutNormPlan p{};
+    int best = -1;
+    for (int vpt = 1; vpt <= (backward ? 3 : 2); ++vpt) {
+        const int W = (nvec + 32 * vpt - 1) / (32 * vpt);
+        const int most = backward || (vpt == 2 && W > 12) ? 16 : 12;
+        for (int groups = most / W < kMaxRowGroupBarriers ? most / W : kMaxRowGroupBarriers; groups >= 1; --groups) {
+            DropoutNormPlan q{};
+            q.vpt = vpt;
+            q.W = W;
+            q.groups = groups;
+            if (!fit_plan(q, H, ntens, backward))
+                continue;
+            int score = groups * H > 6144 ? 6144 : groups * H;
+            score = groups == 1 ? score * 8 / 10 : score;
+            score = q.stages < 3 ? score * 85 / 100 : score;
+            if (score > best) {
+                best = score;
+                p = q;
+            }
+        }
+    }
+    const uint32_t tiles = (rows + p.groups - 1) / p.groups, most = (uint32_t)(kSMsBlock * p.per_sm);
+    const uint32_t ctas = tiles < most ? tiles : most;
     p.rows_per_cta = ctas ? (rows + ctas - 1) / ctas : 0;
     p.ctas = p.rows_per_cta ? (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta) : 0;
     return p;
@@ -435,8 +479,10 @@ cudaError_t launch_dropout(const DropoutParams &p, cudaStream_t stream)
 {
     const uint64_t want = (p.vecs + kDropVecs - 1) / kDropVecs;
     const dim3 grid((unsigned)(want < kDropCtas ? want : kDropCtas));
-    return p.residual.base ? launch_after(dropout_kernel<true>, grid, kDropThreads, 0, stream, p)
-                           : launch_after(dropout_kernel<false>, grid, kDropThreads, 0, stream, p);
+    const bool dense = p.x.dense && p.y.dense && (!p.residual.base || p.residual.dense);
+    auto kern = p.residual.base ? (dense ? dropout_kernel<true, true> : dropout_kernel<true, false>)
+                                : (dense ? dropout_kernel<false, true> : dropout_kernel<false, false>);
+    return launch_after(kern, grid, kDropThreads, 0, stream, p);
 }
 
 cudaError_t launch_dropout_norm_fwd(const DropoutNormParams &p, const DropoutNormPlan &plan, cudaStream_t stream)
@@ -464,8 +510,7 @@ cudaError_t launch_dropout_norm_bwd(const DropoutNormParams &p, const DropoutNor
     switch (plan.vpt) {
     case 1: return launch_dn_bwd<1>(p, plan, stream);
     case 2: return launch_dn_bwd<2>(p, plan, stream);
-    case 3: return launch_dn_bwd<3>(p, plan, stream);
-    default: return launch_dn_bwd<4>(p, plan, stream);
+    default: return launch_dn_bwd<3>(p, plan, stream);
     }
 }
 

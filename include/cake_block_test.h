@@ -1,6 +1,6 @@
 /*
  * cake_block_test.h -- entry points for tests of the block operators' bounded
- * waits; no program needs them.
+ * waits and launch plans; no program needs them.
  */
 #ifndef CAKE_BLOCK_TEST_H
 #define CAKE_BLOCK_TEST_H
@@ -21,6 +21,15 @@ extern "C" {
  * cake_rmsnorm_device_status() gives CAKE_ERR_TIMEOUT.
  */
 cake_status cake_block_wait_test(uint32_t wait_limit_us, int withhold);
+
+/*
+ * The plan of cake_dropout_norm_fwd (backward = 0) or _bwd for a shape and a
+ * number of staged tensors (2, or 3 of the backward with dh): vectors of 8
+ * columns of a thread, warps of a row, rows of a stage, stages, CTAs, rows of a
+ * CTA, bytes of the threads' column sums, and bytes of shared memory.  Host
+ * only.
+ */
+cake_status cake_dropout_norm_plan(const cake_shape *shape, int tensors, int backward, int64_t plan[8]);
 
 #ifdef __cplusplus
 }

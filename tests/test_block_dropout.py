@@ -213,3 +213,29 @@ def test_autograd(cake):
     y, h = cake.cake_dropout_norm(x, e.detach(), w, 0.2, 7, 1)
     gx, = torch.autograd.grad(h, x, dz)
     assert torch.equal(gx, cake.cake_dropout_bwd(dz, 0.2, 7, 1))
+
+
+def test_every_width_has_a_plan_that_fits():
+    """For every width: a row's warps hold it, the ring has two stages, all of it fits an SM's shared memory, the
+    groups' column sums fit the ring, the barriers and reduction slots the space before it."""
+    import ctypes
+
+    import __graft_entry__
+    __graft_entry__.build()
+    import bwd_dw_column_gb300 as cake
+    from bwd_dw_column_gb300.step import _three
+    lib, got = cake.load_library(), (ctypes.c_int64 * 8)()
+    for H in range(8, 8193, 8):
+        for backward, tensors in ((0, 2), (1, 2), (1, 3)):
+            for T in (1, 1000, 2 ** 31 - 1):
+                assert lib.cake_dropout_norm_plan(_three(T, 1, H), tensors, backward, got) == 0
+                vpt, W, groups, stages, ctas, per_cta, lo, smem = got
+                assert 1 <= vpt <= (3 if backward else 2) and 1 <= groups * W <= 16 and 256 * vpt * W >= H
+                assert W == 1 or groups <= 14
+                fixed = 1024 + (4 * H + 1023) // 1024 * 1024 + lo
+                ring = smem - fixed
+                assert 2 <= stages <= 16 and ring >= stages * tensors * groups * H * 2 and smem <= 227 * 1024
+                assert groups * 2 * W * 4 <= 400
+                if backward:  # a float4 of a pair of columns, of each group; and of each of a thread's pairs
+                    assert ring >= groups * H * 8 and lo >= vpt * 4 * 16 * groups * W * 32
+                assert (ctas - 1) * per_cta < T <= ctas * per_cta
