@@ -33,7 +33,12 @@ cake_status check_p(float p, const uint64_t *rng)
 DropoutRng dropout_rng(float p, uint64_t seed, uint64_t offset, const uint64_t *rng)
 {
     const uint32_t cut = (uint32_t)std::nearbyint((double)p * 65536.0);
-    return {seed, offset, rng, cut, cut < 65536 ? (float)(65536.0 / (65536 - (int)cut)) : 0.0f};
+    DropoutRng r{seed, offset, rng, cut, cut < 65536 ? (float)(65536.0 / (65536 - (int)cut)) : 0.0f, {}};
+    for (uint32_t i = 0; i < 10; ++i) {
+        r.keys[2 * i] = (uint32_t)seed + i * 0x9E3779B9u;
+        r.keys[2 * i + 1] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
+    }
+    return r;
 }
 
 Layout rows_layout(const DropoutNormPlan &plan, const cake_shape *shape, uint32_t rows, int ntens)

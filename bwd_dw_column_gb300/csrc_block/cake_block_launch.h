@@ -19,6 +19,7 @@ struct DropoutRng {
     const uint64_t *rng;   // nullptr, or a seed and a number added to offset
     uint32_t cut;          // kept: 16 random bits of at least this
     float scale;           // 65536 / (65536 - cut); 0 where cut is 65536
+    uint32_t keys[20];     // of the generator's ten rounds, without rng
 };
 
 struct DropoutParams {

@@ -7,46 +7,56 @@
 // two 32 x 32 -> 64 bit products.  Sixteen bits an element make that about 9
 // instructions an element; with 32 it would be twice as much.  Nothing of the
 // mask is stored or read, so HBM bounds every kernel here.
+#include <type_traits>
+
 #include "../csrc/cake_rows.cuh"
 #include "cake_block_launch.h"
 
 namespace cake {
 
+// The generator's key and the counter's upper half.  DEV false: known to the
+// host, with the keys of all rounds among the kernel's parameters, where the
+// rounds take them as constants; DEV true: read from the device and counted up
+// from round to round.
+template <bool DEV>
 struct Philox {
+    const DropoutRng &r;
     uint32_t k0, k1, o0, o1;
+
+    __device__ __forceinline__ explicit Philox(const DropoutRng &rng) : r(rng)
+    {
+        uint64_t seed = r.seed, off = r.offset;
+        if (DEV) {
+            seed = r.rng[0];
+            off += r.rng[1];
+        }
+        k0 = (uint32_t)seed;
+        k1 = (uint32_t)(seed >> 32);
+        o0 = (uint32_t)off;
+        o1 = (uint32_t)(off >> 32);
+    }
+
+    // 16 bits for each of the 8 elements of vector b, lowest first.
+    __device__ __forceinline__ uint4 block(uint64_t b) const
+    {
+        uint32_t x = (uint32_t)b, y = (uint32_t)(b >> 32), z = o0, w = o1;
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+            const uint64_t p0 = (uint64_t)x * 0xD2511F53u, p1 = (uint64_t)z * 0xCD9E8D57u;
+            x = (uint32_t)(p1 >> 32) ^ y ^ (DEV ? k0 + i * 0x9E3779B9u : r.keys[2 * i]);
+            z = (uint32_t)(p0 >> 32) ^ w ^ (DEV ? k1 + i * 0xBB67AE85u : r.keys[2 * i + 1]);
+            y = (uint32_t)p1;
+            w = (uint32_t)p0;
+        }
+        return make_uint4(x, y, z, w);
+    }
 };
 
-__device__ __forceinline__ Philox philox_init(const DropoutRng &r)
-{
-    uint64_t seed = r.seed, off = r.offset;
-    if (r.rng) {
-        seed = r.rng[0];
-        off += r.rng[1];
-    }
-    return {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)off, (uint32_t)(off >> 32)};
-}
-
-// 16 bits for each of the 8 elements of vector b, lowest first.
-__device__ __forceinline__ uint4 philox(const Philox &s, uint64_t b)
-{
-    uint32_t x = (uint32_t)b, y = (uint32_t)(b >> 32), z = s.o0, w = s.o1, k0 = s.k0, k1 = s.k1;
-#pragma unroll
-    for (int i = 0; i < 10; ++i) {
-        const uint64_t p0 = (uint64_t)x * 0xD2511F53u, p1 = (uint64_t)z * 0xCD9E8D57u;
-        x = (uint32_t)(p1 >> 32) ^ y ^ k0;
-        z = (uint32_t)(p0 >> 32) ^ w ^ k1;
-        y = (uint32_t)p1;
-        w = (uint32_t)p0;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-    return make_uint4(x, y, z, w);
-}
-
 // The vector's bits, all zero where every element is dropped (cut = 65536).
-__device__ __forceinline__ uint4 random_bits(const DropoutRng &r, const Philox &s, uint64_t b)
+template <bool DEV>
+__device__ __forceinline__ uint4 random_bits(const Philox<DEV> &s, uint64_t b)
 {
-    return r.cut < 65536 ? philox(s, b) : make_uint4(0, 0, 0, 0);
+    return s.r.cut < 65536 ? s.block(b) : make_uint4(0, 0, 0, 0);
 }
 
 // scale * v where kept, 0 elsewhere; `limit` is the cut in the upper half of a word.
@@ -68,18 +78,11 @@ constexpr int kDropPer = 4;
 constexpr uint32_t kDropVecs = kDropThreads * kDropPer;
 constexpr uint64_t kDropCtas = 1 << 20;
 
-// Elements from v's base to vector `at` of the rows from row0 on; at < nvec + kDropVecs.
-__device__ __forceinline__ int64_t vec_off(const RowView &v, const DropoutParams &p, uint32_t row0, uint32_t at)
-{
-    const uint32_t q = __umulhi(2 * at, p.reciprocal); // at / nvec: exact below 2^31 / nvec
-    return row_off(v, row0 + q, p.nh) + (int64_t)((at - q * p.nvec) * 8);
-}
-
-template <bool RES, bool DENSE>
+template <bool RES, bool DENSE, bool DEV>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropoutParams p)
 {
     pdl_wait();
-    const Philox key = philox_init(p.r);
+    const Philox<DEV> key(p.r);
     const uint32_t limit = limit_of(p.r);
     const float2 scale = make_float2(p.r.scale, p.r.scale);
     for (uint64_t v0 = (uint64_t)blockIdx.x * kDropVecs; v0 < p.vecs; v0 += (uint64_t)gridDim.x * kDropVecs) {
@@ -89,17 +92,23 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
             rem = (uint32_t)(v0 - (uint64_t)row0 * p.nvec);
         }
         const uint32_t n = p.vecs - v0 < kDropVecs ? (uint32_t)(p.vecs - v0) : kDropVecs;
-        auto off = [&](const RowView &v, uint32_t i) {
-            return DENSE ? (int64_t)(v0 + i) * 8 : vec_off(v, p, row0, rem + i);
-        };
         uint4 x[kDropPer], e[kDropPer];
+        uint32_t row[kDropPer], col[kDropPer];
+        auto off = [&](const RowView &v, int k, uint32_t i) {
+            return DENSE ? (int64_t)(v0 + i) * 8 : row_off(v, row[k], p.nh) + col[k];
+        };
 #pragma unroll
         for (int k = 0; k < kDropPer; ++k) {
             const uint32_t i = k * kDropThreads + threadIdx.x;
+            if (!DENSE) {
+                const uint32_t q = __umulhi(2 * (rem + i), p.reciprocal); // (rem + i) / nvec: exact below 2^31 / nvec
+                row[k] = row0 + q;
+                col[k] = (rem + i - q * p.nvec) * 8;
+            }
             if (i < n) {
-                x[k] = __ldcs(reinterpret_cast<const uint4 *>(p.x.base + off(p.x, i)));
+                x[k] = __ldcs(reinterpret_cast<const uint4 *>(p.x.base + off(p.x, k, i)));
                 if (RES)
-                    e[k] = __ldcs(reinterpret_cast<const uint4 *>(p.residual.base + off(p.residual, i)));
+                    e[k] = __ldcs(reinterpret_cast<const uint4 *>(p.residual.base + off(p.residual, k, i)));
             }
         }
 #pragma unroll
@@ -107,7 +116,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
             const uint32_t i = k * kDropThreads + threadIdx.x;
             if (i >= n)
                 break;
-            const uint4 bits = random_bits(p.r, key, v0 + i);
+            const uint4 bits = random_bits(key, v0 + i);
             uint32_t o[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -116,7 +125,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
                     v = add2(v, bf2(word(e[k], q)));
                 o[q] = pack2(v);
             }
-            __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.y.base) + off(p.y, i)),
+            __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.y.base) + off(p.y, k, i)),
                    make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
@@ -129,7 +138,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
 constexpr int kDnThreads = 416;      // 12 consumer warps and the producer
 constexpr int kDnWideThreads = 544;  // 16: the forward's rows of more than 6144 columns
 
-template <int VPT, int THREADS>
+template <int VPT, int THREADS, bool DEV>
 __global__ void __launch_bounds__(THREADS, THREADS == kDnThreads ? 2 : 1)
     dropout_norm_fwd_kernel(const __grid_constant__ DropoutNormParams p)
 {
@@ -146,7 +155,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kDnThreads ? 2 : 1)
         return;
     }
     const int gid = warp / W, wig = warp - gid * W, gtid = wig * 32 + lane, vstride = 32 * W, nvec = L.nvec;
-    const Philox key = philox_init(p.r);
+    const Philox<DEV> key(p.r);
     const uint32_t limit = limit_of(p.r);
     const float2 scale = make_float2(p.r.scale, p.r.scale);
     stage_weight(s, L, p.w, p.w_f32);
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kDnThreads ? 2 : 1)
         uint4 bits[VPT]; // before the wait: they need no data
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
-            bits[k] = random_bits(p.r, key, (uint64_t)r * nvec + k * vstride + gtid);
+            bits[k] = random_bits(key, (uint64_t)r * nvec + k * vstride + gtid);
         abort = !mbar_wait(smem_addr(&s.full[st]), ph, p.wait_ns);
         if (r < c.r_end) { // uniform across the group
             const uint8_t *stage = s.ring + st * s.stage_bytes + (size_t)gid * L.H * 2;
@@ -236,7 +245,7 @@ __device__ __forceinline__ void fold_columns(float4 *at, int step, float2 (&sum)
     }
 }
 
-template <int VPT, bool DH>
+template <int VPT, bool DH, bool DEV>
 __global__ void __launch_bounds__(kDnWideThreads, 1)
     dropout_norm_bwd_kernel(const __grid_constant__ DropoutNormParams p)
 {
@@ -254,7 +263,7 @@ __global__ void __launch_bounds__(kDnWideThreads, 1)
     }
     const int gid = warp / W, wig = warp - gid * W, gtid = wig * 32 + lane, vstride = 32 * W, nvec = L.nvec;
     const int nct = L.groups * W * 32;
-    const Philox key = philox_init(p.r);
+    const Philox<DEV> key(p.r);
     const uint32_t limit = limit_of(p.r);
     const float2 scale = make_float2(p.r.scale, p.r.scale);
     stage_weight(s, L, p.w, p.w_f32);
@@ -275,7 +284,7 @@ __global__ void __launch_bounds__(kDnWideThreads, 1)
         uint4 bits[VPT]; // before the wait: they need no data
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
-            bits[k] = random_bits(p.r, key, (uint64_t)r * nvec + k * vstride + gtid);
+            bits[k] = random_bits(key, (uint64_t)r * nvec + k * vstride + gtid);
         abort = !mbar_wait(smem_addr(&s.full[st]), ph, p.wait_ns);
         if (r < c.r_end) { // uniform across the group
             const uint8_t *stage = s.ring + st * s.stage_bytes + (size_t)gid * L.H * 2;
@@ -480,38 +489,41 @@ cudaError_t launch_dropout(const DropoutParams &p, cudaStream_t stream)
     const uint64_t want = (p.vecs + kDropVecs - 1) / kDropVecs;
     const dim3 grid((unsigned)(want < kDropCtas ? want : kDropCtas));
     const bool dense = p.x.dense && p.y.dense && (!p.residual.base || p.residual.dense);
-    auto kern = p.residual.base ? (dense ? dropout_kernel<true, true> : dropout_kernel<true, false>)
-                                : (dense ? dropout_kernel<false, true> : dropout_kernel<false, false>);
-    return launch_after(kern, grid, kDropThreads, 0, stream, p);
+    const auto go = [&](auto dev) {
+        constexpr bool D = decltype(dev)::value;
+        auto kern = p.residual.base ? (dense ? dropout_kernel<true, true, D> : dropout_kernel<true, false, D>)
+                                    : (dense ? dropout_kernel<false, true, D> : dropout_kernel<false, false, D>);
+        return launch_after(kern, grid, kDropThreads, 0, stream, p);
+    };
+    return p.r.rng ? go(std::true_type()) : go(std::false_type());
 }
 
 cudaError_t launch_dropout_norm_fwd(const DropoutNormParams &p, const DropoutNormPlan &plan, cudaStream_t stream)
 {
     const int threads = 32 * (plan.groups * plan.W + 1);
-    const dim3 grid((unsigned)plan.ctas);
-    if (plan.vpt == 1)
-        return launch_after(dropout_norm_fwd_kernel<1, kDnThreads>, grid, threads, plan.smem, stream, p);
-    if (threads <= kDnThreads)
-        return launch_after(dropout_norm_fwd_kernel<2, kDnThreads>, grid, threads, plan.smem, stream, p);
-    return launch_after(dropout_norm_fwd_kernel<2, kDnWideThreads>, grid, threads, plan.smem, stream, p);
-}
-
-template <int VPT>
-static cudaError_t launch_dn_bwd(const DropoutNormParams &p, const DropoutNormPlan &plan, cudaStream_t stream)
-{
-    const int threads = 32 * (plan.groups * plan.W + 1);
-    const dim3 grid((unsigned)plan.ctas);
-    return p.L.ntens == 3 ? launch_after(dropout_norm_bwd_kernel<VPT, true>, grid, threads, plan.smem, stream, p)
-                          : launch_after(dropout_norm_bwd_kernel<VPT, false>, grid, threads, plan.smem, stream, p);
+    const auto go = [&](auto dev) {
+        constexpr bool D = decltype(dev)::value;
+        auto kern = plan.vpt == 1           ? dropout_norm_fwd_kernel<1, kDnThreads, D>
+                    : threads <= kDnThreads ? dropout_norm_fwd_kernel<2, kDnThreads, D>
+                                            : dropout_norm_fwd_kernel<2, kDnWideThreads, D>;
+        return launch_after(kern, dim3((unsigned)plan.ctas), threads, plan.smem, stream, p);
+    };
+    return p.r.rng ? go(std::true_type()) : go(std::false_type());
 }
 
 cudaError_t launch_dropout_norm_bwd(const DropoutNormParams &p, const DropoutNormPlan &plan, cudaStream_t stream)
 {
-    switch (plan.vpt) {
-    case 1: return launch_dn_bwd<1>(p, plan, stream);
-    case 2: return launch_dn_bwd<2>(p, plan, stream);
-    default: return launch_dn_bwd<3>(p, plan, stream);
-    }
+    const int threads = 32 * (plan.groups * plan.W + 1);
+    const auto go = [&](auto dev, auto dh) {
+        constexpr bool D = decltype(dev)::value, E = decltype(dh)::value;
+        auto kern = plan.vpt == 1   ? dropout_norm_bwd_kernel<1, E, D>
+                    : plan.vpt == 2 ? dropout_norm_bwd_kernel<2, E, D>
+                                    : dropout_norm_bwd_kernel<3, E, D>;
+        return launch_after(kern, dim3((unsigned)plan.ctas), threads, plan.smem, stream, p);
+    };
+    if (p.L.ntens == 3)
+        return p.r.rng ? go(std::true_type(), std::true_type()) : go(std::false_type(), std::true_type());
+    return p.r.rng ? go(std::true_type(), std::false_type()) : go(std::false_type(), std::false_type());
 }
 
 cudaError_t launch_column_sum(const ColumnSumParams &p, int lists, cudaStream_t stream)
