@@ -56,11 +56,12 @@ constexpr int kPairStages = 6;
 constexpr int kPairHalf = 16384;              // an operand of a stage: 128 x 64 BF16
 constexpr int kPairStage = 2 * kPairHalf;
 constexpr int kPairBox = 2048;                // a box of the outputs: 32 rows of 64 bytes
-constexpr int kPairBoxes = 4;                 // of each epilogue warp
+constexpr int kPairBoxes = 2;                 // of each epilogue warp
+constexpr int kPairWriters = 8;               // epilogue warps: two to a quarter of the rows
 constexpr int kPairStaging = kPairStages * kPairStage;
-constexpr int kPairBars = kPairStaging + 4 * kPairBoxes * kPairBox;
+constexpr int kPairBars = kPairStaging + kPairWriters * kPairBoxes * kPairBox;
 constexpr int kPairSmem = kPairBars + 256;
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 128 + 32 * kPairWriters;
 constexpr int kPairs = kSMsBlock / 2;
 constexpr int kPairGroup = 8;                 // tiles of m that neighbouring units share, for their reuse in L2
 
@@ -79,7 +80,10 @@ struct PairProblem {
 struct PairParams {
     PairProblem p[2];
     CUtensorMap g, u;     // gated: outputs beside out[0]
-    int units, save, gelu;
+    int save, gelu;
+    // Of the first problem's units a pair takes `each`, the first `more` pairs
+    // one more; of the second's these take `less`, the others `rest`.
+    int pairs, each, more, less, rest;
     int *status;
     uint64_t wait_ns;
     int withhold;         // tests of the waits
@@ -90,14 +94,26 @@ struct PairUnit {
     int half, split, m0, n0, k0, k1;
 };
 
+// The i-th unit of pair q; false: there is none.  Neighbouring pairs work on
+// neighbouring units at a time.
 template <bool GATED>
-__device__ __forceinline__ PairUnit pair_unit(const PairParams &P, int u)
+__device__ __forceinline__ bool pair_unit(const PairParams &P, int q, int i, PairUnit &r)
 {
-    PairUnit r;
-    r.p = &P.p[0];
-    if (!GATED && u >= r.p->units) {
-        u -= r.p->units;
+    const int own = P.each + (q < P.more);
+    int u;
+    if (i < own) {
+        u = i * P.pairs + q;
+        r.p = &P.p[0];
+    } else {
+        if (GATED)
+            return false;
+        i -= own;
+        if (i >= (q < P.more ? P.less : P.rest))
+            return false;
+        u = i < P.less ? i * P.pairs + q : P.less * P.pairs + (i - P.less) * (P.pairs - P.more) + q - P.more;
         r.p = &P.p[1];
+        if (u >= r.p->units)
+            return false;
     }
     const PairProblem &p = *r.p;
     r.split = u % p.splits;
@@ -111,7 +127,7 @@ __device__ __forceinline__ PairUnit pair_unit(const PairParams &P, int u)
     r.n0 = t / size * (GATED ? 128 : 256);
     r.k0 = r.split * p.per_split;
     r.k1 = min(r.k0 + p.per_split, p.kblocks * p.segments);
-    return r;
+    return true;
 }
 
 // 32 rows of 64 bytes in 64-byte swizzled order, one row a lane, to the boxes' next slot and on to memory.
@@ -141,7 +157,8 @@ struct BoxWriter {
 };
 
 // Warp 0 of each CTA copies, warp 1 of the first issues the products, warp 2
-// holds the tensor memory, warps 4 to 7 write the outputs.
+// holds the tensor memory, warps 4 to 11 write the outputs (each a quarter of
+// the CTA's rows, as tensor memory is laid out, and half of the columns).
 template <bool GATED>
 __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __grid_constant__ PairParams P)
 {
@@ -151,7 +168,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
                    drain = tempty + 16, tmem_at = drain + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int pair = blockIdx.x >> 1;
+    PairUnit u;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPairStages; ++i) {
             mbar_init(full + 8 * i, 1);
@@ -159,7 +177,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + 8 * i, 1);
-            mbar_init(tempty + 8 * i, 8);
+            mbar_init(tempty + 8 * i, 2 * kPairWriters);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -179,8 +197,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
     if (warp == 0) {
         if (lane == 0) {
             uint32_t st = 0, ph = 0, issued = 0;
-            for (int i = first; i < P.units && ok; i += step) {
-                const PairUnit u = pair_unit<GATED>(P, i);
+            for (int i = 0; ok && pair_unit<GATED>(P, pair, i, u); ++i) {
                 const PairProblem &p = *u.p;
                 for (int kb = u.k0; kb < u.k1; ++kb) {
                     if (issued >= kPairStages && !(ok = mbar_wait(empty + 8 * st, ph ^ 1u, P.wait_ns)))
@@ -222,9 +239,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            uint32_t st = 0, ph = 0, it = 0;
-            for (int i = first; i < P.units && ok; i += step, ++it) {
-                const PairUnit u = pair_unit<GATED>(P, i);
+            uint32_t st = 0, ph = 0;
+            for (int it = 0; ok && pair_unit<GATED>(P, pair, it, u); ++it) {
                 const PairProblem &p = *u.p;
                 const uint32_t acc = it & 1, desc = mma_desc(256, 256, p.a_mn, p.b_mn);
                 if (it >= 2 && !(ok = mbar_wait_cluster(tempty + 8 * acc, ((it >> 1) & 1) ^ 1u, P.wait_ns)))
@@ -256,11 +272,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
             }
         }
     } else if (warp >= 4) {
-        const int quad = warp - 4;
-        BoxWriter box{smem + kPairStaging + (uint32_t)quad * kPairBoxes * kPairBox, 0};
-        uint32_t it = 0;
-        for (int i = first; i < P.units && ok; i += step, ++it) {
-            const PairUnit u = pair_unit<GATED>(P, i);
+        const int quad = warp & 3, side = (warp - 4) >> 2;
+        BoxWriter box{smem + kPairStaging + (uint32_t)(warp - 4) * kPairBoxes * kPairBox, 0};
+        for (int it = 0; ok && pair_unit<GATED>(P, pair, it, u); ++it) {
             const PairProblem &p = *u.p;
             const uint32_t acc = it & 1;
             ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull + 8 * acc, (it >> 1) & 1, P.wait_ns));
@@ -270,7 +284,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
             const uint32_t t = tmem + ((uint32_t)(quad * 32) << 16) + 256 * acc;
             const int row = u.m0 + 128 * (int)rank + 32 * quad;
             const bool rows = row < p.rows;
-            for (int c = 0; c < (GATED ? 4 : 8); ++c) {
+            constexpr int kSide = GATED ? 2 : 4; // chunks of 32 columns
+            for (int c = kSide * side; c < kSide * (side + 1); ++c) {
                 const int col = u.n0 + 32 * c;
                 if (!rows || col >= p.cols)
                     break;
@@ -685,7 +700,31 @@ static cudaError_t launch_few(const GatedFwdCall &c, cudaStream_t stream)
                           stream, P);
 }
 
-static dim3 pair_grid(int units) { return dim3((unsigned)(2 * (units < kPairs ? units : kPairs))); }
+// Shares of n1 units that take c1 and n2 that take c2 (0: none) among the
+// pairs: the time of the longest.
+static int64_t share_units(PairParams &P, int n1, int64_t c1, int n2, int64_t c2)
+{
+    P.pairs = n1 + n2 < kPairs ? n1 + n2 : kPairs;
+    P.each = n1 / P.pairs;
+    P.more = n1 % P.pairs;
+    P.less = P.rest = 0;
+    int64_t best = -1;
+    for (int less = 0; less <= n2; ++less) {
+        const int rest = (int)(((int64_t)n2 - (int64_t)less * P.more + P.pairs - P.more - 1) / (P.pairs - P.more));
+        if (rest < less)
+            break;
+        const int64_t a = P.more ? c1 * (P.each + 1) + c2 * less : 0, b = c1 * P.each + c2 * rest;
+        const int64_t t = a > b ? a : b;
+        if (best < 0 || t < best) {
+            best = t;
+            P.less = less;
+            P.rest = rest;
+        }
+    }
+    return best;
+}
+
+static dim3 pair_grid(const PairParams &P) { return dim3((unsigned)(2 * P.pairs)); }
 
 cudaError_t launch_gated_fwd(const GatedFwdCall &c, cudaStream_t stream)
 {
@@ -701,7 +740,8 @@ cudaError_t launch_gated_fwd(const GatedFwdCall &c, cudaStream_t stream)
     p.kblocks = p.per_split = ceil_div(c.H, 64);
     p.tiles_m = ceil_div(c.T, 256);
     p.tiles_n = ceil_div(c.F, 128);
-    p.units = P.units = p.tiles_m * p.tiles_n;
+    p.units = p.tiles_m * p.tiles_n;
+    share_units(P, p.units, p.kblocks, 0, 0);
     p.rows = (int)c.T;
     p.cols = (int)c.F;
     P.save = c.g.data != nullptr;
@@ -709,24 +749,51 @@ cudaError_t launch_gated_fwd(const GatedFwdCall &c, cudaStream_t stream)
     P.status = c.status;
     P.wait_ns = c.wait_ns;
     P.withhold = c.withhold;
-    return launch_cluster(gated_pair_kernel<true>, pair_grid(P.units), 2, kPairThreads, kPairSmem, stream, P);
+    return launch_cluster(gated_pair_kernel<true>, pair_grid(P), 2, kPairThreads, kPairSmem, stream, P);
 }
 
-// A sum over `kblocks` of few tiles is split so that every pair has a part, of
-// four blocks at least; the parts go through memory as FP32.
-static void split_sum(PairProblem &p, int kblocks)
+// A unit's time in blocks of k: its own, and what its outputs take where those
+// are more (BF16; FP32 parts, which are read again).
+static int64_t unit_time(const PairProblem &p)
 {
-    const int tiles = p.halves * p.tiles_m * p.tiles_n;
-    int s = kPairs / tiles;
-    if (s > kblocks / 4)
-        s = kblocks / 4;
-    if (s > 16)
-        s = 16;
-    if (s < 1)
-        s = 1;
-    p.per_split = (kblocks + s - 1) / s;
+    const int out = p.splits > 1 ? 8 : 4;
+    return p.per_split + (p.per_split < out ? out - p.per_split : 0) + 1;
+}
+
+static void split_sum(PairProblem &p, int splits)
+{
+    const int kblocks = p.kblocks * p.segments;
+    p.per_split = (kblocks + splits - 1) / splits;
     p.splits = (kblocks + p.per_split - 1) / p.per_split;
-    p.units = tiles * p.splits;
+    p.units = p.halves * p.tiles_m * p.tiles_n * p.splits;
+}
+
+// Sums over k of few tiles are split, as far as that makes the longest share
+// shorter by more than the parts' way through memory takes (a sixteenth of a
+// block of k for each tile's part).
+static void split_sums(PairProblem &a, PairProblem &b)
+{
+    int64_t best = -1;
+    int sa = 1, sb = 1;
+    static constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16};
+    for (int i : kSplits)
+        for (int k : kSplits) {
+            if ((i > 1 && (a.kblocks * a.segments < 4 * i || a.halves * a.tiles_m * a.tiles_n >= kPairs)) ||
+                (k > 1 && (b.kblocks * b.segments < 4 * k || b.halves * b.tiles_m * b.tiles_n >= kPairs)))
+                continue;
+            split_sum(a, i);
+            split_sum(b, k);
+            PairParams P;
+            const int64_t parts = (a.splits > 1 ? a.units : 0) + (b.splits > 1 ? b.units : 0);
+            const int64_t t = 16 * share_units(P, a.units, unit_time(a), b.units, unit_time(b)) + parts;
+            if (best < 0 || t < best) {
+                best = t;
+                sa = i;
+                sb = k;
+            }
+        }
+    split_sum(a, sa);
+    split_sum(b, sb);
 }
 
 struct BwdPlan {
@@ -734,8 +801,15 @@ struct BwdPlan {
     size_t gu_bytes, dx_bytes, dw_bytes;
 };
 
-static void plan_bwd(BwdPlan &b, int64_t T, int64_t H, int64_t F)
+// The plan goes by the sizes alone; a thread keeps its last one, as a training
+// loop asks for the same again.
+static const BwdPlan &plan_bwd(int64_t T, int64_t H, int64_t F)
 {
+    static thread_local BwdPlan b;
+    static thread_local int64_t last[3];
+    if (last[0] == T && last[1] == H && last[2] == F)
+        return b;
+    b = BwdPlan{};
     PairProblem &x = b.dx, &w = b.dw;
     x.segments = 2;
     x.halves = 1;
@@ -746,7 +820,6 @@ static void plan_bwd(BwdPlan &b, int64_t T, int64_t H, int64_t F)
     x.tiles_n = ceil_div(H, 256);
     x.rows = (int)T;
     x.cols = (int)H;
-    split_sum(x, 2 * x.kblocks);
     w.segments = 1;
     w.halves = 2;
     w.a_mn = w.b_mn = 1;
@@ -755,16 +828,19 @@ static void plan_bwd(BwdPlan &b, int64_t T, int64_t H, int64_t F)
     w.tiles_n = ceil_div(H, 256);
     w.rows = (int)F;
     w.cols = (int)H;
-    split_sum(w, w.kblocks);
+    split_sums(x, w);
     b.gu_bytes = ((size_t)T * F * 2 + 255) & ~(size_t)255;
     b.dx_bytes = x.splits > 1 ? ((size_t)x.splits * T * H * 4 + 255) & ~(size_t)255 : 0;
     b.dw_bytes = w.splits > 1 ? ((size_t)w.splits * 2 * F * H * 4 + 255) & ~(size_t)255 : 0;
+    last[0] = T;
+    last[1] = H;
+    last[2] = F;
+    return b;
 }
 
 size_t gated_bwd_workspace(int64_t T, int64_t H, int64_t F)
 {
-    BwdPlan b{};
-    plan_bwd(b, T, H, F);
+    const BwdPlan &b = plan_bwd(T, H, F);
     return 2 * b.gu_bytes + b.dx_bytes + b.dw_bytes;
 }
 
@@ -777,8 +853,7 @@ static cudaError_t launch_join(const JoinParams &j, int outputs, cudaStream_t st
 
 cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
 {
-    BwdPlan b{};
-    plan_bwd(b, c.T, c.H, c.F);
+    const BwdPlan &b = plan_bwd(c.T, c.H, c.F);
     uint8_t *ws = c.workspace;
     const Matrix dg{ws, c.T, c.F, c.F}, du{ws + b.gu_bytes, c.T, c.F, c.F};
     float *part_x = reinterpret_cast<float *>(ws + 2 * b.gu_bytes);
@@ -819,11 +894,11 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
                            : output_map(&p.out[0], c.dw_gate) && output_map(&p.out[1], c.dw_up)))
             return cudaErrorInvalidValue;
     }
-    P.units = P.p[0].units + (n > 1 ? P.p[1].units : 0);
+    share_units(P, P.p[0].units, unit_time(P.p[0]), n > 1 ? P.p[1].units : 0, n > 1 ? unit_time(P.p[1]) : 0);
     P.status = c.status;
     P.wait_ns = c.wait_ns;
     P.withhold = c.withhold;
-    e = launch_cluster(gated_pair_kernel<false>, pair_grid(P.units), 2, kPairThreads, kPairSmem, stream, P);
+    e = launch_cluster(gated_pair_kernel<false>, pair_grid(P), 2, kPairThreads, kPairSmem, stream, P);
     if (e == cudaSuccess && c.dx.data && b.dx.splits > 1) {
         JoinParams j{};
         j.part[0] = part_x;
