@@ -81,6 +81,7 @@ constexpr uint64_t kDropCtas = 1 << 20;
 template <bool RES, bool DENSE, bool DEV>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropoutParams p)
 {
+    pdl_launch_dependents();
     pdl_wait();
     const Philox<DEV> key(p.r);
     const uint32_t limit = limit_of(p.r);
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kDnThreads ? 2 : 1)
     const Chunk c = cta_chunk(L);
     const int W = L.warps_per_row, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     init_ring(s, L);
+    pdl_launch_dependents();
     pdl_wait();
     if (warp == L.groups * W) {
         const RowView views[2] = {p.in[0], p.in[1]};
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(kDnWideThreads, 1)
     const Chunk c = cta_chunk(L);
     const int W = L.warps_per_row, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     init_ring(s, L);
+    pdl_launch_dependents();
     pdl_wait();
     if (warp == L.groups * W) {
         const RowView views[3] = {p.in[0], p.in[1], p.in[2]};
@@ -381,7 +384,6 @@ __global__ void __launch_bounds__(kDnWideThreads, 1)
         }
         reinterpret_cast<float4 *>(p.partials + (size_t)blockIdx.x * L.H)[i] = a;
     }
-    pdl_launch_dependents();
 }
 
 // Column sums of the CTAs' partials in CTA order: a warp takes 32 columns and
@@ -393,6 +395,7 @@ constexpr int kColumnAhead = 8;
 __global__ void __launch_bounds__(32 * kColumnWarps) column_sum_kernel(const __grid_constant__ ColumnSumParams p)
 {
     __shared__ float2 part[kColumnWarps][32];
+    pdl_launch_dependents();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, list = blockIdx.y;
     const int j = blockIdx.x * 32 + lane;

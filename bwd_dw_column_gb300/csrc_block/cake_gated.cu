@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
     tc_fence_after();
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_at) : "memory");
+    pdl_launch_dependents();
     pdl_wait();
     bool ok = true;
     if (warp == 0) {
@@ -372,11 +373,59 @@ struct FewParams {
     int n;                 // T rounded up to 16
     int columns;           // of tensor memory
     int stages, per_rank;  // blocks of k of a CTA of the cluster
+    int ahead;             // of these brought to L2 while the launch before drains: weights that it
+                           // writes are written in L2 too, so what is read after the wait is whole
     int gelu;
     int *status;
     uint64_t wait_ns;
     int withhold;
 };
+
+// Outputs from the cluster's sums: every one is two neighbours of f, and `first`
+// and every `step`-th after it are this thread's, U of them with all their
+// parts on their way at once.
+template <int U>
+__device__ __forceinline__ void few_outputs(const FewParams &P, uint32_t smem, int f0, int first, int step, int C)
+{
+    const int total = P.T * 64;
+    for (int i0 = first; i0 < total; i0 += U * step) {
+        float2 g[U], u[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            g[k] = u[k] = make_float2(0.f, 0.f);
+        for (int r = 0; r < C; ++r) { // in the order of k
+            float2 x[U], y[U];
+            const uint32_t from = map_to_rank(smem, r);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const uint32_t at = from + 8 * (uint32_t)min(i0 + k * step, total - 1); // [n][128] in the order of i
+                x[k] = ld_cluster_f2(at);
+                y[k] = ld_cluster_f2(at + (uint32_t)P.n * 512);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                g[k] = add2(g[k], x[k]);
+                u[k] = add2(u[k], y[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = i0 + k * step, t = i >> 6, f = f0 + 2 * (i & 63);
+            if (i >= total || f >= P.F)
+                continue;
+            float d;
+            const float a = activation<false>(g[k].x, P.gelu, d), b = activation<false>(g[k].y, P.gelu, d);
+            auto put = [&](uint16_t *m, int64_t stride, float lo, float hi) {
+                *reinterpret_cast<uint32_t *>(m + (int64_t)t * stride + f) = pack_bf16(lo, hi);
+            };
+            put(P.h, P.h_stride, a * u[k].x, b * u[k].y);
+            if (P.g) {
+                put(P.g, P.g_stride, g[k].x, g[k].y);
+                put(P.u, P.u_stride, u[k].x, u[k].y);
+            }
+        }
+    }
+}
 
 __global__ void __launch_bounds__(kFewThreads) gated_few_kernel(const __grid_constant__ FewParams P)
 {
@@ -406,6 +455,14 @@ __global__ void __launch_bounds__(kFewThreads) gated_few_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        prefetch_map(&P.x);
+        for (int kb = k0; kb < min(k1, k0 + P.ahead); ++kb) {
+            tile_prefetch(&P.w_gate, kb * 64, f0);
+            tile_prefetch(&P.w_up, kb * 64, f0);
+        }
+    }
     pdl_wait();
     bool ok = true;
     if (warp == 0) {
@@ -484,28 +541,11 @@ __global__ void __launch_bounds__(kFewThreads) gated_few_kernel(const __grid_con
     __syncwarp();
     cluster_sync_all();
     if (!bad) {
-        for (int i = rank * kFewThreads + (int)threadIdx.x; i < P.T * 64; i += C * kFewThreads) {
-            const int t = i >> 6, f = 2 * (i & 63);
-            float2 g = make_float2(0.f, 0.f), u = g;
-            const uint32_t at = smem + (uint32_t)(t * 128 + f) * 4, up = (uint32_t)P.n * 512;
-            for (int r = 0; r < C; ++r) { // in the order of k
-                const uint32_t from = map_to_rank(at, r);
-                g = add2(g, ld_cluster_f2(from));
-                u = add2(u, ld_cluster_f2(from + up));
-            }
-            if (f0 + f >= P.F)
-                continue;
-            float d;
-            const float a = activation<false>(g.x, P.gelu, d), b = activation<false>(g.y, P.gelu, d);
-            auto put = [&](uint16_t *m, int64_t stride, float lo, float hi) {
-                *reinterpret_cast<uint32_t *>(m + (int64_t)t * stride + f0 + f) = pack_bf16(lo, hi);
-            };
-            put(P.h, P.h_stride, a * u.x, b * u.y);
-            if (P.g) {
-                put(P.g, P.g_stride, g.x, g.y);
-                put(P.u, P.u_stride, u.x, u.y);
-            }
-        }
+        const int step = C * kFewThreads, first = rank * kFewThreads + (int)threadIdx.x;
+        if (P.T * 64 <= step)
+            few_outputs<1>(P, smem, f0, first, step, C);
+        else
+            few_outputs<4>(P, smem, f0, first, step, C);
     }
     __syncwarp();
     cluster_sync_all(); // no CTA leaves while another reads its sums
@@ -528,6 +568,7 @@ struct GatedGradParams {
 
 __global__ void __launch_bounds__(kGradGuThreads) gated_grad_kernel(const __grid_constant__ GatedGradParams p)
 {
+    pdl_launch_dependents();
     pdl_wait();
     for (uint64_t i = (uint64_t)blockIdx.x * kGradGuThreads + threadIdx.x; i < p.vecs;
          i += (uint64_t)gridDim.x * kGradGuThreads) {
@@ -563,6 +604,7 @@ struct JoinParams {
 
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p)
 {
+    pdl_launch_dependents();
     pdl_wait();
     const int o = blockIdx.y;
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < p.vecs; i += (uint64_t)gridDim.x * 256) {
@@ -672,12 +714,17 @@ static cudaError_t launch_few(const GatedFwdCall &c, cudaStream_t stream)
     P.columns = 32;
     while (P.columns < 2 * P.n)
         P.columns *= 2;
-    // CTAs that share k: as many as run at a time, two an SM where their stages are small
-    const int per_sm = P.n <= 32 ? 2 : 1, tiles = ceil_div(c.F, 128);
+    // CTAs that share k: as many as run at a time, two an SM where their stages
+    // are small.  Clusters leave some SMs of their processing clusters without
+    // one: GB300, one token, 2048 to 6144 (48 tiles), clusters of 4, 5 and 6
+    // CTAs 11.5, 10.8 and 16.3 us; 64 tokens, 4096 to 8192 (64 tiles, one CTA an
+    // SM), clusters of 1, 2 and 3 31, 26 and 35 us.
+    const int per_sm = P.n <= 32 ? 2 : 1, tiles = ceil_div(c.F, 128), fit = kSMsBlock * per_sm * 27 / 32;
     int cluster = 1;
-    while (cluster < 8 && tiles * cluster * 2 <= kSMsBlock * per_sm && P.kblocks >= 4 * cluster)
-        cluster *= 2;
+    while (cluster < 8 && tiles * (cluster + 1) <= fit && P.kblocks >= 2 * (cluster + 1))
+        ++cluster;
     P.per_rank = ceil_div(P.kblocks, cluster);
+    P.ahead = 4; // (a token 10.8 us against 11.1)
     const size_t stage = kFewWeights + 128 * (size_t)P.n;
     P.stages = (int)((per_sm == 2 ? 112 * 1024 : 224 * 1024) / stage);
     P.stages = P.stages > 8 ? 8 : P.stages;

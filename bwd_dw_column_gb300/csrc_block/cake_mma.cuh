@@ -25,7 +25,13 @@ __device__ __forceinline__ void tile_g2s(uint32_t dst, const CUtensorMap *m, int
                  : "memory");
 }
 
-// The same for a CTA of a pair: `bar` may be the other CTA's (a
+// A tile into L2.
+__device__ __forceinline__ void tile_prefetch(const CUtensorMap *m, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(x), "r"(y) : "memory");
+}
+
+// tile_g2s for a CTA of a pair: `bar` may be the other CTA's (a
 // shared::cluster address).
 __device__ __forceinline__ void tile_g2s_pair(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar)
 {

@@ -341,6 +341,7 @@ template <int LANES, bool ADJ, bool NORM>
 __global__ void __launch_bounds__(kRotThreads, 2) rotary_kernel(const __grid_constant__ RotaryParams p, float sign)
 {
     extern __shared__ __align__(16) uint4 slots_raw[];
+    pdl_launch_dependents();
     pdl_wait();
     uint32_t cta, none;
     const RotaryList &L = cta_list(p, cta);
@@ -454,6 +455,7 @@ __global__ void __launch_bounds__(kRotThreads, 2) rotary_bwd_kernel(const __grid
 {
     // the slots (later the warps' sums [warps][D] (hi, lo)), the threads' column sums, what they share
     extern __shared__ __align__(16) uint4 slots_raw[];
+    pdl_launch_dependents();
     pdl_wait();
     uint32_t cta, none;
     const RotaryList &L = cta_list(p, cta);
@@ -610,7 +612,6 @@ __global__ void __launch_bounds__(kRotThreads, 2) rotary_bwd_kernel(const __grid
         }
         L.partials[(size_t)cta * p.D + j] = f;
     }
-    pdl_launch_dependents();
 }
 
 // ------------------------------------------------------------------- launch
