@@ -80,6 +80,8 @@ _lock = threading.Lock()
 def load_library(path: str = LIB_PATH):
     """Load (once) and return the ctypes handle of libcake_rmsnorm.so."""
     global _lib
+    if _lib is not None:  # (set once everything is bound)
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

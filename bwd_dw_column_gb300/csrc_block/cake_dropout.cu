@@ -70,15 +70,45 @@ __device__ __forceinline__ uint32_t limit_of(const DropoutRng &r) { return r.cut
 
 // -------------------------------------------------------------------- alone
 
-// A CTA takes 1024 neighbouring vectors at a time, four a thread.  Rows that are
-// not one block of memory come from one division for all of them and a product
-// with a reciprocal for each.
+// A CTA takes 1024 neighbouring vectors at a time, four a thread.  SPACING says
+// how they lie in memory: 0 in one block, 1 in equally spaced rows less than 2^31
+// elements apart, 2 in any.  Rows come from one division for all of them and a
+// product with a reciprocal for each (GB300, 16381 x 6144: 59 us in one block,
+// spaced rows 69 us by 64-bit products of every row and column).
 constexpr int kDropThreads = 256;
 constexpr int kDropPer = 4;
 constexpr uint32_t kDropVecs = kDropThreads * kDropPer;
 constexpr uint64_t kDropCtas = 1 << 20;
 
-template <bool RES, bool DENSE, bool DEV>
+// Where a CTA's vectors lie in a view.
+template <int SPACING>
+struct DropPlace {
+    const RowView &v;
+    const uint4 *first;   // 0: the first vector; 1: its row's begin
+    uint32_t row0, nh;
+
+    __device__ __forceinline__ DropPlace(const RowView &view, const DropoutParams &p, uint64_t v0, uint32_t row)
+        : v(view), row0(row), nh(p.nh)
+    {
+        first = reinterpret_cast<const uint4 *>(view.base);
+        if (SPACING == 0)
+            first += v0;
+        if (SPACING == 1)
+            first += (int64_t)row * (view.row_stride / 8);
+    }
+
+    // Vector i of the CTA's: the col-th of the q-th row from row0 on.
+    __device__ __forceinline__ uint4 *at(uint32_t i, uint32_t q, uint32_t col) const
+    {
+        const uint4 *a = SPACING == 0 ? first + i
+                         : SPACING == 1
+                             ? first + (uint64_t)q * (uint32_t)(v.row_stride / 8) + col
+                             : first + row_off(v, row0 + q, nh) / 8 + col;
+        return const_cast<uint4 *>(a);
+    }
+};
+
+template <bool RES, int SPACING, bool DEV>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_constant__ DropoutParams p)
 {
     pdl_launch_dependents();
@@ -88,28 +118,24 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
     const float2 scale = make_float2(p.r.scale, p.r.scale);
     for (uint64_t v0 = (uint64_t)blockIdx.x * kDropVecs; v0 < p.vecs; v0 += (uint64_t)gridDim.x * kDropVecs) {
         uint32_t row0 = 0, rem = 0;
-        if (!DENSE) {
+        if (SPACING) {
             row0 = v0 >> 32 ? (uint32_t)(v0 / p.nvec) : (uint32_t)v0 / p.nvec;
             rem = (uint32_t)(v0 - (uint64_t)row0 * p.nvec);
         }
         const uint32_t n = p.vecs - v0 < kDropVecs ? (uint32_t)(p.vecs - v0) : kDropVecs;
+        const DropPlace<SPACING> px(p.x, p, v0, row0), pe(p.residual, p, v0, row0), py(p.y, p, v0, row0);
         uint4 x[kDropPer], e[kDropPer];
-        uint32_t row[kDropPer], col[kDropPer];
-        auto off = [&](const RowView &v, int k, uint32_t i) {
-            return DENSE ? (int64_t)(v0 + i) * 8 : row_off(v, row[k], p.nh) + col[k];
-        };
+        uint32_t q_of[kDropPer], col_of[kDropPer];
 #pragma unroll
         for (int k = 0; k < kDropPer; ++k) {
             const uint32_t i = k * kDropThreads + threadIdx.x;
-            if (!DENSE) {
-                const uint32_t q = __umulhi(2 * (rem + i), p.reciprocal); // (rem + i) / nvec: exact below 2^31 / nvec
-                row[k] = row0 + q;
-                col[k] = (rem + i - q * p.nvec) * 8;
-            }
+            // (rem + i) / nvec: exact below 2^31 / nvec
+            q_of[k] = SPACING ? __umulhi(2 * (rem + i), p.reciprocal) : 0;
+            col_of[k] = SPACING ? rem + i - q_of[k] * p.nvec : 0;
             if (i < n) {
-                x[k] = __ldcs(reinterpret_cast<const uint4 *>(p.x.base + off(p.x, k, i)));
+                x[k] = __ldcs(px.at(i, q_of[k], col_of[k]));
                 if (RES)
-                    e[k] = __ldcs(reinterpret_cast<const uint4 *>(p.residual.base + off(p.residual, k, i)));
+                    e[k] = __ldcs(pe.at(i, q_of[k], col_of[k]));
             }
         }
 #pragma unroll
@@ -126,8 +152,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
                     v = add2(v, bf2(word(e[k], q)));
                 o[q] = pack2(v);
             }
-            __stcs(reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.y.base) + off(p.y, k, i)),
-                   make_uint4(o[0], o[1], o[2], o[3]));
+            __stcs(py.at(i, q_of[k], col_of[k]), make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
 }
@@ -136,11 +161,10 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
 
 // Both kernels stream rows through shared memory as the RMSNorm kernels do (a
 // producer warp with bulk copies, row groups of W warps, bounded waits).
-constexpr int kDnThreads = 416;      // 12 consumer warps and the producer
-constexpr int kDnWideThreads = 544;  // 16: the forward's rows of more than 6144 columns
+constexpr int kDnThreads = 544; // 16 consumer warps and the producer
 
-template <int VPT, int THREADS, bool DEV>
-__global__ void __launch_bounds__(THREADS, THREADS == kDnThreads ? 2 : 1)
+template <int VPT, bool DEV>
+__global__ void __launch_bounds__(kDnThreads, 2)
     dropout_norm_fwd_kernel(const __grid_constant__ DropoutNormParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -248,7 +272,7 @@ __device__ __forceinline__ void fold_columns(float4 *at, int step, float2 (&sum)
 }
 
 template <int VPT, bool DH, bool DEV>
-__global__ void __launch_bounds__(kDnWideThreads, 1)
+__global__ void __launch_bounds__(kDnThreads, 1)
     dropout_norm_bwd_kernel(const __grid_constant__ DropoutNormParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -432,16 +456,21 @@ static bool fit_plan(DropoutNormPlan &p, int H, int ntens, bool backward)
 {
     p.lo_bytes = backward ? p.vpt * 64 * p.groups * p.W * 32 : 0;
     const size_t fixed = kMiscBytes + weight_smem_bytes(H) + p.lo_bytes, stage = (size_t)ntens * p.groups * H * 2;
-    p.per_sm = !backward && p.groups * p.W <= 12 ? 2 : 1;
+    p.per_sm = backward || p.groups * H >= 7000 ? 1 : 2;
     for (;; --p.per_sm) {
         const size_t room = 228 * 1024 / p.per_sm - 1024; // 1 KB of each CTA is the system's
         p.stages = room > fixed ? (int)((room - fixed) / stage) : 0;
         if (p.stages >= 2 || p.per_sm == 1)
             break;
     }
-    // no more than 3 stages in the forward, 6 in the backward, or what brings 48 KB on their way
+    // The forward runs one CTA an SM with three stages where that has 7000
+    // columns or more in work, else two with two stages, or what brings 48 KB on
+    // their way: GB300, 2^26 values (the copy takes 80 us), one and two CTAs:
+    // H = 4096 83 and 96 us, H = 1024 83 and 95, H = 8192 84 and 91, but H = 6144
+    // 94 and 86, H = 5120 150 and 89, H = 256 113 and 92.
+    const int least = backward ? 6 : p.per_sm == 1 ? 3 : 2;
     int most = (int)((48 * 1024 + stage - 1) / stage);
-    most = most > (backward ? 6 : 3) ? most : backward ? 6 : 3;
+    most = most > least ? most : least;
     most = most > 16 ? 16 : most;
     if (p.stages > most)
         p.stages = most;
@@ -463,8 +492,7 @@ DropoutNormPlan dropout_norm_plan(int H, uint32_t rows, int ntens, bool backward
     int best = -1;
     for (int vpt = 1; vpt <= (backward ? 3 : 2); ++vpt) {
         const int W = (nvec + 32 * vpt - 1) / (32 * vpt);
-        const int most = backward || (vpt == 2 && W > 12) ? 16 : 12;
-        for (int groups = most / W < kMaxRowGroupBarriers ? most / W : kMaxRowGroupBarriers; groups >= 1; --groups) {
+        for (int groups = 16 / W < kMaxRowGroupBarriers ? 16 / W : kMaxRowGroupBarriers; groups >= 1; --groups) {
             DropoutNormPlan q{};
             q.vpt = vpt;
             q.W = W;
@@ -491,11 +519,20 @@ cudaError_t launch_dropout(const DropoutParams &p, cudaStream_t stream)
 {
     const uint64_t want = (p.vecs + kDropVecs - 1) / kDropVecs;
     const dim3 grid((unsigned)(want < kDropCtas ? want : kDropCtas));
-    const bool dense = p.x.dense && p.y.dense && (!p.residual.base || p.residual.dense);
+    int spacing = 0;
+    for (const RowView *v : {&p.x, &p.residual, &p.y})
+        if (v->base) {
+            const int own = v->dense ? 0 : v->uniform && v->row_stride < (int64_t(1) << 31) ? 1 : 2;
+            spacing = own > spacing ? own : spacing;
+        }
     const auto go = [&](auto dev) {
         constexpr bool D = decltype(dev)::value;
-        auto kern = p.residual.base ? (dense ? dropout_kernel<true, true, D> : dropout_kernel<true, false, D>)
-                                    : (dense ? dropout_kernel<false, true, D> : dropout_kernel<false, false, D>);
+        auto kern = p.residual.base ? (spacing == 0   ? dropout_kernel<true, 0, D>
+                                       : spacing == 1 ? dropout_kernel<true, 1, D>
+                                                      : dropout_kernel<true, 2, D>)
+                                    : (spacing == 0   ? dropout_kernel<false, 0, D>
+                                       : spacing == 1 ? dropout_kernel<false, 1, D>
+                                                      : dropout_kernel<false, 2, D>);
         return launch_after(kern, grid, kDropThreads, 0, stream, p);
     };
     return p.r.rng ? go(std::true_type()) : go(std::false_type());
@@ -506,9 +543,7 @@ cudaError_t launch_dropout_norm_fwd(const DropoutNormParams &p, const DropoutNor
     const int threads = 32 * (plan.groups * plan.W + 1);
     const auto go = [&](auto dev) {
         constexpr bool D = decltype(dev)::value;
-        auto kern = plan.vpt == 1           ? dropout_norm_fwd_kernel<1, kDnThreads, D>
-                    : threads <= kDnThreads ? dropout_norm_fwd_kernel<2, kDnThreads, D>
-                                            : dropout_norm_fwd_kernel<2, kDnWideThreads, D>;
+        auto kern = plan.vpt == 1 ? dropout_norm_fwd_kernel<1, D> : dropout_norm_fwd_kernel<2, D>;
         return launch_after(kern, dim3((unsigned)plan.ctas), threads, plan.smem, stream, p);
     };
     return p.r.rng ? go(std::true_type()) : go(std::false_type());

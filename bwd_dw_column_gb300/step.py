@@ -113,7 +113,7 @@ def _on_devices(stream, devices):
         raise ValueError("every tensor must be on the same device")
     dev, = devices
     if stream is None:
-        if torch.cuda.current_device() == dev:
+        if torch._C._cuda_getDevice() == dev:
             return _here
     elif stream.device.index != dev:
         raise ValueError("the stream belongs to another device than the tensors")
@@ -122,7 +122,7 @@ def _on_devices(stream, devices):
 
 def _current() -> int:
     """The current device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def cake_step_wait_test(wait_limit_us: int = 0, withhold: int = 0):
