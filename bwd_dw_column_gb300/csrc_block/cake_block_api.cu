@@ -48,8 +48,8 @@ Layout rows_layout(const DropoutNormPlan &plan, const cake_shape *shape, uint32_
     L.nvec = L.H / 8;
     L.warps_per_row = plan.W;
     L.groups = plan.groups;
-    L.rows_per_group = 1;
-    L.lanes_per_row = 32;
+    L.rows_per_group = 32 / plan.lanes;
+    L.lanes_per_row = plan.lanes;
     L.stages = plan.stages;
     L.lo_bytes = plan.lo_bytes;
     L.ntens = ntens;
@@ -80,7 +80,7 @@ extern "C" cake_status cake_block_wait_test(uint32_t wait_limit_us, int withhold
     return CAKE_OK;
 }
 
-extern "C" cake_status cake_dropout_norm_plan(const cake_shape *shape, int tensors, int backward, int64_t plan[8])
+extern "C" cake_status cake_dropout_norm_plan(const cake_shape *shape, int tensors, int backward, int64_t plan[9])
 {
     uint32_t rows = 0;
     const cake_status st = check_shape(shape, &rows);
@@ -89,8 +89,9 @@ extern "C" cake_status cake_dropout_norm_plan(const cake_shape *shape, int tenso
     if (!plan || rows == 0 || tensors < 2 || tensors > 3)
         return CAKE_ERR_INVALID;
     const DropoutNormPlan p = dropout_norm_plan((int)shape->hidden, rows, tensors, backward != 0);
-    const int64_t got[8] = {p.vpt, p.W, p.groups, p.stages, p.ctas, p.rows_per_cta, p.lo_bytes, (int64_t)p.smem};
-    std::copy(got, got + 8, plan);
+    const int64_t got[9] = {p.vpt,  p.lanes,        p.W,        p.groups,       p.stages,
+                            p.ctas, p.rows_per_cta, p.lo_bytes, (int64_t)p.smem};
+    std::copy(got, got + 9, plan);
     return CAKE_OK;
 }
 

@@ -31,7 +31,7 @@ struct DropoutParams {
 };
 
 struct DropoutNormPlan {
-    int vpt, W, groups, stages, per_sm, ctas;
+    int vpt, lanes, W, groups, stages, per_sm, ctas;
     int lo_bytes;           // backward: the threads' column sums
     uint32_t rows_per_cta;
     size_t smem;

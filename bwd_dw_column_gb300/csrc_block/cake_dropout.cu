@@ -163,7 +163,35 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
 // producer warp with bulk copies, row groups of W warps, bounded waits).
 constexpr int kDnThreads = 544; // 16 consumer warps and the producer
 
-template <int VPT, bool DEV>
+// LPR < 32: rows of LPR lanes, 32 / LPR of them to a warp, which is a row group
+// of its own; otherwise a row spans a group's W warps.
+template <int LPR>
+struct RowLanes {
+    static constexpr int kRows = 32 / LPR; // of a group's stage
+    int sub, tid, stride; // the thread's row among the group's; its first vector, and the step to its next
+
+    __device__ __forceinline__ RowLanes(int lane, int gtid, int W)
+        : sub(LPR < 32 ? lane / LPR : 0), tid(LPR < 32 ? lane % LPR : gtid), stride(LPR < 32 ? LPR : 32 * W)
+    {
+    }
+
+    // Sum over a row's threads; `abort` is joined over the group's.
+    static __device__ __forceinline__ float sum(float v, const Smem &s, const Layout &L, int gid, int wig, int lane,
+                                                uint32_t slot, bool &abort)
+    {
+        if constexpr (LPR == 32) {
+            return group_sum(v, s, L, gid, wig, lane, slot, abort);
+        } else {
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1)
+                v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+            abort = __any_sync(0xffffffffu, abort);
+            return v;
+        }
+    }
+};
+
+template <int VPT, int LPR, bool DEV>
 __global__ void __launch_bounds__(kDnThreads, 2)
     dropout_norm_fwd_kernel(const __grid_constant__ DropoutNormParams p)
 {
@@ -180,7 +208,9 @@ __global__ void __launch_bounds__(kDnThreads, 2)
         produce<2>(s, L, c, views, 2, p.status, p.wait_ns);
         return;
     }
-    const int gid = warp / W, wig = warp - gid * W, gtid = wig * 32 + lane, vstride = 32 * W, nvec = L.nvec;
+    const int gid = warp / W, wig = warp - gid * W, gtid = wig * 32 + lane, nvec = L.nvec;
+    const RowLanes<LPR> own(lane, gtid, W);
+    const int vstride = own.stride, ltid = own.tid;
     const Philox<DEV> key(p.r);
     const uint32_t limit = limit_of(p.r);
     const float2 scale = make_float2(p.r.scale, p.r.scale);
@@ -188,14 +218,16 @@ __global__ void __launch_bounds__(kDnThreads, 2)
     bool abort = false;
     uint32_t slot = 0, st = 0, ph = 0;
     for (uint32_t it = 0; it < c.ntiles && !abort; ++it) {
-        const uint32_t r = c.r0 + it * c.tile_rows + gid;
+        const int tr = gid * RowLanes<LPR>::kRows + own.sub;
+        const uint32_t first = c.r0 + it * c.tile_rows + gid * RowLanes<LPR>::kRows, r = first + own.sub;
         uint4 bits[VPT]; // before the wait: they need no data
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
-            bits[k] = random_bits(key, (uint64_t)r * nvec + k * vstride + gtid);
+            bits[k] = random_bits(key, (uint64_t)r * nvec + k * vstride + ltid);
         abort = !mbar_wait(smem_addr(&s.full[st]), ph, p.wait_ns);
-        if (r < c.r_end) { // uniform across the group
-            const uint8_t *stage = s.ring + st * s.stage_bytes + (size_t)gid * L.H * 2;
+        if (first < c.r_end) { // uniform across the group
+            const bool live = LPR == 32 || r < c.r_end;
+            const uint8_t *stage = s.ring + st * s.stage_bytes + (size_t)tr * L.H * 2;
             const uint4 *xs = reinterpret_cast<const uint4 *>(stage);
             const uint4 *es = reinterpret_cast<const uint4 *>(stage + s.tens_bytes);
             uint4 h[VPT];
@@ -203,9 +235,9 @@ __global__ void __launch_bounds__(kDnThreads, 2)
             uint4 *hrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[1].base) + row_off(p.out[1], r, L.nh));
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int v = k * vstride + gtid;
+                const int v = k * vstride + ltid;
                 h[k] = make_uint4(0, 0, 0, 0);
-                if (v < nvec) {
+                if (live && v < nvec) {
                     const uint4 x = xs[v], e = es[v];
                     uint32_t o[4];
 #pragma unroll
@@ -220,14 +252,14 @@ __global__ void __launch_bounds__(kDnThreads, 2)
                         __stcs(hrow + v, h[k]);
                 }
             }
-            const float tot = group_sum(__fadd_rn(ss.x, ss.y), s, L, gid, wig, lane, slot++, abort);
+            const float tot = own.sum(__fadd_rn(ss.x, ss.y), s, L, gid, wig, lane, slot++, abort);
             const float rs = 1.0f / sqrtf(__fadd_rn(__fmul_rn(tot, L.inv_h), p.eps));
             const float2 rs2 = make_float2(rs, rs);
             uint4 *yrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[0].base) + row_off(p.out[0], r, L.nh));
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int v = k * vstride + gtid;
-                if (v < nvec && !abort) {
+                const int v = k * vstride + ltid;
+                if (live && v < nvec && !abort) {
                     float2 w2[4];
                     weight_pairs(s, L, v, w2);
                     uint32_t o[4];
@@ -237,7 +269,7 @@ __global__ void __launch_bounds__(kDnThreads, 2)
                     __stcs(yrow + v, make_uint4(o[0], o[1], o[2], o[3]));
                 }
             }
-            if (gtid == 0 && !abort)
+            if (live && ltid == 0 && !abort)
                 p.rstd_out[r] = rs;
         }
         __syncwarp();
@@ -271,7 +303,7 @@ __device__ __forceinline__ void fold_columns(float4 *at, int step, float2 (&sum)
     }
 }
 
-template <int VPT, bool DH, bool DEV>
+template <int VPT, int LPR, bool DH, bool DEV>
 __global__ void __launch_bounds__(kDnThreads, 1)
     dropout_norm_bwd_kernel(const __grid_constant__ DropoutNormParams p)
 {
@@ -288,7 +320,9 @@ __global__ void __launch_bounds__(kDnThreads, 1)
         produce<3>(s, L, c, views, L.ntens, p.status, p.wait_ns);
         return;
     }
-    const int gid = warp / W, wig = warp - gid * W, gtid = wig * 32 + lane, vstride = 32 * W, nvec = L.nvec;
+    const int gid = warp / W, wig = warp - gid * W, gtid = wig * 32 + lane, nvec = L.nvec;
+    const RowLanes<LPR> own(lane, gtid, W);
+    const int vstride = own.stride, ltid = own.tid, tr = gid * RowLanes<LPR>::kRows + own.sub;
     const int nct = L.groups * W * 32;
     const Philox<DEV> key(p.r);
     const uint32_t limit = limit_of(p.r);
@@ -306,15 +340,16 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     bool abort = false;
     uint32_t slot = 0, st = 0, ph = 0;
     for (uint32_t it = 0; it < c.ntiles && !abort; ++it) {
-        const uint32_t r = c.r0 + it * c.tile_rows + gid;
+        const uint32_t first = c.r0 + it * c.tile_rows + gid * RowLanes<LPR>::kRows, r = first + own.sub;
         const float rs = r < c.r_end ? __ldg(p.rstd + r) : 0.f;
         uint4 bits[VPT]; // before the wait: they need no data
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
-            bits[k] = random_bits(key, (uint64_t)r * nvec + k * vstride + gtid);
+            bits[k] = random_bits(key, (uint64_t)r * nvec + k * vstride + ltid);
         abort = !mbar_wait(smem_addr(&s.full[st]), ph, p.wait_ns);
-        if (r < c.r_end) { // uniform across the group
-            const uint8_t *stage = s.ring + st * s.stage_bytes + (size_t)gid * L.H * 2;
+        if (first < c.r_end) { // uniform across the group
+            const bool live = LPR == 32 || r < c.r_end;
+            const uint8_t *stage = s.ring + st * s.stage_bytes + (size_t)tr * L.H * 2;
             const uint4 *hs = reinterpret_cast<const uint4 *>(stage);
             const uint4 *ds = reinterpret_cast<const uint4 *>(stage + s.tens_bytes);
             const uint4 *es = reinterpret_cast<const uint4 *>(stage + 2 * s.tens_bytes);
@@ -322,8 +357,8 @@ __global__ void __launch_bounds__(kDnThreads, 1)
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int v = k * vstride + gtid;
-                if (v < nvec) {
+                const int v = k * vstride + ltid;
+                if (live && v < nvec) {
                     const uint4 h = hs[v], d = ds[v];
                     float2 w2[4];
                     weight_pairs(s, L, v, w2);
@@ -335,15 +370,15 @@ __global__ void __launch_bounds__(kDnThreads, 1)
                     }
                 }
             }
-            const float tot = group_sum(__fadd_rn(sum.x, sum.y), s, L, gid, wig, lane, slot++, abort);
+            const float tot = own.sum(__fadd_rn(sum.x, sum.y), s, L, gid, wig, lane, slot++, abort);
             const float m = -__fmul_rn(__fmul_rn(__fmul_rn(tot, L.inv_h), rs), __fmul_rn(rs, rs));
             const float2 m2 = make_float2(m, m);
             uint4 *xrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[0].base) + row_off(p.out[0], r, L.nh));
             uint4 *erow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[1].base) + row_off(p.out[1], r, L.nh));
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int v = k * vstride + gtid;
-                if (v < nvec && !abort) {
+                const int v = k * vstride + ltid;
+                if (live && v < nvec && !abort) {
                     const uint4 h = hs[v], d = ds[v];
                     uint4 e = make_uint4(0, 0, 0, 0);
                     if (DH)
@@ -380,26 +415,26 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     }
     if (abort && lane == 0)
         set_status(p.status, kStatusTimeout);
-    // The CTA partial: the groups' sums in group order, through the drained
-    // ring ([group][4 nvec] float4 (hi, lo, hi, lo) of a column pair).
+    // The CTA partial: the rows' sums in their order, through the drained ring
+    // ([row of a stage][4 nvec] float4 (hi, lo, hi, lo) of a column pair).
     const int nslot = 4 * nvec;
     float4 *comb = reinterpret_cast<float4 *>(s.ring);
     consumer_sync(L);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int v = k * vstride + gtid;
+        const int v = k * vstride + ltid;
         fold_columns(sums + 4 * k * nct, nct, acc[k]);
         if (v < nvec)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float4 f = sums[(4 * k + q) * nct];
-                comb[(size_t)gid * nslot + 4 * v + q] = make_float4(f.x, f.z, f.y, f.w);
+                comb[(size_t)tr * nslot + 4 * v + q] = make_float4(f.x, f.z, f.y, f.w);
             }
     }
     consumer_sync(L);
     for (int i = threadIdx.x; i < nslot; i += nct) {
         float4 a = comb[i];
-        for (int g = 1; g < L.groups; ++g) {
+        for (int g = 1; g < L.groups * RowLanes<LPR>::kRows; ++g) {
             const float4 b = comb[(size_t)g * nslot + i];
             comp_add(a.x, a.y, b.x);
             a.y = __fadd_rn(a.y, b.y);
@@ -451,12 +486,13 @@ __global__ void __launch_bounds__(32 * kColumnWarps) column_sum_kernel(const __g
 
 // ------------------------------------------------------------------- launch
 
-// Shared memory of a plan's CTA for its vpt, W and groups; false: no two stages fit.
+// Shared memory of a plan's CTA for its vpt, lanes, W and groups; false: no two stages fit.
 static bool fit_plan(DropoutNormPlan &p, int H, int ntens, bool backward)
 {
     p.lo_bytes = backward ? p.vpt * 64 * p.groups * p.W * 32 : 0;
-    const size_t fixed = kMiscBytes + weight_smem_bytes(H) + p.lo_bytes, stage = (size_t)ntens * p.groups * H * 2;
-    p.per_sm = backward || p.groups * H >= 7000 ? 1 : 2;
+    const size_t fixed = kMiscBytes + weight_smem_bytes(H) + p.lo_bytes, rows = (size_t)p.groups * (32 / p.lanes),
+                 stage = (size_t)ntens * rows * H * 2;
+    p.per_sm = backward || rows * H >= 7000 ? 1 : 2;
     for (;; --p.per_sm) {
         const size_t room = 228 * 1024 / p.per_sm - 1024; // 1 KB of each CTA is the system's
         p.stages = room > fixed ? (int)((room - fixed) / stage) : 0;
@@ -475,8 +511,8 @@ static bool fit_plan(DropoutNormPlan &p, int H, int ntens, bool backward)
     if (p.stages > most)
         p.stages = most;
     size_t ring = p.stages * stage;
-    if (backward && ring < (size_t)p.groups * H * 8) // the groups' column sums pass through it
-        ring = (size_t)p.groups * H * 8;
+    if (backward && ring < rows * H * 8) // the rows' column sums pass through it
+        ring = rows * H * 8;
     p.smem = fixed + ring;
     return p.stages >= 2 && p.smem <= 227 * 1024;
 }
@@ -495,11 +531,13 @@ DropoutNormPlan dropout_norm_plan(int H, uint32_t rows, int ntens, bool backward
         for (int groups = 16 / W < kMaxRowGroupBarriers ? 16 / W : kMaxRowGroupBarriers; groups >= 1; --groups) {
             DropoutNormPlan q{};
             q.vpt = vpt;
+            q.lanes = H <= 32 ? 4 : H <= 64 ? 8 : H <= 128 ? 16 : 32;
             q.W = W;
             q.groups = groups;
             if (!fit_plan(q, H, ntens, backward))
                 continue;
-            int score = groups * H > 6144 ? 6144 : groups * H;
+            int score = groups * (32 / q.lanes) * H;
+            score = score > 6144 ? 6144 : score;
             score = groups == 1 ? score * 8 / 10 : score;
             score = q.stages < 3 ? score * 85 / 100 : score;
             if (score > best) {
@@ -508,7 +546,7 @@ DropoutNormPlan dropout_norm_plan(int H, uint32_t rows, int ntens, bool backward
             }
         }
     }
-    const uint32_t tiles = (rows + p.groups - 1) / p.groups, most = (uint32_t)(kSMsBlock * p.per_sm);
+    const uint32_t tile = (uint32_t)p.groups * (32 / p.lanes), tiles = (rows + tile - 1) / tile, most = (uint32_t)(kSMsBlock * p.per_sm);
     const uint32_t ctas = tiles < most ? tiles : most;
     p.rows_per_cta = ctas ? (rows + ctas - 1) / ctas : 0;
     p.ctas = p.rows_per_cta ? (int)((rows + p.rows_per_cta - 1) / p.rows_per_cta) : 0;
@@ -543,7 +581,11 @@ cudaError_t launch_dropout_norm_fwd(const DropoutNormParams &p, const DropoutNor
     const int threads = 32 * (plan.groups * plan.W + 1);
     const auto go = [&](auto dev) {
         constexpr bool D = decltype(dev)::value;
-        auto kern = plan.vpt == 1 ? dropout_norm_fwd_kernel<1, D> : dropout_norm_fwd_kernel<2, D>;
+        auto kern = plan.lanes == 4    ? dropout_norm_fwd_kernel<1, 4, D>
+                    : plan.lanes == 8  ? dropout_norm_fwd_kernel<1, 8, D>
+                    : plan.lanes == 16 ? dropout_norm_fwd_kernel<1, 16, D>
+                    : plan.vpt == 1    ? dropout_norm_fwd_kernel<1, 32, D>
+                                       : dropout_norm_fwd_kernel<2, 32, D>;
         return launch_after(kern, dim3((unsigned)plan.ctas), threads, plan.smem, stream, p);
     };
     return p.r.rng ? go(std::true_type()) : go(std::false_type());
@@ -554,9 +596,12 @@ cudaError_t launch_dropout_norm_bwd(const DropoutNormParams &p, const DropoutNor
     const int threads = 32 * (plan.groups * plan.W + 1);
     const auto go = [&](auto dev, auto dh) {
         constexpr bool D = decltype(dev)::value, E = decltype(dh)::value;
-        auto kern = plan.vpt == 1   ? dropout_norm_bwd_kernel<1, E, D>
-                    : plan.vpt == 2 ? dropout_norm_bwd_kernel<2, E, D>
-                                    : dropout_norm_bwd_kernel<3, E, D>;
+        auto kern = plan.lanes == 4    ? dropout_norm_bwd_kernel<1, 4, E, D>
+                    : plan.lanes == 8  ? dropout_norm_bwd_kernel<1, 8, E, D>
+                    : plan.lanes == 16 ? dropout_norm_bwd_kernel<1, 16, E, D>
+                    : plan.vpt == 1    ? dropout_norm_bwd_kernel<1, 32, E, D>
+                    : plan.vpt == 2    ? dropout_norm_bwd_kernel<2, 32, E, D>
+                                       : dropout_norm_bwd_kernel<3, 32, E, D>;
         return launch_after(kern, dim3((unsigned)plan.ctas), threads, plan.smem, stream, p);
     };
     if (p.L.ntens == 3)

@@ -25,11 +25,11 @@ cake_status cake_block_wait_test(uint32_t wait_limit_us, int withhold);
 /*
  * The plan of cake_dropout_norm_fwd (backward = 0) or _bwd for a shape and a
  * number of staged tensors (2, or 3 of the backward with dh): vectors of 8
- * columns of a thread, warps of a row, rows of a stage, stages, CTAs, rows of a
- * CTA, bytes of the threads' column sums, and bytes of shared memory.  Host
+ * columns of a thread, lanes of a row of part of a warp (32: none), warps of a
+ * row, row groups, stages, CTAs, rows of a CTA, bytes of the threads' column sums, and bytes of shared memory.  Host
  * only.
  */
-cake_status cake_dropout_norm_plan(const cake_shape *shape, int tensors, int backward, int64_t plan[8]);
+cake_status cake_dropout_norm_plan(const cake_shape *shape, int tensors, int backward, int64_t plan[9]);
 
 #ifdef __cplusplus
 }

@@ -84,7 +84,8 @@ def test_dropped_elements_take_no_part(cake):
     assert torch.equal(h.cpu(), torch.where(m, 3.0, 1.0).to(BF16)) and bool(torch.isfinite(y).all())
 
 
-SHAPES = [((1, 8), 0), ((1, 2048), 0), ((37, 72), 8), ((129, 264), 0), ((300, 1032), 0), ((64, 1536), 16),
+SHAPES = [((1, 8), 0), ((59, 8), 0), ((203, 24), 8), ((131, 40), 0), ((1, 64), 0), ((77, 120), 0), ((65, 128), 0),
+          ((1, 2048), 0), ((37, 72), 8), ((129, 264), 0), ((300, 1032), 0), ((64, 1536), 16),
           ((257, 2048), 0), ((90, 2560), 0), ((45, 4096), 0), ((33, 5128), 8), ((31, 6144), 0), ((13, 6152), 0),
           ((17, 8192), 0), ((9, 3, 256), 256), ((4097, 64), 0)]
 
@@ -224,18 +225,20 @@ def test_every_width_has_a_plan_that_fits():
     __graft_entry__.build()
     import bwd_dw_column_gb300 as cake
     from bwd_dw_column_gb300.step import _three
-    lib, got = cake.load_library(), (ctypes.c_int64 * 8)()
+    lib, got = cake.load_library(), (ctypes.c_int64 * 9)()
     for H in range(8, 8193, 8):
         for backward, tensors in ((0, 2), (1, 2), (1, 3)):
             for T in (1, 1000, 2 ** 31 - 1):
                 assert lib.cake_dropout_norm_plan(_three(T, 1, H), tensors, backward, got) == 0
-                vpt, W, groups, stages, ctas, per_cta, lo, smem = got
-                assert 1 <= vpt <= (3 if backward else 2) and 1 <= groups * W <= 16 and 256 * vpt * W >= H
+                vpt, lanes, W, groups, stages, ctas, per_cta, lo, smem = got
+                assert 1 <= vpt <= (3 if backward else 2) and 1 <= groups * W <= 16 and 8 * lanes * vpt * W >= H
+                assert lanes == 32 or (W == 1 and vpt == 1)
+                rows = groups * (32 // lanes)
                 assert W == 1 or groups <= 14
                 fixed = 1024 + (4 * H + 1023) // 1024 * 1024 + lo
                 ring = smem - fixed
-                assert 2 <= stages <= 16 and ring >= stages * tensors * groups * H * 2 and smem <= 227 * 1024
+                assert 2 <= stages <= 16 and ring >= stages * tensors * rows * H * 2 and smem <= 227 * 1024
                 assert groups * 2 * W * 4 <= 400
                 if backward:  # a float4 of a pair of columns, of each group; and of each of a thread's pairs
-                    assert ring >= groups * H * 8 and lo >= vpt * 4 * 16 * groups * W * 32
+                    assert ring >= rows * H * 8 and lo >= vpt * 4 * 16 * groups * W * 32
                 assert (ctas - 1) * per_cta < T <= ctas * per_cta
