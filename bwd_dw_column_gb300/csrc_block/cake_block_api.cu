@@ -163,6 +163,7 @@ extern "C" cake_status cake_dropout_norm_fwd(const cake_shape *shape, const cake
     q.eps = eps;
     q.rstd_out = rstd;
     q.wait_ns = t_waits.ns;
+    q.withhold = t_waits.withhold;
     if (step_status_ptr(&q.status) != cudaSuccess)
         return CAKE_ERR_CUDA;
     return cuda_status(launch_dropout_norm_fwd(q, plan, cu(stream)));
@@ -225,6 +226,7 @@ extern "C" cake_status cake_dropout_norm_bwd(const cake_shape *shape, const cake
     q.rstd = rstd;
     q.partials = static_cast<float2 *>(workspace);
     q.wait_ns = t_waits.ns;
+    q.withhold = t_waits.withhold;
     if (step_status_ptr(&q.status) != cudaSuccess || launch_dropout_norm_bwd(q, plan, cu(stream)) != cudaSuccess)
         return CAKE_ERR_CUDA;
     ColumnSumParams s{};

@@ -50,6 +50,7 @@ struct DropoutNormParams {
     float2 *partials;       // backward: [ctas][H] (hi, lo)
     int *status;
     uint64_t wait_ns;
+    int withhold;           // tests of the waits
 };
 
 DropoutNormPlan dropout_norm_plan(int H, uint32_t rows, int ntens, bool backward);

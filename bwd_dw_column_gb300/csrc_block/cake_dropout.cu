@@ -163,6 +163,14 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
 // producer warp with bulk copies, row groups of W warps, bounded waits).
 constexpr int kDnThreads = 544; // 16 consumer warps and the producer
 
+// Tests of the waits: 16 bytes of the first stage that never come.
+__device__ __forceinline__ void withhold_bytes(const Smem &s, int withhold)
+{
+    if (withhold && (threadIdx.x & 31) == 0)
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], 16;" ::"r"(smem_addr(&s.full[0])) : "memory");
+    __syncwarp();
+}
+
 // LPR < 32: rows of LPR lanes, 32 / LPR of them to a warp, which is a row group
 // of its own; otherwise a row spans a group's W warps.
 template <int LPR>
@@ -205,6 +213,7 @@ __global__ void __launch_bounds__(kDnThreads, 2)
     pdl_wait();
     if (warp == L.groups * W) {
         const RowView views[2] = {p.in[0], p.in[1]};
+        withhold_bytes(s, p.withhold);
         produce<2>(s, L, c, views, 2, p.status, p.wait_ns);
         return;
     }
@@ -317,6 +326,7 @@ __global__ void __launch_bounds__(kDnThreads, 1)
     pdl_wait();
     if (warp == L.groups * W) {
         const RowView views[3] = {p.in[0], p.in[1], p.in[2]};
+        withhold_bytes(s, p.withhold);
         produce<3>(s, L, c, views, L.ntens, p.status, p.wait_ns);
         return;
     }

@@ -15,7 +15,7 @@ extern "C" {
  * Sets, for the calls of cake_block.h that this host thread makes from now on,
  * the limit of every wait in their kernels (1 to 1000000 microseconds), and
  * whether a part of what every CTA (of a pair, the first) of the gated block's
- * products copies first never comes.  wait_limit_us = 0 with withhold = 0
+ * products and of the norm after dropout copies first never comes.  wait_limit_us = 0 with withhold = 0
  * restores the ordinary limit.  Anything else is CAKE_ERR_INVALID.  Every such
  * wait ends by its limit, the kernels return, and
  * cake_rmsnorm_device_status() gives CAKE_ERR_TIMEOUT.
