@@ -45,8 +45,8 @@ __all__ = [
     "CakeDropoutNormFunction", "cake_block_wait_test",
 ]
 
-_vp, _i64, _u64, _f32, _int, _size = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float, ctypes.c_int,
-                                      ctypes.c_size_t)
+_vp, _i64, _u64, _int, _size = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_int, ctypes.c_size_t
+_f32, _f64 = ctypes.c_float, ctypes.c_double
 
 
 def _bind(lib):
@@ -60,10 +60,10 @@ def _bind(lib):
         ("cake_rotary_bwd_workspace_size", _size, [_i64, _i64, _i64, _i64]),
         ("cake_rotary_bwd", _int, [_i64, _i64, _i64, _i64, T, T, R, T, T, _vp, _vp, _vp, _int, _vp, _int, T, T, _vp,
                                    _vp, _vp, _size, _vp]),
-        ("cake_dropout", _int, [S, T, T, _f32, _u64, _u64, _vp, T, _vp]),
-        ("cake_dropout_norm_fwd", _int, [S, T, T, _vp, _int, _f32, _u64, _u64, _vp, _f32, T, T, _vp, _vp]),
+        ("cake_dropout", _int, [S, T, T, _f64, _u64, _u64, _vp, T, _vp]),
+        ("cake_dropout_norm_fwd", _int, [S, T, T, _vp, _int, _f64, _u64, _u64, _vp, _f32, T, T, _vp, _vp]),
         ("cake_dropout_norm_bwd_workspace_size", _size, [S]),
-        ("cake_dropout_norm_bwd", _int, [S, T, T, T, _vp, _vp, _int, _f32, _u64, _u64, _vp, T, T, _vp, _vp, _size,
+        ("cake_dropout_norm_bwd", _int, [S, T, T, T, _vp, _vp, _int, _f64, _u64, _u64, _vp, T, T, _vp, _vp, _size,
                                          _vp]),
         ("cake_block_wait_test", _int, [ctypes.c_uint32, _int]),
         ("cake_dropout_norm_plan", _int, [S, _int, _int, ctypes.POINTER(_i64)]),

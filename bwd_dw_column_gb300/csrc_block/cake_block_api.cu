@@ -23,16 +23,16 @@ thread_local Waits t_waits;
 
 // ------------------------------------------------------------------ dropout
 
-cake_status check_p(float p, const uint64_t *rng)
+cake_status check_p(double p, const uint64_t *rng)
 {
-    if (!(p >= 0.0f && p <= 1.0f))
+    if (!(p >= 0.0 && p <= 1.0))
         return CAKE_ERR_INVALID;
     return (reinterpret_cast<uintptr_t>(rng) & 7u) ? CAKE_ERR_UNSUPPORTED : CAKE_OK;
 }
 
-DropoutRng dropout_rng(float p, uint64_t seed, uint64_t offset, const uint64_t *rng)
+DropoutRng dropout_rng(double p, uint64_t seed, uint64_t offset, const uint64_t *rng)
 {
-    const uint32_t cut = (uint32_t)std::nearbyint((double)p * 65536.0);
+    const uint32_t cut = (uint32_t)std::nearbyint(p * 65536.0);
     DropoutRng r{seed, offset, rng, cut, cut < 65536 ? (float)(65536.0 / (65536 - (int)cut)) : 0.0f, {}};
     for (uint32_t i = 0; i < 10; ++i) {
         r.keys[2 * i] = (uint32_t)seed + i * 0x9E3779B9u;
@@ -95,7 +95,7 @@ extern "C" cake_status cake_dropout_norm_plan(const cake_shape *shape, int tenso
     return CAKE_OK;
 }
 
-extern "C" cake_status cake_dropout(const cake_shape *shape, const cake_tensor *x, const cake_tensor *residual, float p,
+extern "C" cake_status cake_dropout(const cake_shape *shape, const cake_tensor *x, const cake_tensor *residual, double p,
                                     uint64_t seed, uint64_t offset, const uint64_t *rng, const cake_tensor *y,
                                     cake_stream_t stream)
 {
@@ -124,7 +124,7 @@ extern "C" cake_status cake_dropout(const cake_shape *shape, const cake_tensor *
 }
 
 extern "C" cake_status cake_dropout_norm_fwd(const cake_shape *shape, const cake_tensor *x, const cake_tensor *residual,
-                                             const void *w, cake_dtype w_dtype, float p, uint64_t seed,
+                                             const void *w, cake_dtype w_dtype, double p, uint64_t seed,
                                              uint64_t offset, const uint64_t *rng, float eps, const cake_tensor *y,
                                              const cake_tensor *h_new, float *rstd, cake_stream_t stream)
 {
@@ -183,7 +183,7 @@ extern "C" size_t cake_dropout_norm_bwd_workspace_size(const cake_shape *shape)
 
 extern "C" cake_status cake_dropout_norm_bwd(const cake_shape *shape, const cake_tensor *dy, const cake_tensor *dh,
                                              const cake_tensor *h_new, const float *rstd, const void *w,
-                                             cake_dtype w_dtype, float p, uint64_t seed, uint64_t offset,
+                                             cake_dtype w_dtype, double p, uint64_t seed, uint64_t offset,
                                              const uint64_t *rng, const cake_tensor *dx, const cake_tensor *dresidual,
                                              float *dw, void *workspace, size_t workspace_bytes, cake_stream_t stream)
 {

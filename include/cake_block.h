@@ -152,12 +152,12 @@ cake_status cake_rotary_bwd(int64_t tokens, int64_t q_heads, int64_t k_heads, in
  * adds 0, also where x is infinite or NaN.  y may be exactly x or residual,
  * and of cake_dropout_norm_fwd y and h_new may be exactly an input view.
  */
-cake_status cake_dropout(const cake_shape *shape, const cake_tensor *x, const cake_tensor *residual, float p,
+cake_status cake_dropout(const cake_shape *shape, const cake_tensor *x, const cake_tensor *residual, double p,
                          uint64_t seed, uint64_t offset, const uint64_t *rng, const cake_tensor *y,
                          cake_stream_t stream);
 
 cake_status cake_dropout_norm_fwd(const cake_shape *shape, const cake_tensor *x, const cake_tensor *residual,
-                                  const void *w, cake_dtype w_dtype, float p, uint64_t seed, uint64_t offset,
+                                  const void *w, cake_dtype w_dtype, double p, uint64_t seed, uint64_t offset,
                                   const uint64_t *rng, float eps, const cake_tensor *y,
                                   const cake_tensor *h_new, float *rstd, cake_stream_t stream);
 
@@ -166,7 +166,7 @@ size_t cake_dropout_norm_bwd_workspace_size(const cake_shape *shape);
 /* dh: NULL, or the gradient that reaches h_new directly. */
 cake_status cake_dropout_norm_bwd(const cake_shape *shape, const cake_tensor *dy, const cake_tensor *dh,
                                   const cake_tensor *h_new, const float *rstd, const void *w,
-                                  cake_dtype w_dtype, float p, uint64_t seed, uint64_t offset,
+                                  cake_dtype w_dtype, double p, uint64_t seed, uint64_t offset,
                                   const uint64_t *rng, const cake_tensor *dx, const cake_tensor *dresidual,
                                   float *dw, void *workspace, size_t workspace_bytes, cake_stream_t stream);
 

@@ -175,3 +175,25 @@ def test_gradients_against_differences(cake):
                 diff = (up - down) / 2e-4
                 # every term carries the roundings of g, u (saved) and of dg, du
                 assert abs(float(d[at]) - float(diff.sum())) <= 4 * 2.0 ** -8 * float(diff.abs().sum()) + 0.02
+
+
+def test_offsets_past_31_bits(cake):
+    """Outputs of more than 2^31 elements: the last rows, and columns of the weights' gradients."""
+    T, H, F = 270000, 64, 8192
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    x, wg, wu, gen = make(T, H, F)
+    h, g, u = cake.cake_gated_fwd(x, wg, wu)
+    for s in (slice(0, 40), slice(262140, 262150), slice(T - 40, T)):
+        want = ref.gated_fwd(x[s], wg, wu, "silu")
+        for name, v in (("h", h), ("g", g), ("u", u)):
+            check(name, v[s], *want[name])
+    del h
+    dh = torch.empty_like(g).normal_(generator=gen)
+    dx, dwg, dwu = cake.cake_gated_bwd(dh, x, g, u, wg, wu)
+    for s in (slice(0, 40), slice(T - 40, T)):
+        check("dx", dx[s], *ref.gated_bwd(dh[s], x[s], g[s], u[s], wg, wu, "silu")["dx"])
+    for s in (slice(0, 8), slice(F - 8, F)):
+        want = ref.gated_bwd(dh[:, s], x, g[:, s], u[:, s], wg[s], wu[s], "silu")
+        check("dw_gate", dwg[s], *want["dw_gate"])
+        check("dw_up", dwu[s], *want["dw_up"])

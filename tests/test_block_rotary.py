@@ -265,3 +265,45 @@ def test_several_axes_with_few_lanes_and_uneven_shares(cake):
             want, allow, dw64, edw = ref.rotary_bwd(y_, angle, v, rs, w, style)
             check("dv", dv, want, allow)
             check("dw", dw, dw64, edw)
+
+
+def test_autograd_without_keys(cake):
+    g = torch.Generator().manual_seed(9)
+    q, w = heads(g, 20, 3, 64).requires_grad_(), weights(g, 64, True).requires_grad_()
+    turns, _ = cake.cake_rotary_table((32,), device=DEV)
+    pos, dy = torch.arange(20, device=DEV), heads(g, 20, 3, 64)
+    y, none = cake.cake_rotary(q, None, pos, turns, None, w)
+    assert none is None
+    y.backward(dy)
+    rstd = cake.cake_rotary_fwd(q.detach(), None, pos, turns, None, w.detach())[2]
+    dq, _, dw, _ = cake.cake_rotary_bwd(dy, None, pos, turns, None, q.detach(), None, rstd, None, w.detach())
+    assert torch.equal(q.grad, dq) and torch.equal(w.grad, dw)
+
+
+def test_head_major_storage(cake):
+    """Heads that step past all tokens: [heads, T, D] in memory."""
+    g = torch.Generator().manual_seed(10)
+    q = heads(g, 5, 70, 64).transpose(0, 1)  # [70, 5, 64]
+    w = weights(g, 64, True)
+    turns, _ = cake.cake_rotary_table((32,), device=DEV)
+    pos = torch.arange(70, device=DEV)
+    want = cake.cake_rotary_fwd(q.contiguous(), None, pos, turns, None, w)
+    out = torch.empty(5, 70, 64, dtype=BF16, device=DEV).transpose(0, 1)
+    got = cake.cake_rotary_fwd(q, None, pos, turns, None, w, q_out=out)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    cake.cake_rotary_fwd(q, None, pos, turns, None, w, q_out=q)
+    assert torch.equal(q, want[0])
+
+
+def test_norm_of_zero_and_special_rows(cake):
+    """A row of zeros is zero (eps), infinities and NaN stay in their row."""
+    q = torch.ones(4, 2, 64, dtype=BF16, device=DEV)
+    q[1] = 0
+    q[2, 0, 5], q[3, 1, 7] = float("nan"), float("inf")
+    w = torch.ones(64, device=DEV)
+    turns, _ = cake.cake_rotary_table((32,), device=DEV)
+    y, _, rstd, _ = cake.cake_rotary_fwd(q, None, torch.arange(4, device=DEV), turns, None, w)
+    # 1 / sqrt(1e-6): the constant, the root and the quotient are rounded to FP32, 2.5 u in all
+    assert not bool(y[1].any()) and bool(((rstd.view(4, 2)[1] / 1000 - 1).abs() <= ref.RSTD_REL).all())
+    finite = torch.isfinite(y.float()).all(-1)
+    assert finite.tolist() == [[True, True], [True, True], [False, True], [True, False]]
