@@ -21,21 +21,23 @@ Devices, streams, workspaces, given outputs and errors are as in the module
 ``stream``; without a workspace from the caller it takes one from torch's
 allocator; tensors that a caller gives to be written count as changed in place.
 Every result is bitwise reproducible for equal inputs and shapes.
+
+The entry points check their tensors, allocate and call the ABI in the compiled
+module ``_cake_block`` (``csrc_block/cake_block_python.cpp``): small calls are
+the host's.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import math
-import struct
 
 import torch
 from torch.autograd.function import once_differentiable
-from torch.autograd.graph import increment_version
 
-from . import load_library
-from .step import (_check, _current, _dtype, _given, _like, _on, _ref, _rows, _rows_f32, _three, _weight,
-                   _workspace)
+from . import CakeError, load_library
+from .step import _check, _on, _rows, _three
 
 __all__ = [
     "cake_gated_fwd", "cake_gated_bwd", "cake_gated_bwd_workspace_size", "cake_gated", "CakeGatedFunction",
@@ -79,30 +81,25 @@ def cake_block_wait_test(wait_limit_us: int = 0, withhold: int = 0):
     _check(load_library().cake_block_wait_test(wait_limit_us, withhold), "cake_block_wait_test")
 
 
+_module = None
+
+
+def _native():
+    """The compiled entry points (loaded once)."""
+    global _module
+    if _module is None:
+        load_library()
+        try:
+            module = importlib.import_module("._cake_block", __package__)
+        except ImportError as e:
+            raise RuntimeError("_cake_block.so is missing or does not load: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        module.set_error(CakeError)
+        _module = module
+    return _module
+
+
 # ------------------------------------------------------------------------ gated
-
-_ACTS = {"silu": 0, "gelu": 1}
-
-
-def _act(act):
-    try:
-        return _ACTS[act]
-    except KeyError:
-        raise ValueError(f"act is 'silu' or 'gelu' (the tanh form), got {act!r}") from None
-
-
-def _matrix(t, rows, cols, what):
-    """A BF16 [rows, cols] matrix as a packed cake_tensor (None: NULL)."""
-    if t is None:
-        return None
-    if t.dim() != 2:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected a matrix")
-    return _ref(t, (rows, cols), what)
-
-
-def _new(rows, cols, like):
-    return torch.empty((rows, cols), dtype=torch.bfloat16, device=like.device)
-
 
 def cake_gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu", *, save: bool = True,
                    h: torch.Tensor | None = None, g: torch.Tensor | None = None, u: torch.Tensor | None = None,
@@ -114,26 +111,10 @@ def cake_gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, ac
     With ``save`` false g and u, which only the backward needs, are not written
     and come back as None.
     """
-    lib = load_library()
-    with _on(stream, x, w_gate, w_up, h, g, u):
-        if x.dim() != 2 or w_gate.dim() != 2:
-            raise ValueError(f"expected x [T, H] and w_gate [F, H], got {tuple(x.shape)} and {tuple(w_gate.shape)}")
-        (T, H), F = x.shape, w_gate.shape[0]
-        if not save and (g is not None or u is not None):
-            raise ValueError("g or u is given, but save is false")
-        given = _given(h, g, u)
-        if h is None:
-            h = _new(T, F, x)
-        if save:
-            g = _new(T, F, x) if g is None else g
-            u = _new(T, F, x) if u is None else u
-        st = lib.cake_gated_fwd(T, H, F, _matrix(x, T, H, "x"), _matrix(w_gate, F, H, "w_gate"),
-                                _matrix(w_up, F, H, "w_up"), _act(act), _matrix(h, T, F, "h"), _matrix(g, T, F, "g"),
-                                _matrix(u, T, F, "u"), _current())
-        _check(st, "cake_gated_fwd")
-        if given:
-            increment_version(given)
-    return h, g, u
+    if stream is not None:
+        with _on(stream, x):
+            return _native().gated_fwd(x, w_gate, w_up, act, save, h, g, u)
+    return _native().gated_fwd(x, w_gate, w_up, act, save, h, g, u)
 
 
 @functools.lru_cache(maxsize=256)
@@ -150,28 +131,10 @@ def cake_gated_bwd(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor, u: torch.
 
     dh: gradient of h, BF16 [T, F]; g and u as the forward gave them.
     """
-    lib = load_library()
-    with _on(stream, dh, x, g, u, w_gate, w_up, workspace, dx, dw_gate, dw_up):
-        if x.dim() != 2 or w_gate.dim() != 2:
-            raise ValueError(f"expected x [T, H] and w_gate [F, H], got {tuple(x.shape)} and {tuple(w_gate.shape)}")
-        (T, H), F = x.shape, w_gate.shape[0]
-        if (dx is not None and not need_dx) or ((dw_gate is not None or dw_up is not None) and not need_dw):
-            raise ValueError("an output is given for a gradient that is not asked for")
-        given = _given(dx, dw_gate, dw_up)
-        if need_dx and dx is None:
-            dx = _new(T, H, x)
-        if need_dw:
-            dw_gate = _new(F, H, x) if dw_gate is None else dw_gate
-            dw_up = _new(F, H, x) if dw_up is None else dw_up
-        workspace, ws, ws_bytes = _workspace(workspace, cake_gated_bwd_workspace_size(T, H, F), x.device)
-        st = lib.cake_gated_bwd(T, H, F, _matrix(dh, T, F, "dh"), _matrix(x, T, H, "x"), _matrix(g, T, F, "g"),
-                                _matrix(u, T, F, "u"), _matrix(w_gate, F, H, "w_gate"), _matrix(w_up, F, H, "w_up"),
-                                _act(act), _matrix(dx, T, H, "dx"), _matrix(dw_gate, F, H, "dw_gate"),
-                                _matrix(dw_up, F, H, "dw_up"), ws, ws_bytes, _current())
-        _check(st, "cake_gated_bwd")
-        if given:
-            increment_version(given)
-    return dx, dw_gate, dw_up
+    if stream is not None:
+        with _on(stream, x):
+            return _native().gated_bwd(dh, x, g, u, w_gate, w_up, act, need_dx, need_dw, workspace, dx, dw_gate, dw_up)
+    return _native().gated_bwd(dh, x, g, u, w_gate, w_up, act, need_dx, need_dw, workspace, dx, dw_gate, dw_up)
 
 
 class CakeGatedFunction(torch.autograd.Function):
@@ -205,10 +168,6 @@ def cake_gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: s
 
 # ----------------------------------------------------------------------- rotary
 
-_STYLES = {"half": 0, "adjacent": 1}
-_rotation = struct.Struct("=qqQQQixxxxqqixxxx").pack  # cake_rotary
-
-
 def cake_rotary_table(sections, base: float = 10000.0, *, shared: bool = False, freqs=None, device="cuda"):
     """(turns, axes) of a rotation: each pair's frequency and the axis whose position turns it.
 
@@ -237,51 +196,6 @@ def cake_rotary_table(sections, base: float = 10000.0, *, shared: bool = False, 
             torch.tensor(axes, dtype=torch.int32, device=device))
 
 
-def _heads(t, what):
-    if t is not None and t.dim() != 3:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected [T, heads, D]")
-    return t
-
-
-def _packed_rotation(positions, turns, axes, style, T):
-    """(the packed cake_rotary, the tensors that it points into)."""
-    if style not in _STYLES:
-        raise ValueError(f"style is 'half' or 'adjacent', got {style!r}")
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"positions are int32 or int64, got {positions.dtype}")
-    if positions.dim() not in (1, 2) or positions.shape[-1] != T:
-        raise ValueError(f"positions have shape {tuple(positions.shape)}, expected [{T}] or [axes, {T}]")
-    if turns.dtype is not torch.int64 or turns.dim() != 1:
-        raise TypeError("turns is an int64 tensor [pairs] (see cake_rotary_table)")
-    turns = turns.contiguous()
-    n_axes = positions.shape[0] if positions.dim() == 2 else 1
-    if axes is None:
-        if n_axes > 1:
-            raise ValueError("positions of several axes need each pair's axis")
-    else:
-        if axes.dtype is not torch.int32 or axes.shape != turns.shape:
-            raise ValueError("axes is an int32 tensor of turns' shape")
-        axes = axes.contiguous()
-    st = positions.stride()
-    packed = _rotation(turns.numel(), n_axes, turns.data_ptr(), 0 if axes is None else axes.data_ptr(),
-                       positions.data_ptr(), int(positions.dtype is torch.int64), st[0] if len(st) == 2 else 0, st[-1],
-                       _STYLES[style])
-    return packed, (turns, axes)
-
-
-def _norm_weights(k, w_q, w_k, D):
-    if k is not None and (w_q is None) != (w_k is None):
-        raise ValueError("queries and keys are normed both or neither: give w_q and w_k, or none")
-    if w_q is None:
-        return None, None
-    return _weight(w_q, D, "w_q"), None if k is None else _weight(w_k, D, "w_k")
-
-
-def _w(w):
-    """A weight's address and dtype (None: NULL)."""
-    return (None, 0) if w is None else (w.data_ptr(), _dtype(w))
-
-
 def cake_rotary_fwd(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, turns: torch.Tensor,
                     axes: torch.Tensor | None = None, w_q: torch.Tensor | None = None,
                     w_k: torch.Tensor | None = None, eps: float = 1e-6, *, style: str = "half",
@@ -297,34 +211,10 @@ def cake_rotary_fwd(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Te
     them there is no norm and rstd_q and rstd_k are None, else they are FP32
     [T * heads].  q_out may be q itself and k_out k itself.
     """
-    lib = load_library()
-    with _on(stream, q, k, positions, turns, axes, w_q, w_k, q_out, k_out, rstd_q, rstd_k):
-        T, nq, D = _heads(q, "q").shape
-        nk = 0 if k is None else _heads(k, "k").shape[1]
-        if k is None and (k_out is not None or rstd_k is not None):
-            raise ValueError("an output for keys is given without keys")
-        w_q, w_k = _norm_weights(k, w_q, w_k, D)
-        if w_q is None and (rstd_q is not None or rstd_k is not None):
-            raise ValueError("rstd is given, but there is no norm")
-        rotation, alive = _packed_rotation(positions, turns, axes, style, T)
-        given = _given(q_out, k_out, rstd_q, rstd_k)
-        if q_out is None:
-            q_out = _like(q)
-        if k is not None and k_out is None:
-            k_out = _like(k)
-        if w_q is not None:
-            if rstd_q is None:
-                rstd_q = torch.empty(T * nq, dtype=torch.float32, device=q.device)
-            if k is not None and rstd_k is None:
-                rstd_k = torch.empty(T * nk, dtype=torch.float32, device=q.device)
-        st = lib.cake_rotary_fwd(T, nq, nk, D, _ref(q, (T, nq, D), "q"), _ref(k, (T, nk, D), "k"), rotation, *_w(w_q),
-                                 *_w(w_k), eps, _ref(q_out, (T, nq, D), "q_out"), _ref(k_out, (T, nk, D), "k_out"),
-                                 None if rstd_q is None else _rows_f32(rstd_q, T * nq, "rstd_q"),
-                                 None if rstd_k is None else _rows_f32(rstd_k, T * nk, "rstd_k"), _current())
-        _check(st, "cake_rotary_fwd")
-        if given:
-            increment_version(given)
-    return q_out, k_out, rstd_q, rstd_k
+    if stream is not None:
+        with _on(stream, q):
+            return _native().rotary_fwd(q, k, positions, turns, axes, w_q, w_k, eps, style, q_out, k_out, rstd_q, rstd_k)
+    return _native().rotary_fwd(q, k, positions, turns, axes, w_q, w_k, eps, style, q_out, k_out, rstd_q, rstd_k)
 
 
 @functools.lru_cache(maxsize=256)
@@ -346,47 +236,12 @@ def cake_rotary_bwd(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.
     the forward's inputs and what it gave (with a norm only).  dq_out may be dq
     itself and dk_out dk itself.
     """
-    lib = load_library()
-    with _on(stream, dq, dk, positions, turns, axes, q, k, rstd_q, rstd_k, w_q, w_k, workspace, dq_out, dk_out, dw_q,
-             dw_k):
-        T, nq, D = _heads(dq, "dq").shape
-        nk = 0 if dk is None else _heads(dk, "dk").shape[1]
-        if dk is None and (dk_out is not None or dw_k is not None):
-            raise ValueError("an output for keys is given without keys")
-        w_q, w_k = _norm_weights(dk, w_q, w_k, D)
-        norm = w_q is not None
-        if norm and (q is None or rstd_q is None or (dk is not None and (k is None or rstd_k is None))):
-            raise ValueError("the norm's gradient needs the forward's inputs and rstd")
-        if not norm and (dw_q is not None or dw_k is not None):
-            raise ValueError("a weight's gradient is given, but there is no norm")
-        rotation, alive = _packed_rotation(positions, turns, axes, style, T)
-        given = _given(dq_out, dk_out, dw_q, dw_k)
-        if dq_out is None:
-            dq_out = _like(dq)
-        if dk is not None and dk_out is None:
-            dk_out = _like(dk)
-        if norm:
-            if dw_q is None:
-                dw_q = torch.empty(D, dtype=torch.float32, device=dq.device)
-            if dk is not None and dw_k is None:
-                dw_k = torch.empty(D, dtype=torch.float32, device=dq.device)
-            for t, what in ((dw_q, "dw_q"), (dw_k, "dw_k")):
-                if t is not None and (t.dtype is not torch.float32 or t.numel() != D or not t.is_contiguous()):
-                    raise ValueError(f"{what} must be a contiguous FP32 tensor of D elements")
-        size = cake_rotary_bwd_workspace_size(T, nq, nk, D) if norm else 0
-        workspace, ws, ws_bytes = _workspace(workspace, size, dq.device)
-        keys = norm and dk is not None
-        st = lib.cake_rotary_bwd(T, nq, nk, D, _ref(dq, (T, nq, D), "dq"), _ref(dk, (T, nk, D), "dk"), rotation,
-                                 _ref(q if norm else None, (T, nq, D), "q"), _ref(k if keys else None, (T, nk, D), "k"),
-                                 _rows_f32(rstd_q, T * nq, "rstd_q") if norm else None,
-                                 _rows_f32(rstd_k, T * nk, "rstd_k") if keys else None, *_w(w_q), *_w(w_k),
-                                 _ref(dq_out, (T, nq, D), "dq_out"), _ref(dk_out, (T, nk, D), "dk_out"),
-                                 dw_q.data_ptr() if norm else None, dw_k.data_ptr() if keys else None, ws, ws_bytes,
-                                 _current())
-        _check(st, "cake_rotary_bwd")
-        if given:
-            increment_version(given)
-    return dq_out, dk_out, dw_q, dw_k
+    if stream is not None:
+        with _on(stream, dq):
+            return _native().rotary_bwd(dq, dk, positions, turns, axes, q, k, rstd_q, rstd_k, w_q, w_k, style, workspace,
+                                    dq_out, dk_out, dw_q, dw_k)
+    return _native().rotary_bwd(dq, dk, positions, turns, axes, q, k, rstd_q, rstd_k, w_q, w_k, style, workspace,
+                                    dq_out, dk_out, dw_q, dw_k)
 
 
 class CakeRotaryFunction(torch.autograd.Function):
@@ -427,16 +282,6 @@ def cake_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor
 
 # ---------------------------------------------------------------------- dropout
 
-def _random(seed):
-    """(host seed, address of a device seed and offset or None) of a number or an int64 tensor of two."""
-    if isinstance(seed, torch.Tensor):
-        if seed.dtype is not torch.int64 or seed.numel() != 2 or not seed.is_contiguous():
-            raise ValueError("a seed on the device is a contiguous int64 tensor of two: the seed, and a number added to "
-                             "offset")
-        return 0, seed.data_ptr()
-    return int(seed), None
-
-
 def _on_device(seed):
     return seed if isinstance(seed, torch.Tensor) else None
 
@@ -452,20 +297,10 @@ def cake_dropout_fwd(x: torch.Tensor, p: float, seed, offset: int = 0, residual:
     of two on the device, the seed and a number that is added to offset, which
     a captured graph reads anew at each replay.  y may be x or residual.
     """
-    lib = load_library()
-    with _on(stream, x, residual, y, _on_device(seed)):
-        T, nh, H = _rows(x)
-        size = x.shape
-        host, rng = _random(seed)
-        given = _given(y)
-        if y is None:
-            y = _like(x)
-        st = lib.cake_dropout(_three(T, nh, H), _ref(x, size, "x"), _ref(residual, size, "residual"), p, host,
-                              int(offset), rng, _ref(y, size, "y"), _current())
-        _check(st, "cake_dropout")
-        if given:
-            increment_version(given)
-    return y
+    if stream is not None:
+        with _on(stream, x):
+            return _native().dropout(x, p, seed, offset, residual, y)
+    return _native().dropout(x, p, seed, offset, residual, y)
 
 
 def cake_dropout_bwd(dy: torch.Tensor, p: float, seed, offset: int = 0, *, dx: torch.Tensor | None = None,
@@ -508,26 +343,10 @@ def cake_dropout_norm_fwd(x: torch.Tensor, residual: torch.Tensor, w: torch.Tens
     [T, nh, H]; w: [H] BF16 or FP32; p, seed, offset: see ``cake_dropout_fwd``.
     y and h_new may be x or residual themselves.
     """
-    lib = load_library()
-    with _on(stream, x, residual, w, y, h_new, rstd, _on_device(seed)):
-        T, nh, H = _rows(x)
-        size, rows = x.shape, T * nh
-        w = _weight(w, H, "w")
-        host, rng = _random(seed)
-        given = _given(y, h_new, rstd)
-        if y is None:
-            y = _like(x)
-        if h_new is None:
-            h_new = _like(x)
-        if rstd is None:
-            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-        st = lib.cake_dropout_norm_fwd(_three(T, nh, H), _ref(x, size, "x"), _ref(residual, size, "residual"),
-                                       w.data_ptr(), _dtype(w), p, host, int(offset), rng, eps, _ref(y, size, "y"),
-                                       _ref(h_new, size, "h_new"), _rows_f32(rstd, rows, "rstd"), _current())
-        _check(st, "cake_dropout_norm_fwd")
-        if given:
-            increment_version(given)
-    return y, h_new, rstd
+    if stream is not None:
+        with _on(stream, x):
+            return _native().dropout_norm_fwd(x, residual, w, p, seed, offset, eps, y, h_new, rstd)
+    return _native().dropout_norm_fwd(x, residual, w, p, seed, offset, eps, y, h_new, rstd)
 
 
 @functools.lru_cache(maxsize=256)
@@ -549,30 +368,10 @@ def cake_dropout_norm_bwd(dy: torch.Tensor, h_new: torch.Tensor, rstd: torch.Ten
     dy: gradient of y; dh: that reaching h_new directly, or None; h_new and rstd
     as the forward gave them, p, seed and offset as it took them.
     """
-    lib = load_library()
-    with _on(stream, dy, h_new, rstd, w, dh, workspace, dx, dresidual, dw, _on_device(seed)):
-        T, nh, H = _rows(dy)
-        size, rows = dy.shape, T * nh
-        w = _weight(w, H, "w")
-        host, rng = _random(seed)
-        given = _given(dx, dresidual, dw)
-        if dx is None:
-            dx = _like(dy)
-        if dresidual is None:
-            dresidual = _like(dy)
-        if dw is None:
-            dw = torch.empty(H, dtype=torch.float32, device=dy.device)
-        elif dw.dtype is not torch.float32 or dw.numel() != H or not dw.is_contiguous():
-            raise ValueError("dw must be a contiguous FP32 tensor of H elements")
-        workspace, ws, ws_bytes = _workspace(workspace, _dropout_norm_bwd_bytes(T, nh, H), dy.device)
-        st = lib.cake_dropout_norm_bwd(_three(T, nh, H), _ref(dy, size, "dy"), _ref(dh, size, "dh"),
-                                       _ref(h_new, size, "h_new"), _rows_f32(rstd, rows, "rstd"), w.data_ptr(),
-                                       _dtype(w), p, host, int(offset), rng, _ref(dx, size, "dx"),
-                                       _ref(dresidual, size, "dresidual"), dw.data_ptr(), ws, ws_bytes, _current())
-        _check(st, "cake_dropout_norm_bwd")
-        if given:
-            increment_version(given)
-    return dresidual, dx, dw
+    if stream is not None:
+        with _on(stream, dy):
+            return _native().dropout_norm_bwd(dy, h_new, rstd, w, p, seed, offset, dh, workspace, dx, dresidual, dw)
+    return _native().dropout_norm_bwd(dy, h_new, rstd, w, p, seed, offset, dh, workspace, dx, dresidual, dw)
 
 
 class CakeDropoutNormFunction(torch.autograd.Function):

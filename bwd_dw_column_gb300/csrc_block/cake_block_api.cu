@@ -174,11 +174,7 @@ extern "C" size_t cake_dropout_norm_bwd_workspace_size(const cake_shape *shape)
     uint32_t rows = 0;
     if (check_shape(shape, &rows) != CAKE_OK || rows == 0)
         return 0;
-    // the plan depends on the number of staged tensors: room for either
-    int ctas = 0;
-    for (int ntens = 2; ntens <= 3; ++ntens)
-        ctas = std::max(ctas, dropout_norm_plan((int)shape->hidden, rows, ntens, true).ctas);
-    return (size_t)ctas * shape->hidden * sizeof(float2);
+    return (size_t)(rows < (uint32_t)kSMsBlock ? rows : kSMsBlock) * shape->hidden * sizeof(float2); // a CTA an SM
 }
 
 extern "C" cake_status cake_dropout_norm_bwd(const cake_shape *shape, const cake_tensor *dy, const cake_tensor *dh,

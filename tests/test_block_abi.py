@@ -4,17 +4,18 @@ ranges are refused before any launch.  No call here reaches a kernel."""
 import ctypes
 import os
 import re
+import struct
 
 import pytest
 import torch
 
-from bwd_dw_column_gb300.block import _rotation
 from bwd_dw_column_gb300.step import _three
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
 MB = 1 << 20
 NAN = float("nan")
+_rotation = struct.Struct("=qqQQQixxxxqqixxxx").pack  # cake_rotary
 
 
 @pytest.fixture(scope="module")
