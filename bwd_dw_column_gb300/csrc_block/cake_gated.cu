@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
                 mbar_arrive_remote(map_to_rank(tempty + 8 * acc, 0));
         }
         if (lane == 0)
-            store_wait_all();
+            store_wait_read<0>(); // (the launch's end completes the writes)
     }
     if (!ok) {
         // Nothing of the pair is left in flight when its CTAs leave: copies of
@@ -362,6 +362,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
 // ---------------------------------------------------------------- few tokens
 
 constexpr int kFewThreads = 256;
+// GB300, pairs of CTAs against this kernel: 4096 to 8192 at 64 tokens 29 us and 26,
+// at 128 30 and 30.5; 1024 to 1024 10.3 and 7.3, 10.5 and 9.5.
 constexpr int kFewMostTokens = 128;
 constexpr int kFewWeights = 32768; // of a stage: 128 rows of each weight, 64 k
 
@@ -381,47 +383,56 @@ struct FewParams {
     int withhold;
 };
 
-// Outputs from the cluster's sums: every one is two neighbours of f, and `first`
-// and every `step`-th after it are this thread's, U of them with all their
-// parts on their way at once.
-template <int U>
+// Outputs from the cluster's sums: every one is four neighbours of f, `first`
+// and every `step`-th after it are this thread's, U of them with the parts of R
+// CTAs on their way at once.
+template <int U, int R>
 __device__ __forceinline__ void few_outputs(const FewParams &P, uint32_t smem, int f0, int first, int step, int C)
 {
-    const int total = P.T * 64;
+    const int total = P.T * 32; // [n][128] in fours, in the order of i
     for (int i0 = first; i0 < total; i0 += U * step) {
-        float2 g[U], u[U];
+        float4 g[U], u[U];
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            g[k] = u[k] = make_float2(0.f, 0.f);
-        for (int r = 0; r < C; ++r) { // in the order of k
-            float2 x[U], y[U];
-            const uint32_t from = map_to_rank(smem, r);
+            g[k] = u[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r0 = 0; r0 < C; r0 += R) { // in the order of k
+            float4 x[R][U], y[R][U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const uint32_t at = from + 8 * (uint32_t)min(i0 + k * step, total - 1); // [n][128] in the order of i
-                x[k] = ld_cluster_f2(at);
-                y[k] = ld_cluster_f2(at + (uint32_t)P.n * 512);
-            }
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                g[k] = add2(g[k], x[k]);
-                u[k] = add2(u[k], y[k]);
-            }
+                for (int k = 0; k < U; ++k)
+                    if (r0 + r < C && i0 + k * step < total) {
+                        const uint32_t at = map_to_rank(smem, r0 + r) + 16 * (uint32_t)(i0 + k * step);
+                        x[r][k] = ld_cluster_f4(at);
+                        y[r][k] = ld_cluster_f4(at + (uint32_t)P.n * 512);
+                    }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    if (r0 + r < C) {
+                        const float4 a = x[r][k], b = y[r][k];
+                        g[k] = make_float4(g[k].x + a.x, g[k].y + a.y, g[k].z + a.z, g[k].w + a.w);
+                        u[k] = make_float4(u[k].x + b.x, u[k].y + b.y, u[k].z + b.z, u[k].w + b.w);
+                    }
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const int i = i0 + k * step, t = i >> 6, f = f0 + 2 * (i & 63);
-            if (i >= total || f >= P.F)
+            const int i = i0 + k * step, t = i >> 5, f = f0 + 4 * (i & 31);
+            if (i >= total || f >= P.F) // (F is a multiple of 8)
                 continue;
             float d;
-            const float a = activation<false>(g[k].x, P.gelu, d), b = activation<false>(g[k].y, P.gelu, d);
-            auto put = [&](uint16_t *m, int64_t stride, float lo, float hi) {
-                *reinterpret_cast<uint32_t *>(m + (int64_t)t * stride + f) = pack_bf16(lo, hi);
+            const float h0 = activation<false>(g[k].x, P.gelu, d) * u[k].x,
+                        h1 = activation<false>(g[k].y, P.gelu, d) * u[k].y,
+                        h2 = activation<false>(g[k].z, P.gelu, d) * u[k].z,
+                        h3 = activation<false>(g[k].w, P.gelu, d) * u[k].w;
+            auto put = [&](uint16_t *m, int64_t stride, float a, float b, float c, float e) {
+                *reinterpret_cast<uint2 *>(m + (int64_t)t * stride + f) = make_uint2(pack_bf16(a, b), pack_bf16(c, e));
             };
-            put(P.h, P.h_stride, a * u[k].x, b * u[k].y);
+            put(P.h, P.h_stride, h0, h1, h2, h3);
             if (P.g) {
-                put(P.g, P.g_stride, g[k].x, g[k].y);
-                put(P.u, P.u_stride, u[k].x, u[k].y);
+                put(P.g, P.g_stride, g[k].x, g[k].y, g[k].z, g[k].w);
+                put(P.u, P.u_stride, u[k].x, u[k].y, u[k].z, u[k].w);
             }
         }
     }
@@ -519,10 +530,11 @@ __global__ void __launch_bounds__(kFewThreads) gated_few_kernel(const __grid_con
     tc_fence_after();
     const bool bad = s_bad;
     float *part = reinterpret_cast<float *>(smem_raw); // [gate, up][n][128]
-    if (warp >= 4 && !bad) {
-        const int f = (warp - 4) * 32 + lane;
-        const uint32_t t = tmem + ((uint32_t)((warp - 4) * 32) << 16);
-        for (int c = 0; c < 2 * P.n; c += 16) {
+    if (!bad) {
+        // a warp's lanes are a quarter of the rows; two warps share it by columns
+        const int f = (warp & 3) * 32 + lane, half = warp >> 2;
+        const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        for (int c = half * P.n; c < (half + 1) * P.n; c += 16) {
             uint32_t v[16];
             if (k1 > k0) {
                 tmem_ld16(t + c, v);
@@ -541,11 +553,11 @@ __global__ void __launch_bounds__(kFewThreads) gated_few_kernel(const __grid_con
     __syncwarp();
     cluster_sync_all();
     if (!bad) {
-        const int step = C * kFewThreads, first = rank * kFewThreads + (int)threadIdx.x;
-        if (P.T * 64 <= step)
-            few_outputs<1>(P, smem, f0, first, step, C);
-        else
-            few_outputs<4>(P, smem, f0, first, step, C);
+        const int first = rank * kFewThreads + (int)threadIdx.x, step = C * kFewThreads;
+        if (C == 1) // (100 tokens, 64 to 128: 6.9 us against 9.7 with one output at a time)
+            few_outputs<4, 1>(P, smem, f0, first, step, C);
+        else // (100 tokens, 696 to 904, clusters of 5: 9.0 us against 9.9 with two)
+            few_outputs<1, 4>(P, smem, f0, first, step, C);
     }
     __syncwarp();
     cluster_sync_all(); // no CTA leaves while another reads its sums

@@ -66,6 +66,17 @@ __device__ __forceinline__ void store_wait_read()
 
 __device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// Load a float4 from a CTA of the cluster's shared memory.
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+
 // ------------------------------------------------------------ tensor memory
 
 // G: 1, or 2 for a pair of CTAs (one warp of each takes part).
