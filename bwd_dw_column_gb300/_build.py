@@ -113,7 +113,7 @@ def _compile_module(nvcc: str) -> str:
 
 def _link_module(obj: str) -> None:
     tmp = PYTHON_MODULE + f".tmp{os.getpid()}"
-    _run(["g++", "-shared", "-o", tmp, obj, f"-L{_torch_dir('lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+    _run(["g++", "-shared", "-o", tmp, obj, f"-L{_torch_dir('lib')}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
           f"-L{HERE}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"], "linking _cake_block.so")
     os.replace(tmp, PYTHON_MODULE)
 
