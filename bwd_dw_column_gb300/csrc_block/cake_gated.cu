@@ -65,14 +65,17 @@ constexpr int kPairThreads = 128 + 32 * kPairWriters;
 constexpr int kPairs = kSMsBlock / 2;
 constexpr int kPairGroup = 8;                 // tiles of m that neighbouring units share, for their reuse in L2
 
-// Products out[half] = sum over segments and k of a b.
+// Products out[half] = sum over segments, k and an a's parts of a b.
 struct PairProblem {
-    CUtensorMap a[2], b[2], out[2];
+    CUtensorMap a[4], b[2], out[2];
     int a_mn, b_mn;       // an operand's rows lie along k in memory
     int segments, halves; // a, b by segment; or a, out by half
+    int parts;            // a is a sum of so many matrices: a[segment or half][part]
+    int stack;            // instead: two of at most 64 rows, above one another in the tile
     int kblocks;          // blocks of 64 k of a segment
     int tiles_m, tiles_n; // of a half
-    int splits, per_split; // of the sum over all segments: FP32 parts in out[.][split] where splits > 1
+    int splits, per_split; // of the sum over all segments
+    int planes;           // FP32 parts of the outputs in out[.][plane] (splits, twice those with stack); 0: none
     int units;
     int rows, cols;       // of a half
 };
@@ -126,7 +129,7 @@ __device__ __forceinline__ bool pair_unit(const PairParams &P, int q, int i, Pai
     r.m0 = (first + t % size) * 256;
     r.n0 = t / size * (GATED ? 128 : 256);
     r.k0 = r.split * p.per_split;
-    r.k1 = min(r.k0 + p.per_split, p.kblocks * p.segments);
+    r.k1 = min(r.k0 + p.per_split, p.kblocks * p.segments * p.parts);
     return true;
 }
 
@@ -209,12 +212,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
                                               2 * kPairStage + (P.withhold && issued == 0 ? 16 : 0));
                     const uint32_t bar = map_to_rank(full + 8 * st, 0);
                     const uint32_t sa = smem + st * kPairStage, sb = sa + kPairHalf;
-                    const int seg = kb >= p.kblocks, k = (kb - seg * p.kblocks) * 64;
-                    const CUtensorMap *ma = &p.a[p.segments == 2 ? seg : u.half];
+                    // (the parts of a block follow one another: the second finds b in L2)
+                    const int part = p.parts == 2 ? kb & 1 : 0, block = p.parts == 2 ? kb >> 1 : kb;
+                    const int seg = block >= p.kblocks, k = (block - seg * p.kblocks) * 64;
+                    const CUtensorMap *ma = &p.a[(p.segments == 2 ? seg : u.half) * p.parts + part];
                     const int m = u.m0 + 128 * rank;
                     if (p.a_mn) {
                         tile_g2s_pair(sa, ma, m, k, bar);
                         tile_g2s_pair(sa + 8192, ma, m + 64, k, bar);
+                    } else if (!GATED && p.stack) { // (the second CTA's rows lie outside: zeros)
+                        tile_g2s_pair(sa, &p.a[2 * seg], k, 128 * rank, bar);
+                        tile_g2s_pair(sa + 8192, &p.a[2 * seg + 1], k, 128 * rank, bar);
                     } else {
                         tile_g2s_pair(sa, ma, k, m, bar);
                     }
@@ -283,7 +291,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
                 break;
             tc_fence_after();
             const uint32_t t = tmem + ((uint32_t)(quad * 32) << 16) + 256 * acc;
-            const int row = u.m0 + 128 * (int)rank + 32 * quad;
+            int row = u.m0 + 128 * (int)rank + 32 * quad, plane = u.split;
+            if (!GATED && p.stack && row >= 64 && row < 128) {
+                row -= 64;
+                plane += p.splits;
+            }
             const bool rows = row < p.rows;
             constexpr int kSide = GATED ? 2 : 4; // chunks of 32 columns
             for (int c = kSide * side; c < kSide * (side + 1); ++c) {
@@ -318,7 +330,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
                     uint32_t v[32];
                     tmem_ld32(t + 32 * c, v);
                     tmem_wait_ld();
-                    if (p.splits == 1) {
+                    if (p.planes == 0) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             w[j] = pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
@@ -331,7 +343,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
                                 w[j] = v[16 * s + j];
                             if (col + 16 * s < p.cols)
                                 box.put(w, lane,
-                                        [&](uint32_t at) { tile_s2g(&p.out[u.half], col + 16 * s, row, u.split, at); });
+                                        [&](uint32_t at) { tile_s2g(&p.out[u.half], col + 16 * s, row, plane, at); });
                         }
                     }
                 }
@@ -573,10 +585,17 @@ struct GatedGradParams {
     const uint16_t *dh, *g, *u;
     int64_t dh_stride, g_stride, u_stride;
     uint16_t *dg, *du;     // rows of 8 nvec
+    int64_t rest;          // bytes from there to what their rounding left; 0: not wanted
     uint32_t nvec;
     uint64_t vecs;
     int gelu;
 };
+
+__device__ __forceinline__ float2 rest_of(float2 v, uint32_t rounded)
+{
+    const float2 r = bf2(rounded);
+    return make_float2(isfinite(r.x) ? v.x - r.x : 0.f, isfinite(r.y) ? v.y - r.y : 0.f);
+}
 
 __global__ void __launch_bounds__(kGradGuThreads) gated_grad_kernel(const __grid_constant__ GatedGradParams p)
 {
@@ -589,25 +608,34 @@ __global__ void __launch_bounds__(kGradGuThreads) gated_grad_kernel(const __grid
         const uint4 d = __ldcs(reinterpret_cast<const uint4 *>(p.dh + t * p.dh_stride + c));
         const uint4 g = __ldcs(reinterpret_cast<const uint4 *>(p.g + t * p.g_stride + c));
         const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p.u + t * p.u_stride + c));
-        uint32_t og[4], ou[4];
+        uint32_t og[4], ou[4], rg[4], ru[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float2 dq = bf2(word(d, q)), gq = bf2(word(g, q)), uq = bf2(word(u, q));
             float d0, d1;
             const float a0 = activation<true>(gq.x, p.gelu, d0), a1 = activation<true>(gq.y, p.gelu, d1);
-            og[q] = pack_bf16(dq.x * uq.x * d0, dq.y * uq.y * d1);
-            ou[q] = pack_bf16(dq.x * a0, dq.y * a1);
+            const float2 vg = make_float2(dq.x * uq.x * d0, dq.y * uq.y * d1), vu = make_float2(dq.x * a0, dq.y * a1);
+            og[q] = pack2(vg);
+            ou[q] = pack2(vu);
+            // (the differences are exact; of what is not finite there is none)
+            rg[q] = pack2(rest_of(vg, og[q]));
+            ru[q] = pack2(rest_of(vu, ou[q]));
         }
-        reinterpret_cast<uint4 *>(p.dg)[i] = make_uint4(og[0], og[1], og[2], og[3]);
-        reinterpret_cast<uint4 *>(p.du)[i] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+        uint4 *const dg = reinterpret_cast<uint4 *>(p.dg) + i, *const du = reinterpret_cast<uint4 *>(p.du) + i;
+        *dg = make_uint4(og[0], og[1], og[2], og[3]);
+        *du = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+        if (p.rest) {
+            dg[p.rest / 16] = make_uint4(rg[0], rg[1], rg[2], rg[3]);
+            du[p.rest / 16] = make_uint4(ru[0], ru[1], ru[2], ru[3]);
+        }
     }
 }
 
 // Sum of a split product's FP32 parts in their order, rounded to BF16.
 struct JoinParams {
-    const float *part[2];  // [splits] planes of rows x cols, dense
-    int64_t plane;         // elements from part to part
-    int splits;
+    const float *part[2];  // [planes] of rows x cols, dense
+    int64_t plane;         // elements from one to the next
+    int planes;
     uint16_t *out[2];
     int64_t stride[2];
     uint32_t nvec;
@@ -622,7 +650,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < p.vecs; i += (uint64_t)gridDim.x * 256) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
         const float *at = p.part[o] + i * 8;
-        for (int s = 0; s < p.splits; ++s, at += p.plane) {
+        for (int s = 0; s < p.planes; ++s, at += p.plane) {
             const float4 x = __ldcs(reinterpret_cast<const float4 *>(at)),
                          y = __ldcs(reinterpret_cast<const float4 *>(at) + 1);
             a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
@@ -795,7 +823,7 @@ cudaError_t launch_gated_fwd(const GatedFwdCall &c, cudaStream_t stream)
         !operand_map(&p.b[1], c.w_up, 128) || !output_map(&p.out[0], c.h) ||
         (c.g.data && (!output_map(&P.g, c.g) || !output_map(&P.u, c.u))))
         return cudaErrorInvalidValue;
-    p.segments = p.halves = p.splits = 1;
+    p.segments = p.halves = p.parts = p.splits = 1;
     p.kblocks = p.per_split = ceil_div(c.H, 64);
     p.tiles_m = ceil_div(c.T, 256);
     p.tiles_n = ceil_div(c.F, 128);
@@ -815,15 +843,16 @@ cudaError_t launch_gated_fwd(const GatedFwdCall &c, cudaStream_t stream)
 // are more (BF16; FP32 parts, which are read again).
 static int64_t unit_time(const PairProblem &p)
 {
-    const int out = p.splits > 1 ? 8 : 4;
+    const int out = p.planes ? 8 : 4;
     return p.per_split + (p.per_split < out ? out - p.per_split : 0) + 1;
 }
 
 static void split_sum(PairProblem &p, int splits)
 {
-    const int kblocks = p.kblocks * p.segments;
+    const int kblocks = p.kblocks * p.segments * p.parts;
     p.per_split = (kblocks + splits - 1) / splits;
     p.splits = (kblocks + p.per_split - 1) / p.per_split;
+    p.planes = p.stack ? 2 * p.splits : p.splits > 1 ? p.splits : 0;
     p.units = p.halves * p.tiles_m * p.tiles_n * p.splits;
 }
 
@@ -837,13 +866,13 @@ static void split_sums(PairProblem &a, PairProblem &b)
     static constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16};
     for (int i : kSplits)
         for (int k : kSplits) {
-            if ((i > 1 && (a.kblocks * a.segments < 4 * i || a.halves * a.tiles_m * a.tiles_n >= kPairs)) ||
-                (k > 1 && (b.kblocks * b.segments < 4 * k || b.halves * b.tiles_m * b.tiles_n >= kPairs)))
+            if ((i > 1 && (a.kblocks * a.segments * a.parts < 4 * i || a.halves * a.tiles_m * a.tiles_n >= kPairs)) ||
+                (k > 1 && (b.kblocks * b.segments * b.parts < 4 * k || b.halves * b.tiles_m * b.tiles_n >= kPairs)))
                 continue;
             split_sum(a, i);
             split_sum(b, k);
             PairParams P;
-            const int64_t parts = (a.splits > 1 ? a.units : 0) + (b.splits > 1 ? b.units : 0);
+            const int64_t parts = (a.planes ? a.units : 0) + (b.planes ? b.units : 0);
             const int64_t t = 16 * share_units(P, a.units, unit_time(a), b.units, unit_time(b)) + parts;
             if (best < 0 || t < best) {
                 best = t;
@@ -855,8 +884,17 @@ static void split_sums(PairProblem &a, PairProblem &b)
     split_sum(b, sb);
 }
 
+// Tokens up to which the gradients of g and u go into the products as two BF16
+// matrices each, the rounded values and the rounded rest (2^-16 of the value):
+// with few tokens a handful of large gradients carries a result, and the error of
+// their one rounding does not average out (2 tokens, 2.7e-3 of the result's norm
+// against 1.7e-3 of its own rounding).  The weights' bytes bound these calls; for
+// dx both lie in one tile, which takes no more products.
+constexpr int64_t kTwoPartTokens = 64;
+
 struct BwdPlan {
     PairProblem dx, dw;
+    int parts;
     size_t gu_bytes, dx_bytes, dw_bytes;
 };
 
@@ -870,6 +908,9 @@ static const BwdPlan &plan_bwd(int64_t T, int64_t H, int64_t F)
         return b;
     b = BwdPlan{};
     PairProblem &x = b.dx, &w = b.dw;
+    b.parts = w.parts = T <= kTwoPartTokens ? 2 : 1;
+    x.parts = 1;
+    x.stack = b.parts == 2;
     x.segments = 2;
     x.halves = 1;
     x.a_mn = 0;
@@ -889,8 +930,8 @@ static const BwdPlan &plan_bwd(int64_t T, int64_t H, int64_t F)
     w.cols = (int)H;
     split_sums(x, w);
     b.gu_bytes = ((size_t)T * F * 2 + 255) & ~(size_t)255;
-    b.dx_bytes = x.splits > 1 ? ((size_t)x.splits * T * H * 4 + 255) & ~(size_t)255 : 0;
-    b.dw_bytes = w.splits > 1 ? ((size_t)w.splits * 2 * F * H * 4 + 255) & ~(size_t)255 : 0;
+    b.dx_bytes = ((size_t)x.planes * T * H * 4 + 255) & ~(size_t)255;
+    b.dw_bytes = ((size_t)w.planes * 2 * F * H * 4 + 255) & ~(size_t)255;
     last[0] = T;
     last[1] = H;
     last[2] = F;
@@ -900,7 +941,7 @@ static const BwdPlan &plan_bwd(int64_t T, int64_t H, int64_t F)
 size_t gated_bwd_workspace(int64_t T, int64_t H, int64_t F)
 {
     const BwdPlan &b = plan_bwd(T, H, F);
-    return 2 * b.gu_bytes + b.dx_bytes + b.dw_bytes;
+    return 2 * b.parts * b.gu_bytes + b.dx_bytes + b.dw_bytes;
 }
 
 static cudaError_t launch_join(const JoinParams &j, int outputs, cudaStream_t stream)
@@ -914,9 +955,18 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
 {
     const BwdPlan &b = plan_bwd(c.T, c.H, c.F);
     uint8_t *ws = c.workspace;
-    const Matrix dg{ws, c.T, c.F, c.F}, du{ws + b.gu_bytes, c.T, c.F, c.F};
-    float *part_x = reinterpret_cast<float *>(ws + 2 * b.gu_bytes);
-    float *part_w = reinterpret_cast<float *>(ws + 2 * b.gu_bytes + b.dx_bytes);
+    Matrix gu[4]; // dg's parts, du's parts
+    for (int i = 0; i < 2 * b.parts; ++i)
+        gu[i] = {ws + i * b.gu_bytes, c.T, c.F, c.F};
+    ws += 2 * b.parts * b.gu_bytes;
+    float *part_x = reinterpret_cast<float *>(ws);
+    float *part_w = reinterpret_cast<float *>(ws + b.dx_bytes);
+    const auto gu_maps = [&](PairProblem &p, int box_rows) {
+        bool ok = true;
+        for (int i = 0; i < 2 * b.parts; ++i)
+            ok = ok && operand_map(&p.a[i], gu[i], box_rows);
+        return ok;
+    };
     GatedGradParams q{};
     q.dh = (const uint16_t *)c.dh.data;
     q.g = (const uint16_t *)c.g.data;
@@ -924,8 +974,9 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
     q.dh_stride = c.dh.stride;
     q.g_stride = c.g.stride;
     q.u_stride = c.u.stride;
-    q.dg = (uint16_t *)dg.data;
-    q.du = (uint16_t *)du.data;
+    q.dg = (uint16_t *)gu[0].data;
+    q.du = (uint16_t *)gu[b.parts].data;
+    q.rest = b.parts == 2 ? (int64_t)b.gu_bytes : 0;
     q.nvec = (uint32_t)(c.F / 8);
     q.vecs = (uint64_t)c.T * q.nvec;
     q.gelu = c.gelu;
@@ -939,18 +990,17 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
     if (c.dx.data) {
         PairProblem &p = P.p[n++] = b.dx;
         const Matrix part{part_x, c.T, c.H, c.H};
-        if (!operand_map(&p.a[0], dg, 128) || !operand_map(&p.a[1], du, 128) || !operand_map(&p.b[0], c.w_gate, 64) ||
-            !operand_map(&p.b[1], c.w_up, 64) ||
-            !(p.splits > 1 ? parts_map(&p.out[0], part, c.T * c.H, p.splits) : output_map(&p.out[0], c.dx)))
+        if (!gu_maps(p, p.stack ? 64 : 128) || !operand_map(&p.b[0], c.w_gate, 64) || !operand_map(&p.b[1], c.w_up, 64) ||
+            !(p.planes ? parts_map(&p.out[0], part, c.T * c.H, p.planes) : output_map(&p.out[0], c.dx)))
             return cudaErrorInvalidValue;
     }
     if (c.dw_gate.data) {
         PairProblem &p = P.p[n++] = b.dw;
         const Matrix part_g{part_w, c.F, c.H, c.H}, part_u{part_w + c.F * c.H, c.F, c.H, c.H};
-        if (!operand_map(&p.a[0], dg, 64) || !operand_map(&p.a[1], du, 64) || !operand_map(&p.b[0], c.x, 64) ||
-            !(p.splits > 1 ? parts_map(&p.out[0], part_g, 2 * c.F * c.H, p.splits) &&
-                                 parts_map(&p.out[1], part_u, 2 * c.F * c.H, p.splits)
-                           : output_map(&p.out[0], c.dw_gate) && output_map(&p.out[1], c.dw_up)))
+        if (!gu_maps(p, 64) || !operand_map(&p.b[0], c.x, 64) ||
+            !(p.planes ? parts_map(&p.out[0], part_g, 2 * c.F * c.H, p.planes) &&
+                             parts_map(&p.out[1], part_u, 2 * c.F * c.H, p.planes)
+                       : output_map(&p.out[0], c.dw_gate) && output_map(&p.out[1], c.dw_up)))
             return cudaErrorInvalidValue;
     }
     share_units(P, P.p[0].units, unit_time(P.p[0]), n > 1 ? P.p[1].units : 0, n > 1 ? unit_time(P.p[1]) : 0);
@@ -958,23 +1008,23 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
     P.wait_ns = c.wait_ns;
     P.withhold = c.withhold;
     e = launch_cluster(gated_pair_kernel<false>, pair_grid(P), 2, kPairThreads, kPairSmem, stream, P);
-    if (e == cudaSuccess && c.dx.data && b.dx.splits > 1) {
+    if (e == cudaSuccess && c.dx.data && b.dx.planes) {
         JoinParams j{};
         j.part[0] = part_x;
         j.plane = c.T * c.H;
-        j.splits = b.dx.splits;
+        j.planes = b.dx.planes;
         j.out[0] = (uint16_t *)c.dx.data;
         j.stride[0] = c.dx.stride;
         j.nvec = (uint32_t)(c.H / 8);
         j.vecs = (uint64_t)c.T * j.nvec;
         e = launch_join(j, 1, stream);
     }
-    if (e == cudaSuccess && c.dw_gate.data && b.dw.splits > 1) {
+    if (e == cudaSuccess && c.dw_gate.data && b.dw.planes) {
         JoinParams j{};
         j.part[0] = part_w;
         j.part[1] = part_w + c.F * c.H;
         j.plane = 2 * c.F * c.H;
-        j.splits = b.dw.splits;
+        j.planes = b.dw.planes;
         j.out[0] = (uint16_t *)c.dw_gate.data;
         j.out[1] = (uint16_t *)c.dw_up.data;
         j.stride[0] = c.dw_gate.stride;

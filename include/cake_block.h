@@ -34,7 +34,7 @@ extern "C" {
 /* ---- gated feed-forward block --------------------------------------------
  *
  *   forward   g = x Wg^T, u = x Wu^T (FP32 sums), h = bf16(act(g) * u)
- *   backward  dg = bf16(dh * u * act'(g)), du = bf16(dh * act(g))
+ *   backward  dg = dh * u * act'(g), du = dh * act(g)
  *             dx = bf16(dg Wg + du Wu), dWg = bf16(dg^T x), dWu = bf16(du^T x)
  *
  * act: v * sigmoid(v) (CAKE_ACT_SILU), or
@@ -48,7 +48,9 @@ extern "C" {
  * The forward writes bf16(g) and bf16(u) too where g and u are given (both or
  * neither); h is computed from the FP32 sums.  The backward takes them as
  * they were written.  dg and du are rounded to BF16 because the tensor cores
- * multiply BF16; sums are FP32, those of a split sum added in a fixed order.
+ * multiply BF16 (with at most 64 tokens what this rounding leaves is multiplied
+ * too, so that they are as good as FP32); sums are FP32, those of a split sum
+ * added in a fixed order.
  * dx NULL leaves it out, and dw_gate and dw_up NULL (both or neither) those.
  */
 typedef enum { CAKE_ACT_SILU = 0, CAKE_ACT_GELU = 1 } cake_act;

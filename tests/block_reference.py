@@ -61,8 +61,10 @@ def _bf16_between(v, err):
     return mid, torch.maximum((mid - lo).abs(), (hi - mid).abs())
 
 
-def gated_bwd(dh, x, g, u, w_gate, w_up, kind):
-    """FP64 (dx, dw_gate, dw_up) of the BF16 gradients of g and u, with bounds."""
+def gated_bwd(dh, x, g, u, w_gate, w_up, kind, two=None):
+    """FP64 (dx, dw_gate, dw_up) of the BF16 gradients of g and u, with bounds; `two`: of the gradients as two BF16
+    matrices, the rounded values and the rounded rest, which is at most 2^-8 of the value, itself within 2^-8."""
+    two = x.shape[0] <= 64 if two is None else two
     dh, x, g, u, wg, wu = (t.double() for t in (dh, x, g, u, w_gate, w_up))
     a, da, rel = act(g, kind)
     # act' = s + v s (1 - s) z': each factor's error, and the cancellation of the two terms where v < 0;
@@ -70,9 +72,13 @@ def gated_bwd(dh, x, g, u, w_gate, w_up, kind):
     s = torch.sigmoid(g if kind == "silu" else 2 * math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3))
     dz = torch.ones_like(g) if kind == "silu" else 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * g ** 2)
     eda = 3 * (rel + 4 * U) * s * (1 + (g * dz).abs()) + 1e-36 * (1 + (g * dz).abs())
-    dg, edg = _bf16_between(dh * u * da, (dh * u).abs() * eda + 3 * U * (dh * u * da).abs())
-    du, edu = _bf16_between(dh * a, dh.abs() * ((rel + U) * a.abs() + 1e-36) + 2 * U * (dh * a).abs())
-    T, F = g.shape
+    dg, edg = dh * u * da, (dh * u).abs() * eda + 3 * U * (dh * u * da).abs()
+    du, edu = dh * a, dh.abs() * ((rel + U) * a.abs() + 1e-36) + 2 * U * (dh * a).abs()
+    if two:
+        edg, edu = edg + 2.0 ** -16 * dg.abs(), edu + 2.0 ** -16 * du.abs()
+    else:
+        (dg, edg), (du, edu) = _bf16_between(dg, edg), _bf16_between(du, edu)
+    T, F = (2 * n for n in g.shape) if two else g.shape  # terms of a sum, over both parts
     dx = dg @ wg + du @ wu
     ex = edg @ wg.abs() + edu @ wu.abs() + (mma_chain(2 * F) + 16) * U * (dg.abs() @ wg.abs() + du.abs() @ wu.abs())
     out = {"dx": (dx, rounded(dx, ex))}

@@ -192,8 +192,35 @@ def test_offsets_past_31_bits(cake):
     dh = torch.empty_like(g).normal_(generator=gen)
     dx, dwg, dwu = cake.cake_gated_bwd(dh, x, g, u, wg, wu)
     for s in (slice(0, 40), slice(T - 40, T)):
-        check("dx", dx[s], *ref.gated_bwd(dh[s], x[s], g[s], u[s], wg, wu, "silu")["dx"])
+        check("dx", dx[s], *ref.gated_bwd(dh[s], x[s], g[s], u[s], wg, wu, "silu", False)["dx"])
     for s in (slice(0, 8), slice(F - 8, F)):
         want = ref.gated_bwd(dh[:, s], x, g[:, s], u[:, s], wg[s], wu[s], "silu")
         check("dw_gate", dwg[s], *want["dw_gate"])
         check("dw_up", dwu[s], *want["dw_up"])
+
+
+def test_few_tokens_lose_nothing_to_a_rounding_of_the_gradients(cake):
+    """One token: a weight's gradient is a single product, which is rounded once (and off by FP32 roundings)."""
+    for T in (1, 2):
+        x, wg, wu, gen = make(T, 64, 1024)
+        g, u, dh = (matrix(gen, T, 1024) for _ in range(3))
+        dx, dwg, dwu = cake.cake_gated_bwd(dh, x, g, u, wg, wu)
+        a, da, _ = ref.act(g.double(), "silu")
+        for got, d in ((dwg, dh.double() * u.double() * da), (dwu, dh.double() * a)):
+            want = d.t() @ x.double()
+            terms = d.abs().t() @ x.double().abs()
+            # half a BF16 step of the result, 2^-16 of each term for the rest's rounding, FP32's of act' and the sum
+            assert bool(((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -15 * terms + 1e-30).all())
+
+
+def test_infinite_gradients_of_few_tokens(cake):
+    """An infinite or NaN gradient stays what it is: no rest is taken of it."""
+    x, wg, wu, gen = make(3, 64, 128)
+    g, u, dh = (matrix(gen, 3, 128).contiguous() for _ in range(3))
+    dh[1, 5], dh[2, 7] = float("inf"), float("nan")
+    u[1, 5] = g[1, 5] = 1
+    x[1, 0] = 2
+    x[0] = x[2] = 0
+    _, dwg, dwu = cake.cake_gated_bwd(dh, x, g, u, wg, wu)
+    assert dwg[5, 0] == float("inf") and dwu[5, 0] == float("inf")
+    assert bool(torch.isnan(dwg[7]).all()) and bool(torch.isfinite(dwg[8:].float()).all())
