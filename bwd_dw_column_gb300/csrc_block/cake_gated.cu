@@ -585,7 +585,7 @@ struct GatedGradParams {
     const uint16_t *dh, *g, *u;
     int64_t dh_stride, g_stride, u_stride;
     uint16_t *dg, *du;     // rows of 8 nvec
-    int64_t rest;          // bytes from there to what their rounding left; 0: not wanted
+    int64_t rest;          // REST: bytes from there to what their rounding left
     uint32_t nvec;
     uint64_t vecs;
     int gelu;
@@ -597,6 +597,7 @@ __device__ __forceinline__ float2 rest_of(float2 v, uint32_t rounded)
     return make_float2(isfinite(r.x) ? v.x - r.x : 0.f, isfinite(r.y) ? v.y - r.y : 0.f);
 }
 
+template <bool REST>
 __global__ void __launch_bounds__(kGradGuThreads) gated_grad_kernel(const __grid_constant__ GatedGradParams p)
 {
     pdl_launch_dependents();
@@ -617,14 +618,15 @@ __global__ void __launch_bounds__(kGradGuThreads) gated_grad_kernel(const __grid
             const float2 vg = make_float2(dq.x * uq.x * d0, dq.y * uq.y * d1), vu = make_float2(dq.x * a0, dq.y * a1);
             og[q] = pack2(vg);
             ou[q] = pack2(vu);
-            // (the differences are exact; of what is not finite there is none)
-            rg[q] = pack2(rest_of(vg, og[q]));
-            ru[q] = pack2(rest_of(vu, ou[q]));
+            if (REST) { // (the differences are exact; of what is not finite there is none)
+                rg[q] = pack2(rest_of(vg, og[q]));
+                ru[q] = pack2(rest_of(vu, ou[q]));
+            }
         }
         uint4 *const dg = reinterpret_cast<uint4 *>(p.dg) + i, *const du = reinterpret_cast<uint4 *>(p.du) + i;
         *dg = make_uint4(og[0], og[1], og[2], og[3]);
         *du = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-        if (p.rest) {
+        if (REST) {
             dg[p.rest / 16] = make_uint4(rg[0], rg[1], rg[2], rg[3]);
             du[p.rest / 16] = make_uint4(ru[0], ru[1], ru[2], ru[3]);
         }
@@ -976,12 +978,13 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
     q.u_stride = c.u.stride;
     q.dg = (uint16_t *)gu[0].data;
     q.du = (uint16_t *)gu[b.parts].data;
-    q.rest = b.parts == 2 ? (int64_t)b.gu_bytes : 0;
+    q.rest = (int64_t)b.gu_bytes;
     q.nvec = (uint32_t)(c.F / 8);
     q.vecs = (uint64_t)c.T * q.nvec;
     q.gelu = c.gelu;
     const uint64_t ctas = (q.vecs + kGradGuThreads - 1) / kGradGuThreads;
-    cudaError_t e = launch_after(gated_grad_kernel, dim3((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20)),
+    const dim3 grid((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20));
+    cudaError_t e = launch_after(b.parts == 2 ? gated_grad_kernel<true> : gated_grad_kernel<false>, grid,
                                  kGradGuThreads, 0, stream, q);
     if (e != cudaSuccess)
         return e;
