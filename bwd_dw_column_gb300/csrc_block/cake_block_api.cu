@@ -307,11 +307,14 @@ void fill_rotary(RotaryParams &p, const cake_rotary *r, int64_t tokens, int64_t 
     p.tokens = (uint32_t)tokens;
     p.D = (int)hidden;
     p.inv_d = 1.0f / (float)hidden;
+    p.axes = 1;
     p.pairs = (int)r->pairs;
-    p.axes = (int)r->axes;
-    p.turns = r->turns;
-    p.axis = r->axis;
-    p.positions = r->positions;
+    if (r->pairs > 0) { // (without pairs none of these is looked at)
+        p.axes = (int)r->axes;
+        p.turns = r->turns;
+        p.axis = r->axis;
+        p.positions = r->positions;
+    }
     p.pos_i64 = r->positions_int64;
     p.axis_stride = r->axis_stride;
     p.token_stride = r->token_stride;

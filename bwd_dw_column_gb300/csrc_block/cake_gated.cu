@@ -10,7 +10,7 @@
 // half of B, and one thread of the pair issues the products.  The forward's 256
 // columns are 128 of g and the same 128 of u, one half of B from each weight, so
 // that the epilogue finds both factors of h in its own registers.  While the
-// tensor cores fill one accumulator of 256 columns, four warps empty the other.
+// tensor cores fill one accumulator of 256 columns, eight warps empty the other.
 // No operand is transposed in memory: the copies and the descriptors take
 // operands along k or across it.
 //

@@ -307,3 +307,20 @@ def test_norm_of_zero_and_special_rows(cake):
     assert not bool(y[1].any()) and bool(((rstd.view(4, 2)[1] / 1000 - 1).abs() <= ref.RSTD_REL).all())
     finite = torch.isfinite(y.float()).all(-1)
     assert finite.tolist() == [[True, True], [True, True], [False, True], [True, False]]
+
+
+def test_no_pairs_need_no_positions(cake):
+    """Through the C ABI: with pairs = 0 the rotation's pointers are not looked at."""
+    import struct
+
+    from bwd_dw_column_gb300.step import _three
+    g = torch.Generator().manual_seed(12)
+    q, w = heads(g, 9, 3, 32), weights(g, 32, True)
+    y, rstd = torch.empty_like(q), torch.empty(27, device=DEV)
+    rotation = struct.pack("=qqQQQixxxxqqixxxx", 0, 7, w.data_ptr(), w.data_ptr(), 0, 1, 5, 1, 0)
+    view = lambda t: _three(t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
+    st = cake.load_library().cake_rotary_fwd(9, 3, 0, 32, view(q), None, rotation, w.data_ptr(), 1, None, 0, 1e-6, view(y),
+                                             None, rstd.data_ptr(), None, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    want, allow, _ = ref.rotary_fwd(q, torch.zeros(9, 0, dtype=torch.float64), w, 1e-6, "half")
+    check("y", y, want, allow)
