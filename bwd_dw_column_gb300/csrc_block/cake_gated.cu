@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
 
 constexpr int kFewThreads = 256;
 // GB300, pairs of CTAs against this kernel: 4096 to 8192 at 64 tokens 29 us and 26,
-// at 128 30 and 30.5; 1024 to 1024 10.3 and 7.3, 10.5 and 9.5.
+// at 128 30 and 29.9; 1024 to 1024 10.3 and 7.3, 10.5 and 9.5.
 constexpr int kFewMostTokens = 128;
 constexpr int kFewWeights = 32768; // of a stage: 128 rows of each weight, 64 k
 
@@ -568,6 +568,8 @@ __global__ void __launch_bounds__(kFewThreads) gated_few_kernel(const __grid_con
         const int first = rank * kFewThreads + (int)threadIdx.x, step = C * kFewThreads;
         if (C == 1) // (100 tokens, 64 to 128: 6.9 us against 9.7 with one output at a time)
             few_outputs<4, 1>(P, smem, f0, first, step, C);
+        else if (C == 2) // (64 tokens, 4096 to 8192: 26.0 us against 26.4 with one; 128 tokens 29.9 against 31.0)
+            few_outputs<2, 2>(P, smem, f0, first, step, C);
         else // (100 tokens, 696 to 904, clusters of 5: 9.0 us against 9.9 with two)
             few_outputs<1, 4>(P, smem, f0, first, step, C);
     }

@@ -153,7 +153,7 @@ __device__ __forceinline__ uint64_t position(const RotaryParams &p, uint32_t axi
 __device__ __forceinline__ void turn_sincos(int32_t phase, float sign, float &sine, float &cosine)
 {
     const int32_t q = (int32_t)((uint32_t)phase + 0x20000000u) >> 30; // the nearest quarter, -2 .. 1
-    const float x = (float)(phase - (int32_t)((uint32_t)q << 30)) * 1.46291807926715968e-9f; // 2 pi / 2^32
+    const float x = (float)(int32_t)((uint32_t)phase - ((uint32_t)q << 30)) * 1.46291807926715968e-9f; // 2 pi / 2^32
     const float y = x * x;
     float s = fmaf(y, 1.0f / 362880.0f, -1.0f / 5040.0f);
     s = fmaf(y, s, 1.0f / 120.0f);
