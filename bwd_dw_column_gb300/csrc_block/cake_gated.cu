@@ -70,7 +70,7 @@ struct PairProblem {
     CUtensorMap a[4], b[2], out[2];
     int a_mn, b_mn;       // an operand's rows lie along k in memory
     int segments, halves; // a, b by segment; or a, out by half
-    int parts;            // a is a sum of so many matrices: a[segment or half][part]
+    int parts;            // a is a sum of so many matrices: a[segment or half][part], with b[part]
     int stack;            // instead: two of at most 64 rows, above one another in the tile
     int kblocks;          // blocks of 64 k of a segment
     int tiles_m, tiles_n; // of a half
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
                                               2 * kPairStage + (P.withhold && issued == 0 ? 16 : 0));
                     const uint32_t bar = map_to_rank(full + 8 * st, 0);
                     const uint32_t sa = smem + st * kPairStage, sb = sa + kPairHalf;
-                    // (the parts of a block follow one another: the second finds b in L2)
+                    // (the parts of a block follow one another)
                     const int part = p.parts == 2 ? kb & 1 : 0, block = p.parts == 2 ? kb >> 1 : kb;
                     const int seg = block >= p.kblocks, k = (block - seg * p.kblocks) * 64;
                     const CUtensorMap *ma = &p.a[(p.segments == 2 ? seg : u.half) * p.parts + part];
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gated_pair_kernel(const __gri
                     if (GATED) {
                         tile_g2s_pair(sb, &p.b[rank], k, u.n0, bar);
                     } else {
-                        const CUtensorMap *mb = &p.b[seg];
+                        const CUtensorMap *mb = &p.b[seg + part]; // (two of either, never of both)
                         const int n = u.n0 + 128 * rank;
                         tile_g2s_pair(sb, mb, n, k, bar);
                         tile_g2s_pair(sb + 8192, mb, n + 64, k, bar);
@@ -591,12 +591,27 @@ struct GatedGradParams {
     uint32_t nvec;
     uint64_t vecs;
     int gelu;
+    // REST: the rests' factor of dWg and dWu, x with 0 for what is not finite.  The
+    // values' products make such a result what it is; a rest of the other sign or of
+    // 0 would turn an infinity into NaN.
+    const uint16_t *x;     // nullptr: not wanted
+    int64_t x_stride;
+    uint16_t *x_finite;    // rows of 8 x_nvec
+    uint32_t x_nvec;
+    uint64_t x_vecs;
 };
 
 __device__ __forceinline__ float2 rest_of(float2 v, uint32_t rounded)
 {
     const float2 r = bf2(rounded);
     return make_float2(isfinite(r.x) ? v.x - r.x : 0.f, isfinite(r.y) ? v.y - r.y : 0.f);
+}
+
+// A word of two BF16 values, 0 for an infinity or NaN.
+__device__ __forceinline__ uint32_t finite2(uint32_t w)
+{
+    const uint32_t e = 0x7f80u;
+    return ((w & e) == e ? 0u : w & 0xffffu) | ((w & e << 16) == e << 16 ? 0u : w & 0xffff0000u);
 }
 
 template <bool REST>
@@ -633,18 +648,34 @@ __global__ void __launch_bounds__(kGradGuThreads) gated_grad_kernel(const __grid
             du[p.rest / 16] = make_uint4(ru[0], ru[1], ru[2], ru[3]);
         }
     }
+    if (REST && p.x)
+        for (uint64_t i = (uint64_t)blockIdx.x * kGradGuThreads + threadIdx.x; i < p.x_vecs;
+             i += (uint64_t)gridDim.x * kGradGuThreads) {
+            const uint64_t t = i / p.x_nvec;
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.x + t * p.x_stride + (i - t * p.x_nvec) * 8));
+            reinterpret_cast<uint4 *>(p.x_finite)[i] = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+        }
 }
 
-// Sum of a split product's FP32 parts in their order, rounded to BF16.
+// Sum of a split product's FP32 parts in their order, rounded to BF16.  Where
+// that is not finite the parts of the rounded gradients are the result: what an
+// infinite factor makes of the rests' parts may be NaN.
 struct JoinParams {
     const float *part[2];  // [planes] of rows x cols, dense
     int64_t plane;         // elements from one to the next
     int planes;
+    int values;            // the first of them: of the rounded gradients
     uint16_t *out[2];
     int64_t stride[2];
     uint32_t nvec;
     uint64_t vecs;         // of one output
 };
+
+__device__ __forceinline__ float4 finite_or(float4 v, float4 w)
+{
+    return make_float4(isfinite(v.x) ? v.x : w.x, isfinite(v.y) ? v.y : w.y, isfinite(v.z) ? v.z : w.z,
+                       isfinite(v.w) ? v.w : w.w);
+}
 
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p)
 {
@@ -652,14 +683,20 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
     pdl_wait();
     const int o = blockIdx.y;
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < p.vecs; i += (uint64_t)gridDim.x * 256) {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a, va = a, vb = a;
         const float *at = p.part[o] + i * 8;
         for (int s = 0; s < p.planes; ++s, at += p.plane) {
             const float4 x = __ldcs(reinterpret_cast<const float4 *>(at)),
                          y = __ldcs(reinterpret_cast<const float4 *>(at) + 1);
             a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
             b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+            if (s == p.values - 1) {
+                va = a;
+                vb = b;
+            }
         }
+        a = finite_or(a, va);
+        b = finite_or(b, vb);
         const uint64_t r = i / p.nvec;
         reinterpret_cast<uint4 *>(p.out[o] + r * p.stride[o])[i - r * p.nvec] =
             make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
@@ -899,7 +936,7 @@ constexpr int64_t kTwoPartTokens = 64;
 struct BwdPlan {
     PairProblem dx, dw;
     int parts;
-    size_t gu_bytes, dx_bytes, dw_bytes;
+    size_t gu_bytes, dx_bytes, dw_bytes, x_bytes;
 };
 
 // The plan goes by the sizes alone; a thread keeps its last one, as a training
@@ -936,6 +973,7 @@ static const BwdPlan &plan_bwd(int64_t T, int64_t H, int64_t F)
     b.gu_bytes = ((size_t)T * F * 2 + 255) & ~(size_t)255;
     b.dx_bytes = ((size_t)x.planes * T * H * 4 + 255) & ~(size_t)255;
     b.dw_bytes = ((size_t)w.planes * 2 * F * H * 4 + 255) & ~(size_t)255;
+    b.x_bytes = b.parts == 2 ? ((size_t)T * H * 2 + 255) & ~(size_t)255 : 0;
     last[0] = T;
     last[1] = H;
     last[2] = F;
@@ -945,7 +983,7 @@ static const BwdPlan &plan_bwd(int64_t T, int64_t H, int64_t F)
 size_t gated_bwd_workspace(int64_t T, int64_t H, int64_t F)
 {
     const BwdPlan &b = plan_bwd(T, H, F);
-    return 2 * b.parts * b.gu_bytes + b.dx_bytes + b.dw_bytes;
+    return 2 * b.parts * b.gu_bytes + b.dx_bytes + b.dw_bytes + b.x_bytes;
 }
 
 static cudaError_t launch_join(const JoinParams &j, int outputs, cudaStream_t stream)
@@ -965,6 +1003,7 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
     ws += 2 * b.parts * b.gu_bytes;
     float *part_x = reinterpret_cast<float *>(ws);
     float *part_w = reinterpret_cast<float *>(ws + b.dx_bytes);
+    const Matrix x_finite{ws + b.dx_bytes + b.dw_bytes, c.T, c.H, c.H};
     const auto gu_maps = [&](PairProblem &p, int box_rows) {
         bool ok = true;
         for (int i = 0; i < 2 * b.parts; ++i)
@@ -984,7 +1023,14 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
     q.nvec = (uint32_t)(c.F / 8);
     q.vecs = (uint64_t)c.T * q.nvec;
     q.gelu = c.gelu;
-    const uint64_t ctas = (q.vecs + kGradGuThreads - 1) / kGradGuThreads;
+    if (b.parts == 2 && c.dw_gate.data) {
+        q.x = (const uint16_t *)c.x.data;
+        q.x_stride = c.x.stride;
+        q.x_finite = (uint16_t *)x_finite.data;
+        q.x_nvec = (uint32_t)(c.H / 8);
+        q.x_vecs = (uint64_t)c.T * q.x_nvec;
+    }
+    const uint64_t most = q.vecs > q.x_vecs ? q.vecs : q.x_vecs, ctas = (most + kGradGuThreads - 1) / kGradGuThreads;
     const dim3 grid((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20));
     cudaError_t e = launch_after(b.parts == 2 ? gated_grad_kernel<true> : gated_grad_kernel<false>, grid,
                                  kGradGuThreads, 0, stream, q);
@@ -1003,6 +1049,7 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
         PairProblem &p = P.p[n++] = b.dw;
         const Matrix part_g{part_w, c.F, c.H, c.H}, part_u{part_w + c.F * c.H, c.F, c.H, c.H};
         if (!gu_maps(p, 64) || !operand_map(&p.b[0], c.x, 64) ||
+            (p.parts == 2 && !operand_map(&p.b[1], x_finite, 64)) ||
             !(p.planes ? parts_map(&p.out[0], part_g, 2 * c.F * c.H, p.planes) &&
                              parts_map(&p.out[1], part_u, 2 * c.F * c.H, p.planes)
                        : output_map(&p.out[0], c.dw_gate) && output_map(&p.out[1], c.dw_up)))
@@ -1018,6 +1065,7 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
         j.part[0] = part_x;
         j.plane = c.T * c.H;
         j.planes = b.dx.planes;
+        j.values = b.dx.splits;
         j.out[0] = (uint16_t *)c.dx.data;
         j.stride[0] = c.dx.stride;
         j.nvec = (uint32_t)(c.H / 8);
@@ -1029,7 +1077,7 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
         j.part[0] = part_w;
         j.part[1] = part_w + c.F * c.H;
         j.plane = 2 * c.F * c.H;
-        j.planes = b.dw.planes;
+        j.planes = j.values = b.dw.planes;
         j.out[0] = (uint16_t *)c.dw_gate.data;
         j.out[1] = (uint16_t *)c.dw_up.data;
         j.stride[0] = c.dw_gate.stride;
