@@ -295,9 +295,9 @@ __global__ void __launch_bounds__(kDnThreads, 2)
 
 // A thread holds 8 VPT columns of a row.  Its terms of dw are added over 16 rows
 // in registers and then to Kahan pairs in shared memory that only it uses.  With
-// h the row, a = dy w and S = sum of a h the gradient is
-//   t = dh + rstd a - rstd^3 (S / H) h,
-// so that the first pass needs no scaled copy of the row but for dw.
+// hh = h rstd, a = dy w and m = mean of a hh the gradient is
+//   t = dh + rstd (a - hh m),
+// in this order: rstd^2 is beyond FP32 for rows below 1e-19 (eps = 0).
 constexpr int kDnBlock = 16;
 
 __device__ __forceinline__ void fold_columns(float4 *at, int step, float2 (&sum)[4])
@@ -374,14 +374,14 @@ __global__ void __launch_bounds__(kDnThreads, 1)
                     weight_pairs(s, L, v, w2);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float2 dq = bf2(word(d, q)), hq = bf2(word(h, q));
-                        sum = fma2(mul2(dq, w2[q]), hq, sum);
-                        acc[k][q] = fma2(mul2(hq, rs2), dq, acc[k][q]);
+                        const float2 dq = bf2(word(d, q)), hh = mul2(bf2(word(h, q)), rs2);
+                        sum = fma2(mul2(dq, w2[q]), hh, sum);
+                        acc[k][q] = fma2(hh, dq, acc[k][q]);
                     }
                 }
             }
             const float tot = own.sum(__fadd_rn(sum.x, sum.y), s, L, gid, wig, lane, slot++, abort);
-            const float m = -__fmul_rn(__fmul_rn(__fmul_rn(tot, L.inv_h), rs), __fmul_rn(rs, rs));
+            const float m = -__fmul_rn(tot, L.inv_h);
             const float2 m2 = make_float2(m, m);
             uint4 *xrow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[0].base) + row_off(p.out[0], r, L.nh));
             uint4 *erow = reinterpret_cast<uint4 *>(const_cast<uint16_t *>(p.out[1].base) + row_off(p.out[1], r, L.nh));
@@ -399,10 +399,8 @@ __global__ void __launch_bounds__(kDnThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float2 a = mul2(bf2(word(d, q)), w2[q]);
-                        float2 t = mul2(bf2(word(h, q)), m2);
-                        t = fma2(rs2, a, t);
-                        if (DH)
-                            t = add2(t, bf2(word(e, q)));
+                        float2 t = fma2(mul2(bf2(word(h, q)), rs2), m2, a);
+                        t = DH ? fma2(rs2, t, bf2(word(e, q))) : mul2(rs2, t);
                         oe[q] = pack2(t);
                         ox[q] = pack2(dropped(t, word(bits[k], q), limit, scale));
                     }
