@@ -34,6 +34,7 @@ import importlib
 import math
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import CakeError, load_library
@@ -160,7 +161,9 @@ class CakeGatedFunction(torch.autograd.Function):
 
 def cake_gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu") -> torch.Tensor:
     """Differentiable gated block: act(x w_gate^T) * (x w_up^T) of x [..., H]; see ``cake_gated_fwd``."""
-    if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
+    if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad) or \
+            forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in (x, w_gate, w_up)):
+        # (of a tangent the function raises: there is no forward mode)
         return CakeGatedFunction.apply(x, w_gate, w_up, act)
     h, _, _ = cake_gated_fwd(x.reshape(-1, x.shape[-1]), w_gate, w_up, act, save=False)
     return h.view(*x.shape[:-1], h.shape[-1])
