@@ -437,18 +437,18 @@ extern "C" cake_status cake_rotary_bwd(int64_t tokens, int64_t q_heads, int64_t 
     const int dtype[2] = {w_q_dtype, w_k_dtype};
     const float *const rstd[2] = {rstd_q, rstd_k};
     float *const dw[2] = {dw_q, dw_k};
-    for (int i = 0; i < c.lists && norm; ++i) {
+    for (int i = 0; i < c.lists && norm; ++i)
         if (!good_dtype(dtype[i]) || !dw[i])
             return CAKE_ERR_INVALID;
+    for (int i = 0; i < 2 && norm; ++i)
         if (!aligned16(dw[i]))
             return CAKE_ERR_UNSUPPORTED;
-    }
-    if (tokens == 0) {
-        for (int i = 0; i < c.lists && norm; ++i)
-            if (cudaMemsetAsync(dw[i], 0, (size_t)hidden * sizeof(float), cu(stream)) != cudaSuccess)
-                return CAKE_ERR_CUDA;
-        return CAKE_OK;
-    }
+    // a sum over nothing: without tokens, and that of keys without heads
+    const auto zero = [&](float *to) {
+        return !norm || !to || cudaMemsetAsync(to, 0, (size_t)hidden * sizeof(float), cu(stream)) == cudaSuccess;
+    };
+    if (tokens == 0)
+        return zero(dw_q) && zero(dw_k) ? CAKE_OK : CAKE_ERR_CUDA;
     for (int i = 0; i < c.lists; ++i)
         if ((st = check_tensor(in[i], &c.shape[i])) != CAKE_OK ||
             (norm && ((st = check_weight(w[i], dtype[i])) != CAKE_OK || (st = check_rows_f32(rstd[i])) != CAKE_OK ||
@@ -465,9 +465,10 @@ extern "C" cake_status cake_rotary_bwd(int64_t tokens, int64_t q_heads, int64_t 
     for (int i = 0; i < c.lists && norm; ++i) {
         lists[3 + i] = memory(w[i], weight_bytes(hidden, dtype[i]));
         lists[5 + i] = memory(rstd[i], (uint64_t)c.rows[i] * 4);
-        scalars[i] = memory(dw[i], (uint64_t)hidden * 4);
         lists[11 + i] = memory(v[i], &c.shape[i]);
     }
+    for (int i = 0; i < 2 && norm; ++i)
+        scalars[i] = memory(dw[i], (uint64_t)hidden * 4);
     scalars[2] = memory(workspace, need);
     for (int i = 0; i < c.lists; ++i) {
         const Memory o = memory(out[i], &c.shape[i]);
@@ -479,7 +480,7 @@ extern "C" cake_status cake_rotary_bwd(int64_t tokens, int64_t q_heads, int64_t 
     if (any_meet(scalars, 3, lists, 13))
         return CAKE_ERR_INVALID;
     RotaryParams p{};
-    if (step_status_ptr(&p.status) != cudaSuccess)
+    if (step_status_ptr(&p.status) != cudaSuccess || (c.lists == 1 && !zero(dw_k)))
         return CAKE_ERR_CUDA;
     fill_rotary(p, rotary, tokens, hidden);
     for (int i = 0; i < c.lists; ++i) {

@@ -98,7 +98,8 @@ cake_status cake_gated_bwd(int64_t tokens, int64_t hidden, int64_t ffn, const ca
  * not used.  rstd_q, rstd_k: FP32 [tokens * heads] in (t, head) order.
  *
  * q_out may be exactly q and k_out exactly k (of the backward, dq_out dq and
- * dk_out dk).  dw_q, dw_k: [hidden] FP32, overwritten.
+ * dk_out dk).  dw_q, dw_k: [hidden] FP32, overwritten (dw_k, where it is given
+ * without keys, with zeros).
  */
 typedef enum { CAKE_ROTARY_HALF = 0, CAKE_ROTARY_ADJACENT = 1 } cake_rotary_style;
 
