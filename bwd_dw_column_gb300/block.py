@@ -38,7 +38,7 @@ from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import CakeError, load_library
-from .step import _check, _on, _rows, _three
+from .step import _check, _gradient, _on, _rows, _three
 
 __all__ = [
     "cake_gated_fwd", "cake_gated_bwd", "cake_gated_bwd_workspace_size", "cake_gated", "CakeGatedFunction",
@@ -153,7 +153,7 @@ class CakeGatedFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dh):
         x, g, u, w_gate, w_up = ctx.saved_tensors
-        dh = dh.to(torch.bfloat16).reshape(g.shape).contiguous()
+        dh = _gradient(dh.reshape(g.shape))
         dx, dwg, dwu = cake_gated_bwd(dh, x, g, u, w_gate, w_up, ctx.act, need_dx=ctx.needs_input_grad[0],
                                       need_dw=ctx.needs_input_grad[1] or ctx.needs_input_grad[2])
         return None if dx is None else dx.view(ctx.size), dwg, dwu, None
@@ -270,7 +270,7 @@ class CakeRotaryFunction(torch.autograd.Function):
         for d, size in zip((dq, dk), ctx.sizes):
             if size is not None and d is None:
                 d = torch.zeros(size, dtype=torch.bfloat16, device=positions.device)
-            grads.append(None if size is None else d.to(torch.bfloat16).contiguous())
+            grads.append(None if size is None else _gradient(d))
         dq, dk, dwq, dwk = cake_rotary_bwd(*grads, positions, turns, axes, q, k, rq, rk, w_q, w_k, style=ctx.style)
         return (dq, dk, None, None, None, None if w_q is None else dwq.to(w_q.dtype),
                 None if w_k is None or dwk is None else dwk.to(w_k.dtype), None, None)
@@ -325,7 +325,7 @@ class CakeDropoutFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         seed, = ctx.saved_tensors
-        dy = dy.to(torch.bfloat16).contiguous()
+        dy = _gradient(dy)
         dx = cake_dropout_bwd(dy, ctx.p, ctx.seed if seed is None else seed, ctx.offset) \
             if ctx.needs_input_grad[0] else None
         return dx, dy if ctx.needs_input_grad[1] else None, None, None, None
@@ -395,8 +395,8 @@ class CakeDropoutNormFunction(torch.autograd.Function):
         if dy is None and dh is None:
             return (None,) * 7
         h, rstd, w, seed = ctx.saved_tensors
-        dy = torch.zeros_like(h) if dy is None else dy.to(torch.bfloat16).contiguous()
-        dh = None if dh is None else dh.to(torch.bfloat16).contiguous()
+        dy = torch.zeros_like(h) if dy is None else _gradient(dy)
+        dh = None if dh is None else _gradient(dh)
         dres, dx, dw = cake_dropout_norm_bwd(dy, h, rstd, w, ctx.p, ctx.seed if seed is None else seed, ctx.offset, dh)
         return dx, dres, dw.to(w.dtype), None, None, None, None
 

@@ -206,6 +206,15 @@ def _workspace(workspace, size, device):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def _gradient(d):
+    """A gradient from autograd as the kernels take it: BF16, contiguous, its rows on 16-byte boundaries.  (A slice of a
+    longer one may be contiguous and lie anywhere, and a single row has whatever stride its buffer has.)"""
+    d = d.to(torch.bfloat16).contiguous()
+    if d.data_ptr() % 16 or any(s % 8 for s in d.stride()[:-1]):
+        d = torch.empty(d.shape, dtype=d.dtype, device=d.device).copy_(d)
+    return d
+
+
 # ---------------------------------------------------------------- sandwich norm
 
 def _gate(gate, z):
@@ -346,8 +355,8 @@ class CakeSandwichFunction(torch.autograd.Function):
         if dy is None and dh is None:
             return (None,) * 7
         h, z, r_post, r_pre, w_post, w_pre, gate = ctx.saved_tensors
-        dy = torch.zeros_like(h) if dy is None else dy.to(torch.bfloat16).contiguous()
-        dh = None if dh is None else dh.to(torch.bfloat16).contiguous()
+        dy = torch.zeros_like(h) if dy is None else _gradient(dy)
+        dh = None if dh is None else _gradient(dh)
         dx, dz, dwo, dwr, dgate = cake_sandwich_bwd(dy, h, z, r_post, r_pre, w_post, w_pre, dh, gate, ctx.scale,
                                                     need_dgate=ctx.needs_input_grad[5])
         return dz, dx, dwo.to(w_post.dtype), dwr.to(w_pre.dtype), None, dgate, None
@@ -575,7 +584,7 @@ class CakeEmbeddingFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         ids, = ctx.saved_tensors
-        dtable = cake_embedding_bwd(dy.to(torch.bfloat16).contiguous(), ids, ctx.vocab, ctx.scale, ctx.padding_idx,
+        dtable = cake_embedding_bwd(_gradient(dy), ids, ctx.vocab, ctx.scale, ctx.padding_idx,
                                     dtype=ctx.dtype)
         return None, dtable, None, None
 

@@ -39,6 +39,7 @@ import torch
 
 from . import (cake_rmsnorm_bwd, cake_rmsnorm_bwd_workspace, cake_rmsnorm_bwd_workspace_size,
                cake_rmsnorm_fwd)
+from .step import _gradient
 
 _ws_lock = threading.Lock()
 _ws_cache: dict = {}
@@ -115,9 +116,9 @@ class CakeRMSNormFunction(torch.autograd.Function):
         h, rstd, w = ctx.saved_tensors
         if dy is None:
             dy = torch.zeros(h.shape, dtype=torch.bfloat16, device=h.device)
-        dy = dy.to(torch.bfloat16).contiguous()
+        dy = _gradient(dy)
         if dh is not None:
-            dh = dh.to(torch.bfloat16).contiguous()
+            dh = _gradient(dh)
         ws = ctx.workspace if ctx.workspace is not None else _cached_workspace(h, w.dtype, ctx.deterministic)
         dx, dw = cake_rmsnorm_bwd(dy, h, rstd, w, dh if ctx.has_res else None, ctx.deterministic, workspace=ws)
         gw = dw if w.dtype == torch.float32 else dw.to(w.dtype)
