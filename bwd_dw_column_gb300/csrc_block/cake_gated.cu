@@ -504,9 +504,10 @@ __global__ void __launch_bounds__(kFewThreads) gated_few_kernel(const __grid_con
                     ph ^= 1u;
                 }
             }
-            if (!ok) // no copy is left in flight
-                for (uint32_t j = issued > (uint32_t)P.stages ? issued - P.stages : 0; j < issued; ++j)
-                    (void)mbar_wait(full + 8 * (j % P.stages), (j / P.stages) & 1, P.wait_ns);
+            // No copy is left in flight, whichever warp's wait ran out: this warp
+            // waits for the last ones itself, for as long as all waits may take.
+            for (uint32_t j = issued > (uint32_t)P.stages ? issued - P.stages : 0; j < issued; ++j)
+                ok = mbar_wait(full + 8 * (j % P.stages), (j / P.stages) & 1, P.wait_ns) && ok;
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -537,8 +538,11 @@ __global__ void __launch_bounds__(kFewThreads) gated_few_kernel(const __grid_con
     if (!ok) {
         s_bad = 1;
         set_status(P.status, kStatusTimeout);
+        // (a copy that the waits have not seen takes some microseconds more at most)
+        for (int i = 0; i < 1000; ++i)
+            __nanosleep(1000);
     }
-    __syncthreads(); // every copy has landed and every product is done: the ring is free
+    __syncthreads(); // where no wait ran out every copy has landed and every product is done: the ring is free
     tc_fence_after();
     const bool bad = s_bad;
     float *part = reinterpret_cast<float *>(smem_raw); // [gate, up][n][128]
