@@ -23,6 +23,7 @@ LIB = os.path.join(HERE, "libcake_rmsnorm.so")
 PYTHON_SOURCE = os.path.join(CSRC_BLOCK, "cake_block_python.cpp")
 PYTHON_MODULE = os.path.join(HERE, "_cake_block.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
+MODULE_STAMP = os.path.join(BUILD_DIR, "cake_block_python.built_for")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
@@ -47,8 +48,23 @@ def _inputs():
     return files
 
 
+def _built_for() -> str:
+    """What _cake_block.so depends on beside its source: the interpreter, and the torch whose headers it is compiled
+    against."""
+    import torch
+    return f"{sys.version}\n{torch.__version__}\n{torch.__file__}\ncxx11 abi {int(torch.compiled_with_cxx11_abi())}\n"
+
+
+def _module_stamp() -> str:
+    try:
+        with open(MODULE_STAMP) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(PYTHON_MODULE):
+    if not os.path.exists(LIB) or not os.path.exists(PYTHON_MODULE) or _module_stamp() != _built_for():
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(PYTHON_MODULE))
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -116,6 +132,8 @@ def _link_module(obj: str) -> None:
     _run(["g++", "-shared", "-o", tmp, obj, f"-L{_torch_dir('lib')}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
           f"-L{HERE}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"], "linking _cake_block.so")
     os.replace(tmp, PYTHON_MODULE)
+    with open(MODULE_STAMP, "w") as f:
+        f.write(_built_for())
 
 
 if __name__ == "__main__":
