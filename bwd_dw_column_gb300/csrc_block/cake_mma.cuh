@@ -64,8 +64,6 @@ __device__ __forceinline__ void store_wait_read()
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // Load a float4 from a CTA of the cluster's shared memory.
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr)
 {
