@@ -29,6 +29,7 @@ the host's.
 from __future__ import annotations
 
 import ctypes
+import decimal
 import functools
 import importlib
 import math
@@ -171,6 +172,31 @@ def cake_gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: s
 
 # ----------------------------------------------------------------------- rotary
 
+@functools.lru_cache(maxsize=8)
+def _two_pi(digits: int) -> decimal.Decimal:
+    """2 pi by the arithmetic-geometric mean (Brent and Salamin, 1976), which doubles its digits with every step."""
+    with decimal.localcontext() as c:
+        c.prec = digits + 10
+        a, b, t, p = decimal.Decimal(1), 1 / decimal.Decimal(2).sqrt(), decimal.Decimal("0.25"), 1
+        while abs(a - b) > decimal.Decimal(10) ** -(digits // 2 + 2):
+            m = (a + b) / 2
+            t -= p * (a - m) ** 2
+            a, b, p = m, (a * b).sqrt(), 2 * p
+        return (a + b) ** 2 / (2 * t)
+
+
+def _ladder(base: float, n: int) -> list:
+    """base^(-i / n) for i < n."""
+    if n <= 1:
+        return [decimal.Decimal(1)] * n
+    if not base > 0:
+        raise ValueError(f"the base of a ladder of frequencies is positive, got {base}")
+    step, out = (-decimal.Decimal(base).ln() / n).exp(), [decimal.Decimal(1)]
+    while len(out) < n:
+        out.append(out[-1] * step)
+    return out
+
+
 def cake_rotary_table(sections, base: float = 10000.0, *, shared: bool = False, freqs=None, device="cuda"):
     """(turns, axes) of a rotation: each pair's frequency and the axis whose position turns it.
 
@@ -178,22 +204,35 @@ def cake_rotary_table(sections, base: float = 10000.0, *, shared: bool = False, 
     has the frequency base^(-i / n) radians a position, or with ``shared`` pair
     j of all of them base^(-j / pairs); ``freqs`` gives every pair's frequency
     instead.  turns: int64, the frequency's share of a turn in units of 2^-64
-    (modulo 2^64).
+    (modulo 2^64), rounded to the nearest one: an angle is off by the position
+    times 2^-65 of a turn at most, besides the kernels' own rounding.
     """
     sections = [int(n) for n in sections]
     pairs = sum(sections)
-    if freqs is None:
-        freqs = [base ** (-j / pairs) for j in range(pairs)] if shared else \
-            [base ** (-i / n) for n in sections for i in range(n)]
-    freqs = [float(f) for f in freqs]
-    if len(freqs) != pairs:
-        raise ValueError(f"{len(freqs)} frequencies for {pairs} pairs")
+    base = float(base)
+    if freqs is not None:
+        freqs = [float(f) for f in freqs]
+        if len(freqs) != pairs:
+            raise ValueError(f"{len(freqs)} frequencies for {pairs} pairs")
+        for f in freqs:
+            if not math.isfinite(f):
+                raise ValueError(f"a frequency is {f}")
+    # 64 bits of a turn, and the whole turns that drop out, are more than a double has
+    largest = max((abs(f) for f in freqs), default=0.0) if freqs is not None else max(1.0, 1 / base if base > 0 else 1.0)
+    digits = 50 + max(0, math.frexp(min(largest, 1e308))[1] // 3)
     turns = []
-    for f in freqs:
-        if not math.isfinite(f):
-            raise ValueError(f"a frequency is {f}")
-        t = round(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64
-        turns.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+    with decimal.localcontext() as c:
+        c.prec = digits
+        if freqs is not None:
+            freqs = [decimal.Decimal(f) for f in freqs]
+        elif shared:
+            freqs = _ladder(base, pairs)
+        else:
+            freqs = [f for n in sections for f in _ladder(base, n)]
+        unit = 2 ** 64 / _two_pi(digits)
+        for f in freqs:
+            t = int((f * unit).to_integral_value()) % 2 ** 64
+            turns.append(t - 2 ** 64 if t >= 2 ** 63 else t)
     axes = [a for a, n in enumerate(sections) for _ in range(n)]
     return (torch.tensor(turns, dtype=torch.int64, device=device),
             torch.tensor(axes, dtype=torch.int32, device=device))

@@ -83,9 +83,10 @@ cake_status cake_gated_bwd(int64_t tokens, int64_t hidden, int64_t ffn, const ca
  * Pair i of `pairs` (a, b) becomes (a cos - b sin, b cos + a sin) with the
  * angle 2 pi * turns[i] * position[axis[i]][t] / 2^64.  It is columns i and
  * pairs + i (CAKE_ROTARY_HALF) or 2 i and 2 i + 1 (CAKE_ROTARY_ADJACENT); the
- * columns from 2 * pairs on are not rotated.  The angle's whole turns drop out
- * of the product modulo 2^64, so it is as exact for far positions as for near
- * ones; turns is a frequency's share of a turn in units of 2^-64.
+ * columns from 2 * pairs on are not rotated.  turns is a frequency's share of a
+ * turn in units of 2^-64; whole turns drop out of the product modulo 2^64 and
+ * nothing else does, so an angle is off by the position times the error of its
+ * turns (2^-65 of a turn where that is rounded once), and 2^-32 of a turn.
  *
  * q, k: BF16 [tokens, heads, hidden] views of the same tokens and hidden (k
  * with k_heads = 0: none).  hidden is a multiple of 16, at most 512; pairs is a
