@@ -598,7 +598,7 @@ struct GatedGradParams {
     // REST: the rests' factor of dWg and dWu, x with 0 for what is not finite.  The
     // values' products make such a result what it is; a rest of the other sign or of
     // 0 would turn an infinity into NaN.
-    const uint16_t *x;     // nullptr: not wanted
+    const uint16_t *x;
     int64_t x_stride;
     uint16_t *x_finite;    // rows of 8 x_nvec
     uint32_t x_nvec;
@@ -623,6 +623,15 @@ __global__ void __launch_bounds__(kGradGuThreads) gated_grad_kernel(const __grid
 {
     pdl_launch_dependents();
     pdl_wait();
+    if (REST && blockIdx.y == 1) { // x, beside the gradients (64 tokens, 4096 to 512: 12.3 us, behind them 12.5)
+        for (uint64_t i = (uint64_t)blockIdx.x * kGradGuThreads + threadIdx.x; i < p.x_vecs;
+             i += (uint64_t)gridDim.x * kGradGuThreads) {
+            const uint64_t t = i / p.x_nvec;
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.x + t * p.x_stride + (i - t * p.x_nvec) * 8));
+            reinterpret_cast<uint4 *>(p.x_finite)[i] = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+        }
+        return;
+    }
     for (uint64_t i = (uint64_t)blockIdx.x * kGradGuThreads + threadIdx.x; i < p.vecs;
          i += (uint64_t)gridDim.x * kGradGuThreads) {
         const uint64_t t = i / p.nvec;
@@ -652,23 +661,16 @@ __global__ void __launch_bounds__(kGradGuThreads) gated_grad_kernel(const __grid
             du[p.rest / 16] = make_uint4(ru[0], ru[1], ru[2], ru[3]);
         }
     }
-    if (REST && p.x)
-        for (uint64_t i = (uint64_t)blockIdx.x * kGradGuThreads + threadIdx.x; i < p.x_vecs;
-             i += (uint64_t)gridDim.x * kGradGuThreads) {
-            const uint64_t t = i / p.x_nvec;
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p.x + t * p.x_stride + (i - t * p.x_nvec) * 8));
-            reinterpret_cast<uint4 *>(p.x_finite)[i] = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
-        }
 }
 
-// Sum of a split product's FP32 parts in their order, rounded to BF16.  Where
-// that is not finite the parts of the rounded gradients are the result: what an
-// infinite factor makes of the rests' parts may be NaN.
+// Sum of a split product's FP32 parts in their order, rounded to BF16.  REST:
+// where that is not finite the parts of the rounded gradients are the result, as
+// what an infinite factor makes of the rests' parts may be NaN.
 struct JoinParams {
     const float *part[2];  // [planes] of rows x cols, dense
     int64_t plane;         // elements from one to the next
     int planes;
-    int values;            // the first of them: of the rounded gradients
+    int values;            // REST: the first of them, of the rounded gradients
     uint16_t *out[2];
     int64_t stride[2];
     uint32_t nvec;
@@ -681,6 +683,7 @@ __device__ __forceinline__ float4 finite_or(float4 v, float4 w)
                        isfinite(v.w) ? v.w : w.w);
 }
 
+template <bool REST>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p)
 {
     pdl_launch_dependents();
@@ -694,13 +697,15 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
                          y = __ldcs(reinterpret_cast<const float4 *>(at) + 1);
             a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
             b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
-            if (s == p.values - 1) {
+            if (REST && s == p.values - 1) {
                 va = a;
                 vb = b;
             }
         }
-        a = finite_or(a, va);
-        b = finite_or(b, vb);
+        if (REST) {
+            a = finite_or(a, va);
+            b = finite_or(b, vb);
+        }
         const uint64_t r = i / p.nvec;
         reinterpret_cast<uint4 *>(p.out[o] + r * p.stride[o])[i - r * p.nvec] =
             make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
@@ -993,8 +998,8 @@ size_t gated_bwd_workspace(int64_t T, int64_t H, int64_t F)
 static cudaError_t launch_join(const JoinParams &j, int outputs, cudaStream_t stream)
 {
     const uint64_t ctas = (j.vecs + 255) / 256;
-    return launch_after(join_kernel, dim3((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20), (unsigned)outputs), 256, 0,
-                        stream, j);
+    const dim3 grid((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20), (unsigned)outputs);
+    return launch_after(j.values < j.planes ? join_kernel<true> : join_kernel<false>, grid, 256, 0, stream, j);
 }
 
 cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
@@ -1035,7 +1040,7 @@ cudaError_t launch_gated_bwd(const GatedBwdCall &c, cudaStream_t stream)
         q.x_vecs = (uint64_t)c.T * q.x_nvec;
     }
     const uint64_t most = q.vecs > q.x_vecs ? q.vecs : q.x_vecs, ctas = (most + kGradGuThreads - 1) / kGradGuThreads;
-    const dim3 grid((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20));
+    const dim3 grid((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20), q.x ? 2 : 1);
     cudaError_t e = launch_after(b.parts == 2 ? gated_grad_kernel<true> : gated_grad_kernel<false>, grid,
                                  kGradGuThreads, 0, stream, q);
     if (e != cudaSuccess)
