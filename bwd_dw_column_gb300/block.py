@@ -131,7 +131,9 @@ def cake_gated_bwd(dh: torch.Tensor, x: torch.Tensor, g: torch.Tensor, u: torch.
                    dw_gate: torch.Tensor | None = None, dw_up: torch.Tensor | None = None, stream=None):
     """Backward: (dx, dw_gate, dw_up), BF16; None for what is not needed.
 
-    dh: gradient of h, BF16 [T, F]; g and u as the forward gave them.
+    dh: gradient of h, BF16 [T, F]; g and u as the forward gave them.  With more
+    than 64 tokens the gradients of g and u are rounded to BF16 once between the
+    two products (see ``include/cake_block.h``).
     """
     if stream is not None:
         with _on(stream, x):
@@ -161,7 +163,7 @@ class CakeGatedFunction(torch.autograd.Function):
 
 
 def cake_gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu") -> torch.Tensor:
-    """Differentiable gated block: act(x w_gate^T) * (x w_up^T) of x [..., H]; see ``cake_gated_fwd``."""
+    """Differentiable gated block: act(x w_gate^T) * (x w_up^T) of x [..., H], reverse mode; see ``cake_gated_fwd``."""
     if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad) or \
             forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in (x, w_gate, w_up)):
         # (of a tangent the function raises: there is no forward mode)
@@ -332,7 +334,9 @@ def cake_dropout_fwd(x: torch.Tensor, p: float, seed, offset: int = 0, residual:
                      y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y = bf16(m * x [+ residual]), m 0 with probability p and else 1 over the share that is kept.
 
-    x, residual: BF16 [T, H] or [T, nh, H] views.  The mask goes by seed,
+    x, residual: BF16 [T, H] or [T, nh, H] views, H a multiple of 8, at most
+    8192 as for the norm (a wider dense tensor goes as [T, n, H / n]: an
+    element's place is the same).  The mask goes by seed,
     offset and an element's place alone and is never stored: calls with the
     same ones drop the same elements, so give every use of a step an offset of
     its own.  p counts in steps of 2^-16.  seed: a number, or an int64 tensor

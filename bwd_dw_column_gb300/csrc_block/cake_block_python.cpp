@@ -2,7 +2,7 @@
 // their C ABI: checks of tensors, allocation of outputs and workspaces on the
 // current stream, and the call.  Small calls are the host's, and this takes
 // less than half of what the same steps take in Python (GB300's host: a token's 24 +
-// 4 heads normed and rotated 7 us against 23.5, a gated backward 12 against 30).
+// 4 heads normed and rotated 7 us against 23.5, a gated backward 11 against 30).
 //
 // Every function takes its arguments by position; block.py has their names,
 // defaults and documentation.

@@ -935,11 +935,12 @@ static void split_sums(PairProblem &a, PairProblem &b)
 }
 
 // Tokens up to which the gradients of g and u go into the products as two BF16
-// matrices each, the rounded values and the rounded rest (2^-16 of the value):
-// with few tokens a handful of large gradients carries a result, and the error of
-// their one rounding does not average out (2 tokens, 2.7e-3 of the result's norm
-// against 1.7e-3 of its own rounding).  The weights' bytes bound these calls; for
-// dx both lie in one tile, which takes no more products.
+// matrices each, the rounded values and the rounded rest (2^-16 of the value).
+// One rounding of them costs a result about as much as its own (333 and 8192
+// tokens: 2.3e-3 of its norm against 1.7e-3 with exact ones), and more where a
+// handful of gradients carries it (2 tokens: 2.7e-3).  A second part takes as
+// many products again, which are the time of large calls.  Here the weights'
+// bytes are, and for dx both parts lie in one tile of 128 rows.
 constexpr int64_t kTwoPartTokens = 64;
 
 struct BwdPlan {

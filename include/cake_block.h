@@ -48,9 +48,10 @@ extern "C" {
  * The forward writes bf16(g) and bf16(u) too where g and u are given (both or
  * neither); h is computed from the FP32 sums.  The backward takes them as
  * they were written.  dg and du are rounded to BF16 because the tensor cores
- * multiply BF16 (with at most 64 tokens what this rounding leaves is multiplied
- * too, so that they are as good as FP32); sums are FP32, those of a split sum
- * added in a fixed order.
+ * multiply BF16: an error of the result's norm of 2.3e-3 where exact ones would
+ * leave the 1.7e-3 of its own rounding.  With at most 64 tokens what this
+ * rounding leaves is multiplied too, so that they are good to 2^-16.  Sums are
+ * FP32, those of a split sum added in a fixed order.
  * dx NULL leaves it out, and dw_gate and dw_up NULL (both or neither) those.
  */
 typedef enum { CAKE_ACT_SILU = 0, CAKE_ACT_GELU = 1 } cake_act;

@@ -69,3 +69,12 @@ def test_nothing_or_everything_dropped(cake, T, H, p):
         want = ref.dropout_norm_bwd(dy, h, rstd, w, dh, m)
         for name, v in zip(("dresidual", "dx", "dw"), cake.cake_dropout_norm_bwd(dy, h, rstd, w, p, seed, 4, dh)):
             assert ref.excess(v, *want[name]) <= 1, name
+
+
+def test_an_elements_place_does_not_go_by_the_shape(cake):
+    """A dense tensor's mask is that of its elements in a row, as [T, H] or as [T, n, H / n]."""
+    g = torch.Generator().manual_seed(1)
+    x, e = rows(g, 33, 8192), rows(g, 33, 8192)
+    want = cake.cake_dropout_fwd(x, 0.3, 5, 6, e)
+    for n in (2, 8, 1024):
+        assert torch.equal(cake.cake_dropout_fwd(x.view(33, n, -1), 0.3, 5, 6, e.view(33, n, -1)).view(33, -1), want)
