@@ -174,11 +174,15 @@ def cake_gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: s
 
 # ----------------------------------------------------------------------- rotary
 
+def _digits(n: int):
+    """Decimal arithmetic of n digits, whatever context the caller has set."""
+    return decimal.localcontext(decimal.Context(prec=n, rounding=decimal.ROUND_HALF_EVEN))
+
+
 @functools.lru_cache(maxsize=8)
 def _two_pi(digits: int) -> decimal.Decimal:
     """2 pi by the arithmetic-geometric mean (Brent and Salamin, 1976), which doubles its digits with every step."""
-    with decimal.localcontext() as c:
-        c.prec = digits + 10
+    with _digits(digits + 10):
         a, b, t, p = decimal.Decimal(1), 1 / decimal.Decimal(2).sqrt(), decimal.Decimal("0.25"), 1
         while abs(a - b) > decimal.Decimal(10) ** -(digits // 2 + 2):
             m = (a + b) / 2
@@ -211,20 +215,21 @@ def cake_rotary_table(sections, base: float = 10000.0, *, shared: bool = False, 
     """
     sections = [int(n) for n in sections]
     pairs = sum(sections)
-    base = float(base)
-    if freqs is not None:
+    if freqs is None:
+        base = float(base)
+        largest = 1 / base if 0 < base < 1 else 1.0
+    else:
         freqs = [float(f) for f in freqs]
         if len(freqs) != pairs:
             raise ValueError(f"{len(freqs)} frequencies for {pairs} pairs")
         for f in freqs:
             if not math.isfinite(f):
                 raise ValueError(f"a frequency is {f}")
+        largest = max(map(abs, freqs), default=0.0)
     # 64 bits of a turn, and the whole turns that drop out, are more than a double has
-    largest = max((abs(f) for f in freqs), default=0.0) if freqs is not None else max(1.0, 1 / base if base > 0 else 1.0)
     digits = 50 + max(0, math.frexp(min(largest, 1e308))[1] // 3)
     turns = []
-    with decimal.localcontext() as c:
-        c.prec = digits
+    with _digits(digits):
         if freqs is not None:
             freqs = [decimal.Decimal(f) for f in freqs]
         elif shared:

@@ -87,3 +87,14 @@ def test_refusals(cake):
     assert turns.numel() == axes.numel() == 0
     turns, _ = cake.cake_rotary_table((0, 8), shared=True, device="cpu")
     assert turns.numel() == 8
+
+
+def test_the_callers_context_and_an_unused_base(cake):
+    import decimal
+    want = cake.cake_rotary_table((16,), device="cpu")[0]
+    given = cake.cake_rotary_table((2,), freqs=[0.5, 0.25], device="cpu")[0]
+    with localcontext() as c:
+        c.prec, c.rounding, c.Emax = 5, decimal.ROUND_DOWN, 20
+        c.traps[decimal.Inexact] = True
+        assert torch.equal(cake.cake_rotary_table((16,), device="cpu")[0], want)
+        assert torch.equal(cake.cake_rotary_table((2,), None, freqs=[0.5, 0.25], device="cpu")[0], given)
